@@ -370,6 +370,153 @@ kda_status_t kda_prefill_backward(const kda_prefill_desc_t *desc, const void *q,
                                   float *dg, float *dbeta, float *dS0, void *workspace,
                                   size_t workspace_bytes, int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Around the mixer: the norms, the token embedding and the loss of a model whose
+ * mixer is the recurrence above, each with its gradient.  Same rules: device
+ * pointers owned by the caller, nothing allocated or synchronised, launches on
+ * the given stream only.  Activations (x, h, y, gate, tables, weights of the
+ * loss, and their gradients) in act_dtype; norm weights and their gradients,
+ * losses and row statistics fp32.  All arithmetic and every sum is in fp32,
+ * rounded once on output.
+ * ------------------------------------------------------------------------ */
+
+typedef enum { KDA_GATE_NONE = 0, KDA_GATE_SIGMOID = 1, KDA_GATE_SILU = 2 } kda_gate_t;
+
+/* Problem description of the norms. */
+typedef struct {
+    int64_t tokens;      /* T >= 0                                                   */
+    int64_t x_stride;    /* elements from one token's x to the next's; 0 = heads x    */
+    int64_t gate_stride; /* width.  The same for gate.  At least heads x width        */
+    int32_t heads;       /* H >= 1 rows per token (1 for the residual norm)           */
+    int32_t width;       /* D, 1..16384: the norm's row                              */
+    int32_t act_dtype;   /* kda_dtype_t                                               */
+    int32_t gate;        /* kda_gate_t (KDA_GATE_NONE for the residual norm)          */
+    float eps;           /* > 0: r = 1 / sqrt(mean(x^2) + eps)                        */
+} kda_norm_desc_t;
+
+/*
+ * The norm of a mixer's output with its gate: per row of D channels
+ *     out = x r weight a(gate),  a = sigmoid, silu (z sigmoid(z)), or 1 without.
+ *   x, gate   [T, H, D], tokens x_stride / gate_stride elements apart (a slice of a
+ *             wider projection's output); gate NULL if and only if KDA_GATE_NONE.
+ *   weight    [D] fp32, shared by all heads, or NULL (ones).
+ *   out       [T, H, D] contiguous.
+ * Pointers aligned to their element (16 bytes, with widths and strides of whole
+ * 16-byte pieces, is the fast case), else KDA_ERR_INVALID_ARG.
+ */
+kda_status_t kda_gated_norm_forward(const kda_norm_desc_t *desc, const void *x, const void *gate,
+                                    const float *weight, void *out, void *stream);
+
+/*
+ * Its gradients for the adjoint d_out [T, H, D] (contiguous): dx, d_gate [T, H, D]
+ * (contiguous; d_gate NULL if and only if KDA_GATE_NONE) and d_weight [D] fp32
+ * (may be NULL; zeros when T = 0), from the forward's inputs alone.  The sum over
+ * rows behind d_weight has a fixed order.  Workspace (for d_weight):
+ * kda_norm_backward_workspace_size(desc), 16-byte aligned (0 on invalid
+ * arguments); KDA_ERR_WORKSPACE if it is short.
+ */
+size_t kda_norm_backward_workspace_size(const kda_norm_desc_t *desc);
+kda_status_t kda_gated_norm_backward(const kda_norm_desc_t *desc, const void *d_out, const void *x,
+                                     const void *gate, const float *weight, void *dx, void *d_gate,
+                                     float *d_weight, void *workspace, size_t workspace_bytes,
+                                     void *stream);
+
+/*
+ * The residual stream between two blocks: the block's output y enters it scaled,
+ * and the next block's input is its norm,
+ *     h_out = h + scale y,   out = h_out r weight      (out from the unrounded sum)
+ * over [T, D] (desc->heads = 1, KDA_GATE_NONE, strides 0).  y and h_out are both
+ * NULL (the first block: out = norm of h) or both given; h_out may equal h.
+ */
+kda_status_t kda_residual_norm_forward(const kda_norm_desc_t *desc, const void *h, const void *y,
+                                       const float *weight, float scale, void *h_out, void *out,
+                                       void *stream);
+
+/*
+ * Its gradients, from h_out: with d_out for out and d_h_out (NULL: zero) for h_out,
+ *     dh = d_h_out + (gradient through the norm),   dy = scale dh,
+ * and d_weight [D] fp32 (may be NULL).  dy may be NULL (scale = 1: dy is dh).  dh may
+ * equal d_h_out.  Workspace as kda_gated_norm_backward.
+ */
+kda_status_t kda_residual_norm_backward(const kda_norm_desc_t *desc, const void *d_out,
+                                        const void *d_h_out, const void *h_out, const float *weight,
+                                        float scale, void *dh, void *dy, float *d_weight,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
+typedef enum { KDA_ID_I32 = 0, KDA_ID_I64 = 1 } kda_id_dtype_t;
+
+/* Problem description of the embedding. */
+typedef struct {
+    int32_t tokens;    /* T, 0..2^30                       */
+    int32_t rows;      /* V, 1..2^30: the table's rows     */
+    int32_t width;     /* D, 1..65536                      */
+    int32_t act_dtype; /* kda_dtype_t of table, out, ...   */
+    int32_t id_dtype;  /* kda_id_dtype_t of ids            */
+    float scale;       /* finite                           */
+} kda_embed_desc_t;
+
+/*
+ * Token embedding: out[t] = scale table[ids[t]], table [V, D], ids [T], out [T, D].
+ * An id outside [0, V) gives a row of zeros and KDA_ERR_INVALID_ARG in dev_status.
+ */
+kda_status_t kda_embedding_forward(const kda_embed_desc_t *desc, const void *table, const void *ids,
+                                   void *out, int32_t *dev_status, void *stream);
+
+/*
+ * The table's gradient, every row of d_table [V, D] (zeros for ids that do not
+ * occur): d_table[v] = scale x sum of d_out[t] over the t with ids[t] = v.  The
+ * tokens are sorted by id (stable), so the sum has a fixed order and needs no
+ * floating-point atomics.  Ids outside [0, V) contribute nothing and are reported
+ * as above.  Workspace: kda_embedding_backward_workspace_size(desc), 16-byte
+ * aligned (0 on invalid arguments).
+ */
+size_t kda_embedding_backward_workspace_size(const kda_embed_desc_t *desc);
+kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_out,
+                                    const void *ids, void *d_table, void *workspace,
+                                    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
+/* Problem description of the cross entropy over a vocabulary. */
+typedef struct {
+    int64_t ignore_index; /* rows with this target have no loss and no gradient       */
+    int32_t tokens;       /* T, 0..2^24                                              */
+    int32_t vocab;        /* V, 1..2^24                                              */
+    int32_t width;        /* D, 1..2^17                                              */
+    int32_t act_dtype;    /* kda_dtype_t of x, weight and their gradients            */
+    int32_t id_dtype;     /* kda_id_dtype_t of targets                               */
+    int32_t piece;        /* backward: vocabulary columns per piece; 0 = choose      */
+} kda_ce_desc_t;
+
+/*
+ * Softmax cross entropy of the logits z = x weight^T, x [T, D], weight [V, D],
+ * which are never stored:
+ *     lse[t] = log sum_v exp(z_tv),   loss[t] = lse[t] - z_{t, targets[t]}
+ * (both [T] fp32; loss 0 where the target is ignore_index), and mean (one fp32, may
+ * be NULL): the mean loss over the other rows, 0 if there are none.  A target
+ * outside [0, V) other than ignore_index counts as ignored and is reported in
+ * dev_status (KDA_ERR_INVALID_ARG).  BF16: products of BF16 on tensor cores with
+ * fp32 accumulation; F32: each operand as three BF16 terms, six products, to
+ * about fp32's own accuracy.  x and weight 16-byte aligned (tensor-map copies).
+ * Workspace: kda_linear_ce_workspace_size(desc, 0), 16-byte aligned.
+ */
+size_t kda_linear_ce_workspace_size(const kda_ce_desc_t *desc, int32_t backward);
+kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, const void *weight,
+                                   const void *targets, float *loss, float *lse, float *mean,
+                                   void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                   void *stream);
+
+/*
+ * Its gradients for the adjoint d_loss [T] fp32 of loss (lse as the forward gave
+ * it): dx [T, D] and d_weight [V, D] (either may be NULL), both overwritten.  Works
+ * through the vocabulary in pieces of desc->piece columns (rounded up to 256): the
+ * piece's logits are computed again, dz = d_loss (softmax - onehot) of the piece is
+ * held in BF16 (F32: three BF16 terms), and both products read it.  Workspace:
+ * kda_linear_ce_workspace_size(desc, 1), 16-byte aligned.
+ */
+kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, const void *weight,
+                                    const void *targets, const float *lse, const float *d_loss,
+                                    void *dx, void *d_weight, void *workspace,
+                                    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char *kda_status_string(kda_status_t status);
 

@@ -27,10 +27,23 @@ from ._native import (  # noqa: F401
     state_compose,
     state_transfer,
 )
+from ._lm import (  # noqa: F401
+    embedding,
+    embedding_backward,
+    gated_norm,
+    gated_norm_backward,
+    linear_cross_entropy,
+    linear_cross_entropy_backward,
+    residual_norm,
+    residual_norm_backward,
+)
 
-__all__ = ["KDAError", "PrefillDesc", "decode_step", "lib", "library_path", "num_checkpoints",
+__all__ = ["KDAError", "PrefillDesc", "decode_step", "embedding", "embedding_backward", "gated_norm",
+           "gated_norm_backward", "lib", "library_path", "linear_cross_entropy",
+           "linear_cross_entropy_backward", "num_checkpoints",
            "prefill_backward",
            "prefill_backward_num_segments", "prefill_backward_workspace_size", "prefill_chunked", "prefill_chunked_ckpt", "prefill_chunked_gated",
            "prefill_ckpt_workspace_size", "prefill_combine", "prefill_desc",
-           "prefill_num_segments", "prefill_segments", "prefill_workspace_size", "state_compose",
+           "prefill_num_segments", "prefill_segments", "prefill_workspace_size", "residual_norm",
+           "residual_norm_backward", "state_compose",
            "state_transfer"]

@@ -1,0 +1,838 @@
+// Softmax cross entropy over a vocabulary from the last hidden states, without the
+// logits ever being an array.  x [T][D], W [V][D], z = x W^T:
+//     lse_t = log sum_v exp(z_tv),   loss_t = lse_t - z_t,y_t
+//     dz_tv = d_loss_t (exp(z_tv - lse_t) - [v = y_t]),  dx = dz W,  dW = dz^T x.
+//
+// Forward: one product whose epilogue keeps, per row and 128 columns, the running
+// maximum and the sum of exponentials (and picks the target's logit); a second
+// kernel joins them.  Backward, per piece of the vocabulary: the piece's logits
+// again, their dz in BF16 (the only array of that shape, one piece wide), then the
+// two products that read it.  The logits cost 2 T V D operations once more; keeping
+// them would cost T V words.
+//
+// All four products run in one persistent kernel on tcgen05 (gemm_kernel).  fp32
+// operands are split into three BF16 terms (8 + 8 + 8 bits of the fp32 mantissa's
+// 24) and the six products of terms whose weight is 2^-16 or more are accumulated,
+// smallest first, so an fp32 problem is the same kernel with six times the steps.
+#include <math.h>
+
+#include "kda_internal.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace {
+
+using namespace sm100;
+
+constexpr int BM = 128, BN = 256, BK = 64;
+constexpr int kStages = 4, kABytes = BM * BK * 2, kBBytes = BN * BK * 2;
+constexpr int kStage = kABytes + kBBytes;
+constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
+constexpr int kGroupM = 16;  // row tiles that share a sweep over the column tiles
+constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint32_t kTmemCols = 512;  // two 256-column accumulators
+
+enum { B_FULL = 0, B_EMPTY = B_FULL + kStages, B_ACCF = B_EMPTY + kStages, B_ACCE = B_ACCF + 2,
+       B_FIN = B_ACCE + 2, B_N = B_FIN + 1 };
+constexpr int kBarOff = kStages * kStage, kMisc = kBarOff + B_N * 8;
+constexpr int kSmem = kMisc + 16 + 1024;
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+
+enum { EPI_STATS = 0, EPI_DZ = 1, EPI_OUT = 2 };
+
+struct Targets {
+    const void *ids;
+    int wide, vocab;
+    long long ignore;
+    int32_t *status;
+    // The target of row t; -1 where it is to be ignored (or, recorded, outside
+    // the vocabulary).
+    __device__ __forceinline__ int at(long long t, bool report) const {
+        const long long y = wide ? ((const long long *)ids)[t] : ((const int *)ids)[t];
+        if (y == ignore) return -1;
+        if (y < 0 || y >= vocab) {
+            if (report) dev_fail(status, KDA_ERR_INVALID_ARG);
+            return -1;
+        }
+        return (int)y;
+    }
+};
+
+struct GemmArgs {
+    int M, N;                  // rows and columns of the product that exist
+    int m_tiles, n_tiles, k_blocks, splits, pairs;
+    int a_row0, b_row0;        // added to the operands' non-contraction coordinate
+    int ak_row0, bk_row0;      // added to the contraction coordinate of MN-major operands
+    // EPI_STATS, EPI_DZ
+    Targets y;
+    float2 *part;              // [2 n_tiles][M] (maximum, sum)
+    float *z_y;                // [M]
+    unsigned *ticket;          // cleared for the join kernel
+    const float *lse, *d_loss;
+    __nv_bfloat16 *dz;         // [planes][M][pitch]
+    int pitch, planes;
+    // EPI_OUT: value (+ acc_in) to acc_out [splits][M][N] fp32, or to out
+    const float *acc_in;
+    float *acc_out;
+    void *out;
+    int out_bf16, vec;
+    int32_t *status;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, uint64_t tmap, int x, int y, int z,
+                                            uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// MN-major operand with 128-byte swizzle, as boxes of 64 elements x BK rows lay it
+// down: 8 rows (along K) of 128 bytes form an atom, atoms follow each other along
+// K (1024 bytes), boxes along M / N (8192 bytes).
+__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((BK * 128) >> 4) << 16;  // between 64-element boxes
+    d |= (uint64_t)(1024 >> 4) << 32;        // between 8-row atoms along K
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+struct Tile {
+    int m, n, split, kb0, kb1;
+};
+__device__ __forceinline__ Tile tile_at(const GemmArgs &p, int w) {
+    Tile t;
+    const int per = p.m_tiles * p.n_tiles;
+    t.split = w / per;
+    const int r = w - t.split * per, g = r / (kGroupM * p.n_tiles), q = r - g * kGroupM * p.n_tiles;
+    const int gm = min(kGroupM, p.m_tiles - g * kGroupM);
+    t.n = q / gm;
+    t.m = g * kGroupM + (q - t.n * gm);
+    t.kb0 = (int)((long long)p.k_blocks * t.split / p.splits);
+    t.kb1 = (int)((long long)p.k_blocks * (t.split + 1) / p.splits);
+    return t;
+}
+
+// Terms of pair i of an fp32 product, smallest weight first: (1,1) (2,0) (0,2)
+// (1,0) (0,1) (0,0); a single pair is (0,0).
+__device__ __forceinline__ int term_a(int i, int pairs) {
+    return pairs == 1 ? 0 : (0x001021 >> (4 * (i))) & 3;
+}
+__device__ __forceinline__ int term_b(int i, int pairs) {
+    return pairs == 1 ? 0 : (0x010201 >> (4 * (i))) & 3;
+}
+
+template <int EPI>
+__device__ __forceinline__ void epilogue(const GemmArgs &p, const Tile &t, uint32_t tacc, int quarter,
+                                         int half, int lane, uint32_t acce) {
+    const long long row = (long long)t.m * BM + 32 * quarter + lane;
+    const bool live = row < p.M;
+    const int c0 = t.n * BN + half * 128;  // first column of this warp, in the launch's columns
+    const uint32_t src = tacc + ((uint32_t)(32 * quarter) << 16) + 128 * half;
+    int y = -1;
+    float mx = -INFINITY, sum = 0.f, lse2 = 0.f, g = 0.f;
+    if (EPI != EPI_OUT && live) {
+        y = p.y.at(row, t.n == 0 && half == 0);
+        if (EPI == EPI_DZ) {
+            lse2 = p.lse[row] * kLog2e;
+            g = y >= 0 ? p.d_loss[row] : 0.f;
+        }
+        y = y >= 0 ? y - p.b_row0 : -1;
+    }
+#pragma unroll 1
+    for (int ch = 0; ch < 4; ++ch) {
+        float v[32];
+        __syncwarp();
+        tmem_ld32(src + 32 * ch, v);
+        if (ch == 3) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acce);  // the accumulator is in registers
+        }
+        const int c = c0 + 32 * ch;
+        const bool mine = y >= c && y < c + 32;
+        if (EPI == EPI_STATS) {
+            if (c + 32 > p.N) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = c + i < p.N ? v[i] : -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, mine)) {
+                float z = 0.f;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z = c + i == y ? v[i] : z;
+                if (mine) p.z_y[row] = z;
+            }
+            float m = mx;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
+            const float ref = m == -INFINITY ? 0.f : m * kLog2e;
+            sum *= exp2f(mx == -INFINITY ? -INFINITY : fmaf(mx, kLog2e, -ref));
+            float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) s[i & 3] += exp2f(fmaf(v[i], kLog2e, -ref));
+            sum += (s[0] + s[1]) + (s[2] + s[3]);
+            mx = m;
+        } else if (EPI == EPI_DZ) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                const float e = g * exp2f(fmaf(v[i], kLog2e, -lse2));
+                v[i] = g != 0.f && c + i < p.N ? e : 0.f;
+            }
+            if (__any_sync(0xffffffffu, mine)) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] -= c + i == y ? g : 0.f;
+            }
+            if (live) {
+                for (int pl = 0; pl < p.planes; ++pl) {
+                    uint4 *dst = (uint4 *)(p.dz + ((size_t)pl * p.M + row) * p.pitch + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            w[k] = pack_bf16x2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+                            v[8 * i + 2 * k] -= __uint_as_float(w[k] << 16);
+                            v[8 * i + 2 * k + 1] -= __uint_as_float(w[k] & 0xffff0000u);
+                        }
+                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+        } else if (live && c < p.N) {
+            const size_t at = (size_t)row * p.N + c;
+            const int n = min(32, p.N - c);
+            if (p.acc_in) {
+                if (p.vec && n == 32) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 a = *(const float4 *)(p.acc_in + at + 4 * i);
+                        v[4 * i] += a.x; v[4 * i + 1] += a.y; v[4 * i + 2] += a.z; v[4 * i + 3] += a.w;
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < n) v[i] += p.acc_in[at + i];
+                }
+            }
+            if (p.out && p.out_bf16) {
+                __nv_bfloat16 *o = (__nv_bfloat16 *)p.out + at;
+                if (p.vec && n == 32) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        *(uint4 *)(o + 8 * i) =
+                            make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]),
+                                       pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
+                                       pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
+                                       pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < n) o[i] = __float2bfloat16_rn(v[i]);
+                }
+            } else {
+                float *o = p.out ? (float *)p.out + at
+                                 : p.acc_out + (size_t)t.split * p.M * p.N + at;
+                if (p.vec && n == 32) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        *(float4 *)(o + 4 * i) =
+                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (i < n) o[i] = v[i];
+                }
+            }
+        }
+    }
+    if (EPI == EPI_STATS && live)
+        p.part[(size_t)(2 * t.n + half) * p.M + row] = make_float2(mx, sum);
+}
+
+// C = A B^T over tiles of 128 x 256 and steps of 64 along the contraction, one
+// persistent CTA per SM:
+//   warp 0   one thread loads both operands' boxes (TMA, 128-byte swizzle) into
+//            four stages;
+//   warp 1   one thread issues four tcgen05.mma (128 x 256 x 16) per stage into one
+//            of two TMEM accumulators;
+//   warps 2-9 the epilogue of the other accumulator: thread = row, 128 columns.
+// An operand is K-major (its contraction index contiguous) or MN-major (its row
+// index contiguous: W and x in dx = dz W, dz and x in dW = dz^T x), so nothing is
+// transposed in memory.
+template <int EPI, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1)
+    gemm_kernel(const __grid_constant__ GemmArgs p, const __grid_constant__ CUtensorMap tm_a,
+                const __grid_constant__ CUtensorMap tm_b) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
+    const uint32_t sb = smem_addr(sm);
+    auto bar = [&](int i) { return sb + kBarOff + 8 * i; };
+    volatile int *abort = (volatile int *)(sm + kMisc);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int work = p.m_tiles * p.n_tiles * p.splits;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(bar(B_FULL + i), 1);
+            mbar_init(bar(B_EMPTY + i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(B_ACCF + i), 1);
+            mbar_init(bar(B_ACCE + i), kEpiWarps);
+        }
+        mbar_init(bar(B_FIN), 1);
+        *abort = 0;
+        mbar_fence_init();
+    }
+    if (warp == 0) {
+        tmem_alloc(sb + kMisc + 4, kTmemCols);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *(volatile uint32_t *)(sm + kMisc + 4);
+    griddep_wait();
+    griddep_launch_dependents();
+    if (EPI == EPI_STATS && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t ta = reinterpret_cast<uint64_t>(&tm_a);
+            const uint64_t tb = reinterpret_cast<uint64_t>(&tm_b);
+            int it = 0;
+            bool ok = true;
+            for (int w = blockIdx.x; w < work && ok; w += gridDim.x) {
+                const Tile t = tile_at(p, w);
+                const int ar = t.m * BM + p.a_row0, br = t.n * BN + p.b_row0;
+                for (int pr = 0; pr < p.pairs && ok; ++pr) {
+                    const int pa = term_a(pr, p.pairs), pb = term_b(pr, p.pairs);
+                    for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
+                        const int s = it % kStages;
+                        ok = mbar_wait(bar(B_EMPTY + s), ((it / kStages) & 1) ^ 1, abort, kWaitLimit);
+                        if (!ok) break;
+                        const uint32_t full = bar(B_FULL + s), a = sb + s * kStage, b = a + kABytes;
+                        mbar_arrive_expect_tx(full, kStage);
+                        if (A_MN) {
+#pragma unroll
+                            for (int i = 0; i < BM / 64; ++i)
+                                tma_load_3d(a + i * BK * 128, ta, ar + 64 * i, kb * BK + p.ak_row0, pa,
+                                            full);
+                        } else {
+                            tma_load_3d(a, ta, kb * BK, ar, pa, full);
+                        }
+                        if (B_MN) {
+#pragma unroll
+                            for (int i = 0; i < BN / 64; ++i)
+                                tma_load_3d(b + i * BK * 128, tb, br + 64 * i, kb * BK + p.bk_row0, pb,
+                                            full);
+                        } else {
+                            tma_load_3d(b, tb, kb * BK, br, pb, full);
+                        }
+                    }
+                }
+            }
+            if (*abort) {  // let the copies in flight land before the CTA exits
+                volatile int never = 0;
+                for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
+                    mbar_wait(bar(B_FULL + k % kStages), (k / kStages) & 1, &never, kWaitLimit);
+            }
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = umma_idesc_bf16(BM, BN) | (A_MN ? 1u << 15 : 0u) |
+                                   (B_MN ? 1u << 16 : 0u);
+            int it = 0, i = 0;
+            bool ok = true;
+            for (int w = blockIdx.x; w < work && ok; w += gridDim.x, ++i) {
+                const Tile t = tile_at(p, w);
+                const int acc = i & 1, steps = (t.kb1 - t.kb0) * p.pairs;
+                ok = mbar_wait(bar(B_ACCE + acc), ((i >> 1) & 1) ^ 1, abort, kWaitLimit);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < steps; ++k, ++it) {
+                    const int s = it % kStages;
+                    ok = mbar_wait(bar(B_FULL + s), (it / kStages) & 1, abort, kWaitLimit);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = sb + s * kStage, b = a + kABytes;
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        umma_bf16(tmem + BN * acc,
+                                  A_MN ? umma_desc_mn_sw128(a + kk * 2048)
+                                       : umma_desc_sw128(a + kk * 32, 1024),
+                                  B_MN ? umma_desc_mn_sw128(b + kk * 2048)
+                                       : umma_desc_sw128(b + kk * 32, 1024),
+                                  idesc, k + kk > 0);
+                    umma_commit(bar(B_EMPTY + s));
+                }
+                if (ok) umma_commit(bar(B_ACCF + acc));
+            }
+            if (*abort) {  // products in flight complete before TMEM is freed
+                umma_commit(bar(B_FIN));
+                volatile int never = 0;
+                mbar_wait(bar(B_FIN), 0, &never, kWaitLimit);
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        int i = 0;
+        for (int w = blockIdx.x; w < work; w += gridDim.x, ++i) {
+            const Tile t = tile_at(p, w);
+            const int acc = i & 1;
+            if (!__all_sync(0xffffffffu,
+                            mbar_wait(bar(B_ACCF + acc), (i >> 1) & 1, abort, kWaitLimit)))
+                break;
+            tc_fence_after();
+            epilogue<EPI>(p, t, tmem + BN * acc, quarter, half, lane, bar(B_ACCE + acc));
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x == 0 && *abort) dev_fail(p.status, KDA_ERR_TIMEOUT);
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Joins the row statistics: 32 rows per block, 32 slices of the partial sums, each
+// slice and then the slices in order.  Writes lse and the loss (0 where the target
+// is ignored), and the mean over the others: per block (sum, count), added up in
+// block order by the block that finishes last.
+__global__ void __launch_bounds__(1024)
+    ce_join_kernel(const float2 *part, int parts, int M, Targets y, const float *z_y, float *loss,
+                   float *lse, float *mean, float2 *sums, unsigned *ticket) {
+    __shared__ float2 sh[32][33];
+    __shared__ bool last;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+    const long long row = (long long)blockIdx.x * 32 + lane;
+    auto join = [](float2 a, float2 b) {
+        const float m = fmaxf(a.x, b.x);
+        if (m == -INFINITY) return make_float2(m, a.y + b.y);
+        return make_float2(m, a.y * exp2f((a.x - m) * kLog2e) + b.y * exp2f((b.x - m) * kLog2e));
+    };
+    float2 v = make_float2(-INFINITY, 0.f);
+    if (row < M) {
+#pragma unroll 4
+        for (int q = sl; q < parts; q += 32) v = join(v, part[(size_t)q * M + row]);
+    }
+    sh[sl][lane] = v;
+    __syncthreads();
+    if (sl != 0) {
+        if (!mean) return;
+    } else {
+        float l = 0.f, n = 0.f;
+        if (row < M) {
+            for (int i = 1; i < 32; ++i) v = join(v, sh[i][lane]);
+            const float e = v.x + kLn2 * log2f(v.y);
+            const int t = y.at(row, false);
+            if (t >= 0) {
+                l = e - z_y[row];
+                n = 1.f;
+            }
+            lse[row] = e;
+            loss[row] = l;
+        }
+        if (!mean) return;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, o);
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+        }
+        if (lane == 0) {
+            sums[blockIdx.x] = make_float2(l, n);
+            __threadfence();
+            last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+        }
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    float2 s = make_float2(0.f, 0.f);
+    for (int b = threadIdx.x; b < (int)gridDim.x; b += 1024) {
+        const float2 u = __ldcg(&sums[b]);
+        s.x += u.x;
+        s.y += u.y;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
+        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    }
+    __syncthreads();
+    if (lane == 0) sh[0][sl] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        s = make_float2(0.f, 0.f);
+        for (int i = 0; i < 32; ++i) {
+            s.x += sh[0][i].x;
+            s.y += sh[0][i].y;
+        }
+        *mean = s.y > 0.f ? s.x / s.y : 0.f;  // no target counts: 0
+    }
+}
+
+// Rows of an operand as `planes` BF16 terms with a pitch of whole 16-byte pieces
+// (zeros past the width): fp32 operands, and BF16 ones whose rows a tensor map
+// cannot address.
+template <typename T>
+__global__ void __launch_bounds__(256) pack_kernel(const T *src, __nv_bfloat16 *dst, long long rows,
+                                                   int D, int pitch, int planes) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int pieces = pitch / 8;
+    const long long total = rows * pieces;
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+        const long long r = i / pieces;
+        const int c = (int)(i - r * pieces) * 8;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = c + j < D ? act_ld(src, (size_t)(r * D + c + j)) : 0.f;
+        for (int pl = 0; pl < planes; ++pl) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+                v[2 * k] -= __uint_as_float(w[k] << 16);
+                v[2 * k + 1] -= __uint_as_float(w[k] & 0xffff0000u);
+            }
+            *(uint4 *)(dst + ((size_t)pl * rows + r) * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// out = sum over splits of acc[s], in order.
+template <typename T>
+__global__ void __launch_bounds__(256) split_sum_kernel(const float *acc, T *out, long long n,
+                                                        int splits) {
+    griddep_wait();
+    griddep_launch_dependents();
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+        float s = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < splits; ++k) s += acc[(size_t)k * n + i];
+        act_st(out, (size_t)i, s);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
+
+int sms() {
+    int dev = 0, n = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+    return n;
+}
+
+// Width of dz's buffer: at most 512 MiB of BF16 (or three fp32 terms) in whole
+// column tiles, unless the caller says.
+int piece_cols(const kda_ce_desc_t *d, int planes) {
+    const long long all = (long long)cdiv(d->vocab, BN) * BN;
+    long long cols = d->piece;
+    if (cols <= 0) {
+        cols = (512ll << 20) / ((long long)(d->tokens > 0 ? d->tokens : 1) * planes * 2);
+        if (cols < 4096) cols = 4096;
+        if (cols < all) {  // equal pieces
+            const int n = cdiv(all, cols);
+            cols = cdiv(all, n);
+        }
+    }
+    cols = (long long)cdiv(cols, BN) * BN;
+    return (int)(cols < all ? cols : all);
+}
+
+struct Layout {
+    int planes, pairs, pitch, piece, pieces, dx_splits;
+    bool pack;
+    size_t xp, wp, part, zy, sums, dz, acc, total;
+};
+
+// Pieces of the workspace.  pack: operands are copied (fp32 terms, or rows padded
+// to the pitch of whole 16-byte pieces that a tensor map needs).
+Layout layout_for(const kda_ce_desc_t *d, bool backward) {
+    Layout l = {};
+    const bool pack = d->act_dtype == KDA_DTYPE_F32 || d->width % 8 != 0;
+    const size_t T = d->tokens, V = d->vocab;
+    l.planes = d->act_dtype == KDA_DTYPE_F32 ? 3 : 1;
+    l.pairs = l.planes == 3 ? 6 : 1;
+    l.pitch = (d->width + 7) / 8 * 8;
+    l.pack = pack;
+    l.xp = pack ? round256(T * l.pitch * l.planes * 2) : 0;
+    l.wp = pack ? round256(V * l.pitch * l.planes * 2) : 0;
+    if (!backward) {
+        l.part = round256((size_t)2 * cdiv(V, BN) * T * sizeof(float2));
+        l.zy = round256(T * 4);
+        l.sums = round256(((T + 31) / 32) * sizeof(float2)) + 256;
+    } else {
+        l.piece = piece_cols(d, l.planes);
+        l.pieces = cdiv(V, l.piece);
+        l.dz = round256(T * l.piece * l.planes * 2);
+        // dx has few tiles when T and D are small: its contraction over the
+        // vocabulary is then split so that every SM has a share
+        const int tiles = cdiv(T, BM) * cdiv(d->width, BN), n = sms();
+        l.dx_splits = 1;
+        if (l.pieces == 1 && tiles > 0 && tiles < n) {
+            l.dx_splits = n / tiles;
+            const int most = l.piece / BK / 4;  // at least four steps each
+            if (l.dx_splits > most) l.dx_splits = most < 1 ? 1 : most;
+        }
+        if (l.pieces > 1 || l.dx_splits > 1)
+            l.acc = round256((size_t)l.dx_splits * T * d->width * 4);
+    }
+    l.total = l.xp + l.wp + l.part + l.zy + l.sums + l.dz + l.acc;
+    return l;
+}
+
+kda_status_t check(const kda_ce_desc_t *d) {
+    if (!d) return KDA_ERR_INVALID_ARG;
+    if (d->tokens < 0 || d->vocab < 1 || d->width < 1 || d->piece < 0) return KDA_ERR_INVALID_ARG;
+    if (d->act_dtype != KDA_DTYPE_F32 && d->act_dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
+    if (d->id_dtype != KDA_ID_I32 && d->id_dtype != KDA_ID_I64) return KDA_ERR_UNSUPPORTED;
+    // tile and coordinate arithmetic is 32-bit
+    if (d->tokens > (1 << 24) || d->vocab > (1 << 24) || d->width > (1 << 17))
+        return KDA_ERR_UNSUPPORTED;
+    if ((long long)cdiv(d->tokens, BM) * cdiv(d->vocab, BN) > (1ll << 30)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, long long pitch, int planes,
+            int box_rows) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
+    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(rows * pitch) * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+               estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap &tb,
+                     cudaStream_t st) {
+    cudaError_t e = set_max_dynamic_smem((const void *)gemm_kernel<EPI, A_MN, B_MN>, kSmem);
+    if (e != cudaSuccess) return e;
+    const long long work = (long long)p.m_tiles * p.n_tiles * p.splits;
+    const int n = sms();
+    return launch_dependent(gemm_kernel<EPI, A_MN, B_MN>, dim3((unsigned)(work < n ? work : n)),
+                            dim3(kThreads), kSmem, st, p, ta, tb);
+}
+
+cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *src, __nv_bfloat16 *dst,
+                     long long rows, cudaStream_t st) {
+    const long long need = (rows * (l.pitch / 8) + 255) / 256, most = 16ll * sms();
+    const dim3 grid((unsigned)(need < most ? need : most));
+    if (d->act_dtype == KDA_DTYPE_F32)
+        return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)src, dst,
+                                rows, d->width, l.pitch, l.planes);
+    return launch_dependent(pack_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
+                            (const __nv_bfloat16 *)src, dst, rows, d->width, l.pitch, l.planes);
+}
+
+bool bad_ids(const kda_ce_desc_t *d, const void *ids) {
+    return !ids || (uintptr_t)ids % (d->id_dtype == KDA_ID_I64 ? 8 : 4);
+}
+bool bad16(const void *p) { return !p || ((uintptr_t)p & 15u); }
+bool bad_f32(const void *p) { return !p || ((uintptr_t)p & 3u); }
+bool bad_act(const kda_ce_desc_t *d, const void *p) {
+    return !p || (uintptr_t)p % (d->act_dtype == KDA_DTYPE_BF16 ? 2 : 4);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+size_t kda_linear_ce_workspace_size(const kda_ce_desc_t *desc, int32_t backward) {
+    if (check(desc) != KDA_OK || desc->tokens == 0) return 0;
+    return layout_for(desc, backward != 0).total;
+}
+
+kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, const void *weight,
+                                   const void *targets, float *loss, float *lse, float *mean,
+                                   void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                   void *stream) {
+    kda_status_t rc = check(desc);
+    if (rc != KDA_OK) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (((uintptr_t)mean & 3u) || ((uintptr_t)dev_status & 3u)) return KDA_ERR_INVALID_ARG;
+    if (desc->tokens == 0) {
+        if (mean && cudaMemsetAsync(mean, 0, 4, st) != cudaSuccess) return KDA_ERR_CUDA;
+        return KDA_OK;
+    }
+    if (bad16(x) || bad16(weight) || bad_ids(desc, targets) || bad_f32(loss) ||
+        bad_f32(lse))
+        return KDA_ERR_INVALID_ARG;
+    const Layout l = layout_for(desc, false);
+    if (!workspace || workspace_bytes < l.total || ((uintptr_t)workspace & 15u))
+        return KDA_ERR_WORKSPACE;
+    uint8_t *ws = (uint8_t *)workspace;
+    const __nv_bfloat16 *xp = (const __nv_bfloat16 *)x, *wp = (const __nv_bfloat16 *)weight;
+    float2 *part = (float2 *)(ws + l.xp + l.wp);
+    float *zy = (float *)(ws + l.xp + l.wp + l.part);
+    float2 *sums = (float2 *)(ws + l.xp + l.wp + l.part + l.zy);
+    unsigned *ticket = (unsigned *)(ws + l.total - 256);
+    if (l.pack) {
+        if (run_pack(desc, l, x, (__nv_bfloat16 *)ws, desc->tokens, st) != cudaSuccess ||
+            run_pack(desc, l, weight, (__nv_bfloat16 *)(ws + l.xp), desc->vocab, st) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        xp = (const __nv_bfloat16 *)ws;
+        wp = (const __nv_bfloat16 *)(ws + l.xp);
+    }
+    const int inner = l.pack ? l.pitch : desc->width;
+    CUtensorMap ta, tb;
+    if (!encode(&ta, xp, inner, desc->tokens, inner, l.planes, BM) ||
+        !encode(&tb, wp, inner, desc->vocab, inner, l.planes, BN))
+        return KDA_ERR_CUDA;
+    GemmArgs p = {};
+    p.M = desc->tokens;
+    p.N = desc->vocab;
+    p.m_tiles = cdiv(p.M, BM);
+    p.n_tiles = cdiv(p.N, BN);
+    p.k_blocks = cdiv(desc->width, BK);
+    p.splits = 1;
+    p.pairs = l.pairs;
+    p.y = {targets, desc->id_dtype == KDA_ID_I64, desc->vocab, desc->ignore_index, dev_status};
+    p.part = part;
+    p.z_y = zy;
+    p.ticket = ticket;
+    p.status = dev_status;
+    if (run_gemm<EPI_STATS, false, false>(p, ta, tb, st) != cudaSuccess) return KDA_ERR_CUDA;
+    if (launch_dependent(ce_join_kernel, dim3(cdiv(p.M, 32)), dim3(1024), 0, st,
+                         (const float2 *)part, 2 * p.n_tiles, p.M, p.y, (const float *)zy, loss, lse,
+                         mean, sums, ticket) != cudaSuccess)
+        return KDA_ERR_CUDA;
+    return KDA_OK;
+}
+
+kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, const void *weight,
+                                    const void *targets, const float *lse, const float *d_loss,
+                                    void *dx, void *d_weight, void *workspace,
+                                    size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    kda_status_t rc = check(desc);
+    if (rc != KDA_OK) return rc;
+    cudaStream_t st = (cudaStream_t)stream;
+    const size_t size = desc->act_dtype == KDA_DTYPE_BF16 ? 2 : 4;
+    if ((dx && bad_act(desc, dx)) || (d_weight && bad_act(desc, d_weight)) ||
+        ((uintptr_t)dev_status & 3u))
+        return KDA_ERR_INVALID_ARG;
+    if (desc->tokens == 0) {
+        if (d_weight && cudaMemsetAsync(d_weight, 0, (size_t)desc->vocab * desc->width * size, st) !=
+                            cudaSuccess)
+            return KDA_ERR_CUDA;
+        return KDA_OK;
+    }
+    if (bad16(x) || bad16(weight) || bad_ids(desc, targets) || bad_f32(lse) ||
+        bad_f32(d_loss))
+        return KDA_ERR_INVALID_ARG;
+    if (!dx && !d_weight) return KDA_OK;
+    const Layout l = layout_for(desc, true);
+    if (!workspace || workspace_bytes < l.total || ((uintptr_t)workspace & 15u))
+        return KDA_ERR_WORKSPACE;
+    uint8_t *ws = (uint8_t *)workspace;
+    const __nv_bfloat16 *xp = (const __nv_bfloat16 *)x, *wp = (const __nv_bfloat16 *)weight;
+    __nv_bfloat16 *dz = (__nv_bfloat16 *)(ws + l.xp + l.wp);
+    float *acc = (float *)(ws + l.xp + l.wp + l.dz);
+    if (l.pack) {
+        if (run_pack(desc, l, x, (__nv_bfloat16 *)ws, desc->tokens, st) != cudaSuccess ||
+            run_pack(desc, l, weight, (__nv_bfloat16 *)(ws + l.xp), desc->vocab, st) != cudaSuccess)
+            return KDA_ERR_CUDA;
+        xp = (const __nv_bfloat16 *)ws;
+        wp = (const __nv_bfloat16 *)(ws + l.xp);
+    }
+    const int T = desc->tokens, V = desc->vocab, D = desc->width;
+    const int inner = l.pack ? l.pitch : D;
+    // x and W as operands of the logits (contraction over D, K-major) and of the
+    // gradients (contraction over tokens or vocabulary, MN-major); dz both ways
+    CUtensorMap x_k, w_k, w_mn, x_mn, dz_k, dz_mn;
+    if (!encode(&x_k, xp, inner, T, inner, l.planes, BM) ||
+        !encode(&w_k, wp, inner, V, inner, l.planes, BN) ||
+        !encode(&w_mn, wp, inner, V, inner, l.planes, BK) ||
+        !encode(&x_mn, xp, inner, T, inner, l.planes, BK) ||
+        !encode(&dz_k, dz, l.piece, T, l.piece, l.planes, BM) ||
+        !encode(&dz_mn, dz, l.piece, T, l.piece, l.planes, BK))
+        return KDA_ERR_CUDA;
+    for (int k = 0; k < l.pieces; ++k) {
+        const int v0 = k * l.piece, cols = V - v0 < l.piece ? V - v0 : l.piece;
+        GemmArgs p = {};
+        p.status = dev_status;
+        p.pairs = l.pairs;
+        p.splits = 1;
+        p.M = T;
+        p.N = cols;
+        p.m_tiles = cdiv(T, BM);
+        p.n_tiles = cdiv(cols, BN);
+        p.k_blocks = cdiv(D, BK);
+        p.b_row0 = v0;
+        p.y = {targets, desc->id_dtype == KDA_ID_I64, V, desc->ignore_index, dev_status};
+        p.lse = lse;
+        p.d_loss = d_loss;
+        p.dz = dz;
+        p.pitch = l.piece;
+        p.planes = l.planes;
+        if (run_gemm<EPI_DZ, false, false>(p, x_k, w_k, st) != cudaSuccess) return KDA_ERR_CUDA;
+        if (dx) {
+            GemmArgs q = {};
+            q.status = dev_status;
+            q.pairs = l.pairs;
+            q.splits = l.dx_splits;
+            q.M = T;
+            q.N = D;
+            q.m_tiles = cdiv(T, BM);
+            q.n_tiles = cdiv(D, BN);
+            q.k_blocks = cdiv(cols, BK);
+            q.bk_row0 = v0;
+            q.acc_in = k > 0 ? acc : nullptr;
+            if (l.dx_splits == 1 && k == l.pieces - 1) q.out = dx;
+            else q.acc_out = acc;
+            q.out_bf16 = size == 2;
+            q.vec = D % 8 == 0 && ((uintptr_t)dx & 15u) == 0;
+            if (q.splits > q.k_blocks) return KDA_ERR_CUDA;
+            if (run_gemm<EPI_OUT, false, true>(q, dz_k, w_mn, st) != cudaSuccess)
+                return KDA_ERR_CUDA;
+            if (l.dx_splits > 1) {
+                const long long n = (long long)T * D, need = (n + 255) / 256, most = 16ll * sms();
+                const dim3 grid((unsigned)(need < most ? need : most));
+                const cudaError_t e =
+                    size == 2 ? launch_dependent(split_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0,
+                                                 st, (const float *)acc, (__nv_bfloat16 *)dx, n,
+                                                 l.dx_splits)
+                              : launch_dependent(split_sum_kernel<float>, grid, dim3(256), 0, st,
+                                                 (const float *)acc, (float *)dx, n, l.dx_splits);
+                if (e != cudaSuccess) return KDA_ERR_CUDA;
+            }
+        }
+        if (d_weight) {
+            GemmArgs q = {};
+            q.status = dev_status;
+            q.pairs = l.pairs;
+            q.splits = 1;
+            q.M = cols;
+            q.N = D;
+            q.m_tiles = cdiv(cols, BM);
+            q.n_tiles = cdiv(D, BN);
+            q.k_blocks = cdiv(T, BK);
+            q.out = (uint8_t *)d_weight + (size_t)v0 * D * size;
+            q.out_bf16 = size == 2;
+            q.vec = D % 8 == 0 && ((uintptr_t)d_weight & 15u) == 0;
+            if (run_gemm<EPI_OUT, true, true>(q, dz_mn, x_mn, st) != cudaSuccess)
+                return KDA_ERR_CUDA;
+        }
+    }
+    return KDA_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,504 @@
+// Token embedding: out[t] = scale table[id_t], and its table gradient
+//     d_table[v] = scale * sum over t with id_t = v, in the order of t, of d_out[t].
+//
+// Both move each row once and are bound by those bytes (the gradient also writes
+// the rows of tokens that do not occur: all V of them).
+//
+// The gradient sorts the tokens by id first (stable, so the sum's order is fixed
+// and there are no floating-point atomics): a radix sort of 32-bit (id, position)
+// pairs with two passes of up to 10 bits for vocabularies below 2^20.  The sorted tokens
+// and the V row ends are then one merged list (a row's tokens, then its end),
+// which is cut into parts of equal length, so a part's work is the same whether a
+// few frequent ids or many absent ones fall into it.  A part sums its tokens'
+// rows in fp32 and writes every row that ends in it; a row that began in an
+// earlier part is finished by a last kernel from the parts' fp32 remainders, in
+// order.
+#include <math.h>
+
+#include "kda_internal.cuh"
+#include "kda_sm100.cuh"
+#include "kda_vec.cuh"
+
+namespace kda {
+namespace {
+
+using sm100::griddep_launch_dependents;
+using sm100::griddep_wait;
+
+// Token id t, or `rows` (one past the table) with the error recorded if it is
+// outside it.
+__device__ __forceinline__ int load_id(const void *ids, int wide, long long t, int rows,
+                                       int32_t *status) {
+    const long long v = wide ? ((const long long *)ids)[t] : ((const int *)ids)[t];
+    if (v < 0 || v >= rows) {
+        dev_fail(status, KDA_ERR_INVALID_ARG);
+        return rows;
+    }
+    return (int)v;
+}
+
+// ------------------------------------------------------------------ look-up
+// `tpr` threads per token (a power of two), each up to four pieces in flight.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(256)
+    embed_kernel(const T *table, const void *ids, int wide, T *out, int tokens, int rows, int D,
+                 int tpr, float scale, int32_t *status) {
+    using P = Piece<T, VEC>;
+    griddep_wait();
+    griddep_launch_dependents();
+    const int per = 256 / tpr, g = threadIdx.x / tpr, lane = threadIdx.x - g * tpr;
+    const int pieces = (D + VEC - 1) / VEC;
+    for (long long t = (long long)blockIdx.x * per + g; t < tokens; t += (long long)gridDim.x * per) {
+        const int id = load_id(ids, wide, t, rows, lane == 0 && blockIdx.y == 0 ? status : nullptr);
+        const T *src = table + (size_t)id * D;
+        T *dst = out + (size_t)t * D;
+        for (int c0 = blockIdx.y * tpr * 4; c0 < pieces; c0 += gridDim.y * tpr * 4) {
+            P p[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * tpr + lane;
+                p[i].zero();
+                if (c < pieces && id < rows) p[i].load(src + (size_t)c * VEC);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int c = c0 + i * tpr + lane;
+                if (c >= pieces) continue;
+                float v[VEC];
+                p[i].get(v);
+#pragma unroll
+                for (int j = 0; j < VEC; ++j) v[j] *= scale;
+                P::store(dst + (size_t)c * VEC, v);
+            }
+        }
+    }
+}
+
+// --------------------------------------------------------------------- sort
+constexpr int kTile = 2048, kSortThreads = 256, kItems = kTile / kSortThreads;
+constexpr int kMaxBits = 10, kMaxDigits = 1 << kMaxBits;
+
+struct SortArgs {
+    const void *ids;
+    int wide, tokens, rows;
+    const int *in_key, *in_pos;  // NULL: the first pass reads ids
+    int *out_key, *out_pos;
+    int *hist;                   // [tiles][digits]
+    int shift, bits, tiles;
+    int32_t *status;
+};
+
+__device__ __forceinline__ int sort_key(const SortArgs &a, int i, bool report) {
+    return a.in_key ? a.in_key[i]
+                    : load_id(a.ids, a.wide, i, a.rows, report ? a.status : nullptr);
+}
+
+// Counts of this pass's digit in every tile of kTile tokens.
+__global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const __grid_constant__ SortArgs a) {
+    __shared__ int cnt[kMaxDigits];
+    const int digits = 1 << a.bits;
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) cnt[d] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+    const int base = blockIdx.x * kTile;
+    for (int k = threadIdx.x; k < kTile && base + k < a.tokens; k += kSortThreads)
+        atomicAdd(&cnt[(sort_key(a, base + k, true) >> a.shift) & (digits - 1)], 1);
+    __syncthreads();
+    for (int d = threadIdx.x; d < digits; d += kSortThreads)
+        a.hist[(size_t)blockIdx.x * digits + d] = cnt[d];
+}
+
+// Moves a tile's tokens to their places: all smaller digits, then the same digit
+// in earlier tiles, then in earlier warps of this tile, then earlier in the warp
+// (a warp holds consecutive tokens, 32 at a time).
+__global__ void __launch_bounds__(kSortThreads)
+    sort_scatter_kernel(const __grid_constant__ SortArgs a) {
+    constexpr int W = kSortThreads / 32;
+    __shared__ int first[kMaxDigits];             // place of this tile's first token per digit
+    __shared__ unsigned short cnt[W][kMaxDigits];  // tokens per warp and digit, then before it
+    __shared__ int part[kSortThreads];
+    const int digits = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int d = threadIdx.x; d < W * kMaxDigits; d += kSortThreads) (&cnt[0][0])[d] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    // per digit: tokens in all tiles, and in the tiles before this one; thread
+    // i takes `per` consecutive digits
+    const int per = (digits + kSortThreads - 1) / kSortThreads;
+    int mine = 0;
+    for (int k = 0; k < per; ++k) {
+        const int d = threadIdx.x * per + k;
+        if (d >= digits) break;
+        int before = 0, all = 0;
+        for (int t = 0; t < a.tiles; ++t) {
+            const int n = a.hist[(size_t)t * digits + d];
+            all += n;
+            before += t < (int)blockIdx.x ? n : 0;
+        }
+        first[d] = mine + before;
+        mine += all;
+    }
+    part[threadIdx.x] = mine;
+    __syncthreads();
+    if (warp == 0) {  // exclusive sums of the threads' totals
+        int v[W], s = 0;
+#pragma unroll
+        for (int k = 0; k < W; ++k) {
+            v[k] = s;
+            s += part[lane * W + k];
+        }
+        int inc = s;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += u;
+        }
+#pragma unroll
+        for (int k = 0; k < W; ++k) part[lane * W + k] = v[k] + inc - s;
+    }
+    __syncthreads();
+    for (int k = 0; k < per; ++k) {
+        const int d = threadIdx.x * per + k;
+        if (d < digits) first[d] += part[threadIdx.x];
+    }
+    const int base = blockIdx.x * kTile + warp * (kTile / W);
+    int key[kItems], rank[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = base + k * 32 + lane;
+        const bool in = i < a.tokens;
+        key[k] = in ? sort_key(a, i, false) : -1;
+        const int d = in ? (key[k] >> a.shift) & (digits - 1) : -1;
+        const unsigned same = __match_any_sync(0xffffffffu, d);
+        const int ahead = __popc(same & ((1u << lane) - 1u));
+        rank[k] = in ? cnt[warp][d] + ahead : 0;
+        __syncwarp();
+        if (in && ahead == 0) cnt[warp][d] += (unsigned short)__popc(same);
+        __syncwarp();
+    }
+    __syncthreads();
+    for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+        int s = 0;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const int n = cnt[w][d];
+            cnt[w][d] = (unsigned short)s;
+            s += n;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const int i = base + k * 32 + lane;
+        if (i >= a.tokens) continue;
+        const int d = (key[k] >> a.shift) & (digits - 1);
+        const int to = first[d] + cnt[warp][d] + rank[k];
+        a.out_key[to] = key[k];
+        a.out_pos[to] = a.in_key ? a.in_pos[i] : i;
+    }
+}
+
+// ---------------------------------------------------------------- segment sums
+struct SumArgs {
+    const int *key, *pos;  // sorted
+    int tokens, rows, D;
+    int parts;
+    long long per;         // entries of the merged list per part
+    float *carry, *head;   // [parts][D] fp32
+    float scale;
+};
+
+// Tokens among the first d entries of the merged list (token j comes before the
+// end of row i when key[j] <= i).
+__device__ __forceinline__ int merged_tokens(const SumArgs &a, long long d) {
+    long long lo = d > a.rows ? d - a.rows : 0, hi = d < a.tokens ? d : a.tokens;
+    while (lo < hi) {
+        const long long mid = (lo + hi) >> 1;
+        if (a.key[mid] <= d - 1 - mid) lo = mid + 1;
+        else hi = mid;
+    }
+    return (int)lo;
+}
+
+constexpr int kSumThreads = 128, kAhead = 4;
+
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kSumThreads)
+    segment_sum_kernel(const __grid_constant__ SumArgs a, const T *d_out, T *d_table) {
+    using P = Piece<T, VEC>;
+    __shared__ int cut[2];
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long total = (long long)a.rows + a.tokens;
+    const long long d0 = blockIdx.x * a.per, d1 = d0 + a.per < total ? d0 + a.per : total;
+    if (threadIdx.x < 2) cut[threadIdx.x] = merged_tokens(a, threadIdx.x ? d1 : d0);
+    __syncthreads();
+    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
+    if (c >= a.D) return;
+    int j = cut[0];
+    const int j1 = cut[1];
+    int i = (int)(d0 - j);
+    const int i1 = (int)(d1 - j1);
+    // a row that an earlier part began
+    bool begun = j > 0 && i < a.rows && a.key[j - 1] == i;
+    float acc[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+    auto end_row = [&]() {
+        float v[VEC];
+        if (begun) {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) a.head[(size_t)blockIdx.x * a.D + c + k] = acc[k];
+            begun = false;
+        } else {
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) v[k] = acc[k] * a.scale;
+            P::store(d_table + (size_t)i * a.D + c, v);
+        }
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+        ++i;
+    };
+    while (j < j1) {
+        P p[kAhead];
+        int id[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            id[u] = j + u < j1 ? a.key[j + u] : -1;
+            if (id[u] >= 0) p[u].load(d_out + (size_t)a.pos[j + u] * a.D + c);
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (id[u] < 0) continue;
+            while (i < id[u] && i < i1) end_row();
+            float v[VEC];
+            p[u].get(v);
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) acc[k] += v[k];
+        }
+        j += kAhead;
+    }
+    while (i < i1) end_row();
+    // what is left belongs to a row that ends in a later part
+    if (j1 <= cut[0] || a.key[j1 - 1] != i1) return;
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) a.carry[(size_t)blockIdx.x * a.D + c + k] = acc[k];
+}
+
+// Rows that span parts: the part in which the row ends adds the remainders of the
+// parts from the row's first token on, in order, and its own head.
+template <typename T, int VEC>
+__global__ void __launch_bounds__(kSumThreads)
+    segment_join_kernel(const __grid_constant__ SumArgs a, T *d_table) {
+    __shared__ int from;
+    griddep_wait();
+    griddep_launch_dependents();
+    const long long total = (long long)a.rows + a.tokens;
+    const long long d0 = blockIdx.x * a.per, d1 = d0 + a.per < total ? d0 + a.per : total;
+    if (threadIdx.x == 0) {
+        from = -1;
+        const int j0 = merged_tokens(a, d0), j1 = merged_tokens(a, d1);
+        const int i = (int)(d0 - j0), i1 = (int)(d1 - j1);
+        if (j0 > 0 && i < a.rows && a.key[j0 - 1] == i && i < i1) {
+            int lo = 0, hi = j0 - 1;  // the row's first token
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (a.key[mid] < i) lo = mid + 1;
+                else hi = mid;
+            }
+            from = (int)(((long long)lo + i) / a.per);
+        }
+    }
+    __syncthreads();
+    if (from < 0) return;
+    const int i = (int)(d0 - merged_tokens(a, d0));
+    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
+    if (c >= a.D) return;
+    float acc[VEC];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int q = from; q < (int)blockIdx.x; ++q)
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] += a.carry[(size_t)q * a.D + c + k];
+#pragma unroll
+    for (int k = 0; k < VEC; ++k)
+        acc[k] = (acc[k] + a.head[(size_t)blockIdx.x * a.D + c + k]) * a.scale;
+    Piece<T, VEC>::store(d_table + (size_t)i * a.D + c, acc);
+}
+
+// ------------------------------------------------------------------ host side
+size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int key_bits(int rows) {  // keys 0 .. rows (rows: an id outside the table)
+    int b = 1;
+    while (b < 31 && (rows >> b) != 0) ++b;
+    return b;
+}
+
+struct Plan {
+    int passes, bits, tiles, parts;
+    long long per;
+    size_t pairs, hist, rem, total;
+};
+
+// Parts of the merged list: at least 64 entries each (a part's binary search and
+// its fp32 remainder stay small beside its rows) and at most about 1,200 parts.
+Plan plan_for(int tokens, int rows, int D) {
+    Plan p;
+    const int b = key_bits(rows);
+    p.passes = (b + kMaxBits - 1) / kMaxBits;
+    p.bits = (b + p.passes - 1) / p.passes;
+    p.tiles = (tokens + kTile - 1) / kTile;
+    const long long total = (long long)tokens + rows;
+    p.per = (total + 1215) / 1216;
+    if (p.per < 64) p.per = 64;
+    p.parts = (int)((total + p.per - 1) / p.per);
+    p.pairs = round256((size_t)tokens * 4);
+    p.hist = round256((size_t)p.tiles * ((size_t)1 << p.bits) * 4);
+    p.rem = round256((size_t)p.parts * D * 4);
+    p.total = 4 * p.pairs + p.hist + 2 * p.rem;
+    return p;
+}
+
+bool wide_rows(int D, int size, const void *a, const void *b) {
+    return D % (16 / size) == 0 && ((uintptr_t)a & 15u) == 0 && ((uintptr_t)b & 15u) == 0;
+}
+
+template <typename T, int VEC>
+cudaError_t run_embed(const void *table, const void *ids, int wide, void *out, int tokens, int rows,
+                      int D, float scale, int32_t *status, cudaStream_t st) {
+    const int pieces = (D + VEC - 1) / VEC;
+    int tpr = 8;
+    while (tpr < 256 && tpr * 4 < pieces) tpr *= 2;
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const long long need = ((long long)tokens * tpr + 255) / 256, most = 8ll * sms;
+    const unsigned gx = (unsigned)(need < most ? need : most);
+    unsigned gy = (pieces + 4 * tpr - 1) / (4 * tpr);  // few tokens: a wide row over blocks
+    if (gy > 64) gy = 64;
+    if ((long long)gx * gy > 4 * most) gy = 1;
+    return launch_dependent(embed_kernel<T, VEC>, dim3(gx, gy), dim3(256), 0, st, (const T *)table,
+                            ids, wide, (T *)out, tokens, rows, D, tpr, scale, status);
+}
+
+template <typename T, int VEC>
+cudaError_t run_sums(const SumArgs &a, const void *d_out, void *d_table, cudaStream_t st) {
+    const dim3 grid(a.parts, (a.D + kSumThreads * VEC - 1) / (kSumThreads * VEC));
+    cudaError_t e = launch_dependent(segment_sum_kernel<T, VEC>, grid, dim3(kSumThreads), 0, st, a,
+                                     (const T *)d_out, (T *)d_table);
+    if (e != cudaSuccess || a.tokens == 0) return e;
+    return launch_dependent(segment_join_kernel<T, VEC>, grid, dim3(kSumThreads), 0, st, a,
+                            (T *)d_table);
+}
+
+kda_status_t check(const kda_embed_desc_t *d) {
+    if (!d) return KDA_ERR_INVALID_ARG;
+    if (d->tokens < 0 || d->rows < 1 || d->width < 1 || !isfinite(d->scale))
+        return KDA_ERR_INVALID_ARG;
+    if (d->act_dtype != KDA_DTYPE_F32 && d->act_dtype != KDA_DTYPE_BF16) return KDA_ERR_UNSUPPORTED;
+    if (d->id_dtype != KDA_ID_I32 && d->id_dtype != KDA_ID_I64) return KDA_ERR_UNSUPPORTED;
+    if (d->width > 65536 || d->rows > (1 << 30) || d->tokens > (1 << 30)) return KDA_ERR_UNSUPPORTED;
+    return KDA_OK;
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+kda_status_t kda_embedding_forward(const kda_embed_desc_t *desc, const void *table, const void *ids,
+                                   void *out, int32_t *dev_status, void *stream) {
+    kda_status_t rc = check(desc);
+    if (rc != KDA_OK) return rc;
+    if (desc->tokens == 0) return KDA_OK;
+    const int size = desc->act_dtype == KDA_DTYPE_BF16 ? 2 : 4, wide = desc->id_dtype == KDA_ID_I64;
+    if (!table || !ids || !out || (uintptr_t)table % size || (uintptr_t)out % size ||
+        (uintptr_t)ids % (wide ? 8 : 4) || (uintptr_t)dev_status % 4)
+        return KDA_ERR_INVALID_ARG;
+    const bool vec = wide_rows(desc->width, size, table, out);
+    cudaStream_t st = (cudaStream_t)stream;
+    const int n = desc->tokens, r = desc->rows, D = desc->width;
+    const float s = desc->scale;
+    cudaError_t e;
+    if (size == 2)
+        e = vec ? run_embed<__nv_bfloat16, 8>(table, ids, wide, out, n, r, D, s, dev_status, st)
+                : run_embed<__nv_bfloat16, 1>(table, ids, wide, out, n, r, D, s, dev_status, st);
+    else
+        e = vec ? run_embed<float, 4>(table, ids, wide, out, n, r, D, s, dev_status, st)
+                : run_embed<float, 1>(table, ids, wide, out, n, r, D, s, dev_status, st);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+size_t kda_embedding_backward_workspace_size(const kda_embed_desc_t *desc) {
+    if (check(desc) != KDA_OK) return 0;
+    return plan_for(desc->tokens, desc->rows, desc->width).total;
+}
+
+kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_out,
+                                    const void *ids, void *d_table, void *workspace,
+                                    size_t workspace_bytes, int32_t *dev_status, void *stream) {
+    kda_status_t rc = check(desc);
+    if (rc != KDA_OK) return rc;
+    const int size = desc->act_dtype == KDA_DTYPE_BF16 ? 2 : 4, wide = desc->id_dtype == KDA_ID_I64;
+    if (!d_table || (uintptr_t)d_table % size || (uintptr_t)dev_status % 4) return KDA_ERR_INVALID_ARG;
+    if (desc->tokens > 0 && (!d_out || !ids || (uintptr_t)d_out % size ||
+                             (uintptr_t)ids % (wide ? 8 : 4)))
+        return KDA_ERR_INVALID_ARG;
+    const Plan p = plan_for(desc->tokens, desc->rows, desc->width);
+    if (!workspace || workspace_bytes < p.total || ((uintptr_t)workspace & 15u))
+        return KDA_ERR_WORKSPACE;
+    cudaStream_t st = (cudaStream_t)stream;
+    uint8_t *w = (uint8_t *)workspace;
+    int *keys[2] = {(int *)w, (int *)(w + p.pairs)};
+    int *poss[2] = {(int *)(w + 2 * p.pairs), (int *)(w + 3 * p.pairs)};
+    int last = 0;
+    if (desc->tokens > 0) {
+        SortArgs a = {};
+        a.ids = ids;
+        a.wide = wide;
+        a.tokens = desc->tokens;
+        a.rows = desc->rows;
+        a.hist = (int *)(w + 4 * p.pairs);
+        a.bits = p.bits;
+        a.tiles = p.tiles;
+        a.status = dev_status;
+        for (int k = 0; k < p.passes; ++k) {
+            a.shift = k * p.bits;
+            a.in_key = k ? keys[last] : nullptr;
+            a.in_pos = k ? poss[last] : nullptr;
+            last = k ? 1 - last : 0;
+            a.out_key = keys[last];
+            a.out_pos = poss[last];
+            if (launch_dependent(sort_hist_kernel, dim3(p.tiles), dim3(kSortThreads), 0, st, a) !=
+                    cudaSuccess ||
+                launch_dependent(sort_scatter_kernel, dim3(p.tiles), dim3(kSortThreads), 0, st, a) !=
+                    cudaSuccess)
+                return KDA_ERR_CUDA;
+        }
+    }
+    SumArgs s = {};
+    s.key = keys[last];
+    s.pos = poss[last];
+    s.tokens = desc->tokens;
+    s.rows = desc->rows;
+    s.D = desc->width;
+    s.parts = p.parts;
+    s.per = p.per;
+    s.carry = (float *)(w + 4 * p.pairs + p.hist);
+    s.head = (float *)(w + 4 * p.pairs + p.hist + p.rem);
+    s.scale = desc->scale;
+    const bool vec = wide_rows(desc->width, size, d_out, d_table);
+    cudaError_t e;
+    if (size == 2)
+        e = vec ? run_sums<__nv_bfloat16, 8>(s, d_out, d_table, st)
+                : run_sums<__nv_bfloat16, 1>(s, d_out, d_table, st);
+    else
+        e = vec ? run_sums<float, 4>(s, d_out, d_table, st) : run_sums<float, 1>(s, d_out, d_table, st);
+    return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,391 @@
+"""The operators around the mixer against their formulas in 64 bits: the norms with
+gate and residual, the embedding and the cross entropy, forward and backward.
+
+Bounds.  BF16 has 8 significant bits, so one rounding is up to 2^-8 of the value;
+fp32 arithmetic adds a few 2^-24 per operation of the sum behind an output; where
+that is a difference of terms (dx of a norm) or a long sum, the bound is relative
+to the sum of the terms' magnitudes.  The cross entropy's dz is rounded to BF16
+before its products, so there each term of the sum carries 2^-8.
+"""
+import math
+
+import pytest
+import torch
+
+import kimi_delta_attention_18_gb300 as kda
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+ROUND = {"f32": 2.0 ** -23, "bf16": 2.0 ** -8}
+FP32 = 2.0 ** -18  # rsqrt, exp and division approximations and a row's fp32 sums
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(shape, g, dt, std=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dt)
+
+
+def _close(got, ref, act, terms=None, extra=0.0):
+    """|got - ref| <= one rounding of ref + (FP32 + extra) of the terms behind it."""
+    assert got.shape == ref.shape
+    terms = ref.abs() if terms is None else terms
+    bound = ROUND[act] * ref.abs() + (FP32 + extra) * terms + 1e-30
+    bad = (got.double() - ref).abs() > bound
+    assert not bad.any(), "%d of %d off, worst %g against %g" % (
+        int(bad.sum()), bad.numel(), float((got.double() - ref).abs().max()),
+        float(ref.abs().max()))
+
+
+# -------------------------------------------------------------------- gated norm
+
+def _gate64(z, act):
+    s = torch.sigmoid(z)
+    if act == "sigmoid":
+        return s, s * torch.sigmoid(-z)
+    return z * s, s + z * s * torch.sigmoid(-z)
+
+
+def _gated64(x, z, w, act, eps):
+    x = x.double()
+    r = (x.pow(2).mean(-1, keepdim=True) + eps).rsqrt()
+    a, da = (torch.ones_like(x), torch.zeros_like(x)) if z is None else _gate64(z.double(), act)
+    w = torch.ones(x.shape[-1], device="cuda", dtype=torch.float64) if w is None else w.double()
+    return x * r, r, a, da, w
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,D,act,weight,strided", [
+    (1, 1, 1, "sigmoid", True, False),
+    (1, 56, 128, "sigmoid", True, False),
+    (300, 3, 128, "silu", True, True),
+    (5, 2, 7, "silu", True, False),
+    (33, 1, 16, "none", False, False),
+    (129, 4, 100, "sigmoid", False, True),
+    (17, 2, 129, "silu", True, True),
+    (7, 1, 1000, "sigmoid", True, False),
+    (3, 2, 1032, "sigmoid", True, False),
+    (2, 1, 4097, "silu", True, False),
+    (5, 1, 16384, "sigmoid", True, False),
+    (2, 1, 16383, "sigmoid", True, False),
+    (4000, 8, 64, "sigmoid", True, False),
+])
+def test_gated_norm(dtype, T, H, D, act, weight, strided):
+    g, dt = _gen(T + D), DT[dtype]
+    x, z = _randn((T, H, D), g, dt, 2.0), None
+    if act != "none":
+        z = _randn((T, 3, H, D), g, dt, 2.0)[:, 1] if strided else _randn((T, H, D), g, dt, 2.0)
+    if strided:
+        x = _randn((T, 2, H, D), g, dt, 2.0)[:, 1]
+    w = _randn((D,), g, torch.float32) if weight else None
+    d = _randn((T, H, D), g, dt)
+    n, r, a, da, w64 = _gated64(x, z, w, act, 1e-5)
+    out = kda.gated_norm(x, z, w, act=act, eps=1e-5)
+    _close(out, n * w64 * a, dtype)
+    dx, dz, dw = kda.gated_norm_backward(d, x, z, w, act=act, eps=1e-5)
+    e = d.double() * a * w64
+    mean = (e * n).mean(-1, keepdim=True)
+    _close(dx, r * (e - n * mean), dtype,
+           r * (e.abs() + n.abs() * (e * n).abs().mean(-1, keepdim=True)))
+    if z is None:
+        assert dz is None
+    else:  # 1 - sigmoid and 1 + z (1 - sigmoid) are differences of terms up to 1 + |z|
+        _close(dz, d.double() * n * w64 * da, dtype,
+               (d.double() * n * w64).abs() * (1.0 + z.double().abs()))
+    assert dw.dtype == torch.float32
+    _close(dw, (d.double() * a * n).sum((0, 1)), "f32", (d.double() * a * n).abs().sum((0, 1)))
+
+
+def test_gated_norm_backward_matches_differences():
+    """The gradients against central differences of the 64-bit formula."""
+    g = _gen(3)
+    x, z = _randn((2, 2, 5), g, torch.float32), _randn((2, 2, 5), g, torch.float32)
+    w, d = _randn((5,), g, torch.float32), _randn((2, 2, 5), g, torch.float32)
+
+    def f(x, z, w):
+        n, _, a, _, w64 = _gated64(x, z, w, "silu", 1e-3)
+        return float((d.double() * n * w64 * a).sum())
+
+    got = kda.gated_norm_backward(d, x, z, w, act="silu", eps=1e-3)
+    args = [x.double(), z.double(), w.double()]
+    for k in range(3):
+        for i in range(args[k].numel()):
+            vals = []
+            for s in (1e-5, -1e-5):
+                moved = [t.clone() for t in args]
+                moved[k].view(-1)[i] += s
+                vals.append(f(*moved))
+            # central difference: error 1e-10 of third derivatives, 1e-11 of rounding
+            assert abs(float(got[k].view(-1)[i]) - (vals[0] - vals[1]) / 2e-5) < 2e-4
+
+
+def test_gated_norm_of_zeros_and_large_rows():
+    x = torch.zeros((3, 1, 128), device="cuda", dtype=torch.bfloat16)
+    x[1] = 3e18  # its square still fits fp32
+    z = torch.full_like(x, -200.0)
+    z[2] = 200.0
+    out = kda.gated_norm(x, z)
+    assert torch.isfinite(out.float()).all() and not out.float().abs().max() > 0
+    out = kda.gated_norm(x, -z)
+    assert torch.equal(out[1].float(), torch.ones((1, 128), device="cuda"))
+    dx, dz, dw = kda.gated_norm_backward(torch.ones_like(x), x, z)
+    for t in (dx, dz, dw):
+        assert torch.isfinite(t.float()).all()
+
+
+def test_norms_without_tokens():
+    x = torch.empty((0, 2, 16), device="cuda")
+    assert kda.gated_norm(x, x).shape == (0, 2, 16)
+    dx, dz, dw = kda.gated_norm_backward(x, x, x)
+    assert dx.numel() == 0 and torch.equal(dw, torch.zeros(16, device="cuda"))
+    h = torch.empty((0, 16), device="cuda")
+    assert kda.residual_norm(h, h)[1].shape == (0, 16)
+    assert torch.equal(kda.residual_norm_backward(h, h)[2], torch.zeros(16, device="cuda"))
+
+
+# ----------------------------------------------------------------- residual norm
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D,scale,weight,with_y", [
+    (1, 1, 1.0, True, True),
+    (1, 7168, 1.0, True, True),
+    (256, 1024, 0.5, True, True),
+    (3, 1001, 0.22, True, True),
+    (37, 515, -2.0, False, True),
+    (9, 12345, 1.0, True, True),
+    (64, 4096, 1.0, True, False),
+    (1, 33, 1.0, False, False),
+    (2049, 192, 0.5, True, True),
+])
+def test_residual_norm(dtype, T, D, scale, weight, with_y):
+    g, dt = _gen(T + D), DT[dtype]
+    h, y = _randn((T, D), g, dt, 2.0), _randn((T, D), g, dt) if with_y else None
+    w = _randn((D,), g, torch.float32) if weight else None
+    w64 = torch.ones(D, device="cuda", dtype=torch.float64) if w is None else w.double()
+    h64 = h.double() + (scale * y.double() if with_y else 0.0)
+    size = h.double().abs() + (abs(scale) * y.double().abs() if with_y else 0.0)
+    r = (h64.pow(2).mean(-1, keepdim=True) + 1e-6).rsqrt()
+    h_out, out = kda.residual_norm(h, y, w, scale=scale)
+    _close(h_out, h64, dtype, size)
+    _close(out, h64 * r * w64, dtype, size * r * w64.abs())
+    # backward, from the rounded h_out
+    d_out, d_h = _randn((T, D), g, dt), _randn((T, D), g, dt)
+    h64 = h_out.double()
+    r = (h64.pow(2).mean(-1, keepdim=True) + 1e-6).rsqrt()
+    n, e = h64 * r, d_out.double() * w64
+    through = r * (e - n * (e * n).mean(-1, keepdim=True))
+    terms = r * (e.abs() + n.abs() * (e * n).abs().mean(-1, keepdim=True))
+    dw = (d_out.double() * n).sum(0)
+    for d in (d_h, None):
+        dh, dy, got_w = kda.residual_norm_backward(d_out, h_out, w, d, scale=scale)
+        ref = through + (0.0 if d is None else d.double())
+        t = terms + (0.0 if d is None else d.double().abs())
+        _close(dh, ref, dtype, t)
+        _close(dy, scale * ref, dtype, abs(scale) * t)
+        _close(got_w, dw, "f32", (d_out.double() * n).abs().sum(0))
+
+
+def test_residual_norm_in_place_and_on_another_stream():
+    g = _gen(5)
+    h, y = _randn((64, 512), g, torch.bfloat16), _randn((64, 512), g, torch.bfloat16)
+    ref_h, ref = kda.residual_norm(h, y)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mine = h.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    h_out, out = kda.residual_norm(mine, y, h_out=mine, stream=s)
+    s.synchronize()
+    assert h_out is mine and torch.equal(mine, ref_h) and torch.equal(out, ref)
+
+
+# --------------------------------------------------------------------- embedding
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D,kind,ids_dtype", [
+    (1, 1, 1, "same", torch.int32),
+    (1, 50, 128, "uniform", torch.int64),
+    (333, 257, 250, "text", torch.int32),
+    (2047, 1000, 64, "text", torch.int32),
+    (2049, 1025, 72, "uniform", torch.int64),
+    (5000, 40, 33, "uniform", torch.int32),
+    (9000, 3, 8, "same", torch.int32),
+    (5000, 100003, 24, "text", torch.int32),
+    (3000, (1 << 20) + 5, 2, "uniform", torch.int64),
+    (20, 300, 4096, "uniform", torch.int32),
+])
+def test_embedding(dtype, T, V, D, kind, ids_dtype):
+    g, dt = _gen(T + V), DT[dtype]
+    u = torch.rand(T, generator=g, device="cuda", dtype=torch.float64)
+    ids = {"same": torch.full_like(u, V - 1), "uniform": u * V,
+           "text": (u * math.log(V + 1.0)).exp() - 1.0}[kind].long().clamp(0, V - 1).to(ids_dtype)
+    table, d = _randn((V, D), g, dt), _randn((T, D), g, dt)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = kda.embedding(table, ids, scale=1.5, dev_status=status)
+    _close(out, 1.5 * table[ids.long()].double(), dtype)
+    got = kda.embedding_backward(d, ids, V, scale=1.5, dev_status=status)
+    ref = torch.zeros((V, D), device="cuda", dtype=torch.float64).index_add_(0, ids.long(), d.double())
+    size = torch.zeros_like(ref).index_add_(0, ids.long(), d.double().abs())
+    _close(got, 1.5 * ref, dtype, 1.5 * size)
+    assert int(status) == 0
+    assert torch.equal(got, kda.embedding_backward(d, ids, V, scale=1.5))  # a fixed order
+
+
+def test_embedding_gradient_of_one_frequent_token_among_many():
+    """An id whose tokens span many parts of the sorted list, absent ids around it."""
+    g = _gen(1)
+    T, V, D = 30000, 5000, 40
+    ids = torch.randint(0, V, (T,), generator=g, device="cuda")
+    ids[::3] = 2500
+    d = _randn((T, D), g, torch.float32)
+    got = kda.embedding_backward(d, ids, V)
+    ref = torch.zeros((V, D), device="cuda", dtype=torch.float64).index_add_(0, ids, d.double())
+    size = torch.zeros_like(ref).index_add_(0, ids, d.double().abs())
+    _close(got, ref, "f32", size)
+
+
+def test_embedding_reports_ids_outside_the_table():
+    table = torch.ones((4, 8), device="cuda")
+    ids = torch.tensor([0, 4, -1, 3], device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = kda.embedding(table, ids, dev_status=status)
+    assert int(status) == 1
+    assert out.sum(1).tolist() == [8.0, 0.0, 0.0, 8.0]
+    status.zero_()
+    got = kda.embedding_backward(torch.ones((4, 8), device="cuda"), ids, 4, dev_status=status)
+    assert int(status) == 1
+    assert got.sum(1).tolist() == [8.0, 0.0, 0.0, 8.0]
+
+
+def test_embedding_without_tokens():
+    ids = torch.empty(0, dtype=torch.int32, device="cuda")
+    d = torch.empty((0, 16), device="cuda")
+    assert kda.embedding(torch.ones((3, 16), device="cuda"), ids).shape == (0, 16)
+    assert torch.equal(kda.embedding_backward(d, ids, 3), torch.zeros((3, 16), device="cuda"))
+
+
+# ----------------------------------------------------------------- cross entropy
+
+def _check_ce(dtype, x, w, y, d_loss, ignore=-100, piece=0):
+    T, V, D = x.shape[0], w.shape[0], x.shape[1]
+    x64, w64 = x.double(), w.double()
+    z = x64 @ w64.T
+    kept = y != ignore
+    at = torch.where(kept, y, 0).long()[:, None]
+    lse = torch.logsumexp(z, 1)
+    loss_ref = torch.where(kept, lse - z.gather(1, at)[:, 0], 0.0)
+    loss, got_lse, mean = kda.linear_cross_entropy(x, w, y, ignore_index=ignore)
+    # a logit: its D products in fp32, one rounding each step of 16
+    steps = (6 if dtype == "f32" else 1) * (D / 16.0) + 16
+    size = (x64.abs() @ w64.abs().T).max(1).values
+    err = 2.0 ** -23 * (steps * size + 8 * lse.abs() + 8)
+    assert ((got_lse.double() - lse).abs() <= err).all()
+    assert ((loss.double() - loss_ref).abs() <= 2 * err).all()
+    assert not loss[~kept].any()
+    n = int(kept.sum())
+    ref_mean = float(loss_ref.sum()) / n if n else 0.0
+    assert abs(float(mean) - ref_mean) <= 2 * float(err.max()) + 1e-6 * float(loss_ref.abs().max())
+    # backward, with the row statistics that the forward gave
+    dx, dw = kda.linear_cross_entropy_backward(x, w, y, got_lse, d_loss, ignore_index=ignore,
+                                               piece=piece)
+    p = torch.exp(z - got_lse.double()[:, None])
+    hot = torch.zeros_like(z).scatter_(1, at, 1.0)
+    g = torch.where(kept, d_loss, 0.0).double()[:, None]
+    dz, dz_size = (p - hot) * g, (p + hot) * g.abs()
+    # dz carries its logit's error (relative) and, in BF16, one rounding; the products
+    # add one fp32 rounding per step of 16
+    for got, ref, terms, k in ((dx, dz @ w64, dz_size @ w64.abs(), V),
+                               (dw, dz.T @ x64, dz_size.T @ x64.abs(), T)):
+        extra = float(err.max()) + 2.0 ** -23 * ((6 if dtype == "f32" else 1) * (k / 16.0) + 16)
+        extra += 2.0 ** -8 if dtype == "bf16" else 2.0 ** -22
+        _close(got, ref, dtype, terms, extra)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D,piece", [
+    (1, 1, 1, 0),
+    (1, 5, 8, 0),
+    (1, 1000, 64, 0),
+    (5, 257, 31, 0),
+    (128, 256, 64, 0),
+    (129, 255, 72, 0),
+    (300, 1000, 520, 256),
+    (257, 2049, 128, 512),
+    (77, 5003, 100, 0),
+    (1000, 700, 1024, 256),
+    (2500, 4000, 256, 0),
+])
+def test_cross_entropy(dtype, T, V, D, piece):
+    g, dt = _gen(T + V + D), DT[dtype]
+    x, w = _randn((T, D), g, dt), _randn((V, D), g, dt, 2.0 / math.sqrt(D))
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    y[torch.rand(T, generator=g, device="cuda") < 0.2] = -100
+    d = torch.rand(T, generator=g, device="cuda") - 0.3
+    _check_ce(dtype, x, w, y.int() if T % 2 else y, d, piece=piece)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_cross_entropy_of_large_logits(dtype):
+    """Logits of hundreds: exp would overflow without the running maximum."""
+    g, dt = _gen(2), DT[dtype]
+    x, w = _randn((40, 64), g, dt, 8.0), _randn((600, 64), g, dt, 8.0)
+    y = torch.randint(0, 600, (40,), generator=g, device="cuda")
+    _check_ce(dtype, x, w, y, torch.ones(40, device="cuda"))
+
+
+def test_cross_entropy_with_nothing_to_predict():
+    x, w = torch.ones((6, 16), device="cuda"), torch.ones((50, 16), device="cuda")
+    y = torch.full((6,), 7, device="cuda")
+    loss, lse, mean = kda.linear_cross_entropy(x, w, y, ignore_index=7)
+    assert not loss.any() and float(mean) == 0.0
+    dx, dw = kda.linear_cross_entropy_backward(x, w, y, lse, torch.ones(6, device="cuda"),
+                                               ignore_index=7)
+    assert not dx.any() and not dw.any()
+    e = torch.empty((0, 16), device="cuda")
+    y = torch.empty(0, dtype=torch.int32, device="cuda")
+    loss, lse, mean = kda.linear_cross_entropy(e, w, y)
+    assert loss.numel() == 0 and float(mean) == 0.0
+    dx, dw = kda.linear_cross_entropy_backward(e, w, y, lse, loss)
+    assert dx.shape == (0, 16) and not dw.any()
+
+
+def test_cross_entropy_reports_targets_outside_the_vocabulary():
+    g = _gen(4)
+    x, w = _randn((4, 32), g, torch.bfloat16), _randn((9, 32), g, torch.bfloat16)
+    y = torch.tensor([3, 9, -1, -100], device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    loss, lse, mean = kda.linear_cross_entropy(x, w, y, dev_status=status)
+    assert int(status) == 1
+    assert loss[1:].tolist() == [0.0, 0.0, 0.0] and float(mean) == float(loss[0])
+    status.zero_()
+    dx, dw = kda.linear_cross_entropy_backward(x, w, y, lse, torch.ones(4, device="cuda"),
+                                               dev_status=status)
+    assert int(status) == 1 and not dx[1:].any() and bool(dx[0].any())
+
+
+def test_cross_entropy_matches_differences():
+    """dx and d_weight against central differences of the forward in 64 bits."""
+    g = _gen(6)
+    x, w = _randn((3, 8), g, torch.float32), _randn((5, 8), g, torch.float32)
+    y, d = torch.tensor([1, -100, 4], device="cuda"), torch.tensor([0.5, 9.0, -1.0], device="cuda")
+
+    def f(x, w):
+        z = x @ w.T
+        rows = torch.tensor([0, 2], device="cuda")
+        return float((d[rows].double() * (torch.logsumexp(z, 1)[rows] - z[rows, y[rows]])).sum())
+
+    _, lse, _ = kda.linear_cross_entropy(x, w, y)
+    got = kda.linear_cross_entropy_backward(x, w, y, lse, d)
+    args = [x.double(), w.double()]
+    for k in range(2):
+        for i in range(args[k].numel()):
+            vals = []
+            for s in (1e-5, -1e-5):
+                moved = [t.clone() for t in args]
+                moved[k].view(-1)[i] += s
+                vals.append(f(*moved))
+            assert abs(float(got[k].view(-1)[i]) - (vals[0] - vals[1]) / 2e-5) < 2e-4
