@@ -11,7 +11,7 @@ import ctypes
 import torch
 
 from . import _native as _k
-from ._native import _ACT, _check, _need, _ptr, _stream
+from ._native import _ACT, _check
 
 ACTS = {"none": 0, "sigmoid": 1, "silu": 2}
 _IDS = {torch.int32: 0, torch.int64: 1}
@@ -59,60 +59,96 @@ def bind(L):
         fn.restype, fn.argtypes = Z, args
 
 
-def _act(t, name):
+# These calls are as short as a decode step's (a few microseconds on the device), so
+# the host's part is kept short: one combined test per tensor (_need, and with it
+# the precise error, only when that fails), plain integers instead of ctypes
+# objects, and the current stream's handle without a Stream object around it.
+
+def _lib():
+    return _k._lib or _k.lib()
+
+
+def _is(t, name, dtype, shape, dev):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
+            t.device == dev and t.is_contiguous()):
+        _k._need(t, name, dtype, shape, dev)
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _stream(stream, dev):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream
+
+
+def _first(t, name, dims):
+    """Device and act_dtype of the operator's first tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError("%s must be a tensor of %d dimensions" % (name, dims))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
     act = _ACT.get(t.dtype)
     if act is None:
         raise ValueError("%s must be float32 or bfloat16" % name)
-    return act
+    return t.device, act
 
 
 def _workspace(workspace, need, dev):
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=dev)
+        return torch.empty(need or 16, dtype=torch.uint8, device=dev), need or 16
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev:
+        raise ValueError("workspace must be a tensor on %s" % dev)
     return workspace, workspace.numel() * workspace.element_size()
 
 
+def _out(out, name, like):
+    """A caller's output of the same type and shape as ``like``, or a new one."""
+    if out is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    _is(out, name, like.dtype, like.shape, like.device)
+    return out
+
+
 def _status(dev_status, dev):
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32, None, dev)
-    return _ptr(dev_status)
+    if dev_status is None:
+        return None
+    _k._need(dev_status, "dev_status", torch.int32, None, dev)
+    return dev_status.data_ptr()
 
 
 # -------------------------------------------------------------------- gated norm
 
-def _rows(t, name, dtype, shape, dev):
-    """A ``[T, H, D]`` tensor whose tokens may lie further apart than H * D (a slice
-    of a wider projection's output); returns the token stride, 0 where it is H * D."""
-    T, H, D = shape
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s must be a torch.Tensor" % name)
-    if not t.is_cuda or t.device != dev:
-        raise ValueError("%s must be a CUDA tensor on %s" % (name, dev))
-    if t.dtype != dtype:
-        raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
-    if tuple(t.shape) != shape:
-        raise ValueError("%s must have shape %s, got %s" % (name, shape, tuple(t.shape)))
-    if t.is_contiguous() or T == 0:
+def _rows(t, name, like):
+    """A ``[T, H, D]`` tensor like ``like`` whose tokens may lie further apart than H D
+    (a slice of a wider projection's output); returns the token stride, 0 for H D."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.shape == like.shape and
+            t.device == like.device):
+        if isinstance(t, torch.Tensor) and not t.is_contiguous():
+            t = t.contiguous()  # for the error: the stride is not what is wrong
+        _k._need(t, name, like.dtype, like.shape, like.device)
+    if t.is_contiguous():
         return 0
-    sT, sH, sD = t.stride()
+    (T, H, D), (sT, sH, sD) = t.shape, t.stride()
     if (D > 1 and sD != 1) or (H > 1 and sH != D) or (T > 1 and sT < H * D):
         raise ValueError("%s must have contiguous heads and channels" % name)
     return sT if T > 1 else 0
 
 
 def _gated(x, gate, weight, act, eps):
-    if not isinstance(x, torch.Tensor) or x.dim() != 3:
-        raise ValueError("x must be a [T, H, D] tensor")
-    if act not in ACTS:
+    dev, dtype = _first(x, "x", 3)
+    kind = ACTS.get(act)
+    if kind is None:
         raise ValueError("act must be one of %s" % ", ".join(sorted(ACTS)))
-    if (gate is None) != (act == "none"):
+    if (gate is None) != (kind == 0):
         raise ValueError("a gate is required unless act is 'none', and not allowed then")
-    dev, shape = x.device, tuple(x.shape)
-    xs = _rows(x, "x", x.dtype, shape, dev)
-    gs = _rows(gate, "gate", x.dtype, shape, dev) if gate is not None else 0
+    T, H, D = x.shape
     if weight is not None:
-        _need(weight, "weight", torch.float32, shape[2:], dev)
-    return NormDesc(shape[0], xs, gs, shape[1], shape[2], _act(x, "x"), ACTS[act], eps)
+        _is(weight, "weight", torch.float32, (D,), dev)
+    return dev, NormDesc(T, _rows(x, "x", x), 0 if gate is None else _rows(gate, "gate", x), H, D,
+                         dtype, kind, eps)
 
 
 def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, stream=None):
@@ -120,14 +156,11 @@ def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, 
     act(gate)`` (see kda_gated_norm_forward in kda.h).  x, gate ``[T, H, D]`` in one
     activation dtype, tokens possibly strided; weight ``[D]`` fp32 or None; act
     "sigmoid", "silu" or "none" (gate None).  Returns out ``[T, H, D]``."""
-    desc = _gated(x, gate, weight, act, eps)
-    dev = x.device
-    if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    _need(out, "out", x.dtype, x.shape, dev)
+    dev, desc = _gated(x, gate, weight, act, eps)
+    out = _out(out, "out", x)
     _check("kda_gated_norm_forward",
-           _k.lib().kda_gated_norm_forward(desc, _ptr(x), _ptr(gate), _ptr(weight), _ptr(out),
-                                           _stream(stream, dev)))
+           _lib().kda_gated_norm_forward(desc, x.data_ptr(), _ptr(gate), _ptr(weight),
+                                         out.data_ptr(), _stream(stream, dev)))
     return out
 
 
@@ -136,32 +169,31 @@ def gated_norm_backward(d_out, x, gate=None, weight=None, *, act="sigmoid", eps=
     """Gradients of ``gated_norm`` for the adjoint d_out ``[T, H, D]`` of its output:
     ``(dx, d_gate, d_weight)``, d_gate None without a gate, d_weight fp32 ``[D]`` (see
     kda_gated_norm_backward in kda.h)."""
-    desc = _gated(x, gate, weight, act, eps)
-    dev = x.device
-    _need(d_out, "d_out", x.dtype, x.shape, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    d_gate = torch.empty(x.shape, dtype=x.dtype, device=dev) if gate is not None else None
+    dev, desc = _gated(x, gate, weight, act, eps)
+    _is(d_out, "d_out", x.dtype, x.shape, dev)
+    L = _lib()
+    dx = _out(None, "dx", x)
+    d_gate = None if gate is None else _out(None, "d_gate", x)
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(x.shape[2], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, _k.lib().kda_norm_backward_workspace_size(desc),
-                                       dev)
+        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
     _check("kda_gated_norm_backward",
-           _k.lib().kda_gated_norm_backward(desc, _ptr(d_out), _ptr(x), _ptr(gate), _ptr(weight),
-                                            _ptr(dx), _ptr(d_gate), _ptr(d_weight),
-                                            _ptr(workspace), ws_len, _stream(stream, dev)))
+           L.kda_gated_norm_backward(desc, d_out.data_ptr(), x.data_ptr(), _ptr(gate),
+                                     _ptr(weight), dx.data_ptr(), _ptr(d_gate), _ptr(d_weight),
+                                     _ptr(workspace), ws_len, _stream(stream, dev)))
     return dx, d_gate, d_weight
 
 
 # ----------------------------------------------------------------- residual norm
 
 def _residual(h, weight, eps, name):
-    if not isinstance(h, torch.Tensor) or h.dim() != 2:
-        raise ValueError("%s must be a [T, D] tensor" % name)
-    _need(h, name, h.dtype)
+    dev, dtype = _first(h, name, 2)
+    _is(h, name, h.dtype, h.shape, dev)
+    T, D = h.shape
     if weight is not None:
-        _need(weight, "weight", torch.float32, h.shape[1:], h.device)
-    return NormDesc(h.shape[0], 0, 0, 1, h.shape[1], _act(h, name), 0, eps)
+        _is(weight, "weight", torch.float32, (D,), dev)
+    return dev, NormDesc(T, 0, 0, 1, D, dtype, 0, eps)
 
 
 def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, out=None,
@@ -169,22 +201,17 @@ def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, ou
     """The residual stream's update and the next block's norm: ``h_out = h + scale y``
     and the RMS norm of it times weight (see kda_residual_norm_forward in kda.h).
     h, y ``[T, D]``; without y, h_out is h.  Returns ``(h_out, out)``."""
-    desc = _residual(h, weight, eps, "h")
-    dev = h.device
-    if y is None:
-        if h_out is not None:
-            raise ValueError("h_out needs y")
-        new_h = None
-    else:
-        _need(y, "y", h.dtype, h.shape, dev)
-        new_h = torch.empty(h.shape, dtype=h.dtype, device=dev) if h_out is None else h_out
-        _need(new_h, "h_out", h.dtype, h.shape, dev)
-    if out is None:
-        out = torch.empty(h.shape, dtype=h.dtype, device=dev)
-    _need(out, "out", h.dtype, h.shape, dev)
+    dev, desc = _residual(h, weight, eps, "h")
+    new_h = None
+    if y is not None:
+        _is(y, "y", h.dtype, h.shape, dev)
+        new_h = _out(h_out, "h_out", h)
+    elif h_out is not None:
+        raise ValueError("h_out needs y")
+    out = _out(out, "out", h)
     _check("kda_residual_norm_forward",
-           _k.lib().kda_residual_norm_forward(desc, _ptr(h), _ptr(y), _ptr(weight), scale,
-                                              _ptr(new_h), _ptr(out), _stream(stream, dev)))
+           _lib().kda_residual_norm_forward(desc, h.data_ptr(), _ptr(y), _ptr(weight), scale,
+                                            _ptr(new_h), out.data_ptr(), _stream(stream, dev)))
     return (h if y is None else new_h), out
 
 
@@ -193,23 +220,22 @@ def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0
     """Gradients of ``residual_norm`` from its h_out, for the adjoints d_out of the
     norm and d_h_out (None: zero) of h_out: ``(dh, dy, d_weight)`` (see
     kda_residual_norm_backward in kda.h).  With scale 1, dy is dh itself."""
-    desc = _residual(h_out, weight, eps, "h_out")
-    dev, like = h_out.device, dict(dtype=h_out.dtype, device=h_out.device)
-    _need(d_out, "d_out", h_out.dtype, h_out.shape, dev)
+    dev, desc = _residual(h_out, weight, eps, "h_out")
+    _is(d_out, "d_out", h_out.dtype, h_out.shape, dev)
     if d_h_out is not None:
-        _need(d_h_out, "d_h_out", h_out.dtype, h_out.shape, dev)
-    dh = torch.empty(h_out.shape, **like)
-    dy = torch.empty(h_out.shape, **like) if want_dy and scale != 1.0 else None
+        _is(d_h_out, "d_h_out", h_out.dtype, h_out.shape, dev)
+    L = _lib()
+    dh = _out(None, "dh", h_out)
+    dy = _out(None, "dy", h_out) if want_dy and scale != 1.0 else None
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(h_out.shape[1], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, _k.lib().kda_norm_backward_workspace_size(desc),
-                                       dev)
+        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
     _check("kda_residual_norm_backward",
-           _k.lib().kda_residual_norm_backward(desc, _ptr(d_out), _ptr(d_h_out), _ptr(h_out),
-                                               _ptr(weight), scale, _ptr(dh), _ptr(dy),
-                                               _ptr(d_weight), _ptr(workspace), ws_len,
-                                               _stream(stream, dev)))
+           L.kda_residual_norm_backward(desc, d_out.data_ptr(), _ptr(d_h_out), h_out.data_ptr(),
+                                        _ptr(weight), scale, dh.data_ptr(), _ptr(dy),
+                                        _ptr(d_weight), _ptr(workspace), ws_len,
+                                        _stream(stream, dev)))
     return dh, (dh if want_dy and scale == 1.0 else dy), d_weight
 
 
@@ -221,7 +247,7 @@ def _ids(ids, name, dev, count=None):
     kind = _IDS.get(ids.dtype)
     if kind is None:
         raise ValueError("%s must be int32 or int64" % name)
-    _need(ids, name, ids.dtype, None if count is None else (count,), dev)
+    _is(ids, name, ids.dtype, ids.shape if count is None else (count,), dev)
     return kind
 
 
@@ -229,19 +255,18 @@ def embedding(table, ids, *, scale=1.0, out=None, dev_status=None, stream=None):
     """``out[t] = scale table[ids[t]]`` (see kda_embedding_forward in kda.h): table
     ``[V, D]``, ids ``[T]`` int32 or int64.  An id outside the table gives a zero row
     and status 1 in dev_status (a device int32)."""
-    if not isinstance(table, torch.Tensor) or table.dim() != 2:
-        raise ValueError("table must be a [V, D] tensor")
-    _need(table, "table")
-    dev = table.device
+    dev, dtype = _first(table, "table", 2)
+    _is(table, "table", table.dtype, table.shape, dev)
     kind = _ids(ids, "ids", dev)
     T, (V, D) = ids.shape[0], table.shape
-    desc = EmbedDesc(T, V, D, _act(table, "table"), kind, scale)
     if out is None:
         out = torch.empty((T, D), dtype=table.dtype, device=dev)
-    _need(out, "out", table.dtype, (T, D), dev)
+    else:
+        _is(out, "out", table.dtype, (T, D), dev)
     _check("kda_embedding_forward",
-           _k.lib().kda_embedding_forward(desc, _ptr(table), _ptr(ids), _ptr(out),
-                                          _status(dev_status, dev), _stream(stream, dev)))
+           _lib().kda_embedding_forward(EmbedDesc(T, V, D, dtype, kind, scale), table.data_ptr(),
+                                        ids.data_ptr(), out.data_ptr(), _status(dev_status, dev),
+                                        _stream(stream, dev)))
     return out
 
 
@@ -249,36 +274,40 @@ def embedding_backward(d_out, ids, num_rows, *, scale=1.0, d_table=None, workspa
                        dev_status=None, stream=None):
     """The gradient ``[num_rows, D]`` of ``embedding``'s table for the adjoint d_out
     ``[T, D]``, in d_out's dtype (see kda_embedding_backward in kda.h)."""
-    if not isinstance(d_out, torch.Tensor) or d_out.dim() != 2:
-        raise ValueError("d_out must be a [T, D] tensor")
-    _need(d_out, "d_out")
-    dev, (T, D) = d_out.device, d_out.shape
-    desc = EmbedDesc(T, num_rows, D, _act(d_out, "d_out"), _ids(ids, "ids", dev, T), scale)
+    dev, dtype = _first(d_out, "d_out", 2)
+    _is(d_out, "d_out", d_out.dtype, d_out.shape, dev)
+    T, D = d_out.shape
+    desc = EmbedDesc(T, num_rows, D, dtype, _ids(ids, "ids", dev, T), scale)
     if d_table is None:
         d_table = torch.empty((num_rows, D), dtype=d_out.dtype, device=dev)
-    _need(d_table, "d_table", d_out.dtype, (num_rows, D), dev)
-    workspace, ws_len = _workspace(
-        workspace, _k.lib().kda_embedding_backward_workspace_size(desc), dev)
+    else:
+        _is(d_table, "d_table", d_out.dtype, (num_rows, D), dev)
+    L = _lib()
+    workspace, ws_len = _workspace(workspace, L.kda_embedding_backward_workspace_size(desc), dev)
     _check("kda_embedding_backward",
-           _k.lib().kda_embedding_backward(desc, _ptr(d_out), _ptr(ids), _ptr(d_table),
-                                           _ptr(workspace), ws_len, _status(dev_status, dev),
-                                           _stream(stream, dev)))
+           L.kda_embedding_backward(desc, d_out.data_ptr(), ids.data_ptr(), d_table.data_ptr(),
+                                    workspace.data_ptr(), ws_len, _status(dev_status, dev),
+                                    _stream(stream, dev)))
     return d_table
 
 
 # ----------------------------------------------------------------- cross entropy
 
 def _ce(x, weight, targets, ignore_index, piece):
-    for t, name in ((x, "x"), (weight, "weight")):
-        if not isinstance(t, torch.Tensor) or t.dim() != 2:
-            raise ValueError("%s must be a matrix" % name)
-    _need(x, "x")
-    dev, (T, D) = x.device, x.shape
-    _need(weight, "weight", x.dtype, None, dev)
-    if weight.shape[1] != D:
-        raise ValueError("weight must have shape [V, %d], got %s" % (D, tuple(weight.shape)))
-    return CrossEntropyDesc(ignore_index, T, weight.shape[0], D, _act(x, "x"),
-                            _ids(targets, "targets", dev, T), piece)
+    dev, dtype = _first(x, "x", 2)
+    _first(weight, "weight", 2)
+    T, D = x.shape
+    _is(x, "x", x.dtype, x.shape, dev)
+    _is(weight, "weight", x.dtype, (weight.shape[0], D), dev)
+    return dev, CrossEntropyDesc(ignore_index, T, weight.shape[0], D, dtype,
+                                 _ids(targets, "targets", dev, T), piece)
+
+
+def _vector(t, name, T, dev):
+    if t is None:
+        return torch.empty(T, dtype=torch.float32, device=dev)
+    _is(t, name, torch.float32, (T,), dev)
+    return t
 
 
 def linear_cross_entropy(x, weight, targets, *, ignore_index=-100, loss=None, lse=None,
@@ -287,17 +316,17 @@ def linear_cross_entropy(x, weight, targets, *, ignore_index=-100, loss=None, ls
     kda_linear_ce_forward in kda.h): x ``[T, D]``, weight ``[V, D]``, targets ``[T]``
     int32 or int64.  Returns ``(loss [T], lse [T], mean)`` in fp32, mean over the rows
     whose target is not ignore_index."""
-    desc = _ce(x, weight, targets, ignore_index, 0)
-    dev, T = x.device, x.shape[0]
-    f32 = dict(dtype=torch.float32, device=dev)
-    loss = torch.empty(T, **f32) if loss is None else _need(loss, "loss", torch.float32, (T,), dev)
-    lse = torch.empty(T, **f32) if lse is None else _need(lse, "lse", torch.float32, (T,), dev)
-    mean = torch.empty((), **f32)
-    workspace, ws_len = _workspace(workspace, _k.lib().kda_linear_ce_workspace_size(desc, 0), dev)
+    dev, desc = _ce(x, weight, targets, ignore_index, 0)
+    T = x.shape[0]
+    loss, lse = _vector(loss, "loss", T, dev), _vector(lse, "lse", T, dev)
+    mean = torch.empty((), dtype=torch.float32, device=dev)
+    L = _lib()
+    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 0), dev)
     _check("kda_linear_ce_forward",
-           _k.lib().kda_linear_ce_forward(desc, _ptr(x), _ptr(weight), _ptr(targets), _ptr(loss),
-                                          _ptr(lse), _ptr(mean), _ptr(workspace), ws_len,
-                                          _status(dev_status, dev), _stream(stream, dev)))
+           L.kda_linear_ce_forward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+                                   loss.data_ptr(), lse.data_ptr(), mean.data_ptr(),
+                                   workspace.data_ptr(), ws_len, _status(dev_status, dev),
+                                   _stream(stream, dev)))
     return loss, lse, mean
 
 
@@ -307,16 +336,17 @@ def linear_cross_entropy_backward(x, weight, targets, lse, d_loss, *, ignore_ind
     """Gradients ``(dx, d_weight)`` of ``linear_cross_entropy`` for the adjoint d_loss
     ``[T]`` fp32 of its per-row loss (see kda_linear_ce_backward in kda.h); ``piece``
     vocabulary columns at a time (0: the library's choice)."""
-    desc = _ce(x, weight, targets, ignore_index, piece)
-    dev, T = x.device, x.shape[0]
-    _need(lse, "lse", torch.float32, (T,), dev)
-    _need(d_loss, "d_loss", torch.float32, (T,), dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if want_dx else None
-    d_weight = torch.empty(weight.shape, dtype=x.dtype, device=dev) if want_d_weight else None
-    workspace, ws_len = _workspace(workspace, _k.lib().kda_linear_ce_workspace_size(desc, 1), dev)
+    dev, desc = _ce(x, weight, targets, ignore_index, piece)
+    T = x.shape[0]
+    _is(lse, "lse", torch.float32, (T,), dev)
+    _is(d_loss, "d_loss", torch.float32, (T,), dev)
+    dx = _out(None, "dx", x) if want_dx else None
+    d_weight = _out(None, "d_weight", weight) if want_d_weight else None
+    L = _lib()
+    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 1), dev)
     _check("kda_linear_ce_backward",
-           _k.lib().kda_linear_ce_backward(desc, _ptr(x), _ptr(weight), _ptr(targets), _ptr(lse),
-                                           _ptr(d_loss), _ptr(dx), _ptr(d_weight),
-                                           _ptr(workspace), ws_len, _status(dev_status, dev),
-                                           _stream(stream, dev)))
+           L.kda_linear_ce_backward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+                                    lse.data_ptr(), d_loss.data_ptr(), _ptr(dx), _ptr(d_weight),
+                                    workspace.data_ptr(), ws_len, _status(dev_status, dev),
+                                    _stream(stream, dev)))
     return dx, d_weight

@@ -127,33 +127,35 @@ __device__ __forceinline__ int term_b(int i, int pairs) {
     return pairs == 1 ? 0 : (0x010201 >> (4 * (i))) & 3;
 }
 
+// One thread's part of the epilogue: a row and 128 of the tile's columns, taken 32
+// at a time.
 template <int EPI>
-__device__ __forceinline__ void epilogue(const GemmArgs &p, const Tile &t, uint32_t tacc, int quarter,
-                                         int half, int lane, uint32_t acce) {
-    const long long row = (long long)t.m * BM + 32 * quarter + lane;
-    const bool live = row < p.M;
-    const int c0 = t.n * BN + half * 128;  // first column of this warp, in the launch's columns
-    const uint32_t src = tacc + ((uint32_t)(32 * quarter) << 16) + 128 * half;
-    int y = -1;
-    float mx = -INFINITY, sum = 0.f, lse2 = 0.f, g = 0.f;
-    if (EPI != EPI_OUT && live) {
-        y = p.y.at(row, t.n == 0 && half == 0);
-        if (EPI == EPI_DZ) {
-            lse2 = p.lse[row] * kLog2e;
-            g = y >= 0 ? p.d_loss[row] : 0.f;
+struct Row {
+    long long row;
+    bool live;
+    int c0;  // first column, in the launch's columns
+    int y;   // the target's column (negative: none)
+    float mx, sum, lse2, g;
+
+    __device__ __forceinline__ void begin(const GemmArgs &p, const Tile &t, int quarter, int half,
+                                          int lane) {
+        row = (long long)t.m * BM + 32 * quarter + lane;
+        live = row < p.M;
+        c0 = t.n * BN + half * 128;
+        y = -1;
+        mx = -INFINITY;
+        sum = lse2 = g = 0.f;
+        if (EPI != EPI_OUT && live) {
+            y = p.y.at(row, t.n == 0 && half == 0);
+            if (EPI == EPI_DZ) {
+                lse2 = p.lse[row] * kLog2e;
+                g = y >= 0 ? p.d_loss[row] : 0.f;
+            }
+            y = y >= 0 ? y - p.b_row0 : -1;
         }
-        y = y >= 0 ? y - p.b_row0 : -1;
     }
-#pragma unroll 1
-    for (int ch = 0; ch < 4; ++ch) {
-        float v[32];
-        __syncwarp();
-        tmem_ld32(src + 32 * ch, v);
-        if (ch == 3) {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(acce);  // the accumulator is in registers
-        }
+
+    __device__ __forceinline__ void take(const GemmArgs &p, const Tile &t, int ch, float (&v)[32]) {
         const int c = c0 + 32 * ch;
         const bool mine = y >= c && y < c + 32;
         if (EPI == EPI_STATS) {
@@ -250,8 +252,18 @@ __device__ __forceinline__ void epilogue(const GemmArgs &p, const Tile &t, uint3
             }
         }
     }
-    if (EPI == EPI_STATS && live)
-        p.part[(size_t)(2 * t.n + half) * p.M + row] = make_float2(mx, sum);
+
+    __device__ __forceinline__ void end(const GemmArgs &p, const Tile &t, int half) {
+        if (EPI == EPI_STATS && live)
+            p.part[(size_t)(2 * t.n + half) * p.M + row] = make_float2(mx, sum);
+    }
+};
+
+__device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
+    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
+        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(x), "+f"(y)
+        : "f"(ax), "f"(ay));
 }
 
 // C = A B^T over tiles of 128 x 256 and steps of 64 along the contraction, one
@@ -264,7 +276,16 @@ __device__ __forceinline__ void epilogue(const GemmArgs &p, const Tile &t, uint3
 // An operand is K-major (its contraction index contiguous) or MN-major (its row
 // index contiguous: W and x in dx = dz W, dz and x in dW = dz^T x), so nothing is
 // transposed in memory.
-template <int EPI, bool A_MN, bool B_MN>
+//
+// FINE, for results that are held in fp32 (lse, loss, and all of an fp32 problem):
+// the tensor core adds each step of 16 to its accumulator with truncation, about
+// 2^-24 of the sum per step and always towards zero, so a long contraction loses
+// bits (at 7,168 measured 2.3e-6 of lse, against 1.4e-7 with fp32 arithmetic).  The
+// accumulator is then handed over every kChunk stages and added up, rounded to
+// nearest, in the epilogue's registers, while the other accumulator fills.
+constexpr int kChunk = 4;
+
+template <int EPI, bool A_MN, bool B_MN, bool FINE>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs p, const __grid_constant__ CUtensorMap tm_a,
                 const __grid_constant__ CUtensorMap tm_b) {
@@ -351,11 +372,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int w = blockIdx.x; w < work && ok; w += gridDim.x, ++i) {
                 const Tile t = tile_at(p, w);
-                const int acc = i & 1, steps = (t.kb1 - t.kb0) * p.pairs;
-                ok = mbar_wait(bar(B_ACCE + acc), ((i >> 1) & 1) ^ 1, abort, kWaitLimit);
-                if (!ok) break;
-                tc_fence_after();
+                const int steps = (t.kb1 - t.kb0) * p.pairs;
                 for (int k = 0; k < steps; ++k, ++it) {
+                    const int first = FINE ? k % kChunk : k;
+                    if (first == 0) {
+                        if (k > 0) umma_commit(bar(B_ACCF + (i++ & 1)));
+                        ok = mbar_wait(bar(B_ACCE + (i & 1)), ((i >> 1) & 1) ^ 1, abort, kWaitLimit);
+                        if (!ok) break;
+                        tc_fence_after();
+                    }
                     const int s = it % kStages;
                     ok = mbar_wait(bar(B_FULL + s), (it / kStages) & 1, abort, kWaitLimit);
                     if (!ok) break;
@@ -363,15 +388,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t a = sb + s * kStage, b = a + kABytes;
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_bf16(tmem + BN * acc,
+                        umma_bf16(tmem + BN * (i & 1),
                                   A_MN ? umma_desc_mn_sw128(a + kk * 2048)
                                        : umma_desc_sw128(a + kk * 32, 1024),
                                   B_MN ? umma_desc_mn_sw128(b + kk * 2048)
                                        : umma_desc_sw128(b + kk * 32, 1024),
-                                  idesc, k + kk > 0);
+                                  idesc, first + kk > 0);
                     umma_commit(bar(B_EMPTY + s));
                 }
-                if (ok) umma_commit(bar(B_ACCF + acc));
+                if (ok) umma_commit(bar(B_ACCF + (i & 1)));
             }
             if (*abort) {  // products in flight complete before TMEM is freed
                 umma_commit(bar(B_FIN));
@@ -381,15 +406,63 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        int i = 0;
-        for (int w = blockIdx.x; w < work; w += gridDim.x, ++i) {
-            const Tile t = tile_at(p, w);
-            const int acc = i & 1;
-            if (!__all_sync(0xffffffffu,
-                            mbar_wait(bar(B_ACCF + acc), (i >> 1) & 1, abort, kWaitLimit)))
-                break;
+        const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + 128 * half;
+        int i = 0;  // accumulators taken
+        auto full = [&]() {
+            const bool ok = __all_sync(
+                0xffffffffu, mbar_wait(bar(B_ACCF + (i & 1)), (i >> 1) & 1, abort, kWaitLimit));
             tc_fence_after();
-            epilogue<EPI>(p, t, tmem + BN * acc, quarter, half, lane, bar(B_ACCE + acc));
+            return ok;
+        };
+        auto release = [&]() {  // the accumulator is in registers
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_ACCE + (i & 1)));
+            ++i;
+        };
+        bool ok = true;
+        for (int w = blockIdx.x; w < work && ok; w += gridDim.x) {
+            const Tile t = tile_at(p, w);
+            Row<EPI> r;
+            r.begin(p, t, quarter, half, lane);
+            __syncwarp();
+            if constexpr (FINE) {
+                float acc[4][32];
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[ch][j] = 0.f;
+                const int steps = (t.kb1 - t.kb0) * p.pairs;
+                for (int k = 0; k < steps && ok; k += kChunk) {
+                    ok = full();
+                    if (!ok) break;
+#pragma unroll
+                    for (int ch = 0; ch < 4; ++ch) {
+                        float v[32];
+                        tmem_ld32(src + BN * (i & 1) + 32 * ch, v);
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2)
+                            add2(acc[ch][j], acc[ch][j + 1], v[j], v[j + 1]);
+                    }
+                    release();
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) r.take(p, t, ch, acc[ch]);
+            } else {
+                ok = full();
+                if (!ok) break;
+#pragma unroll 1
+                for (int ch = 0; ch < 4; ++ch) {
+                    float v[32];
+                    __syncwarp();
+                    tmem_ld32(src + BN * (i & 1) + 32 * ch, v);
+                    if (ch == 3) release();
+                    r.take(p, t, ch, v);
+                }
+            }
+            r.end(p, t, half);
+            __syncwarp();
         }
     }
     tc_fence_before();
@@ -618,15 +691,24 @@ bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, long l
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, bool A_MN, bool B_MN>
+template <int EPI, bool A_MN, bool B_MN, bool FINE>
 cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap &tb,
                      cudaStream_t st) {
-    cudaError_t e = set_max_dynamic_smem((const void *)gemm_kernel<EPI, A_MN, B_MN>, kSmem);
+    const auto kernel = gemm_kernel<EPI, A_MN, B_MN, FINE>;
+    cudaError_t e = set_max_dynamic_smem((const void *)kernel, kSmem);
     if (e != cudaSuccess) return e;
     const long long work = (long long)p.m_tiles * p.n_tiles * p.splits;
     const int n = sms();
-    return launch_dependent(gemm_kernel<EPI, A_MN, B_MN>, dim3((unsigned)(work < n ? work : n)),
-                            dim3(kThreads), kSmem, st, p, ta, tb);
+    return launch_dependent(kernel, dim3((unsigned)(work < n ? work : n)), dim3(kThreads), kSmem, st,
+                            p, ta, tb);
+}
+// The backward's products: in fp32 problems FINE, in BF16 ones (whose results are
+// rounded to 2^-8 of their value) not.
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t run_gemm(const GemmArgs &p, bool fine, const CUtensorMap &ta, const CUtensorMap &tb,
+                     cudaStream_t st) {
+    return fine ? run_gemm<EPI, A_MN, B_MN, true>(p, ta, tb, st)
+                : run_gemm<EPI, A_MN, B_MN, false>(p, ta, tb, st);
 }
 
 cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *src, __nv_bfloat16 *dst,
@@ -710,7 +792,7 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     p.z_y = zy;
     p.ticket = ticket;
     p.status = dev_status;
-    if (run_gemm<EPI_STATS, false, false>(p, ta, tb, st) != cudaSuccess) return KDA_ERR_CUDA;
+    if (run_gemm<EPI_STATS, false, false, true>(p, ta, tb, st) != cudaSuccess) return KDA_ERR_CUDA;
     if (launch_dependent(ce_join_kernel, dim3(cdiv(p.M, 32)), dim3(1024), 0, st,
                          (const float2 *)part, 2 * p.n_tiles, p.M, p.y, (const float *)zy, loss, lse,
                          mean, sums, ticket) != cudaSuccess)
@@ -754,6 +836,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         wp = (const __nv_bfloat16 *)(ws + l.xp);
     }
     const int T = desc->tokens, V = desc->vocab, D = desc->width;
+    const bool fine = l.planes > 1;
     const int inner = l.pack ? l.pitch : D;
     // x and W as operands of the logits (contraction over D, K-major) and of the
     // gradients (contraction over tokens or vocabulary, MN-major); dz both ways
@@ -783,7 +866,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.dz = dz;
         p.pitch = l.piece;
         p.planes = l.planes;
-        if (run_gemm<EPI_DZ, false, false>(p, x_k, w_k, st) != cudaSuccess) return KDA_ERR_CUDA;
+        if (run_gemm<EPI_DZ, false, false>(p, fine, x_k, w_k, st) != cudaSuccess) return KDA_ERR_CUDA;
         if (dx) {
             GemmArgs q = {};
             q.status = dev_status;
@@ -801,7 +884,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)dx & 15u) == 0;
             if (q.splits > q.k_blocks) return KDA_ERR_CUDA;
-            if (run_gemm<EPI_OUT, false, true>(q, dz_k, w_mn, st) != cudaSuccess)
+            if (run_gemm<EPI_OUT, false, true>(q, fine, dz_k, w_mn, st) != cudaSuccess)
                 return KDA_ERR_CUDA;
             if (l.dx_splits > 1) {
                 const long long n = (long long)T * D, need = (n + 255) / 256, most = 16ll * sms();
@@ -828,7 +911,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.out = (uint8_t *)d_weight + (size_t)v0 * D * size;
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)d_weight & 15u) == 0;
-            if (run_gemm<EPI_OUT, true, true>(q, dz_mn, x_mn, st) != cudaSuccess)
+            if (run_gemm<EPI_OUT, true, true>(q, fine, dz_mn, x_mn, st) != cudaSuccess)
                 return KDA_ERR_CUDA;
         }
     }
