@@ -24,20 +24,24 @@ namespace {
 
 using namespace sm100;
 
-constexpr int BM = 128, BN = 256, BK = 64;
-constexpr int kStages = 4, kABytes = BM * BK * 2, kBBytes = BN * BK * 2;
-constexpr int kStage = kABytes + kBBytes;
+constexpr int BM = 128, BN = 256, BK = 64;  // rows per CTA, columns, contraction per stage
+constexpr int kABytes = BM * BK * 2, kBBytes = BN * BK * 2;
 constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
-constexpr int kGroupM = 16;  // row tiles that share a sweep over the column tiles
+constexpr int kGroupRows = 2048;  // rows whose tiles share a sweep over the column tiles
 constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTmemCols = 512;  // two 256-column accumulators
 
-enum { B_FULL = 0, B_EMPTY = B_FULL + kStages, B_ACCF = B_EMPTY + kStages, B_ACCE = B_ACCF + 2,
-       B_FIN = B_ACCE + 2, B_N = B_FIN + 1 };
-constexpr int kBarOff = kStages * kStage, kMisc = kBarOff + B_N * 8;
-constexpr int kSmem = kMisc + 16 + 1024;
-static_assert(kSmem <= 227 * 1024, "shared memory budget");
+// Shared memory of a CTA alone (CTAS = 1) or of each CTA of a pair: a pair's CTAs
+// hold half of B's rows each.
+template <int CTAS>
+struct Smem {
+    static constexpr int stage = kABytes + kBBytes / CTAS, stages = CTAS == 1 ? 4 : 6;
+    static constexpr int full = stages * stage, empty = full + 8 * stages, accf = empty + 8 * stages,
+                         acce = accf + 16, fin = acce + 16, misc = fin + 8;
+    static constexpr int bytes = misc + 16 + 1024;
+    static_assert(bytes <= 227 * 1024, "shared memory budget");
+};
 
 enum { EPI_STATS = 0, EPI_DZ = 1, EPI_OUT = 2 };
 
@@ -61,7 +65,8 @@ struct Targets {
 
 struct GemmArgs {
     int M, N;                  // rows and columns of the product that exist
-    int m_tiles, n_tiles, k_blocks, splits, pairs;
+    int k_blocks, splits, pairs;
+    int m_tiles, n_tiles;      // set at the launch
     int a_row0, b_row0;        // added to the operands' non-contraction coordinate
     int ak_row0, bk_row0;      // added to the contraction coordinate of MN-major operands
     // EPI_STATS, EPI_DZ
@@ -80,15 +85,6 @@ struct GemmArgs {
     int32_t *status;
 };
 
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, uint64_t tmap, int x, int y, int z,
-                                            uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
 // MN-major operand with 128-byte swizzle, as boxes of 64 elements x BK rows lay it
 // down: 8 rows (along K) of 128 bytes form an atom, atoms follow each other along
 // K (1024 bytes), boxes along M / N (8192 bytes).
@@ -105,14 +101,16 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr) {
 struct Tile {
     int m, n, split, kb0, kb1;
 };
+template <int CTAS>
 __device__ __forceinline__ Tile tile_at(const GemmArgs &p, int w) {
+    constexpr int G = kGroupRows / (BM * CTAS);
     Tile t;
     const int per = p.m_tiles * p.n_tiles;
     t.split = w / per;
-    const int r = w - t.split * per, g = r / (kGroupM * p.n_tiles), q = r - g * kGroupM * p.n_tiles;
-    const int gm = min(kGroupM, p.m_tiles - g * kGroupM);
+    const int r = w - t.split * per, g = r / (G * p.n_tiles), q = r - g * G * p.n_tiles;
+    const int gm = min(G, p.m_tiles - g * G);
     t.n = q / gm;
-    t.m = g * kGroupM + (q - t.n * gm);
+    t.m = g * G + (q - t.n * gm);
     t.kb0 = (int)((long long)p.k_blocks * t.split / p.splits);
     t.kb1 = (int)((long long)p.k_blocks * (t.split + 1) / p.splits);
     return t;
@@ -137,9 +135,8 @@ struct Row {
     int y;   // the target's column (negative: none)
     float mx, sum, lse2, g;
 
-    __device__ __forceinline__ void begin(const GemmArgs &p, const Tile &t, int quarter, int half,
-                                          int lane) {
-        row = (long long)t.m * BM + 32 * quarter + lane;
+    __device__ __forceinline__ void begin(const GemmArgs &p, const Tile &t, int row0, int half) {
+        row = row0;
         live = row < p.M;
         c0 = t.n * BN + half * 128;
         y = -1;
@@ -266,13 +263,15 @@ __device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
         : "f"(ax), "f"(ay));
 }
 
-// C = A B^T over tiles of 128 x 256 and steps of 64 along the contraction, one
-// persistent CTA per SM:
-//   warp 0   one thread loads both operands' boxes (TMA, 128-byte swizzle) into
-//            four stages;
-//   warp 1   one thread issues four tcgen05.mma (128 x 256 x 16) per stage into one
-//            of two TMEM accumulators;
+// C = A B^T over tiles of 128 CTAS x 256 and steps of 64 along the contraction,
+// one persistent CTA per SM, alone or in pairs (CTAS = 2):
+//   warp 0   one thread loads the CTA's rows of both operands (TMA, 128-byte
+//            swizzle) into four or six stages;
+//   warp 1   one thread (of the pair's even CTA) issues four tcgen05.mma (128 CTAS x
+//            256 x 16) per stage into one of two TMEM accumulators;
 //   warps 2-9 the epilogue of the other accumulator: thread = row, 128 columns.
+// A pair reads each operand row from shared memory once for 256 x 256 products
+// instead of 128 x 256, and fetches a third fewer bytes from L2.
 // An operand is K-major (its contraction index contiguous) or MN-major (its row
 // index contiguous: W and x in dx = dz W, dz and x in dW = dz^T x), so nothing is
 // transposed in memory.
@@ -285,39 +284,44 @@ __device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
 // nearest, in the epilogue's registers, while the other accumulator fills.
 constexpr int kChunk = 4;
 
-template <int EPI, bool A_MN, bool B_MN, bool FINE>
+template <int EPI, bool A_MN, bool B_MN, bool FINE, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs p, const __grid_constant__ CUtensorMap tm_a,
                 const __grid_constant__ CUtensorMap tm_b) {
+    using S = Smem<CTAS>;
+    constexpr int kRowsB = BN / CTAS;  // B's rows in this CTA
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_addr(sm);
-    auto bar = [&](int i) { return sb + kBarOff + 8 * i; };
-    volatile int *abort = (volatile int *)(sm + kMisc);
+    auto full_bar = [&](int s) { return sb + S::full + 8 * s; };
+    auto empty_bar = [&](int s) { return sb + S::empty + 8 * s; };
+    auto accf_bar = [&](int i) { return sb + S::accf + 8 * (i & 1); };
+    auto acce_bar = [&](int i) { return sb + S::acce + 8 * (i & 1); };
+    volatile int *abort = (volatile int *)(sm + S::misc);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CTAS == 1 ? 0 : (int)cluster_ctarank();
     const int work = p.m_tiles * p.n_tiles * p.splits;
+    const int w0 = blockIdx.x / CTAS, wstep = gridDim.x / CTAS;
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kStages; ++i) {
-            mbar_init(bar(B_FULL + i), 1);
-            mbar_init(bar(B_EMPTY + i), 1);
+        for (int i = 0; i < S::stages; ++i) {
+            mbar_init(full_bar(i), 1);
+            mbar_init(empty_bar(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(bar(B_ACCF + i), 1);
-            mbar_init(bar(B_ACCE + i), kEpiWarps);
+            mbar_init(accf_bar(i), 1);
+            mbar_init(acce_bar(i), kEpiWarps * CTAS);
         }
-        mbar_init(bar(B_FIN), 1);
+        mbar_init(sb + S::fin, 1);
         *abort = 0;
         mbar_fence_init();
     }
-    if (warp == 0) {
-        tmem_alloc(sb + kMisc + 4, kTmemCols);
-        tmem_relinquish();
-    }
+    if (warp == 0) tmem_alloc_group<CTAS>(sb + S::misc + 4, kTmemCols);
     tc_fence_before();
     __syncthreads();
+    if (CTAS == 2) cluster_sync_all();
     tc_fence_after();
-    const uint32_t tmem = *(volatile uint32_t *)(sm + kMisc + 4);
+    const uint32_t tmem = *(volatile uint32_t *)(sm + S::misc + 4);
     griddep_wait();
     griddep_launch_dependents();
     if (EPI == EPI_STATS && blockIdx.x == 0 && threadIdx.x == 0) *p.ticket = 0;
@@ -328,80 +332,95 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t tb = reinterpret_cast<uint64_t>(&tm_b);
             int it = 0;
             bool ok = true;
-            for (int w = blockIdx.x; w < work && ok; w += gridDim.x) {
-                const Tile t = tile_at(p, w);
-                const int ar = t.m * BM + p.a_row0, br = t.n * BN + p.b_row0;
+            for (int w = w0; w < work && ok; w += wstep) {
+                const Tile t = tile_at<CTAS>(p, w);
+                const int ar = (t.m * CTAS + rank) * BM + p.a_row0;
+                const int br = t.n * BN + rank * kRowsB + p.b_row0;
                 for (int pr = 0; pr < p.pairs && ok; ++pr) {
                     const int pa = term_a(pr, p.pairs), pb = term_b(pr, p.pairs);
                     for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
-                        const int s = it % kStages;
-                        ok = mbar_wait(bar(B_EMPTY + s), ((it / kStages) & 1) ^ 1, abort, kWaitLimit);
+                        const int s = it % S::stages;
+                        ok = mbar_wait(empty_bar(s), ((it / S::stages) & 1) ^ 1, abort, kWaitLimit);
                         if (!ok) break;
-                        const uint32_t full = bar(B_FULL + s), a = sb + s * kStage, b = a + kABytes;
-                        mbar_arrive_expect_tx(full, kStage);
+                        const uint32_t a = sb + s * S::stage, b = a + kABytes;
+                        uint32_t full = full_bar(s);
+                        if (CTAS == 2) full = cluster_map(full, 0);  // the issuing CTA waits for
+                                                                     // both CTAs' bytes
+                        if (rank == 0) mbar_arrive_expect_tx(full_bar(s), CTAS * S::stage);
                         if (A_MN) {
 #pragma unroll
                             for (int i = 0; i < BM / 64; ++i)
-                                tma_load_3d(a + i * BK * 128, ta, ar + 64 * i, kb * BK + p.ak_row0, pa,
-                                            full);
+                                tma_load_3d<CTAS>(a + i * BK * 128, ta, ar + 64 * i,
+                                                  kb * BK + p.ak_row0, pa, full);
                         } else {
-                            tma_load_3d(a, ta, kb * BK, ar, pa, full);
+                            tma_load_3d<CTAS>(a, ta, kb * BK, ar, pa, full);
                         }
                         if (B_MN) {
 #pragma unroll
-                            for (int i = 0; i < BN / 64; ++i)
-                                tma_load_3d(b + i * BK * 128, tb, br + 64 * i, kb * BK + p.bk_row0, pb,
-                                            full);
+                            for (int i = 0; i < kRowsB / 64; ++i)
+                                tma_load_3d<CTAS>(b + i * BK * 128, tb, br + 64 * i,
+                                                  kb * BK + p.bk_row0, pb, full);
                         } else {
-                            tma_load_3d(b, tb, kb * BK, br, pb, full);
+#pragma unroll
+                            for (int i = 0; i < kRowsB / 128; ++i)
+                                tma_load_3d<CTAS>(b + i * BK * 256, tb, kb * BK, br + 128 * i, pb,
+                                                  full);
                         }
                     }
                 }
             }
             if (*abort) {  // let the copies in flight land before the CTA exits
-                volatile int never = 0;
-                for (int k = it > kStages ? it - kStages : 0; k < it; ++k)
-                    mbar_wait(bar(B_FULL + k % kStages), (k / kStages) & 1, &never, kWaitLimit);
+                if (rank == 0) {
+                    volatile int never = 0;
+                    for (int k = it > S::stages ? it - S::stages : 0; k < it; ++k)
+                        mbar_wait(full_bar(k % S::stages), (k / S::stages) & 1, &never, kWaitLimit);
+                } else {  // their barrier is the other CTA's
+                    const long long t0 = clock64();
+                    while (clock64() - t0 < 4000000) {
+                    }
+                }
             }
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = umma_idesc_bf16(BM, BN) | (A_MN ? 1u << 15 : 0u) |
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = umma_idesc_bf16(BM * CTAS, BN) | (A_MN ? 1u << 15 : 0u) |
                                    (B_MN ? 1u << 16 : 0u);
             int it = 0, i = 0;
             bool ok = true;
-            for (int w = blockIdx.x; w < work && ok; w += gridDim.x, ++i) {
-                const Tile t = tile_at(p, w);
+            for (int w = w0; w < work && ok; w += wstep, ++i) {
+                const Tile t = tile_at<CTAS>(p, w);
                 const int steps = (t.kb1 - t.kb0) * p.pairs;
                 for (int k = 0; k < steps; ++k, ++it) {
                     const int first = FINE ? k % kChunk : k;
                     if (first == 0) {
-                        if (k > 0) umma_commit(bar(B_ACCF + (i++ & 1)));
-                        ok = mbar_wait(bar(B_ACCE + (i & 1)), ((i >> 1) & 1) ^ 1, abort, kWaitLimit);
+                        if (k > 0) umma_commit_group<CTAS>(accf_bar(i++));
+                        ok = CTAS == 1 ? mbar_wait(acce_bar(i), ((i >> 1) & 1) ^ 1, abort, kWaitLimit)
+                                       : mbar_wait_cluster(acce_bar(i), ((i >> 1) & 1) ^ 1, abort,
+                                                           kWaitLimit);
                         if (!ok) break;
                         tc_fence_after();
                     }
-                    const int s = it % kStages;
-                    ok = mbar_wait(bar(B_FULL + s), (it / kStages) & 1, abort, kWaitLimit);
+                    const int s = it % S::stages;
+                    ok = mbar_wait(full_bar(s), (it / S::stages) & 1, abort, kWaitLimit);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = sb + s * kStage, b = a + kABytes;
+                    const uint32_t a = sb + s * S::stage, b = a + kABytes;
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
-                        umma_bf16(tmem + BN * (i & 1),
-                                  A_MN ? umma_desc_mn_sw128(a + kk * 2048)
-                                       : umma_desc_sw128(a + kk * 32, 1024),
-                                  B_MN ? umma_desc_mn_sw128(b + kk * 2048)
-                                       : umma_desc_sw128(b + kk * 32, 1024),
-                                  idesc, first + kk > 0);
-                    umma_commit(bar(B_EMPTY + s));
+                        umma_bf16_group<CTAS>(tmem + BN * (i & 1),
+                                              A_MN ? umma_desc_mn_sw128(a + kk * 2048)
+                                                   : umma_desc_sw128(a + kk * 32, 1024),
+                                              B_MN ? umma_desc_mn_sw128(b + kk * 2048)
+                                                   : umma_desc_sw128(b + kk * 32, 1024),
+                                              idesc, first + kk > 0);
+                    umma_commit_group<CTAS>(empty_bar(s));
                 }
-                if (ok) umma_commit(bar(B_ACCF + (i & 1)));
+                if (ok) umma_commit_group<CTAS>(accf_bar(i));
             }
             if (*abort) {  // products in flight complete before TMEM is freed
-                umma_commit(bar(B_FIN));
+                umma_commit_group<CTAS>(sb + S::fin);
                 volatile int never = 0;
-                mbar_wait(bar(B_FIN), 0, &never, kWaitLimit);
+                mbar_wait(sb + S::fin, 0, &never, kWaitLimit);
             }
         }
     } else {
@@ -409,22 +428,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + 128 * half;
         int i = 0;  // accumulators taken
         auto full = [&]() {
-            const bool ok = __all_sync(
-                0xffffffffu, mbar_wait(bar(B_ACCF + (i & 1)), (i >> 1) & 1, abort, kWaitLimit));
+            const bool ok =
+                __all_sync(0xffffffffu, mbar_wait(accf_bar(i), (i >> 1) & 1, abort, kWaitLimit));
             tc_fence_after();
             return ok;
         };
         auto release = [&]() {  // the accumulator is in registers
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(bar(B_ACCE + (i & 1)));
+            if (lane == 0) {
+                if (CTAS == 1) mbar_arrive(acce_bar(i));
+                else mbar_arrive_cluster(cluster_map(acce_bar(i), 0));
+            }
             ++i;
         };
         bool ok = true;
-        for (int w = blockIdx.x; w < work && ok; w += gridDim.x) {
-            const Tile t = tile_at(p, w);
+        for (int w = w0; w < work && ok; w += wstep) {
+            const Tile t = tile_at<CTAS>(p, w);
             Row<EPI> r;
-            r.begin(p, t, quarter, half, lane);
+            r.begin(p, t, (t.m * CTAS + rank) * BM + 32 * quarter + lane, half);
             __syncwarp();
             if constexpr (FINE) {
                 float acc[4][32];
@@ -452,11 +474,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 ok = full();
                 if (!ok) break;
+                const uint32_t at = src + BN * (i & 1);
 #pragma unroll 1
                 for (int ch = 0; ch < 4; ++ch) {
                     float v[32];
                     __syncwarp();
-                    tmem_ld32(src + BN * (i & 1) + 32 * ch, v);
+                    tmem_ld32(at + 32 * ch, v);
                     if (ch == 3) release();
                     r.take(p, t, ch, v);
                 }
@@ -467,10 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
+    if (CTAS == 2) cluster_sync_all();  // the pair's products read both CTAs' memory
     if (threadIdx.x == 0 && *abort) dev_fail(p.status, KDA_ERR_TIMEOUT);
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, kTmemCols);
+        tmem_dealloc_group<CTAS>(tmem, kTmemCols);
     }
 }
 
@@ -691,16 +715,47 @@ bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, long l
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int EPI, bool A_MN, bool B_MN, bool FINE, int CTAS>
+cudaError_t start_gemm(GemmArgs p, const CUtensorMap &ta, const CUtensorMap &tb, int n,
+                       cudaStream_t st) {
+    const auto kernel = gemm_kernel<EPI, A_MN, B_MN, FINE, CTAS>;
+    cudaError_t e = set_max_dynamic_smem((const void *)kernel, Smem<CTAS>::bytes);
+    if (e != cudaSuccess) return e;
+    p.m_tiles = cdiv(p.M, BM * CTAS);
+    p.n_tiles = cdiv(p.N, BN);
+    const long long work = (long long)p.m_tiles * p.n_tiles * p.splits;
+    const int groups = (int)(work < n / CTAS ? work : n / CTAS);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(groups * CTAS);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Smem<CTAS>::bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CTAS;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS == 1 ? 1 : 2;
+    return cudaLaunchKernelEx(&cfg, kernel, p, ta, tb);
+}
+
+// Pairs of CTAs unless single ones finish in fewer rounds over the SMs (few rows:
+// a pair's second half would be idle).
+bool use_pairs(const GemmArgs &p, int n) {
+    const long long cols = (long long)cdiv(p.N, BN) * p.splits;
+    const long long one = (cdiv(p.M, BM) * cols + n - 1) / n;
+    const long long two = (cdiv(p.M, 2 * BM) * cols + n / 2 - 1) / (n / 2);
+    return n >= 2 && two <= one;
+}
+
 template <int EPI, bool A_MN, bool B_MN, bool FINE>
 cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap &tb,
                      cudaStream_t st) {
-    const auto kernel = gemm_kernel<EPI, A_MN, B_MN, FINE>;
-    cudaError_t e = set_max_dynamic_smem((const void *)kernel, kSmem);
-    if (e != cudaSuccess) return e;
-    const long long work = (long long)p.m_tiles * p.n_tiles * p.splits;
     const int n = sms();
-    return launch_dependent(kernel, dim3((unsigned)(work < n ? work : n)), dim3(kThreads), kSmem, st,
-                            p, ta, tb);
+    return use_pairs(p, n) ? start_gemm<EPI, A_MN, B_MN, FINE, 2>(p, ta, tb, n, st)
+                           : start_gemm<EPI, A_MN, B_MN, FINE, 1>(p, ta, tb, n, st);
 }
 // The backward's products: in fp32 problems FINE, in BF16 ones (whose results are
 // rounded to 2^-8 of their value) not.
@@ -776,14 +831,12 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     }
     const int inner = l.pack ? l.pitch : desc->width;
     CUtensorMap ta, tb;
-    if (!encode(&ta, xp, inner, desc->tokens, inner, l.planes, BM) ||
-        !encode(&tb, wp, inner, desc->vocab, inner, l.planes, BN))
+    if (!encode(&ta, xp, inner, desc->tokens, inner, l.planes, 128) ||
+        !encode(&tb, wp, inner, desc->vocab, inner, l.planes, 128))
         return KDA_ERR_CUDA;
     GemmArgs p = {};
     p.M = desc->tokens;
     p.N = desc->vocab;
-    p.m_tiles = cdiv(p.M, BM);
-    p.n_tiles = cdiv(p.N, BN);
     p.k_blocks = cdiv(desc->width, BK);
     p.splits = 1;
     p.pairs = l.pairs;
@@ -794,7 +847,7 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     p.status = dev_status;
     if (run_gemm<EPI_STATS, false, false, true>(p, ta, tb, st) != cudaSuccess) return KDA_ERR_CUDA;
     if (launch_dependent(ce_join_kernel, dim3(cdiv(p.M, 32)), dim3(1024), 0, st,
-                         (const float2 *)part, 2 * p.n_tiles, p.M, p.y, (const float *)zy, loss, lse,
+                         (const float2 *)part, 2 * cdiv(p.N, BN), p.M, p.y, (const float *)zy, loss, lse,
                          mean, sums, ticket) != cudaSuccess)
         return KDA_ERR_CUDA;
     return KDA_OK;
@@ -841,11 +894,11 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
     // x and W as operands of the logits (contraction over D, K-major) and of the
     // gradients (contraction over tokens or vocabulary, MN-major); dz both ways
     CUtensorMap x_k, w_k, w_mn, x_mn, dz_k, dz_mn;
-    if (!encode(&x_k, xp, inner, T, inner, l.planes, BM) ||
-        !encode(&w_k, wp, inner, V, inner, l.planes, BN) ||
+    if (!encode(&x_k, xp, inner, T, inner, l.planes, 128) ||
+        !encode(&w_k, wp, inner, V, inner, l.planes, 128) ||
         !encode(&w_mn, wp, inner, V, inner, l.planes, BK) ||
         !encode(&x_mn, xp, inner, T, inner, l.planes, BK) ||
-        !encode(&dz_k, dz, l.piece, T, l.piece, l.planes, BM) ||
+        !encode(&dz_k, dz, l.piece, T, l.piece, l.planes, 128) ||
         !encode(&dz_mn, dz, l.piece, T, l.piece, l.planes, BK))
         return KDA_ERR_CUDA;
     for (int k = 0; k < l.pieces; ++k) {
@@ -856,8 +909,6 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.splits = 1;
         p.M = T;
         p.N = cols;
-        p.m_tiles = cdiv(T, BM);
-        p.n_tiles = cdiv(cols, BN);
         p.k_blocks = cdiv(D, BK);
         p.b_row0 = v0;
         p.y = {targets, desc->id_dtype == KDA_ID_I64, V, desc->ignore_index, dev_status};
@@ -874,8 +925,6 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.splits = l.dx_splits;
             q.M = T;
             q.N = D;
-            q.m_tiles = cdiv(T, BM);
-            q.n_tiles = cdiv(D, BN);
             q.k_blocks = cdiv(cols, BK);
             q.bk_row0 = v0;
             q.acc_in = k > 0 ? acc : nullptr;
@@ -905,8 +954,6 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.splits = 1;
             q.M = cols;
             q.N = D;
-            q.m_tiles = cdiv(cols, BM);
-            q.n_tiles = cdiv(D, BN);
             q.k_blocks = cdiv(T, BK);
             q.out = (uint8_t *)d_weight + (size_t)v0 * D * size;
             q.out_bf16 = size == 2;

@@ -376,6 +376,118 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
         : "memory");
 }
 
+// ---------------------------------------------------------------- CTA pairs
+// A cluster of two CTAs on neighbouring SMs works on one tcgen05.mma of 256 rows
+// (cta_group::2): each CTA holds half of the rows of A, of the rows of B and of the
+// accumulator; the even CTA issues.
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// All threads of the cluster meet (their earlier writes, barrier initialisations
+// included, are visible after it).
+__device__ __forceinline__ void cluster_sync_all() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+// Address, in the cluster's shared window, of what CTA `rank` has at `addr`.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+// Arrive on a barrier of the cluster (address from cluster_map).
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+// As mbar_wait for a barrier that threads of the other CTA arrive on.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort,
+                                                  long long limit_cycles) {
+    const long long t0 = clock64();
+#pragma unroll 1
+    while (true) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (ok) return true;
+        if (*abort) return false;
+        if (clock64() - t0 > limit_cycles) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+template <int CTAS>
+__device__ __forceinline__ void tmem_alloc_group(uint32_t dst_smem, uint32_t ncols) {
+    if (CTAS == 1) {
+        tmem_alloc(dst_smem, ncols);
+        tmem_relinquish();
+    } else {
+        asm volatile(
+            "tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n\t"
+            "tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::"r"(dst_smem),
+            "r"(ncols)
+            : "memory");
+    }
+}
+template <int CTAS>
+__device__ __forceinline__ void tmem_dealloc_group(uint32_t taddr, uint32_t ncols) {
+    if (CTAS == 1)
+        tmem_dealloc(taddr, ncols);
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols)
+                     : "memory");
+}
+template <int CTAS>
+__device__ __forceinline__ void umma_bf16_group(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                uint32_t idesc, uint32_t accumulate) {
+    if (CTAS == 1)
+        umma_bf16(d_tmem, adesc, bdesc, idesc, accumulate);
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+            : "memory");
+}
+// Arrive on `bar`, in every CTA of the group, once this thread's tcgen05 operations
+// so far have completed.
+template <int CTAS>
+__device__ __forceinline__ void umma_commit_group(uint32_t bar) {
+    if (CTAS == 1)
+        umma_commit(bar);
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
+            " [%0], %1;" ::"r"(bar),
+            "h"((unsigned short)3)
+            : "memory");
+}
+// 3D tiled tensor copy into this CTA's shared memory; in a pair, `bar` may be the
+// other CTA's barrier (address from cluster_map).
+template <int CTAS>
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, uint64_t tmap, int x, int y, int z,
+                                            uint32_t bar) {
+    if (CTAS == 1)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+            "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+            : "memory");
+}
+
 // ---------------------------------------------------------------- mma.sync
 // ldmatrix / mma.sync are not volatile: the scheduler may move them for latency.
 // The loads keep a memory clobber, so they stay ordered against other memory
