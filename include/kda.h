@@ -402,10 +402,13 @@ typedef struct {
  *   weight    [D] fp32, shared by all heads, or NULL (ones).
  *   out       [T, H, D] contiguous.
  * Pointers aligned to their element (16 bytes, with widths and strides of whole
- * 16-byte pieces, is the fast case), else KDA_ERR_INVALID_ARG.
+ * 16-byte pieces, is the fast case), else KDA_ERR_INVALID_ARG.  dev_status (device
+ * int32 or NULL), here and in the next three: KDA_ERR_TIMEOUT if a bounded wait of
+ * the kernel gave up, its outputs being incomplete then.
  */
 kda_status_t kda_gated_norm_forward(const kda_norm_desc_t *desc, const void *x, const void *gate,
-                                    const float *weight, void *out, void *stream);
+                                    const float *weight, void *out, int32_t *dev_status,
+                                    void *stream);
 
 /*
  * Its gradients for the adjoint d_out [T, H, D] (contiguous): dx, d_gate [T, H, D]
@@ -419,7 +422,7 @@ size_t kda_norm_backward_workspace_size(const kda_norm_desc_t *desc);
 kda_status_t kda_gated_norm_backward(const kda_norm_desc_t *desc, const void *d_out, const void *x,
                                      const void *gate, const float *weight, void *dx, void *d_gate,
                                      float *d_weight, void *workspace, size_t workspace_bytes,
-                                     void *stream);
+                                     int32_t *dev_status, void *stream);
 
 /*
  * The residual stream between two blocks: the block's output y enters it scaled,
@@ -430,7 +433,7 @@ kda_status_t kda_gated_norm_backward(const kda_norm_desc_t *desc, const void *d_
  */
 kda_status_t kda_residual_norm_forward(const kda_norm_desc_t *desc, const void *h, const void *y,
                                        const float *weight, float scale, void *h_out, void *out,
-                                       void *stream);
+                                       int32_t *dev_status, void *stream);
 
 /*
  * Its gradients, from h_out: with d_out for out and d_h_out (NULL: zero) for h_out,
@@ -441,7 +444,8 @@ kda_status_t kda_residual_norm_forward(const kda_norm_desc_t *desc, const void *
 kda_status_t kda_residual_norm_backward(const kda_norm_desc_t *desc, const void *d_out,
                                         const void *d_h_out, const void *h_out, const float *weight,
                                         float scale, void *dh, void *dy, float *d_weight,
-                                        void *workspace, size_t workspace_bytes, void *stream);
+                                        void *workspace, size_t workspace_bytes,
+                                        int32_t *dev_status, void *stream);
 
 typedef enum { KDA_ID_I32 = 0, KDA_ID_I64 = 1 } kda_id_dtype_t;
 

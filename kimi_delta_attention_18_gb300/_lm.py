@@ -42,10 +42,10 @@ def bind(L):
     P, I, Z, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
     N, E, C = (ctypes.POINTER(t) for t in (NormDesc, EmbedDesc, CrossEntropyDesc))
     for name, args in (
-            ("kda_gated_norm_forward", [N] + [P] * 5),
-            ("kda_gated_norm_backward", [N] + [P] * 8 + [Z, P]),
-            ("kda_residual_norm_forward", [N] + [P] * 3 + [F] + [P] * 3),
-            ("kda_residual_norm_backward", [N] + [P] * 4 + [F] + [P] * 4 + [Z, P]),
+            ("kda_gated_norm_forward", [N] + [P] * 6),
+            ("kda_gated_norm_backward", [N] + [P] * 8 + [Z, P, P]),
+            ("kda_residual_norm_forward", [N] + [P] * 3 + [F] + [P] * 4),
+            ("kda_residual_norm_backward", [N] + [P] * 4 + [F] + [P] * 4 + [Z, P, P]),
             ("kda_embedding_forward", [E] + [P] * 5),
             ("kda_embedding_backward", [E] + [P] * 4 + [Z, P, P]),
             ("kda_linear_ce_forward", [C] + [P] * 7 + [Z, P, P]),
@@ -69,9 +69,12 @@ def _lib():
 
 
 def _is(t, name, dtype, shape, dev):
-    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and
-            t.device == dev and t.is_contiguous()):
-        _k._need(t, name, dtype, shape, dev)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return
+    except AttributeError:  # no tensor: _need says so
+        pass
+    _k._need(t, name, dtype, shape, dev)
 
 
 def _ptr(t):
@@ -86,14 +89,16 @@ def _stream(stream, dev):
 
 def _first(t, name, dims):
     """Device and act_dtype of the operator's first tensor."""
+    try:
+        if len(t.shape) == dims and t.is_cuda:
+            return t.device, _ACT[t.dtype]
+    except (AttributeError, KeyError):
+        pass
     if not isinstance(t, torch.Tensor) or t.dim() != dims:
         raise ValueError("%s must be a tensor of %d dimensions" % (name, dims))
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
-    act = _ACT.get(t.dtype)
-    if act is None:
-        raise ValueError("%s must be float32 or bfloat16" % name)
-    return t.device, act
+    raise ValueError("%s must be float32 or bfloat16" % name)
 
 
 def _workspace(workspace, need, dev):
@@ -107,6 +112,8 @@ def _workspace(workspace, need, dev):
 def _out(out, name, like):
     """A caller's output of the same type and shape as ``like``, or a new one."""
     if out is None:
+        if like.is_contiguous():
+            return torch.empty_like(like)
         return torch.empty(like.shape, dtype=like.dtype, device=like.device)
     _is(out, name, like.dtype, like.shape, like.device)
     return out
@@ -124,11 +131,15 @@ def _status(dev_status, dev):
 def _rows(t, name, like):
     """A ``[T, H, D]`` tensor like ``like`` whose tokens may lie further apart than H D
     (a slice of a wider projection's output); returns the token stride, 0 for H D."""
-    if not (isinstance(t, torch.Tensor) and t.dtype is like.dtype and t.shape == like.shape and
-            t.device == like.device):
-        if isinstance(t, torch.Tensor) and not t.is_contiguous():
-            t = t.contiguous()  # for the error: the stride is not what is wrong
-        _k._need(t, name, like.dtype, like.shape, like.device)
+    if t is not like:
+        try:
+            ok = t.dtype is like.dtype and t.shape == like.shape and t.device == like.device
+        except AttributeError:
+            ok = False
+        if not ok:
+            if isinstance(t, torch.Tensor) and not t.is_contiguous():
+                t = t.contiguous()  # for the error: the stride is not what is wrong
+            _k._need(t, name, like.dtype, like.shape, like.device)
     if t.is_contiguous():
         return 0
     (T, H, D), (sT, sH, sD) = t.shape, t.stride()
@@ -151,7 +162,8 @@ def _gated(x, gate, weight, act, eps):
                          dtype, kind, eps)
 
 
-def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, stream=None):
+def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, dev_status=None,
+               stream=None):
     """RMS norm of a mixer's output per (token, head) with its gate: ``x r weight
     act(gate)`` (see kda_gated_norm_forward in kda.h).  x, gate ``[T, H, D]`` in one
     activation dtype, tokens possibly strided; weight ``[D]`` fp32 or None; act
@@ -160,12 +172,13 @@ def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, 
     out = _out(out, "out", x)
     _check("kda_gated_norm_forward",
            _lib().kda_gated_norm_forward(desc, x.data_ptr(), _ptr(gate), _ptr(weight),
-                                         out.data_ptr(), _stream(stream, dev)))
+                                         out.data_ptr(), _status(dev_status, dev),
+                                         _stream(stream, dev)))
     return out
 
 
 def gated_norm_backward(d_out, x, gate=None, weight=None, *, act="sigmoid", eps=1e-6,
-                        want_d_weight=True, workspace=None, stream=None):
+                        want_d_weight=True, workspace=None, dev_status=None, stream=None):
     """Gradients of ``gated_norm`` for the adjoint d_out ``[T, H, D]`` of its output:
     ``(dx, d_gate, d_weight)``, d_gate None without a gate, d_weight fp32 ``[D]`` (see
     kda_gated_norm_backward in kda.h)."""
@@ -181,7 +194,8 @@ def gated_norm_backward(d_out, x, gate=None, weight=None, *, act="sigmoid", eps=
     _check("kda_gated_norm_backward",
            L.kda_gated_norm_backward(desc, d_out.data_ptr(), x.data_ptr(), _ptr(gate),
                                      _ptr(weight), dx.data_ptr(), _ptr(d_gate), _ptr(d_weight),
-                                     _ptr(workspace), ws_len, _stream(stream, dev)))
+                                     _ptr(workspace), ws_len, _status(dev_status, dev),
+                                     _stream(stream, dev)))
     return dx, d_gate, d_weight
 
 
@@ -197,7 +211,7 @@ def _residual(h, weight, eps, name):
 
 
 def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, out=None,
-                  stream=None):
+                  dev_status=None, stream=None):
     """The residual stream's update and the next block's norm: ``h_out = h + scale y``
     and the RMS norm of it times weight (see kda_residual_norm_forward in kda.h).
     h, y ``[T, D]``; without y, h_out is h.  Returns ``(h_out, out)``."""
@@ -211,12 +225,14 @@ def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, ou
     out = _out(out, "out", h)
     _check("kda_residual_norm_forward",
            _lib().kda_residual_norm_forward(desc, h.data_ptr(), _ptr(y), _ptr(weight), scale,
-                                            _ptr(new_h), out.data_ptr(), _stream(stream, dev)))
+                                            _ptr(new_h), out.data_ptr(),
+                                            _status(dev_status, dev), _stream(stream, dev)))
     return (h if y is None else new_h), out
 
 
 def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0, eps=1e-6,
-                           want_dy=True, want_d_weight=True, workspace=None, stream=None):
+                           want_dy=True, want_d_weight=True, workspace=None, dev_status=None,
+                           stream=None):
     """Gradients of ``residual_norm`` from its h_out, for the adjoints d_out of the
     norm and d_h_out (None: zero) of h_out: ``(dh, dy, d_weight)`` (see
     kda_residual_norm_backward in kda.h).  With scale 1, dy is dh itself."""
@@ -235,18 +251,21 @@ def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0
            L.kda_residual_norm_backward(desc, d_out.data_ptr(), _ptr(d_h_out), h_out.data_ptr(),
                                         _ptr(weight), scale, dh.data_ptr(), _ptr(dy),
                                         _ptr(d_weight), _ptr(workspace), ws_len,
-                                        _stream(stream, dev)))
+                                        _status(dev_status, dev), _stream(stream, dev)))
     return dh, (dh if want_dy and scale == 1.0 else dy), d_weight
 
 
 # --------------------------------------------------------------------- embedding
 
 def _ids(ids, name, dev, count=None):
-    if not isinstance(ids, torch.Tensor) or ids.dim() != 1:
-        raise ValueError("%s must be a [T] tensor" % name)
-    kind = _IDS.get(ids.dtype)
-    if kind is None:
-        raise ValueError("%s must be int32 or int64" % name)
+    try:
+        kind = _IDS[ids.dtype]
+        if len(ids.shape) != 1:
+            raise ValueError("%s must be a [T] tensor" % name)
+    except AttributeError:
+        raise TypeError("%s must be a torch.Tensor" % name) from None
+    except KeyError:
+        raise ValueError("%s must be int32 or int64" % name) from None
     _is(ids, name, ids.dtype, ids.shape if count is None else (count,), dev)
     return kind
 

@@ -66,6 +66,7 @@ struct Targets {
 struct GemmArgs {
     int M, N;                  // rows and columns of the product that exist
     int k_blocks, splits, pairs;
+    int chunk;                 // FINE: stages per accumulator
     int m_tiles, n_tiles;      // set at the launch
     int a_row0, b_row0;        // added to the operands' non-contraction coordinate
     int ak_row0, bk_row0;      // added to the contraction coordinate of MN-major operands
@@ -280,9 +281,13 @@ __device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
 // the tensor core adds each step of 16 to its accumulator with truncation, about
 // 2^-24 of the sum per step and always towards zero, so a long contraction loses
 // bits (at 7,168 measured 2.3e-6 of lse, against 1.4e-7 with fp32 arithmetic).  The
-// accumulator is then handed over every kChunk stages and added up, rounded to
-// nearest, in the epilogue's registers, while the other accumulator fills.
-constexpr int kChunk = 4;
+// accumulator is then handed over every `chunk` stages and added up, rounded to
+// nearest, in the epilogue's registers, while the other accumulator fills.  16
+// stages for BF16 operands (lse within 3e-7, no slower than one accumulator for
+// all: 1.93 ms at 2,048 x 131,072 x 7,168), 8 for fp32 ones (gradients within
+// 6e-7); 4 would cost a third more time, the hand-over then being longer than the
+// products it overlaps.
+constexpr int kChunkBf16 = 16, kChunkF32 = 8;
 
 template <int EPI, bool A_MN, bool B_MN, bool FINE, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -390,8 +395,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int w = w0; w < work && ok; w += wstep, ++i) {
                 const Tile t = tile_at<CTAS>(p, w);
                 const int steps = (t.kb1 - t.kb0) * p.pairs;
-                for (int k = 0; k < steps; ++k, ++it) {
-                    const int first = FINE ? k % kChunk : k;
+                int first = 0;  // stages in this accumulator
+                for (int k = 0; k < steps; ++k, ++it, ++first) {
+                    if (FINE && first == p.chunk) first = 0;
                     if (first == 0) {
                         if (k > 0) umma_commit_group<CTAS>(accf_bar(i++));
                         ok = CTAS == 1 ? mbar_wait(acce_bar(i), ((i >> 1) & 1) ^ 1, abort, kWaitLimit)
@@ -455,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < 32; ++j) acc[ch][j] = 0.f;
                 const int steps = (t.kb1 - t.kb0) * p.pairs;
-                for (int k = 0; k < steps && ok; k += kChunk) {
+                for (int k = 0; k < steps && ok; k += p.chunk) {
                     ok = full();
                     if (!ok) break;
 #pragma unroll
@@ -649,20 +655,23 @@ int piece_cols(const kda_ce_desc_t *d, int planes) {
 }
 
 struct Layout {
-    int planes, pairs, pitch, piece, pieces, dx_splits;
+    int planes, pairs, chunk, pitch, piece, pieces, dx_splits;
     bool pack;
     size_t xp, wp, part, zy, sums, dz, acc, total;
 };
 
-// Pieces of the workspace.  pack: operands are copied (fp32 terms, or rows padded
-// to the pitch of whole 16-byte pieces that a tensor map needs).
+// Pieces of the workspace.  pack: operands are copied (fp32 terms, or BF16 rows
+// whose width is no multiple of the 16 bytes that a tensor map needs).
 Layout layout_for(const kda_ce_desc_t *d, bool backward) {
     Layout l = {};
     const bool pack = d->act_dtype == KDA_DTYPE_F32 || d->width % 8 != 0;
     const size_t T = d->tokens, V = d->vocab;
     l.planes = d->act_dtype == KDA_DTYPE_F32 ? 3 : 1;
     l.pairs = l.planes == 3 ? 6 : 1;
-    l.pitch = (d->width + 7) / 8 * 8;
+    l.chunk = l.planes == 3 ? kChunkF32 : kChunkBf16;
+    // whole 128-byte lines: with rows of 1,040 bytes the copies of 128-byte boxes ran at
+    // half the rate
+    l.pitch = (d->width + 63) / 64 * 64;
     l.pack = pack;
     l.xp = pack ? round256(T * l.pitch * l.planes * 2) : 0;
     l.wp = pack ? round256(V * l.pitch * l.planes * 2) : 0;
@@ -840,6 +849,7 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     p.k_blocks = cdiv(desc->width, BK);
     p.splits = 1;
     p.pairs = l.pairs;
+    p.chunk = l.chunk;
     p.y = {targets, desc->id_dtype == KDA_ID_I64, desc->vocab, desc->ignore_index, dev_status};
     p.part = part;
     p.z_y = zy;
@@ -906,6 +916,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         GemmArgs p = {};
         p.status = dev_status;
         p.pairs = l.pairs;
+        p.chunk = l.chunk;
         p.splits = 1;
         p.M = T;
         p.N = cols;
@@ -922,6 +933,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             GemmArgs q = {};
             q.status = dev_status;
             q.pairs = l.pairs;
+            q.chunk = l.chunk;
             q.splits = l.dx_splits;
             q.M = T;
             q.N = D;
@@ -951,6 +963,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             GemmArgs q = {};
             q.status = dev_status;
             q.pairs = l.pairs;
+            q.chunk = l.chunk;
             q.splits = 1;
             q.M = cols;
             q.N = D;

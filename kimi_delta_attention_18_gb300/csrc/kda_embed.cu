@@ -111,63 +111,46 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const __grid_co
 
 // Moves a tile's tokens to their places: all smaller digits, then the same digit
 // in earlier tiles, then in earlier warps of this tile, then earlier in the warp
-// (a warp holds consecutive tokens, 32 at a time).
+// (a warp holds consecutive tokens, 32 at a time).  A single tile needs no counts
+// of others, so up to kTile tokens take one launch per pass.
 __global__ void __launch_bounds__(kSortThreads)
     sort_scatter_kernel(const __grid_constant__ SortArgs a) {
-    constexpr int W = kSortThreads / 32;
+    constexpr int W = kSortThreads / 32, kPer = kMaxDigits / kSortThreads;
     __shared__ int first[kMaxDigits];             // place of this tile's first token per digit
+    __shared__ int total[kMaxDigits];             // tokens per digit, in all tiles
     __shared__ unsigned short cnt[W][kMaxDigits];  // tokens per warp and digit, then before it
-    __shared__ int part[kSortThreads];
+    __shared__ int warp_sum[W];
     const int digits = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int d = threadIdx.x; d < W * kMaxDigits; d += kSortThreads) (&cnt[0][0])[d] = 0;
+    for (int d = threadIdx.x; d < W * kMaxDigits / 2; d += kSortThreads) ((unsigned *)cnt)[d] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    // per digit: tokens in all tiles, and in the tiles before this one; thread
-    // i takes `per` consecutive digits
-    const int per = (digits + kSortThreads - 1) / kSortThreads;
-    int mine = 0;
-    for (int k = 0; k < per; ++k) {
-        const int d = threadIdx.x * per + k;
-        if (d >= digits) break;
-        int before = 0, all = 0;
-        for (int t = 0; t < a.tiles; ++t) {
-            const int n = a.hist[(size_t)t * digits + d];
-            all += n;
-            before += t < (int)blockIdx.x ? n : 0;
-        }
-        first[d] = mine + before;
-        mine += all;
-    }
-    part[threadIdx.x] = mine;
     __syncthreads();
-    if (warp == 0) {  // exclusive sums of the threads' totals
-        int v[W], s = 0;
-#pragma unroll
-        for (int k = 0; k < W; ++k) {
-            v[k] = s;
-            s += part[lane * W + k];
-        }
-        int inc = s;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += u;
-        }
-#pragma unroll
-        for (int k = 0; k < W; ++k) part[lane * W + k] = v[k] + inc - s;
-    }
-    __syncthreads();
-    for (int k = 0; k < per; ++k) {
-        const int d = threadIdx.x * per + k;
-        if (d < digits) first[d] += part[threadIdx.x];
-    }
     const int base = blockIdx.x * kTile + warp * (kTile / W);
     int key[kItems], rank[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const int i = base + k * 32 + lane;
-        const bool in = i < a.tokens;
-        key[k] = in ? sort_key(a, i, false) : -1;
+        key[k] = i < a.tokens ? sort_key(a, i, a.tiles == 1) : -1;
+    }
+    // per digit: tokens in all tiles, and in the tiles before this one
+    int before[kPer], all[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) before[k] = all[k] = 0;
+    if (a.tiles > 1) {
+#pragma unroll 8
+        for (int t = 0; t < a.tiles; ++t) {
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int d = threadIdx.x + k * kSortThreads;
+                const int n = d < digits ? a.hist[(size_t)t * digits + d] : 0;
+                all[k] += n;
+                before[k] += t < (int)blockIdx.x ? n : 0;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+        const bool in = key[k] >= 0;
         const int d = in ? (key[k] >> a.shift) & (digits - 1) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, d);
         const int ahead = __popc(same & ((1u << lane) - 1u));
@@ -177,7 +160,9 @@ __global__ void __launch_bounds__(kSortThreads)
         __syncwarp();
     }
     __syncthreads();
-    for (int d = threadIdx.x; d < digits; d += kSortThreads) {
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        const int d = threadIdx.x + k * kSortThreads;
         int s = 0;
 #pragma unroll
         for (int w = 0; w < W; ++w) {
@@ -185,12 +170,36 @@ __global__ void __launch_bounds__(kSortThreads)
             cnt[w][d] = (unsigned short)s;
             s += n;
         }
+        total[d] = a.tiles == 1 ? s : all[k];
     }
+    __syncthreads();
+    // exclusive sums over the digits: kPer consecutive ones per thread
+    int v[kPer], mine = 0;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        v[k] = mine;
+        mine += total[threadIdx.x * kPer + k];
+    }
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += u;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    int ahead = inc - mine;
+    for (int w = 0; w < warp; ++w) ahead += warp_sum[w];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) first[threadIdx.x * kPer + k] = ahead + v[k];
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) first[threadIdx.x + k * kSortThreads] += before[k];
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const int i = base + k * 32 + lane;
-        if (i >= a.tokens) continue;
+        if (key[k] < 0) continue;
         const int d = (key[k] >> a.shift) & (digits - 1);
         const int to = first[d] + cnt[warp][d] + rank[k];
         a.out_key[to] = key[k];
@@ -205,6 +214,7 @@ struct SumArgs {
     int parts;
     long long per;         // entries of the merged list per part
     float *carry, *head;   // [parts][D] fp32
+    int *cut;              // [parts]: tokens before the part
     float scale;
 };
 
@@ -233,6 +243,7 @@ __global__ void __launch_bounds__(kSumThreads)
     const long long d0 = blockIdx.x * a.per, d1 = d0 + a.per < total ? d0 + a.per : total;
     if (threadIdx.x < 2) cut[threadIdx.x] = merged_tokens(a, threadIdx.x ? d1 : d0);
     __syncthreads();
+    if (threadIdx.x == 0 && blockIdx.y == 0) a.cut[blockIdx.x] = cut[0];
     const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
     if (c >= a.D) return;
     int j = cut[0];
@@ -293,25 +304,21 @@ __global__ void __launch_bounds__(kSumThreads)
     __shared__ int from;
     griddep_wait();
     griddep_launch_dependents();
-    const long long total = (long long)a.rows + a.tokens;
-    const long long d0 = blockIdx.x * a.per, d1 = d0 + a.per < total ? d0 + a.per : total;
+    const long long d0 = blockIdx.x * a.per;
+    const int j0 = a.cut[blockIdx.x], i = (int)(d0 - j0);
+    const int i1 = blockIdx.x + 1 < (unsigned)a.parts
+                       ? (int)(d0 + a.per - a.cut[blockIdx.x + 1]) : a.rows;
+    if (j0 == 0 || i >= i1 || a.key[j0 - 1] != i) return;
     if (threadIdx.x == 0) {
-        from = -1;
-        const int j0 = merged_tokens(a, d0), j1 = merged_tokens(a, d1);
-        const int i = (int)(d0 - j0), i1 = (int)(d1 - j1);
-        if (j0 > 0 && i < a.rows && a.key[j0 - 1] == i && i < i1) {
-            int lo = 0, hi = j0 - 1;  // the row's first token
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (a.key[mid] < i) lo = mid + 1;
-                else hi = mid;
-            }
-            from = (int)(((long long)lo + i) / a.per);
+        int lo = 0, hi = j0 - 1;  // the row's first token
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (a.key[mid] < i) lo = mid + 1;
+            else hi = mid;
         }
+        from = (int)(((long long)lo + i) / a.per);
     }
     __syncthreads();
-    if (from < 0) return;
-    const int i = (int)(d0 - merged_tokens(a, d0));
     const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
     if (c >= a.D) return;
     float acc[VEC];
@@ -339,11 +346,11 @@ int key_bits(int rows) {  // keys 0 .. rows (rows: an id outside the table)
 struct Plan {
     int passes, bits, tiles, parts;
     long long per;
-    size_t pairs, hist, rem, total;
+    size_t pairs, hist, rem, cut, total;
 };
 
-// Parts of the merged list: at least 64 entries each (a part's binary search and
-// its fp32 remainder stay small beside its rows) and at most about 1,200 parts.
+// Parts of the merged list: at most 1,216 (with the column blocks enough for every
+// SM), at least 8 entries each.
 Plan plan_for(int tokens, int rows, int D) {
     Plan p;
     const int b = key_bits(rows);
@@ -352,12 +359,13 @@ Plan plan_for(int tokens, int rows, int D) {
     p.tiles = (tokens + kTile - 1) / kTile;
     const long long total = (long long)tokens + rows;
     p.per = (total + 1215) / 1216;
-    if (p.per < 64) p.per = 64;
+    if (p.per < 8) p.per = 8;
     p.parts = (int)((total + p.per - 1) / p.per);
     p.pairs = round256((size_t)tokens * 4);
     p.hist = round256((size_t)p.tiles * ((size_t)1 << p.bits) * 4);
     p.rem = round256((size_t)p.parts * D * 4);
-    p.total = 4 * p.pairs + p.hist + 2 * p.rem;
+    p.cut = round256((size_t)p.parts * 4);
+    p.total = 4 * p.pairs + p.hist + 2 * p.rem + p.cut;
     return p;
 }
 
@@ -473,8 +481,8 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
             last = k ? 1 - last : 0;
             a.out_key = keys[last];
             a.out_pos = poss[last];
-            if (launch_dependent(sort_hist_kernel, dim3(p.tiles), dim3(kSortThreads), 0, st, a) !=
-                    cudaSuccess ||
+            if ((p.tiles > 1 && launch_dependent(sort_hist_kernel, dim3(p.tiles), dim3(kSortThreads),
+                                                 0, st, a) != cudaSuccess) ||
                 launch_dependent(sort_scatter_kernel, dim3(p.tiles), dim3(kSortThreads), 0, st, a) !=
                     cudaSuccess)
                 return KDA_ERR_CUDA;
@@ -490,6 +498,7 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
     s.per = p.per;
     s.carry = (float *)(w + 4 * p.pairs + p.hist);
     s.head = (float *)(w + 4 * p.pairs + p.hist + p.rem);
+    s.cut = (int *)(w + 4 * p.pairs + p.hist + 2 * p.rem);
     s.scale = desc->scale;
     const bool vec = wide_rows(desc->width, size, d_out, d_table);
     cudaError_t e;

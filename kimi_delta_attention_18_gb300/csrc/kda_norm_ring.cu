@@ -1,0 +1,286 @@
+// The norms of many contiguous rows of whole 16-byte pieces: rows stream through
+// shared memory (bulk copies, a ring of stages), so the bytes in flight do not
+// depend on the registers that the arithmetic takes.
+#include "kda_norm_math.cuh"
+#include "kda_sm100.cuh"
+
+namespace kda {
+namespace {
+
+using namespace sm100;
+
+// 512 working threads and a warpgroup of which one thread copies.  Launched with 96
+// registers each; that warpgroup gives up 72 of them and the others take 16 more:
+// 512 x 112 + 128 x 24 = 60,416 of the 61,440 at launch.
+constexpr int kWork = 512, kWarps = kWork / 32, kThreads = kWork + 128;
+constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
+constexpr int kRingBytes = 208 * 1024, kMaxStages = 8;
+
+struct Ring {
+    int tpr, rows, arrays, stages;  // threads per row, rows per tile, arrays read
+    int array_bytes, stage_bytes;
+    long long tiles;
+};
+
+// A thread holds 16 elements (two BF16 pieces, four fp32); a tile is one row per group
+// of tpr threads: 16 KB per array where the width fills its threads.
+Ring ring_for(const NormArgs &a, int op, bool bwd, int size) {
+    Ring r = {};
+    const int pieces = a.D / (16 / size), nv = size;
+    r.tpr = 1;
+    while (r.tpr * nv < pieces) r.tpr *= 2;
+    if (pieces < nv || r.tpr > kWork) return r;  // arrays = 0: does not apply
+    r.rows = kWork / r.tpr;
+    r.tiles = (a.rows + r.rows - 1) / r.rows;
+    r.arrays = 1 + (bwd ? 1 : 0);
+    if (op == OP_SIGMOID || op == OP_SILU || (op == OP_RESIDUAL && (bwd ? a.d_res : a.gate))) ++r.arrays;
+    r.array_bytes = r.rows * a.D * size;
+    r.stage_bytes = r.arrays * r.array_bytes;
+    r.stages = kRingBytes / r.stage_bytes;
+    if (r.stages > kMaxStages) r.stages = kMaxStages;
+    return r;
+}
+
+// SKEW, for rows of more than a warp: a row's outputs come after the next row's sums,
+// so no warp waits at a barrier for its row's other warps.  The pieces are then read
+// from shared memory twice and the stage is released after the outputs.
+template <int OP, bool BWD, typename T, bool SKEW>
+__global__ void __launch_bounds__(kThreads, 1)
+    norm_ring_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ Ring r) {
+    constexpr int VEC = 16 / sizeof(T), NV = sizeof(T), VP = kPairs<VEC>, kRed = SKEW ? 4 : 2;
+    using P = Piece<T, VEC>;
+    extern __shared__ __align__(128) uint8_t sm[];
+    __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
+    __shared__ __align__(8) uint64_t sum_bars[kRed][kWarps / 2];
+    __shared__ float2 red[kRed][kWarps];
+    __shared__ int abort_flag;
+    volatile int *abort = &abort_flag;
+    const uint32_t sb = smem_addr(sm), bb = smem_addr(bars);
+    auto full = [&](int s) { return bb + 8 * s; };
+    auto empty = [&](int s) { return bb + 8 * (kMaxStages + s); };
+    const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < r.stages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), kWarps);
+        }
+        if (SKEW)
+            for (int k = 0; k < kRed; ++k)
+                for (int g = 0; g < r.rows; ++g) mbar_init(smem_addr(&sum_bars[k][g]), r.tpr / 32);
+        abort_flag = 0;
+        mbar_fence_init();
+    }
+    __syncthreads();
+    griddep_wait();
+
+    if (warp >= kWarps) {  // producer
+        regs_dealloc<24>();
+        if (threadIdx.x == kWork) {
+            const uint8_t *src[3] = {(const uint8_t *)p.x, nullptr, nullptr};
+            int n = 1;
+            const void *second = OP == OP_RESIDUAL && BWD ? p.d_res : p.gate;
+            if (OP != OP_NORM && second) src[n++] = (const uint8_t *)second;
+            if (BWD) src[n++] = (const uint8_t *)p.d_out;
+            int i = 0;
+            for (long long t = blockIdx.x; t < r.tiles; t += gridDim.x, ++i) {
+                const int s = i % r.stages;
+                if (!mbar_wait(empty(s), ((i / r.stages) & 1) ^ 1, abort, kWaitLimit)) break;
+                const long long row = t * r.rows, left = p.rows - row;
+                const uint32_t bytes =
+                    (uint32_t)((left < r.rows ? left : r.rows) * p.D * (long long)sizeof(T));
+                mbar_arrive_expect_tx(full(s), n * bytes);
+                for (int k = 0; k < n; ++k)
+                    bulk_g2s(sb + s * r.stage_bytes + k * r.array_bytes,
+                             src[k] + row * p.D * (long long)sizeof(T), bytes, full(s));
+            }
+            if (*abort) {  // let the copies in flight land before the block exits
+                volatile int never = 0;
+                for (int k = i > r.stages ? i - r.stages : 0; k < i; ++k)
+                    mbar_wait(full(k % r.stages), (k / r.stages) & 1, &never, kWaitLimit);
+            }
+        }
+        return;
+    }
+
+    regs_alloc<112>();
+    const int group = threadIdx.x / r.tpr, lane = threadIdx.x - group * r.tpr;
+    auto column = [&](int i) { return (lane + i * r.tpr) * VEC; };
+    auto load_w = [&](int i, f2 (&w)[VP]) {
+#pragma unroll
+        for (int j = 0; j < VP; ++j) {
+            w[j] = both(1.f);
+            if (p.w && column(i) < p.D) w[j] = *(const f2 *)(p.w + column(i) + 2 * j);
+        }
+    };
+    RowMath<OP, BWD, T, VEC, NV, !SKEW> math;
+    math.begin(load_w);
+    bool failed = false;  // a wait gave up: go through the motions, store nothing
+    P px[NV], pg[NV], pd[NV];
+    auto row_of = [&](long long t) { return t * r.rows + group; };
+    auto wait = [&](uint32_t bar, int parity) {
+        int ok = 1;
+        if (wl == 0) ok = mbar_wait(bar, parity, abort, kWaitLimit);
+        failed = failed || !__shfl_sync(0xffffffffu, ok, 0);
+    };
+    auto load = [&](long long t, int i) {
+        const uint8_t *at = sm + (i % r.stages) * r.stage_bytes + (size_t)group * p.D * sizeof(T);
+        const int second = r.array_bytes, third = (r.arrays - 1) * r.array_bytes;
+        const bool live = row_of(t) < p.rows, has_g = r.arrays == (BWD ? 3 : 2);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = column(k);
+            px[k].zero();
+            pg[k].zero();
+            pd[k].zero();
+            if (live && c < p.D) {
+                px[k].load((const T *)at + c);
+                if (OP != OP_NORM && has_g) pg[k].load((const T *)(at + second) + c);
+                if (BWD) pd[k].load((const T *)(at + third) + c);
+            }
+        }
+    };
+    auto release = [&](int i) {
+        __syncwarp();
+        if (wl == 0) mbar_arrive(empty(i % r.stages));
+    };
+    auto warp_sums = [&](float &ss, float &se, int w) {
+        for (int o = w >> 1; o > 0; o >>= 1) {
+            ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (BWD) se += __shfl_xor_sync(0xffffffffu, se, o);
+        }
+    };
+    const int nw = r.tpr >> 5;  // warps of a row
+    auto row_sums = [&](int buf, float &ss, float &se) {
+        const float2 u = red[buf][group * nw + (wl & (nw - 1))];
+        ss = u.x;
+        se = u.y;
+        warp_sums(ss, se, nw);
+    };
+    auto outputs = [&](long long t, float ss, float se) {
+        const long long row = row_of(t);
+        math.outputs(p, px, pg, pd, load_w, ss, se, [&](int k, f2 (&a1)[VP], f2 (&a2)[VP]) {
+            const int c = column(k);
+            if (row >= p.rows || failed || c >= p.D) return;
+            float v[VEC];
+            if (p.o1) {
+                floats<VEC>(a1, v);
+                P::store((T *)p.o1 + row * p.D + c, v);
+            }
+            if ((BWD || OP == OP_RESIDUAL) && p.o2) {
+                floats<VEC>(a2, v);
+                P::store((T *)p.o2 + row * p.D + c, v);
+            }
+        });
+    };
+    int i = 0;
+    if constexpr (SKEW) {
+        auto first_half = [&](long long t, int i) {
+            wait(full(i % r.stages), (i / r.stages) & 1);
+            load(t, i);
+            float ss, se;
+            math.sums(p, px, pg, pd, load_w, ss, se);
+            warp_sums(ss, se, 32);
+            if (wl == 0) {
+                red[i % kRed][warp] = make_float2(ss, se);
+                mbar_arrive(smem_addr(&sum_bars[i % kRed][group]));
+            }
+        };
+        if (blockIdx.x < r.tiles) first_half(blockIdx.x, 0);
+        for (long long t = blockIdx.x; t < r.tiles; t += gridDim.x, ++i) {
+            if (t + gridDim.x < r.tiles) first_half(t + gridDim.x, i + 1);
+            wait(smem_addr(&sum_bars[i % kRed][group]), (i / kRed) & 1);
+            float ss, se;
+            row_sums(i % kRed, ss, se);
+            load(t, i);
+            outputs(t, ss, se);
+            release(i);
+        }
+    } else {
+        for (long long t = blockIdx.x; t < r.tiles; t += gridDim.x, ++i) {
+            wait(full(i % r.stages), (i / r.stages) & 1);
+            load(t, i);
+            release(i);  // the stage is in registers
+            float ss, se;
+            math.sums(p, px, pg, pd, load_w, ss, se);
+            warp_sums(ss, se, r.tpr < 32 ? r.tpr : 32);
+            if (r.tpr > 32) {
+                if (wl == 0) red[i % kRed][warp] = make_float2(ss, se);
+                named_bar_sync(1 + group, r.tpr);
+                row_sums(i % kRed, ss, se);
+            }
+            outputs(t, ss, se);
+        }
+    }
+    griddep_launch_dependents();
+    if (threadIdx.x == 0 && *abort) dev_fail(p.status, KDA_ERR_TIMEOUT);
+    if (!BWD || !p.partial) return;
+    // dw: the block's groups in group order, in the ring (every copy has been used)
+    named_bar_sync(15, kWork);
+    if (*abort) return;
+    float *sh = (float *)sm;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        float v[VEC];
+        floats<VEC>(math.dw[k % (BWD ? NV : 1)], v);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (column(k) < p.D) sh[group * p.D + column(k) + j] = v[j];
+    }
+    named_bar_sync(15, kWork);
+    for (int c = threadIdx.x; c < p.D; c += kWork) {
+        float s = 0.f;
+        for (int g = 0; g < r.rows; ++g) s += sh[g * p.D + c];
+        p.partial[(size_t)blockIdx.x * p.D + c] = s;
+    }
+}
+
+template <int OP, bool BWD, typename T, bool SKEW>
+cudaError_t launch_k(const NormArgs &a, const Ring &r, int blocks, cudaStream_t st) {
+    cudaError_t e =
+        set_max_dynamic_smem((const void *)norm_ring_kernel<OP, BWD, T, SKEW>, kRingBytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(norm_ring_kernel<OP, BWD, T, SKEW>, dim3(blocks), dim3(kThreads),
+                            r.stages * r.stage_bytes, st, a, r);
+}
+
+template <int OP, bool BWD>
+cudaError_t launch_op(const NormArgs &a, const Ring &r, int size, int blocks, cudaStream_t st) {
+    // two stages are in use at a time with SKEW
+    const bool skew = r.tpr > 32 && r.stages >= 4;
+    if (size == 4)
+        return skew ? launch_k<OP, BWD, float, true>(a, r, blocks, st)
+                    : launch_k<OP, BWD, float, false>(a, r, blocks, st);
+    return skew ? launch_k<OP, BWD, __nv_bfloat16, true>(a, r, blocks, st)
+                : launch_k<OP, BWD, __nv_bfloat16, false>(a, r, blocks, st);
+}
+
+template <bool BWD>
+cudaError_t launch_b(const NormArgs &a, const Ring &r, int op, int size, int blocks,
+                     cudaStream_t st) {
+    switch (op) {
+        case OP_NORM: return launch_op<OP_NORM, BWD>(a, r, size, blocks, st);
+        case OP_SIGMOID: return launch_op<OP_SIGMOID, BWD>(a, r, size, blocks, st);
+        case OP_SILU: return launch_op<OP_SILU, BWD>(a, r, size, blocks, st);
+    }
+    return launch_op<OP_RESIDUAL, BWD>(a, r, size, blocks, st);
+}
+
+}  // namespace
+
+int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size) {
+    const Ring r = ring_for(a, op, bwd, size);
+    int dev = 0, sms = 152;
+    if (cudaGetDevice(&dev) == cudaSuccess)
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    // fewer than a few tiles per SM: the ring would not fill, and its start costs more
+    return r.arrays && r.stages >= 2 && r.tiles >= 4ll * sms ? sms : 0;
+}
+
+cudaError_t launch_norm_ring(const NormArgs &a, int op, bool bwd, int size, cudaStream_t st) {
+    const Ring r = ring_for(a, op, bwd, size);
+    const int blocks = norm_ring_blocks(a, op, bwd, size);
+    return bwd ? launch_b<true>(a, r, op, size, blocks, st)
+               : launch_b<false>(a, r, op, size, blocks, st);
+}
+
+}  // namespace kda

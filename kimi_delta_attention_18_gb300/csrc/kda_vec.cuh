@@ -17,6 +17,12 @@ struct Piece<float, 4> {
     __device__ __forceinline__ void get(float (&v)[4]) const {
         v[0] = raw.x; v[1] = raw.y; v[2] = raw.z; v[3] = raw.w;
     }
+    __device__ __forceinline__ void set(int j, float x) {
+        if (j == 0) raw.x = x;
+        if (j == 1) raw.y = x;
+        if (j == 2) raw.z = x;
+        if (j == 3) raw.w = x;
+    }
     static __device__ __forceinline__ void store(float *p, const float (&v)[4]) {
         *(float4 *)p = make_float4(v[0], v[1], v[2], v[3]);
     }
@@ -36,6 +42,13 @@ struct Piece<__nv_bfloat16, 8> {
             v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
         }
     }
+    __device__ __forceinline__ void set(int j, __nv_bfloat16 x) {
+        const uint32_t b = (uint32_t)__bfloat16_as_ushort(x) << (16 * (j & 1));
+        if (j / 2 == 0) raw.x |= b;  // after zero()
+        if (j / 2 == 1) raw.y |= b;
+        if (j / 2 == 2) raw.z |= b;
+        if (j / 2 == 3) raw.w |= b;
+    }
     static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&v)[8]) {
         uint32_t w[4];
 #pragma unroll
@@ -52,11 +65,40 @@ struct Piece<T, 1> {
     T raw;
     __device__ __forceinline__ void load(const T *p) { raw = *p; }
     __device__ __forceinline__ void zero() { raw = T(0.f); }
+    __device__ __forceinline__ void set(int, T x) { raw = x; }
     __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = (float)raw; }
     static __device__ __forceinline__ void store(T *p, const float (&v)[1]) { act_st(p, 0, v[0]); }
 };
 
-template <typename T>
-constexpr int kFullVec = 16 / (int)sizeof(T);
+// Columns [c, c + VEC) of a row of D: without SHIFT c is a multiple of VEC and a piece
+// is in the row or past it; with it rows start anywhere, pieces are aligned in memory
+// (c may be negative) and those at the row's two ends are moved element by element
+// (loading them whole and cutting them was 5 % slower).
+template <bool SHIFT, typename T, int VEC>
+__device__ __forceinline__ void load_piece(Piece<T, VEC> &p, const T *row, int c, int D) {
+    if (!SHIFT) {
+        if (c < D) p.load(row + c);
+        else p.zero();
+    } else if (c >= 0 && c + VEC <= D) {
+        p.load(row + c);
+    } else {
+        p.zero();
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c + j >= 0 && c + j < D) p.set(j, row[c + j]);
+    }
+}
+template <bool SHIFT, typename T, int VEC>
+__device__ __forceinline__ void store_piece(T *row, int c, int D, const float (&v)[VEC]) {
+    if (!SHIFT) {
+        if (c < D) Piece<T, VEC>::store(row + c, v);
+    } else if (c >= 0 && c + VEC <= D) {
+        Piece<T, VEC>::store(row + c, v);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+            if (c + j >= 0 && c + j < D) act_st(row, c + j, v[j]);
+    }
+}
 
 }  // namespace kda
