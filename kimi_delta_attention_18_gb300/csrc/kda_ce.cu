@@ -25,7 +25,7 @@ namespace {
 using namespace sm100;
 
 constexpr int BM = 128, BN = 256, BK = 64;  // rows per CTA, columns, contraction per stage
-constexpr int kABytes = BM * BK * 2, kBBytes = BN * BK * 2;
+constexpr int kABytes = BM * BK * 2, kBBytes = BN * BK * 2, kBox = 64 * BK * 2;
 constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
 constexpr int kGroupRows = 2048;  // rows whose tiles share a sweep over the column tiles
 constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
@@ -37,7 +37,8 @@ constexpr uint32_t kTmemCols = 512;  // two 256-column accumulators
 template <int CTAS>
 struct Smem {
     static constexpr int stage = kABytes + kBBytes / CTAS, stages = CTAS == 1 ? 4 : 6;
-    static constexpr int full = stages * stage, empty = full + 8 * stages, accf = empty + 8 * stages,
+    static constexpr int out = stages * stage;  // 4 KB per epilogue warp
+    static constexpr int full = out + kEpiWarps * 4096, empty = full + 8 * stages, accf = empty + 8 * stages,
                          acce = accf + 16, fin = acce + 16, misc = fin + 8;
     static constexpr int bytes = misc + 16 + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory budget");
@@ -67,7 +68,7 @@ struct GemmArgs {
     int M, N;                  // rows and columns of the product that exist
     int k_blocks, splits, pairs;
     int chunk;                 // FINE: stages per accumulator
-    int m_tiles, n_tiles;      // set at the launch
+    int m_tiles, n_tiles, bn;  // set at the launch; bn: columns per tile, a multiple of 64
     int a_row0, b_row0;        // added to the operands' non-contraction coordinate
     int ak_row0, bk_row0;      // added to the contraction coordinate of MN-major operands
     // EPI_STATS, EPI_DZ
@@ -126,20 +127,58 @@ __device__ __forceinline__ int term_b(int i, int pairs) {
     return pairs == 1 ? 0 : (0x010201 >> (4 * (i))) & 3;
 }
 
-// One thread's part of the epilogue: a row and 128 of the tile's columns, taken 32
-// at a time.
+// A warp's 32 rows x 128 bytes on their way to memory: a thread has a row, but a store
+// should have whole lines (with a row per thread each store instruction touched 32 of
+// them, and storing three terms of dz took as long as half of the tile's products).
+struct Turn {
+    uint32_t at;
+    int lane;
+    // 16-byte piece q of this thread's row
+    __device__ __forceinline__ void put(int q, uint4 v) const {
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
+                         at + lane * 128 + ((q ^ (lane & 7)) << 4)),
+                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                     : "memory");
+    }
+    __device__ __forceinline__ int row(int it) const { return 4 * it + (lane >> 3); }
+    // piece lane % 8 of row(it), it = 0 .. 7
+    __device__ __forceinline__ uint4 get(int it) const {
+        uint4 v;
+        const int r = row(it);
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                     : "r"(at + r * 128 + (((lane & 7) ^ (r & 7)) << 4))
+                     : "memory");
+        return v;
+    }
+    // word `lane` of row r
+    __device__ __forceinline__ float word(int r) const {
+        float v;
+        asm volatile("ld.shared.f32 %0, [%1];"
+                     : "=f"(v)
+                     : "r"(at + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3))
+                     : "memory");
+        return v;
+    }
+};
+
+// One thread's part of the epilogue: a row and up to 128 of the tile's columns, taken
+// 32 at a time.
 template <int EPI>
 struct Row {
-    long long row;
+    int row0;       // the warp's first row
+    long long row;  // this thread's
     bool live;
     int c0;  // first column, in the launch's columns
     int y;   // the target's column (negative: none)
     float mx, sum, lse2, g;
 
-    __device__ __forceinline__ void begin(const GemmArgs &p, const Tile &t, int row0, int half) {
-        row = row0;
+    __device__ __forceinline__ void begin(const GemmArgs &p, const Tile &t, int first_row, int lane,
+                                          int half) {
+        row0 = first_row;
+        row = first_row + lane;
         live = row < p.M;
-        c0 = t.n * BN + half * 128;
+        c0 = t.n * p.bn + half * 128;
         y = -1;
         mx = -INFINITY;
         sum = lse2 = g = 0.f;
@@ -153,101 +192,141 @@ struct Row {
         }
     }
 
-    __device__ __forceinline__ void take(const GemmArgs &p, const Tile &t, int ch, float (&v)[32]) {
-        const int c = c0 + 32 * ch;
+    // 32 values as BF16 into half `h` of the warp's lines; what the rounding left stays
+    // in v if LEFT.
+    template <bool LEFT>
+    __device__ __forceinline__ void put_bf16(const Turn &turn, int h, float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = pack_bf16x2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+                if (LEFT) {
+                    v[8 * i + 2 * k] -= __uint_as_float(w[k] << 16);
+                    v[8 * i + 2 * k + 1] -= __uint_as_float(w[k] & 0xffff0000u);
+                }
+            }
+            turn.put(4 * h + i, make_uint4(w[0], w[1], w[2], w[3]));
+        }
+    }
+    // The lines to memory: row r's at base + r pitch.
+    __device__ __forceinline__ void lines(const GemmArgs &p, const Turn &turn, __nv_bfloat16 *base,
+                                          size_t pitch) {
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const long long r = row0 + turn.row(it);
+            const uint4 u = turn.get(it);
+            if (r < p.M) *(uint4 *)(base + (size_t)r * pitch + 8 * (turn.lane & 7)) = u;
+        }
+        __syncwarp();
+    }
+
+    // v -> d_loss (softmax - onehot) for columns c .. c + 31
+    __device__ __forceinline__ void dz_of(const GemmArgs &p, int c, float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            const float e = g * exp2f(fmaf(v[i], kLog2e, -lse2));
+            v[i] = g != 0.f && c + i < p.N ? e : 0.f;
+        }
+        if (__any_sync(0xffffffffu, y >= c && y < c + 32)) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] -= c + i == y ? g : 0.f;
+        }
+    }
+
+    __device__ __forceinline__ void stats(const GemmArgs &p, int c, float (&v)[32]) {
+        if (c + 32 > p.N) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = c + i < p.N ? v[i] : -INFINITY;
+        }
         const bool mine = y >= c && y < c + 32;
+        if (__any_sync(0xffffffffu, mine)) {
+            float z = 0.f;
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z = c + i == y ? v[i] : z;
+            if (mine) p.z_y[row] = z;
+        }
+        float m = mx;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
+        const float ref = m == -INFINITY ? 0.f : m * kLog2e;
+        sum *= exp2f(mx == -INFINITY ? -INFINITY : fmaf(mx, kLog2e, -ref));
+        float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s[i & 3] += exp2f(fmaf(v[i], kLog2e, -ref));
+        sum += (s[0] + s[1]) + (s[2] + s[3]);
+        mx = m;
+    }
+
+    // 32 columns of fp32 (+ acc_in) to acc_out or out
+    __device__ __forceinline__ void out32(const GemmArgs &p, const Tile &t, const Turn &turn, int c,
+                                          float (&v)[32]) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            turn.put(i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
+        __syncwarp();
+        const bool narrow = p.out && p.out_bf16;
+        float *o32 = p.out ? (float *)p.out : p.acc_out + (size_t)t.split * p.M * p.N;
+        __nv_bfloat16 *o16 = (__nv_bfloat16 *)p.out;
+        if (p.vec) {  // widths and bases of whole pieces: four columns are in or out together
+            const int col = c + 4 * (turn.lane & 7);
+#pragma unroll
+            for (int it = 0; it < 8; ++it) {
+                const long long r = row0 + turn.row(it);
+                const uint4 u = turn.get(it);
+                if (r >= p.M || col >= p.N) continue;
+                const size_t at = (size_t)r * p.N + col;
+                float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
+                                       __uint_as_float(u.z), __uint_as_float(u.w));
+                if (p.acc_in) {
+                    const float4 a = *(const float4 *)(p.acc_in + at);
+                    f = make_float4(f.x + a.x, f.y + a.y, f.z + a.z, f.w + a.w);
+                }
+                if (narrow)
+                    *(uint2 *)(o16 + at) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
+                else
+                    *(float4 *)(o32 + at) = f;
+            }
+        } else {
+            const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32);
+#pragma unroll 4
+            for (int r = 0; r < rows; ++r) {
+                float f = turn.word(r);
+                if (c + turn.lane >= p.N) continue;
+                const size_t at = (size_t)(row0 + r) * p.N + c + turn.lane;
+                if (p.acc_in) f += p.acc_in[at];
+                if (narrow) o16[at] = __float2bfloat16_rn(f);
+                else o32[at] = f;
+            }
+        }
+        __syncwarp();
+    }
+
+    // Columns c0 + 64 q .. + 63 as two halves a, b.
+    __device__ __forceinline__ void pair(const GemmArgs &p, const Tile &t, const Turn &turn, int q,
+                                         float (&a)[32], float (&b)[32]) {
+        const int c = c0 + 64 * q;
         if (EPI == EPI_STATS) {
-            if (c + 32 > p.N) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = c + i < p.N ? v[i] : -INFINITY;
-            }
-            if (__any_sync(0xffffffffu, mine)) {
-                float z = 0.f;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) z = c + i == y ? v[i] : z;
-                if (mine) p.z_y[row] = z;
-            }
-            float m = mx;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
-            const float ref = m == -INFINITY ? 0.f : m * kLog2e;
-            sum *= exp2f(mx == -INFINITY ? -INFINITY : fmaf(mx, kLog2e, -ref));
-            float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int i = 0; i < 32; ++i) s[i & 3] += exp2f(fmaf(v[i], kLog2e, -ref));
-            sum += (s[0] + s[1]) + (s[2] + s[3]);
-            mx = m;
+            stats(p, c, a);
+            stats(p, c + 32, b);
         } else if (EPI == EPI_DZ) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                const float e = g * exp2f(fmaf(v[i], kLog2e, -lse2));
-                v[i] = g != 0.f && c + i < p.N ? e : 0.f;
+            dz_of(p, c, a);
+            dz_of(p, c + 32, b);
+            for (int pl = 0; pl < p.planes; ++pl) {
+                put_bf16<true>(turn, 0, a);
+                put_bf16<true>(turn, 1, b);
+                lines(p, turn, p.dz + (size_t)pl * p.M * p.pitch + c, p.pitch);
             }
-            if (__any_sync(0xffffffffu, mine)) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] -= c + i == y ? g : 0.f;
-            }
-            if (live) {
-                for (int pl = 0; pl < p.planes; ++pl) {
-                    uint4 *dst = (uint4 *)(p.dz + ((size_t)pl * p.M + row) * p.pitch + c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            w[k] = pack_bf16x2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-                            v[8 * i + 2 * k] -= __uint_as_float(w[k] << 16);
-                            v[8 * i + 2 * k + 1] -= __uint_as_float(w[k] & 0xffff0000u);
-                        }
-                        dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-            }
-        } else if (live && c < p.N) {
-            const size_t at = (size_t)row * p.N + c;
-            const int n = min(32, p.N - c);
-            if (p.acc_in) {
-                if (p.vec && n == 32) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float4 a = *(const float4 *)(p.acc_in + at + 4 * i);
-                        v[4 * i] += a.x; v[4 * i + 1] += a.y; v[4 * i + 2] += a.z; v[4 * i + 3] += a.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < n) v[i] += p.acc_in[at + i];
-                }
-            }
-            if (p.out && p.out_bf16) {
-                __nv_bfloat16 *o = (__nv_bfloat16 *)p.out + at;
-                if (p.vec && n == 32) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        *(uint4 *)(o + 8 * i) =
-                            make_uint4(pack_bf16x2(v[8 * i], v[8 * i + 1]),
-                                       pack_bf16x2(v[8 * i + 2], v[8 * i + 3]),
-                                       pack_bf16x2(v[8 * i + 4], v[8 * i + 5]),
-                                       pack_bf16x2(v[8 * i + 6], v[8 * i + 7]));
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < n) o[i] = __float2bfloat16_rn(v[i]);
-                }
-            } else {
-                float *o = p.out ? (float *)p.out + at
-                                 : p.acc_out + (size_t)t.split * p.M * p.N + at;
-                if (p.vec && n == 32) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        *(float4 *)(o + 4 * i) =
-                            make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (i < n) o[i] = v[i];
-                }
-            }
+        } else if (p.out && p.out_bf16 && !p.acc_in && p.vec && c + 64 <= p.N) {
+            put_bf16<false>(turn, 0, a);
+            put_bf16<false>(turn, 1, b);
+            lines(p, turn, (__nv_bfloat16 *)p.out + c, p.N);
+        } else {
+            if (c < p.N) out32(p, t, turn, c, a);
+            if (c + 32 < p.N) out32(p, t, turn, c + 32, b);
         }
     }
 
@@ -294,7 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs p, const __grid_constant__ CUtensorMap tm_a,
                 const __grid_constant__ CUtensorMap tm_b) {
     using S = Smem<CTAS>;
-    constexpr int kRowsB = BN / CTAS;  // B's rows in this CTA
     extern __shared__ uint8_t smem_raw[];
     uint8_t *sm = smem_raw + ((1024u - (smem_addr(smem_raw) & 1023u)) & 1023u);
     const uint32_t sb = smem_addr(sm);
@@ -335,12 +413,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const uint64_t ta = reinterpret_cast<uint64_t>(&tm_a);
             const uint64_t tb = reinterpret_cast<uint64_t>(&tm_b);
+            const int boxes = (p.bn / CTAS + 63) / 64;  // of B
             int it = 0;
             bool ok = true;
             for (int w = w0; w < work && ok; w += wstep) {
                 const Tile t = tile_at<CTAS>(p, w);
                 const int ar = (t.m * CTAS + rank) * BM + p.a_row0;
-                const int br = t.n * BN + rank * kRowsB + p.b_row0;
+                const int br = t.n * p.bn + rank * (p.bn / CTAS) + p.b_row0;
                 for (int pr = 0; pr < p.pairs && ok; ++pr) {
                     const int pa = term_a(pr, p.pairs), pb = term_b(pr, p.pairs);
                     for (int kb = t.kb0; kb < t.kb1; ++kb, ++it) {
@@ -351,26 +430,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t full = full_bar(s);
                         if (CTAS == 2) full = cluster_map(full, 0);  // the issuing CTA waits for
                                                                      // both CTAs' bytes
-                        if (rank == 0) mbar_arrive_expect_tx(full_bar(s), CTAS * S::stage);
-                        if (A_MN) {
+                        if (rank == 0)
+                            mbar_arrive_expect_tx(full_bar(s), CTAS * (kABytes + boxes * kBox));
+                        // boxes of 64 x 64: 64 rows of the contraction's 64, or the other
+                        // way round
 #pragma unroll
-                            for (int i = 0; i < BM / 64; ++i)
-                                tma_load_3d<CTAS>(a + i * BK * 128, ta, ar + 64 * i,
-                                                  kb * BK + p.ak_row0, pa, full);
-                        } else {
-                            tma_load_3d<CTAS>(a, ta, kb * BK, ar, pa, full);
-                        }
-                        if (B_MN) {
-#pragma unroll
-                            for (int i = 0; i < kRowsB / 64; ++i)
-                                tma_load_3d<CTAS>(b + i * BK * 128, tb, br + 64 * i,
-                                                  kb * BK + p.bk_row0, pb, full);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < kRowsB / 128; ++i)
-                                tma_load_3d<CTAS>(b + i * BK * 256, tb, kb * BK, br + 128 * i, pb,
-                                                  full);
-                        }
+                        for (int i = 0; i < BM / 64; ++i)
+                            tma_load_3d<CTAS>(a + i * kBox, ta, A_MN ? ar + 64 * i : kb * BK,
+                                              A_MN ? kb * BK + p.ak_row0 : ar + 64 * i, pa, full);
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_3d<CTAS>(b + i * kBox, tb, B_MN ? br + 64 * i : kb * BK,
+                                              B_MN ? kb * BK + p.bk_row0 : br + 64 * i, pb, full);
                     }
                 }
             }
@@ -388,7 +458,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == 1) {
         if (lane == 0 && rank == 0) {
-            const uint32_t idesc = umma_idesc_bf16(BM * CTAS, BN) | (A_MN ? 1u << 15 : 0u) |
+            const uint32_t idesc = umma_idesc_bf16(BM * CTAS, p.bn) | (A_MN ? 1u << 15 : 0u) |
                                    (B_MN ? 1u << 16 : 0u);
             int it = 0, i = 0;
             bool ok = true;
@@ -431,6 +501,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const int chunks = min(4, max(0, p.bn / 32 - 4 * half));  // of 32 columns
+        const Turn turn = {sb + S::out + (warp - 2) * 4096, lane};
         const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + 128 * half;
         int i = 0;  // accumulators taken
         auto full = [&]() {
@@ -452,7 +524,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = w0; w < work && ok; w += wstep) {
             const Tile t = tile_at<CTAS>(p, w);
             Row<EPI> r;
-            r.begin(p, t, (t.m * CTAS + rank) * BM + 32 * quarter + lane, half);
+            r.begin(p, t, (t.m * CTAS + rank) * BM + 32 * quarter, lane, half);
             __syncwarp();
             if constexpr (FINE) {
                 float acc[4][32];
@@ -466,6 +538,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
 #pragma unroll
                     for (int ch = 0; ch < 4; ++ch) {
+                        if (ch >= chunks) break;
                         float v[32];
                         tmem_ld32(src + BN * (i & 1) + 32 * ch, v);
 #pragma unroll
@@ -476,18 +549,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (!ok) break;
 #pragma unroll
-                for (int ch = 0; ch < 4; ++ch) r.take(p, t, ch, acc[ch]);
+                for (int q = 0; q < 2; ++q)
+                    if (2 * q < chunks) r.pair(p, t, turn, q, acc[2 * q], acc[2 * q + 1]);
             } else {
                 ok = full();
                 if (!ok) break;
                 const uint32_t at = src + BN * (i & 1);
+                if (chunks == 0) release();
 #pragma unroll 1
-                for (int ch = 0; ch < 4; ++ch) {
-                    float v[32];
+                for (int ch = 0; ch < chunks; ch += 2) {
+                    float v[64];
                     __syncwarp();
-                    tmem_ld32(at + 32 * ch, v);
-                    if (ch == 3) release();
-                    r.take(p, t, ch, v);
+                    tmem_ld64(at + 32 * ch, v);
+                    if (ch == chunks - 2) release();
+                    r.pair(p, t, turn, ch / 2, *(float (*)[32])v, *(float (*)[32])(v + 32));
                 }
             }
             r.end(p, t, half);
@@ -504,19 +579,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the row statistics: 32 rows per block, 32 slices of the partial sums, each
-// slice and then the slices in order.  Writes lse and the loss (0 where the target
-// is ignored), and the mean over the others: per block (sum, count), added up in
-// block order by the block that finishes last.
-__global__ void __launch_bounds__(1024)
+// Joins the row statistics: 8 rows per block and 128 slices of the partial sums, each
+// slice in order, then the slices pairwise.  Writes lse and the loss (0 where the
+// target is ignored), and the mean over the others: per block (sum, count), added up
+// in block order by the block that finishes last.
+constexpr int kJoinRows = 8, kJoinSlices = 128;
+__global__ void __launch_bounds__(kJoinRows * kJoinSlices)
     ce_join_kernel(const float2 *part, int parts, int M, Targets y, const float *z_y, float *loss,
                    float *lse, float *mean, float2 *sums, unsigned *ticket) {
-    __shared__ float2 sh[32][33];
+    __shared__ float2 sh[kJoinSlices][kJoinRows + 1];
     __shared__ bool last;
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
-    const long long row = (long long)blockIdx.x * 32 + lane;
+    const int r = threadIdx.x % kJoinRows, sl = threadIdx.x / kJoinRows, lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * kJoinRows + r;
     auto join = [](float2 a, float2 b) {
         const float m = fmaxf(a.x, b.x);
         if (m == -INFINITY) return make_float2(m, a.y + b.y);
@@ -524,90 +600,96 @@ __global__ void __launch_bounds__(1024)
     };
     float2 v = make_float2(-INFINITY, 0.f);
     if (row < M) {
-#pragma unroll 4
-        for (int q = sl; q < parts; q += 32) v = join(v, part[(size_t)q * M + row]);
+#pragma unroll 8
+        for (int q = sl; q < parts; q += kJoinSlices) v = join(v, part[(size_t)q * M + row]);
     }
-    sh[sl][lane] = v;
+    sh[sl][r] = v;
     __syncthreads();
-    if (sl != 0) {
-        if (!mean) return;
-    } else {
+    for (int o = kJoinSlices / 2; o > 0; o >>= 1) {
+        if (sl < o) sh[sl][r] = join(sh[sl][r], sh[sl + o][r]);
+        __syncthreads();
+    }
+    if (threadIdx.x < 32) {
         float l = 0.f, n = 0.f;
-        if (row < M) {
-            for (int i = 1; i < 32; ++i) v = join(v, sh[i][lane]);
+        if (sl == 0 && row < M) {
+            v = sh[0][r];
             const float e = v.x + kLn2 * log2f(v.y);
-            const int t = y.at(row, false);
-            if (t >= 0) {
+            if (y.at(row, false) >= 0) {
                 l = e - z_y[row];
                 n = 1.f;
             }
             lse[row] = e;
             loss[row] = l;
         }
-        if (!mean) return;
+        if (mean) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            l += __shfl_xor_sync(0xffffffffu, l, o);
-            n += __shfl_xor_sync(0xffffffffu, n, o);
-        }
-        if (lane == 0) {
-            sums[blockIdx.x] = make_float2(l, n);
-            __threadfence();
-            last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+            for (int o = kJoinRows / 2; o > 0; o >>= 1) {
+                l += __shfl_xor_sync(0xffffffffu, l, o);
+                n += __shfl_xor_sync(0xffffffffu, n, o);
+            }
+            if (lane == 0) {
+                sums[blockIdx.x] = make_float2(l, n);
+                __threadfence();
+                last = atomicAdd(ticket, 1u) == gridDim.x - 1;
+            }
         }
     }
+    if (!mean) return;
     __syncthreads();
     if (!last) return;
     __threadfence();
     float2 s = make_float2(0.f, 0.f);
-    for (int b = threadIdx.x; b < (int)gridDim.x; b += 1024) {
+    for (int b = threadIdx.x; b < (int)gridDim.x; b += kJoinRows * kJoinSlices) {
         const float2 u = __ldcg(&sums[b]);
         s.x += u.x;
         s.y += u.y;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s.x += __shfl_xor_sync(0xffffffffu, s.x, o);
-        s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
-    }
+    float2 *flat = &sh[0][0];  // kJoinSlices (kJoinRows + 1) entries
     __syncthreads();
-    if (lane == 0) sh[0][sl] = s;
+    flat[threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        s = make_float2(0.f, 0.f);
-        for (int i = 0; i < 32; ++i) {
-            s.x += sh[0][i].x;
-            s.y += sh[0][i].y;
+    for (int o = kJoinRows * kJoinSlices / 2; o > 0; o >>= 1) {
+        if (threadIdx.x < o) {
+            flat[threadIdx.x].x += flat[threadIdx.x + o].x;
+            flat[threadIdx.x].y += flat[threadIdx.x + o].y;
         }
-        *mean = s.y > 0.f ? s.x / s.y : 0.f;  // no target counts: 0
+        __syncthreads();
     }
+    if (threadIdx.x == 0) *mean = flat[0].y > 0.f ? flat[0].x / flat[0].y : 0.f;  // none counts: 0
 }
 
 // Rows of an operand as `planes` BF16 terms with a pitch of whole 16-byte pieces
 // (zeros past the width): fp32 operands, and BF16 ones whose rows a tensor map
 // cannot address.
+// x and W in one launch.
 template <typename T>
-__global__ void __launch_bounds__(256) pack_kernel(const T *src, __nv_bfloat16 *dst, long long rows,
-                                                   int D, int pitch, int planes) {
+__global__ void __launch_bounds__(256)
+    pack_kernel(const T *x, long long x_rows, __nv_bfloat16 *xp, const T *w, long long w_rows,
+                __nv_bfloat16 *wp, int D, int pitch, int planes) {
     griddep_wait();
     griddep_launch_dependents();
     const int pieces = pitch / 8;
-    const long long total = rows * pieces;
+    const long long total = (x_rows + w_rows) * pieces;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-        const long long r = i / pieces;
+        long long r = i / pieces;
         const int c = (int)(i - r * pieces) * 8;
+        const bool second = r >= x_rows;
+        if (second) r -= x_rows;
+        const T *src = second ? w : x;
+        __nv_bfloat16 *dst = second ? wp : xp;
+        const long long rows = second ? w_rows : x_rows;
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = c + j < D ? act_ld(src, (size_t)(r * D + c + j)) : 0.f;
         for (int pl = 0; pl < planes; ++pl) {
-            uint32_t w[4];
+            uint32_t u[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                w[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
-                v[2 * k] -= __uint_as_float(w[k] << 16);
-                v[2 * k + 1] -= __uint_as_float(w[k] & 0xffff0000u);
+                u[k] = pack_bf16x2(v[2 * k], v[2 * k + 1]);
+                v[2 * k] -= __uint_as_float(u[k] << 16);
+                v[2 * k + 1] -= __uint_as_float(u[k] & 0xffff0000u);
             }
-            *(uint4 *)(dst + ((size_t)pl * rows + r) * pitch + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *(uint4 *)(dst + ((size_t)pl * rows + r) * pitch + c) = make_uint4(u[0], u[1], u[2], u[3]);
         }
     }
 }
@@ -678,7 +760,7 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
     if (!backward) {
         l.part = round256((size_t)2 * cdiv(V, BN) * T * sizeof(float2));
         l.zy = round256(T * 4);
-        l.sums = round256(((T + 31) / 32) * sizeof(float2)) + 256;
+        l.sums = round256((T / kJoinRows + 1) * sizeof(float2)) + 256;
     } else {
         l.piece = piece_cols(d, l.planes);
         l.pieces = cdiv(V, l.piece);
@@ -711,13 +793,14 @@ kda_status_t check(const kda_ce_desc_t *d) {
     return KDA_OK;
 }
 
-bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, long long pitch, int planes,
-            int box_rows) {
+// An operand [planes][rows][pitch] in boxes of 64 x 64 elements, for either of its
+// indexes as the contraction's.
+bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, int planes) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
-    const cuuint64_t strides[2] = {(cuuint64_t)pitch * 2, (cuuint64_t)(rows * pitch) * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
+    const cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)(rows * inner) * 2};
+    const cuuint32_t box[3] = {64, 64, 1}, estr[3] = {1, 1, 1};
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -732,6 +815,7 @@ cudaError_t start_gemm(GemmArgs p, const CUtensorMap &ta, const CUtensorMap &tb,
     if (e != cudaSuccess) return e;
     p.m_tiles = cdiv(p.M, BM * CTAS);
     p.n_tiles = cdiv(p.N, BN);
+    p.bn = cdiv(cdiv(p.N, p.n_tiles), 64) * 64;  // tiles of about equal width
     const long long work = (long long)p.m_tiles * p.n_tiles * p.splits;
     const int groups = (int)(work < n / CTAS ? work : n / CTAS);
     cudaLaunchConfig_t cfg = {};
@@ -775,15 +859,18 @@ cudaError_t run_gemm(const GemmArgs &p, bool fine, const CUtensorMap &ta, const 
                 : run_gemm<EPI, A_MN, B_MN, false>(p, ta, tb, st);
 }
 
-cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *src, __nv_bfloat16 *dst,
-                     long long rows, cudaStream_t st) {
-    const long long need = (rows * (l.pitch / 8) + 255) / 256, most = 16ll * sms();
+cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *x, const void *w,
+                     uint8_t *ws, cudaStream_t st) {
+    __nv_bfloat16 *xp = (__nv_bfloat16 *)ws, *wp = (__nv_bfloat16 *)(ws + l.xp);
+    const long long T = d->tokens, V = d->vocab;
+    const long long need = ((T + V) * (l.pitch / 8) + 255) / 256, most = 16ll * sms();
     const dim3 grid((unsigned)(need < most ? need : most));
     if (d->act_dtype == KDA_DTYPE_F32)
-        return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)src, dst,
-                                rows, d->width, l.pitch, l.planes);
+        return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)x, T, xp,
+                                (const float *)w, V, wp, d->width, l.pitch, l.planes);
     return launch_dependent(pack_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
-                            (const __nv_bfloat16 *)src, dst, rows, d->width, l.pitch, l.planes);
+                            (const __nv_bfloat16 *)x, T, xp, (const __nv_bfloat16 *)w, V, wp,
+                            d->width, l.pitch, l.planes);
 }
 
 bool bad_ids(const kda_ce_desc_t *d, const void *ids) {
@@ -832,16 +919,14 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     float2 *sums = (float2 *)(ws + l.xp + l.wp + l.part + l.zy);
     unsigned *ticket = (unsigned *)(ws + l.total - 256);
     if (l.pack) {
-        if (run_pack(desc, l, x, (__nv_bfloat16 *)ws, desc->tokens, st) != cudaSuccess ||
-            run_pack(desc, l, weight, (__nv_bfloat16 *)(ws + l.xp), desc->vocab, st) != cudaSuccess)
-            return KDA_ERR_CUDA;
+        if (run_pack(desc, l, x, weight, ws, st) != cudaSuccess) return KDA_ERR_CUDA;
         xp = (const __nv_bfloat16 *)ws;
         wp = (const __nv_bfloat16 *)(ws + l.xp);
     }
     const int inner = l.pack ? l.pitch : desc->width;
     CUtensorMap ta, tb;
-    if (!encode(&ta, xp, inner, desc->tokens, inner, l.planes, 128) ||
-        !encode(&tb, wp, inner, desc->vocab, inner, l.planes, 128))
+    if (!encode(&ta, xp, inner, desc->tokens, l.planes) ||
+        !encode(&tb, wp, inner, desc->vocab, l.planes))
         return KDA_ERR_CUDA;
     GemmArgs p = {};
     p.M = desc->tokens;
@@ -856,7 +941,7 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     p.ticket = ticket;
     p.status = dev_status;
     if (run_gemm<EPI_STATS, false, false, true>(p, ta, tb, st) != cudaSuccess) return KDA_ERR_CUDA;
-    if (launch_dependent(ce_join_kernel, dim3(cdiv(p.M, 32)), dim3(1024), 0, st,
+    if (launch_dependent(ce_join_kernel, dim3(cdiv(p.M, kJoinRows)), dim3(kJoinRows * kJoinSlices), 0, st,
                          (const float2 *)part, 2 * cdiv(p.N, BN), p.M, p.y, (const float *)zy, loss, lse,
                          mean, sums, ticket) != cudaSuccess)
         return KDA_ERR_CUDA;
@@ -892,24 +977,16 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
     __nv_bfloat16 *dz = (__nv_bfloat16 *)(ws + l.xp + l.wp);
     float *acc = (float *)(ws + l.xp + l.wp + l.dz);
     if (l.pack) {
-        if (run_pack(desc, l, x, (__nv_bfloat16 *)ws, desc->tokens, st) != cudaSuccess ||
-            run_pack(desc, l, weight, (__nv_bfloat16 *)(ws + l.xp), desc->vocab, st) != cudaSuccess)
-            return KDA_ERR_CUDA;
+        if (run_pack(desc, l, x, weight, ws, st) != cudaSuccess) return KDA_ERR_CUDA;
         xp = (const __nv_bfloat16 *)ws;
         wp = (const __nv_bfloat16 *)(ws + l.xp);
     }
     const int T = desc->tokens, V = desc->vocab, D = desc->width;
     const bool fine = l.planes > 1;
     const int inner = l.pack ? l.pitch : D;
-    // x and W as operands of the logits (contraction over D, K-major) and of the
-    // gradients (contraction over tokens or vocabulary, MN-major); dz both ways
-    CUtensorMap x_k, w_k, w_mn, x_mn, dz_k, dz_mn;
-    if (!encode(&x_k, xp, inner, T, inner, l.planes, 128) ||
-        !encode(&w_k, wp, inner, V, inner, l.planes, 128) ||
-        !encode(&w_mn, wp, inner, V, inner, l.planes, BK) ||
-        !encode(&x_mn, xp, inner, T, inner, l.planes, BK) ||
-        !encode(&dz_k, dz, l.piece, T, l.piece, l.planes, 128) ||
-        !encode(&dz_mn, dz, l.piece, T, l.piece, l.planes, BK))
+    CUtensorMap tx, tw, tz;
+    if (!encode(&tx, xp, inner, T, l.planes) || !encode(&tw, wp, inner, V, l.planes) ||
+        !encode(&tz, dz, l.piece, T, l.planes))
         return KDA_ERR_CUDA;
     for (int k = 0; k < l.pieces; ++k) {
         const int v0 = k * l.piece, cols = V - v0 < l.piece ? V - v0 : l.piece;
@@ -928,7 +1005,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.dz = dz;
         p.pitch = l.piece;
         p.planes = l.planes;
-        if (run_gemm<EPI_DZ, false, false>(p, fine, x_k, w_k, st) != cudaSuccess) return KDA_ERR_CUDA;
+        if (run_gemm<EPI_DZ, false, false>(p, fine, tx, tw, st) != cudaSuccess) return KDA_ERR_CUDA;
         if (dx) {
             GemmArgs q = {};
             q.status = dev_status;
@@ -945,7 +1022,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)dx & 15u) == 0;
             if (q.splits > q.k_blocks) return KDA_ERR_CUDA;
-            if (run_gemm<EPI_OUT, false, true>(q, fine, dz_k, w_mn, st) != cudaSuccess)
+            if (run_gemm<EPI_OUT, false, true>(q, fine, tz, tw, st) != cudaSuccess)
                 return KDA_ERR_CUDA;
             if (l.dx_splits > 1) {
                 const long long n = (long long)T * D, need = (n + 255) / 256, most = 16ll * sms();
@@ -971,7 +1048,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.out = (uint8_t *)d_weight + (size_t)v0 * D * size;
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)d_weight & 15u) == 0;
-            if (run_gemm<EPI_OUT, true, true>(q, fine, dz_mn, x_mn, st) != cudaSuccess)
+            if (run_gemm<EPI_OUT, true, true>(q, fine, tz, tx, st) != cudaSuccess)
                 return KDA_ERR_CUDA;
         }
     }

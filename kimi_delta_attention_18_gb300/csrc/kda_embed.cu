@@ -75,8 +75,10 @@ __global__ void __launch_bounds__(256)
 }
 
 // --------------------------------------------------------------------- sort
-constexpr int kTile = 2048, kSortThreads = 256, kItems = kTile / kSortThreads;
+constexpr int kTile = 4096, kSortThreads = 1024, kItems = kTile / kSortThreads;
+constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kMaxBits = 10, kMaxDigits = 1 << kMaxBits;
+static_assert(kMaxDigits <= kSortThreads, "a thread per digit");
 
 struct SortArgs {
     const void *ids;
@@ -112,40 +114,36 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const __grid_co
 // Moves a tile's tokens to their places: all smaller digits, then the same digit
 // in earlier tiles, then in earlier warps of this tile, then earlier in the warp
 // (a warp holds consecutive tokens, 32 at a time).  A single tile needs no counts
-// of others, so up to kTile tokens take one launch per pass.
+// of others, so up to kTile tokens take one launch per pass.  The pass is all
+// latency; large tiles keep the loop over the tiles' counts short.
 __global__ void __launch_bounds__(kSortThreads)
     sort_scatter_kernel(const __grid_constant__ SortArgs a) {
-    constexpr int W = kSortThreads / 32, kPer = kMaxDigits / kSortThreads;
-    __shared__ int first[kMaxDigits];             // place of this tile's first token per digit
-    __shared__ int total[kMaxDigits];             // tokens per digit, in all tiles
-    __shared__ unsigned short cnt[W][kMaxDigits];  // tokens per warp and digit, then before it
-    __shared__ int warp_sum[W];
+    extern __shared__ unsigned short cnt[];  // [warps][digits]: tokens, then those before
+    __shared__ int first[kMaxDigits];        // place of this tile's first token per digit
+    __shared__ int warp_sum[kSortWarps];
     const int digits = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int d = threadIdx.x; d < W * kMaxDigits / 2; d += kSortThreads) ((unsigned *)cnt)[d] = 0;
+    unsigned short *mine = cnt + warp * digits;
+    for (int d = lane; d < digits; d += 32) mine[d] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    __syncthreads();
-    const int base = blockIdx.x * kTile + warp * (kTile / W);
-    int key[kItems], rank[kItems];
+    __syncwarp();
+    const int base = blockIdx.x * kTile + warp * (kTile / kSortWarps);
+    int key[kItems], pos[kItems], rank[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const int i = base + k * 32 + lane;
         key[k] = i < a.tokens ? sort_key(a, i, a.tiles == 1) : -1;
+        pos[k] = a.in_key && i < a.tokens ? a.in_pos[i] : i;
     }
-    // per digit: tokens in all tiles, and in the tiles before this one
-    int before[kPer], all[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) before[k] = all[k] = 0;
-    if (a.tiles > 1) {
-#pragma unroll 8
+    // thread d: tokens of digit d in all tiles, and in the tiles before this one
+    const int dig = threadIdx.x;
+    int before = 0, all = 0;
+    if (a.tiles > 1 && dig < digits) {
+#pragma unroll 10
         for (int t = 0; t < a.tiles; ++t) {
-#pragma unroll
-            for (int k = 0; k < kPer; ++k) {
-                const int d = threadIdx.x + k * kSortThreads;
-                const int n = d < digits ? a.hist[(size_t)t * digits + d] : 0;
-                all[k] += n;
-                before[k] += t < (int)blockIdx.x ? n : 0;
-            }
+            const int n = a.hist[(size_t)t * digits + dig];
+            all += n;
+            before += t < (int)blockIdx.x ? n : 0;
         }
     }
 #pragma unroll
@@ -154,33 +152,24 @@ __global__ void __launch_bounds__(kSortThreads)
         const int d = in ? (key[k] >> a.shift) & (digits - 1) : -1;
         const unsigned same = __match_any_sync(0xffffffffu, d);
         const int ahead = __popc(same & ((1u << lane) - 1u));
-        rank[k] = in ? cnt[warp][d] + ahead : 0;
+        rank[k] = in ? mine[d] + ahead : 0;
         __syncwarp();
-        if (in && ahead == 0) cnt[warp][d] += (unsigned short)__popc(same);
+        if (in && ahead == 0) mine[d] += (unsigned short)__popc(same);
         __syncwarp();
     }
     __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        const int d = threadIdx.x + k * kSortThreads;
+    if (dig < digits) {
         int s = 0;
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const int n = cnt[w][d];
-            cnt[w][d] = (unsigned short)s;
+#pragma unroll 8
+        for (int w = 0; w < kSortWarps; ++w) {
+            const int n = cnt[w * digits + dig];
+            cnt[w * digits + dig] = (unsigned short)s;
             s += n;
         }
-        total[d] = a.tiles == 1 ? s : all[k];
+        if (a.tiles == 1) all = s;
     }
-    __syncthreads();
-    // exclusive sums over the digits: kPer consecutive ones per thread
-    int v[kPer], mine = 0;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-        v[k] = mine;
-        mine += total[threadIdx.x * kPer + k];
-    }
-    int inc = mine;
+    // exclusive sums over the digits
+    int inc = all;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(0xffffffffu, inc, o);
@@ -188,22 +177,19 @@ __global__ void __launch_bounds__(kSortThreads)
     }
     if (lane == 31) warp_sum[warp] = inc;
     __syncthreads();
-    int ahead = inc - mine;
-    for (int w = 0; w < warp; ++w) ahead += warp_sum[w];
+    int ahead = warp_sum[lane < warp ? lane : 0];  // the warps' totals before this one
+    if (lane >= warp) ahead = 0;
 #pragma unroll
-    for (int k = 0; k < kPer; ++k) first[threadIdx.x * kPer + k] = ahead + v[k];
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) first[threadIdx.x + k * kSortThreads] += before[k];
+    for (int o = 16; o > 0; o >>= 1) ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+    first[dig] = ahead + inc - all + before;
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-        const int i = base + k * 32 + lane;
         if (key[k] < 0) continue;
         const int d = (key[k] >> a.shift) & (digits - 1);
-        const int to = first[d] + cnt[warp][d] + rank[k];
+        const int to = first[d] + mine[d] + rank[k];
         a.out_key[to] = key[k];
-        a.out_pos[to] = a.in_key ? a.in_pos[i] : i;
+        a.out_pos[to] = pos[k];
     }
 }
 
@@ -219,15 +205,19 @@ struct SumArgs {
 };
 
 // Tokens among the first d entries of the merged list (token j comes before the
-// end of row i when key[j] <= i).
-__device__ __forceinline__ int merged_tokens(const SumArgs &a, long long d) {
-    long long lo = d > a.rows ? d - a.rows : 0, hi = d < a.tokens ? d : a.tokens;
-    while (lo < hi) {
-        const long long mid = (lo + hi) >> 1;
-        if (a.key[mid] <= d - 1 - mid) lo = mid + 1;
-        else hi = mid;
+// end of row i when key[j] <= i).  One warp, which probes 32 places at a time.
+__device__ __forceinline__ int merged_tokens(const SumArgs &a, long long d, int lane) {
+    int lo = (int)(d > a.rows ? d - a.rows : 0), hi = (int)(d < a.tokens ? d : a.tokens);
+    while (lo < hi) {  // the same in all lanes
+        const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+        const bool before = at < hi && a.key[at] <= d - 1 - at;
+        const int n = __popc(__ballot_sync(0xffffffffu, before));  // the first n probes hold
+        if (n == 0) break;
+        const int next = lo + n * step;
+        lo += (n - 1) * step + 1;
+        if (next < hi) hi = next;
     }
-    return (int)lo;
+    return lo;
 }
 
 constexpr int kSumThreads = 128, kAhead = 4;
@@ -241,7 +231,10 @@ __global__ void __launch_bounds__(kSumThreads)
     griddep_launch_dependents();
     const long long total = (long long)a.rows + a.tokens;
     const long long d0 = blockIdx.x * a.per, d1 = d0 + a.per < total ? d0 + a.per : total;
-    if (threadIdx.x < 2) cut[threadIdx.x] = merged_tokens(a, threadIdx.x ? d1 : d0);
+    if (threadIdx.x < 64) {
+        const int n = merged_tokens(a, threadIdx.x < 32 ? d0 : d1, threadIdx.x & 31);
+        if ((threadIdx.x & 31) == 0) cut[threadIdx.x >> 5] = n;
+    }
     __syncthreads();
     if (threadIdx.x == 0 && blockIdx.y == 0) a.cut[blockIdx.x] = cut[0];
     const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
@@ -309,14 +302,18 @@ __global__ void __launch_bounds__(kSumThreads)
     const int i1 = blockIdx.x + 1 < (unsigned)a.parts
                        ? (int)(d0 + a.per - a.cut[blockIdx.x + 1]) : a.rows;
     if (j0 == 0 || i >= i1 || a.key[j0 - 1] != i) return;
-    if (threadIdx.x == 0) {
-        int lo = 0, hi = j0 - 1;  // the row's first token
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (a.key[mid] < i) lo = mid + 1;
-            else hi = mid;
+    if (threadIdx.x < 32) {  // back to the part in which the row begins, 32 at a time
+        int q = blockIdx.x - 1;
+        while (true) {
+            const int at = q - (int)threadIdx.x, n = at >= 0 ? a.cut[at] : 0;
+            const unsigned in = __ballot_sync(0xffffffffu, n > 0 && a.key[n > 0 ? n - 1 : 0] == i);
+            if (in != 0xffffffffu) {  // part `at` continues the row for the lowest lanes
+                q -= __ffs(~in) - 1;
+                break;
+            }
+            q -= 32;
         }
-        from = (int)(((long long)lo + i) / a.per);
+        if (threadIdx.x == 0) from = q;
     }
     __syncthreads();
     const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
@@ -474,6 +471,10 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
         a.bits = p.bits;
         a.tiles = p.tiles;
         a.status = dev_status;
+        const size_t scatter_smem = ((size_t)2 * kSortWarps) << p.bits;
+        if (set_max_dynamic_smem((const void *)sort_scatter_kernel, (2 * kSortWarps) << kMaxBits) !=
+            cudaSuccess)
+            return KDA_ERR_CUDA;
         for (int k = 0; k < p.passes; ++k) {
             a.shift = k * p.bits;
             a.in_key = k ? keys[last] : nullptr;
@@ -483,8 +484,8 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
             a.out_pos = poss[last];
             if ((p.tiles > 1 && launch_dependent(sort_hist_kernel, dim3(p.tiles), dim3(kSortThreads),
                                                  0, st, a) != cudaSuccess) ||
-                launch_dependent(sort_scatter_kernel, dim3(p.tiles), dim3(kSortThreads), 0, st, a) !=
-                    cudaSuccess)
+                launch_dependent(sort_scatter_kernel, dim3(p.tiles), dim3(kSortThreads), scatter_smem,
+                                 st, a) != cudaSuccess)
                 return KDA_ERR_CUDA;
         }
     }
