@@ -3,6 +3,7 @@
 #include <stdint.h>
 #include <string.h>
 
+#include <atomic>
 #include <mutex>
 #include <vector>
 
@@ -165,6 +166,16 @@ size_t ckpt_scratch_bytes(const kda_prefill_desc_t *d, int Sg, int interval) {
 }
 
 }  // namespace
+
+int kda::device_sms() {
+    constexpr int kMax = 64;
+    static std::atomic<int> known[kMax];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMax) return sm_count();
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n == 0) known[dev].store(n = sm_count(), std::memory_order_relaxed);
+    return n;
+}
 
 cudaError_t kda::set_max_dynamic_smem(const void *kernel, int bytes) {
     struct Entry {

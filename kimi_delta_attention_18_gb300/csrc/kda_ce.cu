@@ -712,13 +712,6 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float *acc, T *out
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
-int sms() {
-    int dev = 0, n = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-    return n;
-}
-
 // Width of dz's buffer: at most 512 MiB of BF16 (or three fp32 terms) in whole
 // column tiles, unless the caller says.
 int piece_cols(const kda_ce_desc_t *d, int planes) {
@@ -767,7 +760,7 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
         l.dz = round256(T * l.piece * l.planes * 2);
         // dx has few tiles when T and D are small: its contraction over the
         // vocabulary is then split so that every SM has a share
-        const int tiles = cdiv(T, BM) * cdiv(d->width, BN), n = sms();
+        const int tiles = cdiv(T, BM) * cdiv(d->width, BN), n = device_sms();
         l.dx_splits = 1;
         if (l.pieces == 1 && tiles > 0 && tiles < n) {
             l.dx_splits = n / tiles;
@@ -846,7 +839,7 @@ bool use_pairs(const GemmArgs &p, int n) {
 template <int EPI, bool A_MN, bool B_MN, bool FINE>
 cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap &tb,
                      cudaStream_t st) {
-    const int n = sms();
+    const int n = device_sms();
     return use_pairs(p, n) ? start_gemm<EPI, A_MN, B_MN, FINE, 2>(p, ta, tb, n, st)
                            : start_gemm<EPI, A_MN, B_MN, FINE, 1>(p, ta, tb, n, st);
 }
@@ -863,7 +856,7 @@ cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *x, con
                      uint8_t *ws, cudaStream_t st) {
     __nv_bfloat16 *xp = (__nv_bfloat16 *)ws, *wp = (__nv_bfloat16 *)(ws + l.xp);
     const long long T = d->tokens, V = d->vocab;
-    const long long need = ((T + V) * (l.pitch / 8) + 255) / 256, most = 16ll * sms();
+    const long long need = ((T + V) * (l.pitch / 8) + 255) / 256, most = 16ll * device_sms();
     const dim3 grid((unsigned)(need < most ? need : most));
     if (d->act_dtype == KDA_DTYPE_F32)
         return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)x, T, xp,
@@ -1025,7 +1018,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             if (run_gemm<EPI_OUT, false, true>(q, fine, tz, tw, st) != cudaSuccess)
                 return KDA_ERR_CUDA;
             if (l.dx_splits > 1) {
-                const long long n = (long long)T * D, need = (n + 255) / 256, most = 16ll * sms();
+                const long long n = (long long)T * D, need = (n + 255) / 256, most = 16ll * device_sms();
                 const dim3 grid((unsigned)(need < most ? need : most));
                 const cudaError_t e =
                     size == 2 ? launch_dependent(split_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0,

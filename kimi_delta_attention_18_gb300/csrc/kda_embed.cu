@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kSumThreads)
     float acc[VEC];
 #pragma unroll
     for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int q = from; q < (int)blockIdx.x; ++q)
 #pragma unroll
         for (int k = 0; k < VEC; ++k) acc[k] += a.carry[(size_t)q * a.D + c + k];
@@ -376,10 +376,7 @@ cudaError_t run_embed(const void *table, const void *ids, int wide, void *out, i
     const int pieces = (D + VEC - 1) / VEC;
     int tpr = 8;
     while (tpr < 256 && tpr * 4 < pieces) tpr *= 2;
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    const long long need = ((long long)tokens * tpr + 255) / 256, most = 8ll * sms;
+    const long long need = ((long long)tokens * tpr + 255) / 256, most = 8ll * device_sms();
     const unsigned gx = (unsigned)(need < most ? need : most);
     unsigned gy = (pieces + 4 * tpr - 1) / (4 * tpr);  // few tokens: a wide row over blocks
     if (gy > 64) gy = 64;

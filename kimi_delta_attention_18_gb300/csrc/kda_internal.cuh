@@ -161,6 +161,9 @@ cudaError_t launch_dependent(void (*kernel)(KArgs...), dim3 grid, dim3 block, si
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
 }
 
+// SMs of the current device (asked for once per device).  Thread-safe.
+int device_sms();
+
 // Raise a kernel's dynamic shared-memory limit to `bytes` on the current device
 // once: the attribute stays set in the context, so later launches skip the
 // runtime call.  Thread-safe.

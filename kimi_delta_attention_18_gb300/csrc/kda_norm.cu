@@ -229,14 +229,11 @@ Shape norm_shape(int D, int size, int move, long long rows, bool bwd) {
     s.tpr = tpr;
     s.threads = tpr > 32 ? tpr : 256;
     s.groups = s.threads / tpr;
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     // A forward pass has a block for each of its row groups; a backward pass as many as
     // are resident, each with the same number of rows, for their dw.
     long long blocks = (rows + s.groups - 1) / s.groups;
     if (bwd) {
-        const long long most = (long long)sms * (2048 / s.threads);
+        const long long most = (long long)device_sms() * (2048 / s.threads);
         const long long rounds = (blocks + most - 1) / most;
         if (rounds > 1) blocks = (blocks + rounds - 1) / rounds;
     }
@@ -360,14 +357,11 @@ NormArgs make_args(const kda_norm_desc_t *d) {
 // rows could take.
 size_t norm_ws(const kda_norm_desc_t *d) {
     const NormArgs a = make_args(d);
-    int most = 0;
-    for (int move : {BY_ELEMENT, PIECES, SHIFTED})
-        for (int op : {(int)OP_SIGMOID, (int)OP_RESIDUAL}) {
-            const int n = norm_blocks(a, op, true, size_of(d), move);
-            most = n > most ? n : most;
-        }
-    const int n = norm_shape(d->width, size_of(d), PIECES, a.rows, true).blocks;
-    most = n > most ? n : most;
+    int most = device_sms();  // the ring's
+    for (int move : {BY_ELEMENT, PIECES, SHIFTED}) {
+        const int n = norm_shape(d->width, size_of(d), move, a.rows, true).blocks;
+        most = n > most ? n : most;
+    }
     return ((size_t)most * d->width * sizeof(float) + 255) & ~(size_t)255;
 }
 

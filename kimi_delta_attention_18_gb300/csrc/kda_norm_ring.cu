@@ -269,9 +269,7 @@ cudaError_t launch_b(const NormArgs &a, const Ring &r, int op, int size, int blo
 
 int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size) {
     const Ring r = ring_for(a, op, bwd, size);
-    int dev = 0, sms = 152;
-    if (cudaGetDevice(&dev) == cudaSuccess)
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    const int sms = device_sms();
     // fewer than a few tiles per SM: the ring would not fill, and its start costs more
     return r.arrays && r.stages >= 2 && r.tiles >= 4ll * sms ? sms : 0;
 }

@@ -389,3 +389,107 @@ def test_cross_entropy_matches_differences():
                 moved[k].view(-1)[i] += s
                 vals.append(f(*moved))
             assert abs(float(got[k].view(-1)[i]) - (vals[0] - vals[1]) / 2e-5) < 2e-4
+
+
+# --------------------------------------------------------------- refusals, autograd
+
+def test_binding_refuses_what_the_kernels_do_not_take():
+    x = torch.zeros((4, 2, 8), device="cuda")
+    w, h = torch.ones(8, device="cuda"), torch.zeros((4, 8), device="cuda")
+    for bad in (lambda: kda.gated_norm(x, x.bfloat16(), w),
+                lambda: kda.gated_norm(x, x[:3], w),
+                lambda: kda.gated_norm(x, x, w.double()),
+                lambda: kda.gated_norm(x, x, w, act="tanh"),
+                lambda: kda.gated_norm(x, None, w),
+                lambda: kda.gated_norm(x, x, w, act="none"),
+                lambda: kda.gated_norm(x.half(), x.half(), w),
+                lambda: kda.gated_norm(x.transpose(0, 1), x.transpose(0, 1), w),
+                lambda: kda.gated_norm(x[:, :, ::2], x[:, :, ::2], w[:4]),
+                lambda: kda.gated_norm(x, x, w, out=x[:2]),
+                lambda: kda.residual_norm(h.T, None),
+                lambda: kda.residual_norm(h, h.bfloat16()),
+                lambda: kda.residual_norm(h, None, h_out=h),
+                lambda: kda.embedding(h, torch.zeros(2, device="cuda")),
+                lambda: kda.embedding(h, torch.zeros((2, 2), device="cuda", dtype=torch.int32)),
+                lambda: kda.embedding_backward(h, torch.zeros(3, device="cuda", dtype=torch.int32), 5),
+                lambda: kda.linear_cross_entropy(h, w[None, :4], torch.zeros(4, device="cuda").long()),
+                lambda: kda.linear_cross_entropy(h, h, torch.zeros(3, device="cuda").long()),
+                lambda: kda.linear_cross_entropy(h, h.bfloat16(), torch.zeros(4, device="cuda").long())):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        kda.gated_norm(x, [1.0], w)
+    with pytest.raises(kda.KDAError):
+        kda.gated_norm(x, x, w, eps=0.0)
+    with pytest.raises(kda.KDAError):  # x is not on a 16-byte boundary
+        kda.linear_cross_entropy(torch.zeros(33, device="cuda")[1:].view(4, 8), h,
+                                 torch.zeros(4, device="cuda").long())
+
+
+def test_autograd_matches_torch():
+    """The differentiable forms in one small network against torch's own autograd in 64
+    bits (fp32 activations)."""
+    from kimi_delta_attention_18_gb300 import autograd as ag
+    g = _gen(8)
+    table, head = _randn((11, 12), g, torch.float32), _randn((11, 12), g, torch.float32)
+    z, w1, w2 = _randn((7, 12), g, torch.float32), _randn((4,), g, torch.float32), _randn((12,), g, torch.float32)
+    ids = torch.randint(0, 11, (7,), generator=g, device="cuda")
+    y = torch.randint(0, 11, (7,), generator=g, device="cuda")
+    y[2] = -100
+    for reduction in ("mean", "sum", "none"):
+        mine = [t.clone().requires_grad_() for t in (table, z, w1, w2, head)]
+        e = ag.kda_embedding(mine[0], ids, scale=2.0)
+        h, n = ag.kda_residual_norm(e, None, mine[3])
+        u = ag.kda_gated_norm(n.view(7, 3, 4), mine[1].view(7, 3, 4), mine[2], act="silu")
+        h, n = ag.kda_residual_norm(h, u.view(7, 12), mine[3], scale=0.5)
+        loss = ag.kda_linear_cross_entropy(n + h, mine[4], y, reduction=reduction)
+        (loss * 3.0).sum().backward()
+        ref = [t.double().requires_grad_() for t in (table, z, w1, w2, head)]
+
+        def norm(v):
+            return v * (v.pow(2).mean(-1, keepdim=True) + 1e-6).rsqrt()
+
+        h = 2.0 * ref[0][ids]
+        n = norm(h) * ref[3]
+        u = norm(n.view(7, 3, 4)) * ref[2] * torch.nn.functional.silu(ref[1].view(7, 3, 4))
+        h = h + 0.5 * u.view(7, 12)
+        want = torch.nn.functional.cross_entropy((norm(h) * ref[3] + h) @ ref[4].T, y,
+                                                 reduction=reduction)
+        (want * 3.0).sum().backward()
+        assert torch.allclose(loss.double(), want, rtol=1e-5, atol=1e-5)
+        for a, b in zip(mine, ref):
+            assert a.grad.dtype == torch.float32
+            assert torch.allclose(a.grad.double(), b.grad, rtol=1e-4, atol=1e-4)
+
+
+def test_example_trains():
+    """The operators together, as they are used: the loss of the example's model falls
+    from that of a uniform guess (log 199 = 5.3)."""
+    from examples.train_lm import train
+    losses = train(steps=40, log=lambda s: None)
+    assert 4.5 < losses[0] < 6.5 and losses[-1] < 0.5 * losses[0]
+
+
+def test_calls_are_captured_in_a_graph():
+    """Nothing is allocated or synchronised behind a capture's back."""
+    g = _gen(9)
+    x, w = _randn((64, 256), g, torch.bfloat16), _randn((500, 256), g, torch.bfloat16, 0.1)
+    y = torch.randint(0, 500, (64,), generator=g, device="cuda")
+    d = torch.rand(64, generator=g, device="cuda")
+
+    def run():
+        h, n = kda.residual_norm(x, x, None, scale=0.5)
+        loss, lse, mean = kda.linear_cross_entropy(n, w, y)
+        dx, dw = kda.linear_cross_entropy_backward(n, w, y, lse, d)
+        return [mean, dw, kda.residual_norm_backward(dx, h, None)[0],
+                kda.embedding_backward(dx, y, 500)]
+
+    want = run()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
