@@ -10,27 +10,17 @@
 // two products that read it.  The logits cost 2 T V D operations once more; keeping
 // them would cost T V words.
 //
-// All four products run in one persistent kernel on tcgen05 (gemm_kernel).  fp32
-// operands are split into three BF16 terms (8 + 8 + 8 bits of the fp32 mantissa's
-// 24) and the six products of terms whose weight is 2^-16 or more are accumulated,
-// smallest first, so an fp32 problem is the same kernel with six times the steps.
+// All four products run in persistent kernels on tcgen05.  fp32 operands are split
+// into three BF16 terms (8 + 8 + 8 bits of the fp32 mantissa's 24) and the six
+// products of terms whose weight is 2^-16 or more are accumulated, smallest first.
+// They are stored as such terms first; only W, where there are few tokens, is split on
+// its way through shared memory instead (kda_ce_w32.cu).
 #include <math.h>
 
-#include "kda_internal.cuh"
-#include "kda_sm100.cuh"
+#include "kda_ce_gemm.cuh"
 
 namespace kda {
 namespace {
-
-using namespace sm100;
-
-constexpr int BM = 128, BN = 256, BK = 64;  // rows per CTA, columns, contraction per stage
-constexpr int kABytes = BM * BK * 2, kBBytes = BN * BK * 2, kBox = 64 * BK * 2;
-constexpr int kEpiWarps = 8, kThreads = 32 * (2 + kEpiWarps);
-constexpr int kGroupRows = 2048;  // rows whose tiles share a sweep over the column tiles
-constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr uint32_t kTmemCols = 512;  // two 256-column accumulators
 
 // Shared memory of a CTA alone (CTAS = 1) or of each CTA of a pair: a pair's CTAs
 // hold half of B's rows each.
@@ -43,305 +33,6 @@ struct Smem {
     static constexpr int bytes = misc + 16 + 1024;
     static_assert(bytes <= 227 * 1024, "shared memory budget");
 };
-
-enum { EPI_STATS = 0, EPI_DZ = 1, EPI_OUT = 2 };
-
-struct Targets {
-    const void *ids;
-    int wide, vocab;
-    long long ignore;
-    int32_t *status;
-    // The target of row t; -1 where it is to be ignored (or, recorded, outside
-    // the vocabulary).
-    __device__ __forceinline__ int at(long long t, bool report) const {
-        const long long y = wide ? ((const long long *)ids)[t] : ((const int *)ids)[t];
-        if (y == ignore) return -1;
-        if (y < 0 || y >= vocab) {
-            if (report) dev_fail(status, KDA_ERR_INVALID_ARG);
-            return -1;
-        }
-        return (int)y;
-    }
-};
-
-struct GemmArgs {
-    int M, N;                  // rows and columns of the product that exist
-    int k_blocks, splits, pairs;
-    int chunk;                 // FINE: stages per accumulator
-    int m_tiles, n_tiles, bn;  // set at the launch; bn: columns per tile, a multiple of 64
-    int a_row0, b_row0;        // added to the operands' non-contraction coordinate
-    int ak_row0, bk_row0;      // added to the contraction coordinate of MN-major operands
-    // EPI_STATS, EPI_DZ
-    Targets y;
-    float2 *part;              // [2 n_tiles][M] (maximum, sum)
-    float *z_y;                // [M]
-    unsigned *ticket;          // cleared for the join kernel
-    const float *lse, *d_loss;
-    __nv_bfloat16 *dz;         // [planes][M][pitch]
-    int pitch, planes;
-    // EPI_OUT: value (+ acc_in) to acc_out [splits][M][N] fp32, or to out
-    const float *acc_in;
-    float *acc_out;
-    void *out;
-    int out_bf16, vec;
-    int32_t *status;
-};
-
-// MN-major operand with 128-byte swizzle, as boxes of 64 elements x BK rows lay it
-// down: 8 rows (along K) of 128 bytes form an atom, atoms follow each other along
-// K (1024 bytes), boxes along M / N (8192 bytes).
-__device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((BK * 128) >> 4) << 16;  // between 64-element boxes
-    d |= (uint64_t)(1024 >> 4) << 32;        // between 8-row atoms along K
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
-}
-
-struct Tile {
-    int m, n, split, kb0, kb1;
-};
-template <int CTAS>
-__device__ __forceinline__ Tile tile_at(const GemmArgs &p, int w) {
-    constexpr int G = kGroupRows / (BM * CTAS);
-    Tile t;
-    const int per = p.m_tiles * p.n_tiles;
-    t.split = w / per;
-    const int r = w - t.split * per, g = r / (G * p.n_tiles), q = r - g * G * p.n_tiles;
-    const int gm = min(G, p.m_tiles - g * G);
-    t.n = q / gm;
-    t.m = g * G + (q - t.n * gm);
-    t.kb0 = (int)((long long)p.k_blocks * t.split / p.splits);
-    t.kb1 = (int)((long long)p.k_blocks * (t.split + 1) / p.splits);
-    return t;
-}
-
-// Terms of pair i of an fp32 product, smallest weight first: (1,1) (2,0) (0,2)
-// (1,0) (0,1) (0,0); a single pair is (0,0).
-__device__ __forceinline__ int term_a(int i, int pairs) {
-    return pairs == 1 ? 0 : (0x001021 >> (4 * (i))) & 3;
-}
-__device__ __forceinline__ int term_b(int i, int pairs) {
-    return pairs == 1 ? 0 : (0x010201 >> (4 * (i))) & 3;
-}
-
-// A warp's 32 rows x 128 bytes on their way to memory: a thread has a row, but a store
-// should have whole lines (with a row per thread each store instruction touched 32 of
-// them, and storing three terms of dz took as long as half of the tile's products).
-struct Turn {
-    uint32_t at;
-    int lane;
-    // 16-byte piece q of this thread's row
-    __device__ __forceinline__ void put(int q, uint4 v) const {
-        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(
-                         at + lane * 128 + ((q ^ (lane & 7)) << 4)),
-                     "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                     : "memory");
-    }
-    __device__ __forceinline__ int row(int it) const { return 4 * it + (lane >> 3); }
-    // piece lane % 8 of row(it), it = 0 .. 7
-    __device__ __forceinline__ uint4 get(int it) const {
-        uint4 v;
-        const int r = row(it);
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                     : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                     : "r"(at + r * 128 + (((lane & 7) ^ (r & 7)) << 4))
-                     : "memory");
-        return v;
-    }
-    // word `lane` of row r
-    __device__ __forceinline__ float word(int r) const {
-        float v;
-        asm volatile("ld.shared.f32 %0, [%1];"
-                     : "=f"(v)
-                     : "r"(at + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + 4 * (lane & 3))
-                     : "memory");
-        return v;
-    }
-};
-
-// One thread's part of the epilogue: a row and up to 128 of the tile's columns, taken
-// 32 at a time.
-template <int EPI>
-struct Row {
-    int row0;       // the warp's first row
-    long long row;  // this thread's
-    bool live;
-    int c0;  // first column, in the launch's columns
-    int y;   // the target's column (negative: none)
-    float mx, sum, lse2, g;
-
-    __device__ __forceinline__ void begin(const GemmArgs &p, const Tile &t, int first_row, int lane,
-                                          int half) {
-        row0 = first_row;
-        row = first_row + lane;
-        live = row < p.M;
-        c0 = t.n * p.bn + half * 128;
-        y = -1;
-        mx = -INFINITY;
-        sum = lse2 = g = 0.f;
-        if (EPI != EPI_OUT && live) {
-            y = p.y.at(row, t.n == 0 && half == 0);
-            if (EPI == EPI_DZ) {
-                lse2 = p.lse[row] * kLog2e;
-                g = y >= 0 ? p.d_loss[row] : 0.f;
-            }
-            y = y >= 0 ? y - p.b_row0 : -1;
-        }
-    }
-
-    // 32 values as BF16 into half `h` of the warp's lines; what the rounding left stays
-    // in v if LEFT.
-    template <bool LEFT>
-    __device__ __forceinline__ void put_bf16(const Turn &turn, int h, float (&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                w[k] = pack_bf16x2(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-                if (LEFT) {
-                    v[8 * i + 2 * k] -= __uint_as_float(w[k] << 16);
-                    v[8 * i + 2 * k + 1] -= __uint_as_float(w[k] & 0xffff0000u);
-                }
-            }
-            turn.put(4 * h + i, make_uint4(w[0], w[1], w[2], w[3]));
-        }
-    }
-    // The lines to memory: row r's at base + r pitch.
-    __device__ __forceinline__ void lines(const GemmArgs &p, const Turn &turn, __nv_bfloat16 *base,
-                                          size_t pitch) {
-        __syncwarp();
-#pragma unroll
-        for (int it = 0; it < 8; ++it) {
-            const long long r = row0 + turn.row(it);
-            const uint4 u = turn.get(it);
-            if (r < p.M) *(uint4 *)(base + (size_t)r * pitch + 8 * (turn.lane & 7)) = u;
-        }
-        __syncwarp();
-    }
-
-    // v -> d_loss (softmax - onehot) for columns c .. c + 31
-    __device__ __forceinline__ void dz_of(const GemmArgs &p, int c, float (&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-            const float e = g * exp2f(fmaf(v[i], kLog2e, -lse2));
-            v[i] = g != 0.f && c + i < p.N ? e : 0.f;
-        }
-        if (__any_sync(0xffffffffu, y >= c && y < c + 32)) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] -= c + i == y ? g : 0.f;
-        }
-    }
-
-    __device__ __forceinline__ void stats(const GemmArgs &p, int c, float (&v)[32]) {
-        if (c + 32 > p.N) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = c + i < p.N ? v[i] : -INFINITY;
-        }
-        const bool mine = y >= c && y < c + 32;
-        if (__any_sync(0xffffffffu, mine)) {
-            float z = 0.f;
-#pragma unroll
-            for (int i = 0; i < 32; ++i) z = c + i == y ? v[i] : z;
-            if (mine) p.z_y[row] = z;
-        }
-        float m = mx;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) m = fmaxf(m, v[i]);
-        const float ref = m == -INFINITY ? 0.f : m * kLog2e;
-        sum *= exp2f(mx == -INFINITY ? -INFINITY : fmaf(mx, kLog2e, -ref));
-        float s[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < 32; ++i) s[i & 3] += exp2f(fmaf(v[i], kLog2e, -ref));
-        sum += (s[0] + s[1]) + (s[2] + s[3]);
-        mx = m;
-    }
-
-    // 32 columns of fp32 (+ acc_in) to acc_out or out
-    __device__ __forceinline__ void out32(const GemmArgs &p, const Tile &t, const Turn &turn, int c,
-                                          float (&v)[32]) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            turn.put(i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
-                                   __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
-        __syncwarp();
-        const bool narrow = p.out && p.out_bf16;
-        float *o32 = p.out ? (float *)p.out : p.acc_out + (size_t)t.split * p.M * p.N;
-        __nv_bfloat16 *o16 = (__nv_bfloat16 *)p.out;
-        if (p.vec) {  // widths and bases of whole pieces: four columns are in or out together
-            const int col = c + 4 * (turn.lane & 7);
-#pragma unroll
-            for (int it = 0; it < 8; ++it) {
-                const long long r = row0 + turn.row(it);
-                const uint4 u = turn.get(it);
-                if (r >= p.M || col >= p.N) continue;
-                const size_t at = (size_t)r * p.N + col;
-                float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
-                                       __uint_as_float(u.z), __uint_as_float(u.w));
-                if (p.acc_in) {
-                    const float4 a = *(const float4 *)(p.acc_in + at);
-                    f = make_float4(f.x + a.x, f.y + a.y, f.z + a.z, f.w + a.w);
-                }
-                if (narrow)
-                    *(uint2 *)(o16 + at) = make_uint2(pack_bf16x2(f.x, f.y), pack_bf16x2(f.z, f.w));
-                else
-                    *(float4 *)(o32 + at) = f;
-            }
-        } else {
-            const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32);
-#pragma unroll 4
-            for (int r = 0; r < rows; ++r) {
-                float f = turn.word(r);
-                if (c + turn.lane >= p.N) continue;
-                const size_t at = (size_t)(row0 + r) * p.N + c + turn.lane;
-                if (p.acc_in) f += p.acc_in[at];
-                if (narrow) o16[at] = __float2bfloat16_rn(f);
-                else o32[at] = f;
-            }
-        }
-        __syncwarp();
-    }
-
-    // Columns c0 + 64 q .. + 63 as two halves a, b.
-    __device__ __forceinline__ void pair(const GemmArgs &p, const Tile &t, const Turn &turn, int q,
-                                         float (&a)[32], float (&b)[32]) {
-        const int c = c0 + 64 * q;
-        if (EPI == EPI_STATS) {
-            stats(p, c, a);
-            stats(p, c + 32, b);
-        } else if (EPI == EPI_DZ) {
-            dz_of(p, c, a);
-            dz_of(p, c + 32, b);
-            for (int pl = 0; pl < p.planes; ++pl) {
-                put_bf16<true>(turn, 0, a);
-                put_bf16<true>(turn, 1, b);
-                lines(p, turn, p.dz + (size_t)pl * p.M * p.pitch + c, p.pitch);
-            }
-        } else if (p.out && p.out_bf16 && !p.acc_in && p.vec && c + 64 <= p.N) {
-            put_bf16<false>(turn, 0, a);
-            put_bf16<false>(turn, 1, b);
-            lines(p, turn, (__nv_bfloat16 *)p.out + c, p.N);
-        } else {
-            if (c < p.N) out32(p, t, turn, c, a);
-            if (c + 32 < p.N) out32(p, t, turn, c + 32, b);
-        }
-    }
-
-    __device__ __forceinline__ void end(const GemmArgs &p, const Tile &t, int half) {
-        if (EPI == EPI_STATS && live)
-            p.part[(size_t)(2 * t.n + half) * p.M + row] = make_float2(mx, sum);
-    }
-};
-
-__device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
-    asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
-        "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
-        : "+f"(x), "+f"(y)
-        : "f"(ax), "f"(ay));
-}
 
 // C = A B^T over tiles of 128 CTAS x 256 and steps of 64 along the contraction,
 // one persistent CTA per SM, alone or in pairs (CTAS = 2):
@@ -363,9 +54,7 @@ __device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
 // accumulator is then handed over every `chunk` stages and added up, rounded to
 // nearest, in the epilogue's registers, while the other accumulator fills.  16
 // stages for BF16 operands (lse within 3e-7, no slower than one accumulator for
-// all: 1.93 ms at 2,048 x 131,072 x 7,168), 8 for fp32 ones (gradients within
-// 6e-7); 4 would cost a third more time, the hand-over then being longer than the
-// products it overlaps.
+// all: 1.93 ms at 2,048 x 131,072 x 7,168), 8 for fp32 ones (gradients within 6e-7).
 constexpr int kChunkBf16 = 16, kChunkF32 = 8;
 
 template <int EPI, bool A_MN, bool B_MN, bool FINE, int CTAS>
@@ -413,7 +102,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
             const uint64_t ta = reinterpret_cast<uint64_t>(&tm_a);
             const uint64_t tb = reinterpret_cast<uint64_t>(&tm_b);
-            const int boxes = (p.bn / CTAS + 63) / 64;  // of B
+            // boxes of 64 x 64 of B; K-major ones come in twos
+            const int boxes = B_MN ? (p.bn / CTAS + 63) / 64 : 2 * ((p.bn / CTAS + 127) / 128);
             int it = 0;
             bool ok = true;
             for (int w = w0; w < work && ok; w += wstep) {
@@ -432,13 +122,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                                      // both CTAs' bytes
                         if (rank == 0)
                             mbar_arrive_expect_tx(full_bar(s), CTAS * (kABytes + boxes * kBox));
-                        // boxes of 64 x 64: 64 rows of the contraction's 64, or the other
-                        // way round
+                        // K-major: boxes of 128 rows x 64 of the contraction; MN-major: of
+                        // 64 rows of the contraction x 64
+                        if (A_MN) {
 #pragma unroll
-                        for (int i = 0; i < BM / 64; ++i)
-                            tma_load_3d<CTAS>(a + i * kBox, ta, A_MN ? ar + 64 * i : kb * BK,
-                                              A_MN ? kb * BK + p.ak_row0 : ar + 64 * i, pa, full);
-                        for (int i = 0; i < boxes; ++i)
+                            for (int i = 0; i < BM / 64; ++i)
+                                tma_load_3d<CTAS>(a + i * kBox, ta, ar + 64 * i,
+                                                  kb * BK + p.ak_row0, pa, full);
+                        } else {
+                            tma_load_3d<CTAS>(a, ta, kb * BK, ar, pa, full);
+                        }
+                        for (int i = 0; i < boxes; i += B_MN ? 1 : 2)
                             tma_load_3d<CTAS>(b + i * kBox, tb, B_MN ? br + 64 * i : kb * BK,
                                               B_MN ? kb * BK + p.bk_row0 : br + 64 * i, pb, full);
                     }
@@ -484,9 +178,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
                         umma_bf16_group<CTAS>(tmem + BN * (i & 1),
-                                              A_MN ? umma_desc_mn_sw128(a + kk * 2048)
+                                              A_MN ? umma_desc_mn_sw128(a + kk * 2048, BK)
                                                    : umma_desc_sw128(a + kk * 32, 1024),
-                                              B_MN ? umma_desc_mn_sw128(b + kk * 2048)
+                                              B_MN ? umma_desc_mn_sw128(b + kk * 2048, BK)
                                                    : umma_desc_sw128(b + kk * 32, 1024),
                                               idesc, first + kk > 0);
                     umma_commit_group<CTAS>(empty_bar(s));
@@ -516,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 if (CTAS == 1) mbar_arrive(acce_bar(i));
-                else mbar_arrive_cluster(cluster_map(acce_bar(i), 0));
+                else mbar_arrive_tmem(cluster_map(acce_bar(i), 0));
             }
             ++i;
         };
@@ -524,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int w = w0; w < work && ok; w += wstep) {
             const Tile t = tile_at<CTAS>(p, w);
             Row<EPI> r;
-            r.begin(p, t, (t.m * CTAS + rank) * BM + 32 * quarter, lane, half);
+            r.begin(p, t, (t.m * CTAS + rank) * BM + 32 * quarter, lane, half, 128);
             __syncwarp();
             if constexpr (FINE) {
                 float acc[4][32];
@@ -658,10 +352,9 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
     if (threadIdx.x == 0) *mean = flat[0].y > 0.f ? flat[0].x / flat[0].y : 0.f;  // none counts: 0
 }
 
-// Rows of an operand as `planes` BF16 terms with a pitch of whole 16-byte pieces
-// (zeros past the width): fp32 operands, and BF16 ones whose rows a tensor map
-// cannot address.
-// x and W in one launch.
+// Rows of x and, if w_rows, of W as `planes` BF16 terms with a pitch of whole 128-byte
+// lines (zeros past the width): fp32 operands, and BF16 rows whose width is no multiple
+// of the 16 bytes that a tensor map needs.
 template <typename T>
 __global__ void __launch_bounds__(256)
     pack_kernel(const T *x, long long x_rows, __nv_bfloat16 *xp, const T *w, long long w_rows,
@@ -710,8 +403,6 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float *acc, T *out
 
 // ------------------------------------------------------------------ host side
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
-
 // Width of dz's buffer: at most 512 MiB of BF16 (or three fp32 terms) in whole
 // column tiles, unless the caller says.
 int piece_cols(const kda_ce_desc_t *d, int planes) {
@@ -730,28 +421,34 @@ int piece_cols(const kda_ce_desc_t *d, int planes) {
 }
 
 struct Layout {
-    int planes, pairs, chunk, pitch, piece, pieces, dx_splits;
-    bool pack;
+    bool f32, w32, pack_x, pack_w;
+    int planes, pairs, chunk, x_pitch, w_pitch, piece, pieces, dx_splits;
     size_t xp, wp, part, zy, sums, dz, acc, total;
 };
 
-// Pieces of the workspace.  pack: operands are copied (fp32 terms, or BF16 rows
-// whose width is no multiple of the 16 bytes that a tensor map needs).
+// Pieces of the workspace.
 Layout layout_for(const kda_ce_desc_t *d, bool backward) {
     Layout l = {};
-    const bool pack = d->act_dtype == KDA_DTYPE_F32 || d->width % 8 != 0;
     const size_t T = d->tokens, V = d->vocab;
-    l.planes = d->act_dtype == KDA_DTYPE_F32 ? 3 : 1;
-    l.pairs = l.planes == 3 ? 6 : 1;
-    l.chunk = l.planes == 3 ? kChunkF32 : kChunkBf16;
-    // whole 128-byte lines: with rows of 1,040 bytes the copies of 128-byte boxes ran at
-    // half the rate
-    l.pitch = (d->width + 63) / 64 * 64;
-    l.pack = pack;
-    l.xp = pack ? round256(T * l.pitch * l.planes * 2) : 0;
-    l.wp = pack ? round256(V * l.pitch * l.planes * 2) : 0;
+    const int D = d->width;
+    l.f32 = d->act_dtype == KDA_DTYPE_F32;
+    // fp32: a weight that is read for one row of tiles only is split on its way; one that
+    // is read more often is copied in terms (at 2,000 x 20,000 x 1,024 334 us, against
+    // 423), and so is one whose rows a tensor map cannot address
+    l.w32 = l.f32 && d->tokens <= BM && d->width % 4 == 0;
+    l.planes = l.f32 ? 3 : 1;
+    l.pairs = l.f32 ? 6 : 1;
+    l.chunk = l.f32 ? kChunkF32 : kChunkBf16;
+    // Copies: whole 128-byte lines where x and W are copied as BF16 (with rows of 1,040
+    // bytes the copies of 128-byte boxes ran at half the rate)
+    l.pack_x = l.f32 || D % 8 != 0;
+    l.pack_w = l.f32 ? !l.w32 : D % 8 != 0;
+    l.x_pitch = l.pack_x ? (D + 63) / 64 * 64 : D;
+    l.w_pitch = l.pack_w ? l.x_pitch : D;
+    l.xp = l.pack_x ? round256(T * l.x_pitch * l.planes * 2) : 0;
+    l.wp = l.pack_w ? round256(V * l.w_pitch * l.planes * 2) : 0;
     if (!backward) {
-        l.part = round256((size_t)2 * cdiv(V, BN) * T * sizeof(float2));
+        l.part = round256((size_t)2 * cdiv(V, l.w32 ? kW32Cols : BN) * T * sizeof(float2));
         l.zy = round256(T * 4);
         l.sums = round256((T / kJoinRows + 1) * sizeof(float2)) + 256;
     } else {
@@ -760,15 +457,14 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
         l.dz = round256(T * l.piece * l.planes * 2);
         // dx has few tiles when T and D are small: its contraction over the
         // vocabulary is then split so that every SM has a share
-        const int tiles = cdiv(T, BM) * cdiv(d->width, BN), n = device_sms();
+        const int tiles = cdiv(T, BM) * cdiv(D, l.w32 ? kW32Cols : BN), n = device_sms();
         l.dx_splits = 1;
         if (l.pieces == 1 && tiles > 0 && tiles < n) {
             l.dx_splits = n / tiles;
             const int most = l.piece / BK / 4;  // at least four steps each
             if (l.dx_splits > most) l.dx_splits = most < 1 ? 1 : most;
         }
-        if (l.pieces > 1 || l.dx_splits > 1)
-            l.acc = round256((size_t)l.dx_splits * T * d->width * 4);
+        if (l.pieces > 1 || l.dx_splits > 1) l.acc = round256((size_t)l.dx_splits * T * D * 4);
     }
     l.total = l.xp + l.wp + l.part + l.zy + l.sums + l.dz + l.acc;
     return l;
@@ -786,14 +482,17 @@ kda_status_t check(const kda_ce_desc_t *d) {
     return KDA_OK;
 }
 
-// An operand [planes][rows][pitch] in boxes of 64 x 64 elements, for either of its
-// indexes as the contraction's.
-bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, int planes) {
+constexpr int kMajor = 128, kMnMajor = BK;  // rows of a box
+
+// An operand [planes][rows][pitch] in boxes of 128 rows x 64 elements of the contraction
+// (K-major), or 64 rows of the contraction x 64 (MN-major).  Fewer and larger copies
+// are faster: with 64 rows for both the loss's gradient took 2 % longer.
+bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, int planes, int box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;
     const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)rows, (cuuint64_t)planes};
     const cuuint64_t strides[2] = {(cuuint64_t)inner * 2, (cuuint64_t)(rows * inner) * 2};
-    const cuuint32_t box[3] = {64, 64, 1}, estr[3] = {1, 1, 1};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_rows, 1}, estr[3] = {1, 1, 1};
     return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -843,27 +542,22 @@ cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap
     return use_pairs(p, n) ? start_gemm<EPI, A_MN, B_MN, FINE, 2>(p, ta, tb, n, st)
                            : start_gemm<EPI, A_MN, B_MN, FINE, 1>(p, ta, tb, n, st);
 }
-// The backward's products: in fp32 problems FINE, in BF16 ones (whose results are
-// rounded to 2^-8 of their value) not.
-template <int EPI, bool A_MN, bool B_MN>
-cudaError_t run_gemm(const GemmArgs &p, bool fine, const CUtensorMap &ta, const CUtensorMap &tb,
-                     cudaStream_t st) {
-    return fine ? run_gemm<EPI, A_MN, B_MN, true>(p, ta, tb, st)
-                : run_gemm<EPI, A_MN, B_MN, false>(p, ta, tb, st);
-}
-
+// Copies x and W where the layout wants them; xp, wp are what the products read.
 cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *x, const void *w,
-                     uint8_t *ws, cudaStream_t st) {
-    __nv_bfloat16 *xp = (__nv_bfloat16 *)ws, *wp = (__nv_bfloat16 *)(ws + l.xp);
-    const long long T = d->tokens, V = d->vocab;
-    const long long need = ((T + V) * (l.pitch / 8) + 255) / 256, most = 16ll * device_sms();
+                     uint8_t *ws, const void *&xp, const void *&wp, cudaStream_t st) {
+    xp = l.pack_x ? ws : x;
+    wp = l.pack_w ? ws + l.xp : w;
+    if (!l.pack_x) return cudaSuccess;
+    const long long T = d->tokens, V = l.pack_w ? d->vocab : 0, most = 16ll * device_sms();
+    const long long need = ((T + V) * (l.x_pitch / 8) + 255) / 256;
     const dim3 grid((unsigned)(need < most ? need : most));
-    if (d->act_dtype == KDA_DTYPE_F32)
-        return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)x, T, xp,
-                                (const float *)w, V, wp, d->width, l.pitch, l.planes);
+    __nv_bfloat16 *to = (__nv_bfloat16 *)ws, *to_w = (__nv_bfloat16 *)(ws + l.xp);
+    if (l.f32)
+        return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)x, T, to,
+                                (const float *)w, V, to_w, d->width, l.x_pitch, l.planes);
     return launch_dependent(pack_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
-                            (const __nv_bfloat16 *)x, T, xp, (const __nv_bfloat16 *)w, V, wp,
-                            d->width, l.pitch, l.planes);
+                            (const __nv_bfloat16 *)x, T, to, (const __nv_bfloat16 *)w, V, to_w,
+                            d->width, l.x_pitch, l.planes);
 }
 
 bool bad_ids(const kda_ce_desc_t *d, const void *ids) {
@@ -906,25 +600,15 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     if (!workspace || workspace_bytes < l.total || ((uintptr_t)workspace & 15u))
         return KDA_ERR_WORKSPACE;
     uint8_t *ws = (uint8_t *)workspace;
-    const __nv_bfloat16 *xp = (const __nv_bfloat16 *)x, *wp = (const __nv_bfloat16 *)weight;
     float2 *part = (float2 *)(ws + l.xp + l.wp);
     float *zy = (float *)(ws + l.xp + l.wp + l.part);
     float2 *sums = (float2 *)(ws + l.xp + l.wp + l.part + l.zy);
     unsigned *ticket = (unsigned *)(ws + l.total - 256);
-    if (l.pack) {
-        if (run_pack(desc, l, x, weight, ws, st) != cudaSuccess) return KDA_ERR_CUDA;
-        xp = (const __nv_bfloat16 *)ws;
-        wp = (const __nv_bfloat16 *)(ws + l.xp);
-    }
-    const int inner = l.pack ? l.pitch : desc->width;
-    CUtensorMap ta, tb;
-    if (!encode(&ta, xp, inner, desc->tokens, l.planes) ||
-        !encode(&tb, wp, inner, desc->vocab, l.planes))
-        return KDA_ERR_CUDA;
+    const void *xp, *wp;
+    if (run_pack(desc, l, x, weight, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
     GemmArgs p = {};
     p.M = desc->tokens;
     p.N = desc->vocab;
-    p.k_blocks = cdiv(desc->width, BK);
     p.splits = 1;
     p.pairs = l.pairs;
     p.chunk = l.chunk;
@@ -933,9 +617,22 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     p.z_y = zy;
     p.ticket = ticket;
     p.status = dev_status;
-    if (run_gemm<EPI_STATS, false, false, true>(p, ta, tb, st) != cudaSuccess) return KDA_ERR_CUDA;
+    cudaError_t e;
+    const int tile_cols = l.w32 ? kW32Cols : BN;
+    if (l.w32) {
+        p.k_blocks = cdiv(desc->width, kW32Step);
+        e = launch_w32(EPI_STATS, p, {xp, l.x_pitch, (const float *)wp, p.N, l.w_pitch}, st);
+    } else {
+        CUtensorMap ta, tb;
+        p.k_blocks = cdiv(desc->width, BK);
+        if (!encode(&ta, xp, l.x_pitch, p.M, l.planes, kMajor) ||
+            !encode(&tb, wp, l.w_pitch, p.N, l.planes, kMajor))
+            return KDA_ERR_CUDA;
+        e = run_gemm<EPI_STATS, false, false, true>(p, ta, tb, st);
+    }
+    if (e != cudaSuccess) return KDA_ERR_CUDA;
     if (launch_dependent(ce_join_kernel, dim3(cdiv(p.M, kJoinRows)), dim3(kJoinRows * kJoinSlices), 0, st,
-                         (const float2 *)part, 2 * cdiv(p.N, BN), p.M, p.y, (const float *)zy, loss, lse,
+                         (const float2 *)part, 2 * cdiv(p.N, tile_cols), p.M, p.y, (const float *)zy, loss, lse,
                          mean, sums, ticket) != cudaSuccess)
         return KDA_ERR_CUDA;
     return KDA_OK;
@@ -966,21 +663,24 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
     if (!workspace || workspace_bytes < l.total || ((uintptr_t)workspace & 15u))
         return KDA_ERR_WORKSPACE;
     uint8_t *ws = (uint8_t *)workspace;
-    const __nv_bfloat16 *xp = (const __nv_bfloat16 *)x, *wp = (const __nv_bfloat16 *)weight;
     __nv_bfloat16 *dz = (__nv_bfloat16 *)(ws + l.xp + l.wp);
     float *acc = (float *)(ws + l.xp + l.wp + l.dz);
-    if (l.pack) {
-        if (run_pack(desc, l, x, weight, ws, st) != cudaSuccess) return KDA_ERR_CUDA;
-        xp = (const __nv_bfloat16 *)ws;
-        wp = (const __nv_bfloat16 *)(ws + l.xp);
-    }
+    const void *xp, *wp;
+    if (run_pack(desc, l, x, weight, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
     const int T = desc->tokens, V = desc->vocab, D = desc->width;
-    const bool fine = l.planes > 1;
-    const int inner = l.pack ? l.pitch : D;
-    CUtensorMap tx, tw, tz;
-    if (!encode(&tx, xp, inner, T, l.planes) || !encode(&tw, wp, inner, V, l.planes) ||
-        !encode(&tz, dz, l.piece, T, l.planes))
+    const int step = l.w32 ? kW32Step : BK;
+    // as K-major and MN-major operands
+    CUtensorMap xk, xm, zk, zm, wk, wm;
+    if (!encode(&xm, xp, l.x_pitch, T, l.planes, kMnMajor) ||
+        !encode(&zm, dz, l.piece, T, l.planes, kMnMajor))
         return KDA_ERR_CUDA;
+    if (!l.w32 && (!encode(&xk, xp, l.x_pitch, T, l.planes, kMajor) ||
+                   !encode(&zk, dz, l.piece, T, l.planes, kMajor) ||
+                   !encode(&wk, wp, l.w_pitch, V, l.planes, kMajor) ||
+                   !encode(&wm, wp, l.w_pitch, V, l.planes, kMnMajor)))
+        return KDA_ERR_CUDA;
+    const W32Operands logits = {xp, l.x_pitch, (const float *)wp, V, l.w_pitch};
+    const W32Operands back = {dz, l.piece, (const float *)wp, V, l.w_pitch};
     for (int k = 0; k < l.pieces; ++k) {
         const int v0 = k * l.piece, cols = V - v0 < l.piece ? V - v0 : l.piece;
         GemmArgs p = {};
@@ -990,7 +690,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.splits = 1;
         p.M = T;
         p.N = cols;
-        p.k_blocks = cdiv(D, BK);
+        p.k_blocks = cdiv(D, step);
         p.b_row0 = v0;
         p.y = {targets, desc->id_dtype == KDA_ID_I64, V, desc->ignore_index, dev_status};
         p.lse = lse;
@@ -998,7 +698,10 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.dz = dz;
         p.pitch = l.piece;
         p.planes = l.planes;
-        if (run_gemm<EPI_DZ, false, false>(p, fine, tx, tw, st) != cudaSuccess) return KDA_ERR_CUDA;
+        if ((l.w32   ? launch_w32(EPI_DZ, p, logits, st)
+             : l.f32 ? run_gemm<EPI_DZ, false, false, true>(p, xk, wk, st)
+                     : run_gemm<EPI_DZ, false, false, false>(p, xk, wk, st)) != cudaSuccess)
+            return KDA_ERR_CUDA;
         if (dx) {
             GemmArgs q = {};
             q.status = dev_status;
@@ -1007,7 +710,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.splits = l.dx_splits;
             q.M = T;
             q.N = D;
-            q.k_blocks = cdiv(cols, BK);
+            q.k_blocks = cdiv(cols, step);
             q.bk_row0 = v0;
             q.acc_in = k > 0 ? acc : nullptr;
             if (l.dx_splits == 1 && k == l.pieces - 1) q.out = dx;
@@ -1015,7 +718,9 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)dx & 15u) == 0;
             if (q.splits > q.k_blocks) return KDA_ERR_CUDA;
-            if (run_gemm<EPI_OUT, false, true>(q, fine, tz, tw, st) != cudaSuccess)
+            if ((l.w32   ? launch_w32(EPI_OUT, q, back, st)
+                 : l.f32 ? run_gemm<EPI_OUT, false, true, true>(q, zk, wm, st)
+                         : run_gemm<EPI_OUT, false, true, false>(q, zk, wm, st)) != cudaSuccess)
                 return KDA_ERR_CUDA;
             if (l.dx_splits > 1) {
                 const long long n = (long long)T * D, need = (n + 255) / 256, most = 16ll * device_sms();
@@ -1041,7 +746,8 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.out = (uint8_t *)d_weight + (size_t)v0 * D * size;
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)d_weight & 15u) == 0;
-            if (run_gemm<EPI_OUT, true, true>(q, fine, tz, tx, st) != cudaSuccess)
+            if ((l.f32 ? run_gemm<EPI_OUT, true, true, true>(q, zm, xm, st)
+                       : run_gemm<EPI_OUT, true, true, false>(q, zm, xm, st)) != cudaSuccess)
                 return KDA_ERR_CUDA;
         }
     }

@@ -397,9 +397,11 @@ __device__ __forceinline__ uint32_t cluster_map(uint32_t addr, uint32_t rank) {
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
     return r;
 }
-// Arrive on a barrier of the cluster (address from cluster_map).
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+// Arrive on a barrier of the cluster (address from cluster_map), for a thread that hands
+// over nothing but tensor memory it has read (tc_fence_before orders those loads; a
+// release of its other memory operations to the cluster takes over a thousand cycles).
+__device__ __forceinline__ void mbar_arrive_tmem(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // As mbar_wait for a barrier that threads of the other CTA arrive on.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity, volatile int *abort,
