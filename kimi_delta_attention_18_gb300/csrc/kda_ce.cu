@@ -485,8 +485,7 @@ kda_status_t check(const kda_ce_desc_t *d) {
 constexpr int kMajor = 128, kMnMajor = BK;  // rows of a box
 
 // An operand [planes][rows][pitch] in boxes of 128 rows x 64 elements of the contraction
-// (K-major), or 64 rows of the contraction x 64 (MN-major).  Fewer and larger copies
-// are faster: with 64 rows for both the loss's gradient took 2 % longer.
+// (K-major), or 64 rows of the contraction x 64 (MN-major).
 bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, int planes, int box_rows) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (!enc) return false;

@@ -1,6 +1,7 @@
-// The norms of many contiguous rows of whole 16-byte pieces: rows stream through
-// shared memory (bulk copies, a ring of stages), so the bytes in flight do not
-// depend on the registers that the arithmetic takes.
+// The norms of many contiguous rows: rows stream through shared memory (bulk copies, a
+// ring of stages), so the bytes in flight do not depend on the registers that the
+// arithmetic takes, and rows of odd widths need no aligned access of their own: a tile
+// of eight (BF16) or four (fp32) of them, or a multiple, starts on a 16-byte boundary.
 #include "kda_norm_math.cuh"
 #include "kda_sm100.cuh"
 
@@ -22,15 +23,17 @@ struct Ring {
     long long tiles;
 };
 
-// A thread holds 16 elements (two BF16 pieces, four fp32); a tile is one row per group
-// of tpr threads: 16 KB per array where the width fills its threads.
-Ring ring_for(const NormArgs &a, int op, bool bwd, int size) {
+// A thread holds 16 elements: 16-byte pieces (two of BF16, four of fp32), or eight pairs
+// where rows are not whole pieces (`pairs`).  A tile is one row per group of tpr
+// threads: 16 KB per array where the width fills its threads.
+Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
     Ring r = {};
-    const int pieces = a.D / (16 / size), nv = size;
+    const int vec = pairs ? 2 : 16 / size, pieces = (a.D + vec - 1) / vec, nv = 16 / vec;
     r.tpr = 1;
     while (r.tpr * nv < pieces) r.tpr *= 2;
     if (pieces < nv || r.tpr > kWork) return r;  // arrays = 0: does not apply
     r.rows = kWork / r.tpr;
+    if (pairs && r.rows % (16 / size) != 0) return r;  // tiles would start anywhere
     r.tiles = (a.rows + r.rows - 1) / r.rows;
     r.arrays = 1 + (bwd ? 1 : 0);
     if (op == OP_SIGMOID || op == OP_SILU || (op == OP_RESIDUAL && (bwd ? a.d_res : a.gate))) ++r.arrays;
@@ -44,10 +47,11 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size) {
 // SKEW, for rows of more than a warp: a row's outputs come after the next row's sums,
 // so no warp waits at a barrier for its row's other warps.  The pieces are then read
 // from shared memory twice and the stage is released after the outputs.
-template <int OP, bool BWD, typename T, bool SKEW>
+template <int OP, bool BWD, typename T, bool SKEW, bool PAIRS>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_ring_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ Ring r) {
-    constexpr int VEC = 16 / sizeof(T), NV = sizeof(T), VP = kPairs<VEC>, kRed = SKEW ? 4 : 2;
+    constexpr int VEC = PAIRS ? 2 : 16 / sizeof(T), NV = 16 / VEC, VP = kPairs<VEC>;
+    constexpr int kRed = SKEW ? 4 : 2;
     using P = Piece<T, VEC>;
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
@@ -88,10 +92,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const long long row = t * r.rows, left = p.rows - row;
                 const uint32_t bytes =
                     (uint32_t)((left < r.rows ? left : r.rows) * p.D * (long long)sizeof(T));
-                mbar_arrive_expect_tx(full(s), n * bytes);
-                for (int k = 0; k < n; ++k)
+                const uint32_t whole = bytes & ~15u;  // the last tile may end inside a piece
+                for (int k = 0; PAIRS && k < n && whole < bytes; ++k)
+                    for (uint32_t b = whole; b < bytes; b += sizeof(T))
+                        *(T *)(sm + s * r.stage_bytes + k * r.array_bytes + b) =
+                            *(const T *)(src[k] + row * p.D * (long long)sizeof(T) + b);
+                mbar_arrive_expect_tx(full(s), n * whole);
+                for (int k = 0; k < n && whole > 0; ++k)
                     bulk_g2s(sb + s * r.stage_bytes + k * r.array_bytes,
-                             src[k] + row * p.D * (long long)sizeof(T), bytes, full(s));
+                             src[k] + row * p.D * (long long)sizeof(T), whole, full(s));
             }
             if (*abort) {  // let the copies in flight land before the block exits
                 volatile int never = 0;
@@ -109,7 +118,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int j = 0; j < VP; ++j) {
             w[j] = both(1.f);
-            if (p.w && column(i) < p.D) w[j] = *(const f2 *)(p.w + column(i) + 2 * j);
+            const int c = column(i) + 2 * j;
+            if (p.w && c < p.D) {
+                if (PAIRS) w[j] = pk(p.w[c], c + 1 < p.D ? p.w[c + 1] : 1.f);
+                else w[j] = *(const f2 *)(p.w + c);
+            }
         }
     };
     RowMath<OP, BWD, T, VEC, NV, !SKEW> math;
@@ -133,9 +146,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             pg[k].zero();
             pd[k].zero();
             if (live && c < p.D) {
-                px[k].load((const T *)at + c);
-                if (OP != OP_NORM && has_g) pg[k].load((const T *)(at + second) + c);
-                if (BWD) pd[k].load((const T *)(at + third) + c);
+                auto get = [&](P &to, const uint8_t *from) {
+                    if constexpr (PAIRS) to.load((const T *)from + c, c + 1 < p.D);
+                    else to.load((const T *)from + c);
+                };
+                get(px[k], at);
+                if (OP != OP_NORM && has_g) get(pg[k], at + second);
+                if (BWD) get(pd[k], at + third);
             }
         }
     };
@@ -161,15 +178,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         math.outputs(p, px, pg, pd, load_w, ss, se, [&](int k, f2 (&a1)[VP], f2 (&a2)[VP]) {
             const int c = column(k);
             if (row >= p.rows || failed || c >= p.D) return;
-            float v[VEC];
-            if (p.o1) {
-                floats<VEC>(a1, v);
-                P::store((T *)p.o1 + row * p.D + c, v);
-            }
-            if ((BWD || OP == OP_RESIDUAL) && p.o2) {
-                floats<VEC>(a2, v);
-                P::store((T *)p.o2 + row * p.D + c, v);
-            }
+            auto put = [&](void *to, f2 (&o)[VP]) {
+                float v[VEC];
+                floats<VEC>(o, v);
+                if constexpr (PAIRS) P::store((T *)to + row * p.D + c, v, c + 1 < p.D);
+                else P::store((T *)to + row * p.D + c, v);
+            };
+            if (p.o1) put(p.o1, a1);
+            if ((BWD || OP == OP_RESIDUAL) && p.o2) put(p.o2, a2);
         });
     };
     int i = 0;
@@ -224,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         floats<VEC>(math.dw[k % (BWD ? NV : 1)], v);
 #pragma unroll
         for (int j = 0; j < VEC; ++j)
-            if (column(k) < p.D) sh[group * p.D + column(k) + j] = v[j];
+            if (column(k) + j < p.D) sh[group * p.D + column(k) + j] = v[j];
     }
     named_bar_sync(15, kWork);
     for (int c = threadIdx.x; c < p.D; c += kWork) {
@@ -234,51 +250,61 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int OP, bool BWD, typename T, bool SKEW>
+template <int OP, bool BWD, typename T, bool SKEW, bool PAIRS>
 cudaError_t launch_k(const NormArgs &a, const Ring &r, int blocks, cudaStream_t st) {
-    cudaError_t e =
-        set_max_dynamic_smem((const void *)norm_ring_kernel<OP, BWD, T, SKEW>, kRingBytes);
+    const auto kernel = norm_ring_kernel<OP, BWD, T, SKEW, PAIRS>;
+    cudaError_t e = set_max_dynamic_smem((const void *)kernel, kRingBytes);
     if (e != cudaSuccess) return e;
-    return launch_dependent(norm_ring_kernel<OP, BWD, T, SKEW>, dim3(blocks), dim3(kThreads),
-                            r.stages * r.stage_bytes, st, a, r);
+    return launch_dependent(kernel, dim3(blocks), dim3(kThreads), r.stages * r.stage_bytes, st, a, r);
+}
+
+template <int OP, bool BWD, typename T>
+cudaError_t launch_t(const NormArgs &a, const Ring &r, bool pairs, int blocks, cudaStream_t st) {
+    // two stages are in use at a time with SKEW
+    const bool skew = r.tpr > 32 && r.stages >= 4;
+    if (pairs)
+        return skew ? launch_k<OP, BWD, T, true, true>(a, r, blocks, st)
+                    : launch_k<OP, BWD, T, false, true>(a, r, blocks, st);
+    return skew ? launch_k<OP, BWD, T, true, false>(a, r, blocks, st)
+                : launch_k<OP, BWD, T, false, false>(a, r, blocks, st);
 }
 
 template <int OP, bool BWD>
-cudaError_t launch_op(const NormArgs &a, const Ring &r, int size, int blocks, cudaStream_t st) {
-    // two stages are in use at a time with SKEW
-    const bool skew = r.tpr > 32 && r.stages >= 4;
-    if (size == 4)
-        return skew ? launch_k<OP, BWD, float, true>(a, r, blocks, st)
-                    : launch_k<OP, BWD, float, false>(a, r, blocks, st);
-    return skew ? launch_k<OP, BWD, __nv_bfloat16, true>(a, r, blocks, st)
-                : launch_k<OP, BWD, __nv_bfloat16, false>(a, r, blocks, st);
+cudaError_t launch_op(const NormArgs &a, const Ring &r, int size, bool pairs, int blocks,
+                      cudaStream_t st) {
+    return size == 4 ? launch_t<OP, BWD, float>(a, r, pairs, blocks, st)
+                     : launch_t<OP, BWD, __nv_bfloat16>(a, r, pairs, blocks, st);
 }
 
 template <bool BWD>
-cudaError_t launch_b(const NormArgs &a, const Ring &r, int op, int size, int blocks,
+cudaError_t launch_b(const NormArgs &a, const Ring &r, int op, int size, bool pairs, int blocks,
                      cudaStream_t st) {
     switch (op) {
-        case OP_NORM: return launch_op<OP_NORM, BWD>(a, r, size, blocks, st);
-        case OP_SIGMOID: return launch_op<OP_SIGMOID, BWD>(a, r, size, blocks, st);
-        case OP_SILU: return launch_op<OP_SILU, BWD>(a, r, size, blocks, st);
+        case OP_NORM: return launch_op<OP_NORM, BWD>(a, r, size, pairs, blocks, st);
+        case OP_SIGMOID: return launch_op<OP_SIGMOID, BWD>(a, r, size, pairs, blocks, st);
+        case OP_SILU: return launch_op<OP_SILU, BWD>(a, r, size, pairs, blocks, st);
     }
-    return launch_op<OP_RESIDUAL, BWD>(a, r, size, blocks, st);
+    return launch_op<OP_RESIDUAL, BWD>(a, r, size, pairs, blocks, st);
 }
 
 }  // namespace
 
-int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size) {
-    const Ring r = ring_for(a, op, bwd, size);
+int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
+    const Ring r = ring_for(a, op, bwd, size, pairs);
     const int sms = device_sms();
     // fewer than a few tiles per SM: the ring would not fill, and its start costs more
+    // forward passes with more than a warp per row are faster as shifted pieces (fp32,
+    // 20,011 x 1,001: 51 us, and 57 this way; BF16, 72,896 x 281: 81, and 57 this way)
+    if (pairs && !bwd && r.tpr > 32) return 0;
     return r.arrays && r.stages >= 2 && r.tiles >= 4ll * sms ? sms : 0;
 }
 
-cudaError_t launch_norm_ring(const NormArgs &a, int op, bool bwd, int size, cudaStream_t st) {
-    const Ring r = ring_for(a, op, bwd, size);
-    const int blocks = norm_ring_blocks(a, op, bwd, size);
-    return bwd ? launch_b<true>(a, r, op, size, blocks, st)
-               : launch_b<false>(a, r, op, size, blocks, st);
+cudaError_t launch_norm_ring(const NormArgs &a, int op, bool bwd, int size, bool pairs,
+                             cudaStream_t st) {
+    const Ring r = ring_for(a, op, bwd, size, pairs);
+    const int blocks = norm_ring_blocks(a, op, bwd, size, pairs);
+    return bwd ? launch_b<true>(a, r, op, size, pairs, blocks, st)
+               : launch_b<false>(a, r, op, size, pairs, blocks, st);
 }
 
 }  // namespace kda

@@ -60,6 +60,25 @@ struct Piece<__nv_bfloat16, 8> {
     }
 };
 
+// Two elements of a row that starts anywhere; the second may be past its end.
+template <typename T>
+struct Piece<T, 2> {
+    T raw[2];
+    __device__ __forceinline__ void load(const T *p, bool second) {
+        raw[0] = p[0];
+        raw[1] = second ? p[1] : T(0.f);
+    }
+    __device__ __forceinline__ void zero() { raw[0] = raw[1] = T(0.f); }
+    __device__ __forceinline__ void get(float (&v)[2]) const {
+        v[0] = (float)raw[0];
+        v[1] = (float)raw[1];
+    }
+    static __device__ __forceinline__ void store(T *p, const float (&v)[2], bool second) {
+        act_st(p, 0, v[0]);
+        if (second) act_st(p, 1, v[1]);
+    }
+};
+
 template <typename T>
 struct Piece<T, 1> {
     T raw;
