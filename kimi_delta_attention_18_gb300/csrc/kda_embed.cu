@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256)
 
 // --------------------------------------------------------------------- sort
 constexpr int kTile = 4096, kSortThreads = 1024, kItems = kTile / kSortThreads;
-constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kSortWarps = kSortThreads / 32, kFewTiles = 4;
 constexpr int kMaxBits = 10, kMaxDigits = 1 << kMaxBits;
 static_assert(kMaxDigits <= kSortThreads, "a thread per digit");
 
@@ -113,32 +113,50 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const __grid_co
 
 // Moves a tile's tokens to their places: all smaller digits, then the same digit
 // in earlier tiles, then in earlier warps of this tile, then earlier in the warp
-// (a warp holds consecutive tokens, 32 at a time).  A single tile needs no counts
-// of others, so up to kTile tokens take one launch per pass.  The pass is all
-// latency; large tiles keep the loop over the tiles' counts short.
+// (a warp holds consecutive tokens, 32 at a time).  With up to kFewTiles tiles each block
+// counts the other tiles itself, so up to 16,384 tokens take one launch per pass.  The
+// pass is all latency; large tiles keep the loop over the tiles' counts short.
 __global__ void __launch_bounds__(kSortThreads)
     sort_scatter_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ unsigned short cnt[];  // [warps][digits]: tokens, then those before
     __shared__ int first[kMaxDigits];        // place of this tile's first token per digit
+    __shared__ int others[kMaxDigits];       // few tiles: tokens of the others
     __shared__ int warp_sum[kSortWarps];
     const int digits = 1 << a.bits, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     unsigned short *mine = cnt + warp * digits;
     for (int d = lane; d < digits; d += 32) mine[d] = 0;
+    const bool few = a.tiles <= kFewTiles;
+    first[threadIdx.x] = others[threadIdx.x] = 0;
     griddep_wait();
     griddep_launch_dependents();
-    __syncwarp();
+    __syncthreads();
     const int base = blockIdx.x * kTile + warp * (kTile / kSortWarps);
     int key[kItems], pos[kItems], rank[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
         const int i = base + k * 32 + lane;
-        key[k] = i < a.tokens ? sort_key(a, i, a.tiles == 1) : -1;
+        key[k] = i < a.tokens ? sort_key(a, i, few) : -1;
         pos[k] = a.in_key && i < a.tokens ? a.in_pos[i] : i;
     }
     // thread d: tokens of digit d in all tiles, and in the tiles before this one
     const int dig = threadIdx.x;
     int before = 0, all = 0;
-    if (a.tiles > 1 && dig < digits) {
+    if (few) {  // first: in the tiles before this one
+        for (int t = 0; t < a.tiles; ++t) {
+            if (t == (int)blockIdx.x) continue;
+#pragma unroll
+            for (int k = 0; k < kItems; ++k) {
+                const int i = t * kTile + k * kSortThreads + threadIdx.x;
+                if (i >= a.tokens) continue;
+                const int d = (sort_key(a, i, false) >> a.shift) & (digits - 1);
+                atomicAdd(&others[d], 1);
+                if (t < (int)blockIdx.x) atomicAdd(&first[d], 1);
+            }
+        }
+        __syncthreads();
+        before = first[dig];
+        all = others[dig];
+    } else if (dig < digits) {
 #pragma unroll 10
         for (int t = 0; t < a.tiles; ++t) {
             const int n = a.hist[(size_t)t * digits + dig];
@@ -166,7 +184,7 @@ __global__ void __launch_bounds__(kSortThreads)
             cnt[w * digits + dig] = (unsigned short)s;
             s += n;
         }
-        if (a.tiles == 1) all = s;
+        if (few) all += s;
     }
     // exclusive sums over the digits
     int inc = all;
@@ -220,9 +238,11 @@ __device__ __forceinline__ int merged_tokens(const SumArgs &a, long long d, int 
     return lo;
 }
 
+// A block has up to 128 threads, each with NC pieces of VEC columns (four single
+// columns of wide rows that are not whole 16-byte pieces), and four tokens in flight.
 constexpr int kSumThreads = 128, kAhead = 4;
 
-template <typename T, int VEC>
+template <typename T, int VEC, int NC>
 __global__ void __launch_bounds__(kSumThreads)
     segment_sum_kernel(const __grid_constant__ SumArgs a, const T *d_out, T *d_table) {
     using P = Piece<T, VEC>;
@@ -231,67 +251,87 @@ __global__ void __launch_bounds__(kSumThreads)
     griddep_launch_dependents();
     const long long total = (long long)a.rows + a.tokens;
     const long long d0 = blockIdx.x * a.per, d1 = d0 + a.per < total ? d0 + a.per : total;
-    if (threadIdx.x < 64) {
-        const int n = merged_tokens(a, threadIdx.x < 32 ? d0 : d1, threadIdx.x & 31);
-        if ((threadIdx.x & 31) == 0) cut[threadIdx.x >> 5] = n;
+    for (int k = threadIdx.x >> 5; k < 2; k += blockDim.x >> 5) {
+        const int n = merged_tokens(a, k ? d1 : d0, threadIdx.x & 31);
+        if ((threadIdx.x & 31) == 0) cut[k] = n;
     }
     __syncthreads();
     if (threadIdx.x == 0 && blockIdx.y == 0) a.cut[blockIdx.x] = cut[0];
-    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
-    if (c >= a.D) return;
+    const int c0 = (blockIdx.y * NC * blockDim.x + threadIdx.x) * VEC, step = blockDim.x * VEC;
+    if (c0 >= a.D) return;
     int j = cut[0];
     const int j1 = cut[1];
     int i = (int)(d0 - j);
     const int i1 = (int)(d1 - j1);
     // a row that an earlier part began
     bool begun = j > 0 && i < a.rows && a.key[j - 1] == i;
-    float acc[VEC];
+    float acc[NC][VEC];
+    auto clear = [&]() {
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k) acc[n][k] = 0.f;
+    };
+    auto keep = [&](float *to) {  // as a remainder
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int k = 0; k < VEC; ++k)
+                if (c0 + n * step < a.D)
+                    to[(size_t)blockIdx.x * a.D + c0 + n * step + k] = acc[n][k];
+    };
     auto end_row = [&]() {
-        float v[VEC];
         if (begun) {
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) a.head[(size_t)blockIdx.x * a.D + c + k] = acc[k];
+            keep(a.head);
             begun = false;
         } else {
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) v[k] = acc[k] * a.scale;
-            P::store(d_table + (size_t)i * a.D + c, v);
-        }
+            for (int n = 0; n < NC; ++n) {
+                float v[VEC];
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+                for (int k = 0; k < VEC; ++k) v[k] = acc[n][k] * a.scale;
+                if (c0 + n * step < a.D) P::store(d_table + (size_t)i * a.D + c0 + n * step, v);
+            }
+        }
+        clear();
         ++i;
     };
+    clear();
     while (j < j1) {
-        P p[kAhead];
+        P p[kAhead][NC];
         int id[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             id[u] = j + u < j1 ? a.key[j + u] : -1;
-            if (id[u] >= 0) p[u].load(d_out + (size_t)a.pos[j + u] * a.D + c);
+            const T *row = d_out + (size_t)(id[u] >= 0 ? a.pos[j + u] : 0) * a.D + c0;
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+                p[u][n].zero();
+                if (id[u] >= 0 && c0 + n * step < a.D) p[u][n].load(row + n * step);
+            }
         }
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (id[u] < 0) continue;
             while (i < id[u] && i < i1) end_row();
-            float v[VEC];
-            p[u].get(v);
 #pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] += v[k];
+            for (int n = 0; n < NC; ++n) {
+                float v[VEC];
+                p[u][n].get(v);
+#pragma unroll
+                for (int k = 0; k < VEC; ++k) acc[n][k] += v[k];
+            }
         }
         j += kAhead;
     }
     while (i < i1) end_row();
     // what is left belongs to a row that ends in a later part
-    if (j1 <= cut[0] || a.key[j1 - 1] != i1) return;
-#pragma unroll
-    for (int k = 0; k < VEC; ++k) a.carry[(size_t)blockIdx.x * a.D + c + k] = acc[k];
+    if (j1 > cut[0] && a.key[j1 - 1] == i1) keep(a.carry);
 }
 
 // Rows that span parts: the part in which the row ends adds the remainders of the
 // parts from the row's first token on, in order, and its own head.
-template <typename T, int VEC>
+template <typename T, int VEC, int NC>
 __global__ void __launch_bounds__(kSumThreads)
     segment_join_kernel(const __grid_constant__ SumArgs a, T *d_table) {
     __shared__ int from;
@@ -316,19 +356,22 @@ __global__ void __launch_bounds__(kSumThreads)
         if (threadIdx.x == 0) from = q;
     }
     __syncthreads();
-    const int c = (blockIdx.y * kSumThreads + threadIdx.x) * VEC;
-    if (c >= a.D) return;
-    float acc[VEC];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
+    for (int n = 0; n < NC; ++n) {
+        const int c = ((blockIdx.y * NC + n) * blockDim.x + threadIdx.x) * VEC;
+        if (c >= a.D) return;
+        float acc[VEC];
+#pragma unroll
+        for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
 #pragma unroll 8
-    for (int q = from; q < (int)blockIdx.x; ++q)
+        for (int q = from; q < (int)blockIdx.x; ++q)
 #pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] += a.carry[(size_t)q * a.D + c + k];
+            for (int k = 0; k < VEC; ++k) acc[k] += a.carry[(size_t)q * a.D + c + k];
 #pragma unroll
-    for (int k = 0; k < VEC; ++k)
-        acc[k] = (acc[k] + a.head[(size_t)blockIdx.x * a.D + c + k]) * a.scale;
-    Piece<T, VEC>::store(d_table + (size_t)i * a.D + c, acc);
+        for (int k = 0; k < VEC; ++k)
+            acc[k] = (acc[k] + a.head[(size_t)blockIdx.x * a.D + c + k]) * a.scale;
+        Piece<T, VEC>::store(d_table + (size_t)i * a.D + c, acc);
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -346,17 +389,39 @@ struct Plan {
     size_t pairs, hist, rem, cut, total;
 };
 
-// Parts of the merged list: at most 1,216 (with the column blocks enough for every
-// SM), at least 8 entries each.
-Plan plan_for(int tokens, int rows, int D) {
+// Columns of a block of the sums (vec per piece; four single ones per thread in wide
+// rows) and its threads.
+struct Columns {
+    int nc, threads, blocks;
+};
+Columns columns_for(int D, int vec) {
+    Columns c;
+    c.nc = vec == 1 && D >= 512 ? 4 : 1;
+    const int per = vec * c.nc, threads = ((D + per - 1) / per + 31) / 32 * 32;
+    c.threads = threads < kSumThreads ? threads : kSumThreads;
+    c.blocks = (D + c.threads * per - 1) / (c.threads * per);
+    return c;
+}
+
+// Parts of the merged list: as many as give every SM 64 warps, but 1,216 where rows are
+// wide, of at least four entries and sqrt(tokens / 32): a frequent id's n tokens are
+// added up `per` at a time, then n / per remainders one after another, and text's most
+// frequent id has about 1 / 16 of the tokens (5,000 tokens of 128 BF16: 42 us with parts
+// of four, 29 with parts of eight).
+Plan plan_for(int tokens, int rows, int D, int size) {
     Plan p;
     const int b = key_bits(rows);
     p.passes = (b + kMaxBits - 1) / kMaxBits;
     p.bits = (b + p.passes - 1) / p.passes;
     p.tiles = (tokens + kTile - 1) / kTile;
     const long long total = (long long)tokens + rows;
-    p.per = (total + 1215) / 1216;
-    if (p.per < 8) p.per = 8;
+    const Columns c = columns_for(D, D % (16 / size) == 0 ? 16 / size : 1);
+    long long most = 152ll * 64 * 32 / (c.threads * c.blocks);
+    if (most < 1216) most = 1216;
+    p.per = (total + most - 1) / most;
+    const long long least = (long long)sqrt(tokens / 32.0);
+    if (p.per < least) p.per = least;
+    if (p.per < 4) p.per = 4;
     p.parts = (int)((total + p.per - 1) / p.per);
     p.pairs = round256((size_t)tokens * 4);
     p.hist = round256((size_t)p.tiles * ((size_t)1 << p.bits) * 4);
@@ -385,15 +450,26 @@ cudaError_t run_embed(const void *table, const void *ids, int wide, void *out, i
                             ids, wide, (T *)out, tokens, rows, D, tpr, scale, status);
 }
 
-template <typename T, int VEC>
-cudaError_t run_sums(const SumArgs &a, const void *d_out, void *d_table, cudaStream_t st) {
-    const dim3 grid(a.parts, (a.D + kSumThreads * VEC - 1) / (kSumThreads * VEC));
-    cudaError_t e = launch_dependent(segment_sum_kernel<T, VEC>, grid, dim3(kSumThreads), 0, st, a,
+template <typename T, int VEC, int NC>
+cudaError_t run_sums(const SumArgs &a, const Columns &c, const void *d_out, void *d_table,
+                     cudaStream_t st) {
+    const dim3 grid(a.parts, c.blocks), block(c.threads);
+    cudaError_t e = launch_dependent(segment_sum_kernel<T, VEC, NC>, grid, block, 0, st, a,
                                      (const T *)d_out, (T *)d_table);
     if (e != cudaSuccess || a.tokens == 0) return e;
-    return launch_dependent(segment_join_kernel<T, VEC>, grid, dim3(kSumThreads), 0, st, a,
-                            (T *)d_table);
+    return launch_dependent(segment_join_kernel<T, VEC, NC>, grid, block, 0, st, a, (T *)d_table);
 }
+
+template <typename T>
+cudaError_t run_sums(const SumArgs &a, bool wide, const void *d_out, void *d_table, cudaStream_t st) {
+    constexpr int V = 16 / sizeof(T);
+    const Columns c = columns_for(a.D, wide ? V : 1);
+    if (wide) return run_sums<T, V, 1>(a, c, d_out, d_table, st);
+    return c.nc == 4 ? run_sums<T, 1, 4>(a, c, d_out, d_table, st)
+                     : run_sums<T, 1, 1>(a, c, d_out, d_table, st);
+}
+
+int size_of(const kda_embed_desc_t *d) { return d->act_dtype == KDA_DTYPE_BF16 ? 2 : 4; }
 
 kda_status_t check(const kda_embed_desc_t *d) {
     if (!d) return KDA_ERR_INVALID_ARG;
@@ -417,7 +493,7 @@ kda_status_t kda_embedding_forward(const kda_embed_desc_t *desc, const void *tab
     kda_status_t rc = check(desc);
     if (rc != KDA_OK) return rc;
     if (desc->tokens == 0) return KDA_OK;
-    const int size = desc->act_dtype == KDA_DTYPE_BF16 ? 2 : 4, wide = desc->id_dtype == KDA_ID_I64;
+    const int size = size_of(desc), wide = desc->id_dtype == KDA_ID_I64;
     if (!table || !ids || !out || (uintptr_t)table % size || (uintptr_t)out % size ||
         (uintptr_t)ids % (wide ? 8 : 4) || (uintptr_t)dev_status % 4)
         return KDA_ERR_INVALID_ARG;
@@ -437,7 +513,7 @@ kda_status_t kda_embedding_forward(const kda_embed_desc_t *desc, const void *tab
 
 size_t kda_embedding_backward_workspace_size(const kda_embed_desc_t *desc) {
     if (check(desc) != KDA_OK) return 0;
-    return plan_for(desc->tokens, desc->rows, desc->width).total;
+    return plan_for(desc->tokens, desc->rows, desc->width, size_of(desc)).total;
 }
 
 kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_out,
@@ -445,12 +521,12 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
                                     size_t workspace_bytes, int32_t *dev_status, void *stream) {
     kda_status_t rc = check(desc);
     if (rc != KDA_OK) return rc;
-    const int size = desc->act_dtype == KDA_DTYPE_BF16 ? 2 : 4, wide = desc->id_dtype == KDA_ID_I64;
+    const int size = size_of(desc), wide = desc->id_dtype == KDA_ID_I64;
     if (!d_table || (uintptr_t)d_table % size || (uintptr_t)dev_status % 4) return KDA_ERR_INVALID_ARG;
     if (desc->tokens > 0 && (!d_out || !ids || (uintptr_t)d_out % size ||
                              (uintptr_t)ids % (wide ? 8 : 4)))
         return KDA_ERR_INVALID_ARG;
-    const Plan p = plan_for(desc->tokens, desc->rows, desc->width);
+    const Plan p = plan_for(desc->tokens, desc->rows, desc->width, size_of(desc));
     if (!workspace || workspace_bytes < p.total || ((uintptr_t)workspace & 15u))
         return KDA_ERR_WORKSPACE;
     cudaStream_t st = (cudaStream_t)stream;
@@ -479,7 +555,7 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
             last = k ? 1 - last : 0;
             a.out_key = keys[last];
             a.out_pos = poss[last];
-            if ((p.tiles > 1 && launch_dependent(sort_hist_kernel, dim3(p.tiles), dim3(kSortThreads),
+            if ((p.tiles > kFewTiles && launch_dependent(sort_hist_kernel, dim3(p.tiles), dim3(kSortThreads),
                                                  0, st, a) != cudaSuccess) ||
                 launch_dependent(sort_scatter_kernel, dim3(p.tiles), dim3(kSortThreads), scatter_smem,
                                  st, a) != cudaSuccess)
@@ -499,12 +575,8 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
     s.cut = (int *)(w + 4 * p.pairs + p.hist + 2 * p.rem);
     s.scale = desc->scale;
     const bool vec = wide_rows(desc->width, size, d_out, d_table);
-    cudaError_t e;
-    if (size == 2)
-        e = vec ? run_sums<__nv_bfloat16, 8>(s, d_out, d_table, st)
-                : run_sums<__nv_bfloat16, 1>(s, d_out, d_table, st);
-    else
-        e = vec ? run_sums<float, 4>(s, d_out, d_table, st) : run_sums<float, 1>(s, d_out, d_table, st);
+    const cudaError_t e = size == 2 ? run_sums<__nv_bfloat16>(s, vec, d_out, d_table, st)
+                                    : run_sums<float>(s, vec, d_out, d_table, st);
     return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
