@@ -239,8 +239,8 @@ __device__ __forceinline__ int merged_tokens(const SumArgs &a, long long d, int 
 }
 
 // A block has up to 128 threads, each with NC pieces of VEC columns (four single
-// columns of wide rows that are not whole 16-byte pieces), and four tokens in flight.
-constexpr int kSumThreads = 128, kAhead = 4;
+// columns of wide rows that are not whole 16-byte pieces), and eight tokens in flight.
+constexpr int kSumThreads = 128, kAhead = 8;
 
 template <typename T, int VEC, int NC>
 __global__ void __launch_bounds__(kSumThreads)
