@@ -513,8 +513,9 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
  * it): dx [T, D] and d_weight [V, D] (either may be NULL), both overwritten.  Works
  * through the vocabulary in pieces of desc->piece columns (rounded up to 256): the
  * piece's logits are computed again, dz = d_loss (softmax - onehot) of the piece is
- * held in BF16 (F32: three BF16 terms), and both products read it.  Workspace:
- * kda_linear_ce_workspace_size(desc, 1), 16-byte aligned.
+ * held in BF16 (F32: three BF16 terms), and both products read it.  Rows whose target is
+ * ignored have no part in d_weight whatever x holds there (NaN, say), and dx 0.
+ * Workspace: kda_linear_ce_workspace_size(desc, 1), 16-byte aligned.
  */
 kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, const void *weight,
                                     const void *targets, const float *lse, const float *d_loss,

@@ -101,9 +101,12 @@ def _first(t, name, dims):
     raise ValueError("%s must be float32 or bfloat16" % name)
 
 
-def _workspace(workspace, need, dev):
+def _workspace(workspace, need, dev, stream):
     if workspace is None:
-        return torch.empty(need or 16, dtype=torch.uint8, device=dev), need or 16
+        workspace = torch.empty(need or 16, dtype=torch.uint8, device=dev)
+        if stream is not None:  # it must outlive the kernels on a stream not its own
+            workspace.record_stream(stream)
+        return workspace, need or 16
     if not isinstance(workspace, torch.Tensor) or workspace.device != dev:
         raise ValueError("workspace must be a tensor on %s" % dev)
     return workspace, workspace.numel() * workspace.element_size()
@@ -190,7 +193,8 @@ def gated_norm_backward(d_out, x, gate=None, weight=None, *, act="sigmoid", eps=
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(x.shape[2], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
+        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev,
+                                       stream)
     _check("kda_gated_norm_backward",
            L.kda_gated_norm_backward(desc, d_out.data_ptr(), x.data_ptr(), _ptr(gate),
                                      _ptr(weight), dx.data_ptr(), _ptr(d_gate), _ptr(d_weight),
@@ -246,7 +250,8 @@ def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(h_out.shape[1], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
+        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev,
+                                       stream)
     _check("kda_residual_norm_backward",
            L.kda_residual_norm_backward(desc, d_out.data_ptr(), _ptr(d_h_out), h_out.data_ptr(),
                                         _ptr(weight), scale, dh.data_ptr(), _ptr(dy),
@@ -302,7 +307,8 @@ def embedding_backward(d_out, ids, num_rows, *, scale=1.0, d_table=None, workspa
     else:
         _is(d_table, "d_table", d_out.dtype, (num_rows, D), dev)
     L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_embedding_backward_workspace_size(desc), dev)
+    workspace, ws_len = _workspace(workspace, L.kda_embedding_backward_workspace_size(desc), dev,
+                                   stream)
     _check("kda_embedding_backward",
            L.kda_embedding_backward(desc, d_out.data_ptr(), ids.data_ptr(), d_table.data_ptr(),
                                     workspace.data_ptr(), ws_len, _status(dev_status, dev),
@@ -340,7 +346,7 @@ def linear_cross_entropy(x, weight, targets, *, ignore_index=-100, loss=None, ls
     loss, lse = _vector(loss, "loss", T, dev), _vector(lse, "lse", T, dev)
     mean = torch.empty((), dtype=torch.float32, device=dev)
     L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 0), dev)
+    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 0), dev, stream)
     _check("kda_linear_ce_forward",
            L.kda_linear_ce_forward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
                                    loss.data_ptr(), lse.data_ptr(), mean.data_ptr(),
@@ -362,7 +368,7 @@ def linear_cross_entropy_backward(x, weight, targets, lse, d_loss, *, ignore_ind
     dx = _out(None, "dx", x) if want_dx else None
     d_weight = _out(None, "d_weight", weight) if want_d_weight else None
     L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 1), dev)
+    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 1), dev, stream)
     _check("kda_linear_ce_backward",
            L.kda_linear_ce_backward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
                                     lse.data_ptr(), d_loss.data_ptr(), _ptr(dx), _ptr(d_weight),

@@ -354,11 +354,13 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
 
 // Rows of x and, if w_rows, of W as `planes` BF16 terms with a pitch of whole 128-byte
 // lines (zeros past the width): fp32 operands, and BF16 rows whose width is no multiple
-// of the 16 bytes that a tensor map needs.
+// of the 16 bytes that a tensor map needs.  With targets, rows of x whose target is
+// ignored become zeros: dW is a sum over all rows, and what a padded position holds
+// (NaN perhaps) has no part in it.
 template <typename T>
 __global__ void __launch_bounds__(256)
     pack_kernel(const T *x, long long x_rows, __nv_bfloat16 *xp, const T *w, long long w_rows,
-                __nv_bfloat16 *wp, int D, int pitch, int planes) {
+                __nv_bfloat16 *wp, int D, int pitch, int planes, Targets y) {
     griddep_wait();
     griddep_launch_dependents();
     const int pieces = pitch / 8;
@@ -374,6 +376,10 @@ __global__ void __launch_bounds__(256)
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = c + j < D ? act_ld(src, (size_t)(r * D + c + j)) : 0.f;
+        if (!second && y.ids && y.at(r, false) < 0) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        }
         for (int pl = 0; pl < planes; ++pl) {
             uint32_t u[4];
 #pragma unroll
@@ -439,12 +445,12 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
     l.planes = l.f32 ? 3 : 1;
     l.pairs = l.f32 ? 6 : 1;
     l.chunk = l.f32 ? kChunkF32 : kChunkBf16;
-    // Copies: whole 128-byte lines where x and W are copied as BF16 (with rows of 1,040
+    // Copies: x in a backward pass (ignored rows become zeros); whole 128-byte lines where x and W are copied as BF16 (with rows of 1,040
     // bytes the copies of 128-byte boxes ran at half the rate)
-    l.pack_x = l.f32 || D % 8 != 0;
+    l.pack_x = l.f32 || D % 8 != 0 || backward;
     l.pack_w = l.f32 ? !l.w32 : D % 8 != 0;
     l.x_pitch = l.pack_x ? (D + 63) / 64 * 64 : D;
-    l.w_pitch = l.pack_w ? l.x_pitch : D;
+    l.w_pitch = l.pack_w ? (D + 63) / 64 * 64 : D;
     l.xp = l.pack_x ? round256(T * l.x_pitch * l.planes * 2) : 0;
     l.wp = l.pack_w ? round256(V * l.w_pitch * l.planes * 2) : 0;
     if (!backward) {
@@ -543,7 +549,8 @@ cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap
 }
 // Copies x and W where the layout wants them; xp, wp are what the products read.
 cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *x, const void *w,
-                     uint8_t *ws, const void *&xp, const void *&wp, cudaStream_t st) {
+                     const Targets &y, uint8_t *ws, const void *&xp, const void *&wp,
+                     cudaStream_t st) {
     xp = l.pack_x ? ws : x;
     wp = l.pack_w ? ws + l.xp : w;
     if (!l.pack_x) return cudaSuccess;
@@ -553,10 +560,10 @@ cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *x, con
     __nv_bfloat16 *to = (__nv_bfloat16 *)ws, *to_w = (__nv_bfloat16 *)(ws + l.xp);
     if (l.f32)
         return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)x, T, to,
-                                (const float *)w, V, to_w, d->width, l.x_pitch, l.planes);
+                                (const float *)w, V, to_w, d->width, l.x_pitch, l.planes, y);
     return launch_dependent(pack_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
                             (const __nv_bfloat16 *)x, T, to, (const __nv_bfloat16 *)w, V, to_w,
-                            d->width, l.x_pitch, l.planes);
+                            d->width, l.x_pitch, l.planes, y);
 }
 
 bool bad_ids(const kda_ce_desc_t *d, const void *ids) {
@@ -604,7 +611,7 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     float2 *sums = (float2 *)(ws + l.xp + l.wp + l.part + l.zy);
     unsigned *ticket = (unsigned *)(ws + l.total - 256);
     const void *xp, *wp;
-    if (run_pack(desc, l, x, weight, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
+    if (run_pack(desc, l, x, weight, Targets{}, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
     GemmArgs p = {};
     p.M = desc->tokens;
     p.N = desc->vocab;
@@ -665,7 +672,9 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
     __nv_bfloat16 *dz = (__nv_bfloat16 *)(ws + l.xp + l.wp);
     float *acc = (float *)(ws + l.xp + l.wp + l.dz);
     const void *xp, *wp;
-    if (run_pack(desc, l, x, weight, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
+    const Targets y = {targets, desc->id_dtype == KDA_ID_I64, desc->vocab, desc->ignore_index,
+                       dev_status};
+    if (run_pack(desc, l, x, weight, y, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
     const int T = desc->tokens, V = desc->vocab, D = desc->width;
     const int step = l.w32 ? kW32Step : BK;
     // as K-major and MN-major operands
@@ -691,7 +700,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.N = cols;
         p.k_blocks = cdiv(D, step);
         p.b_row0 = v0;
-        p.y = {targets, desc->id_dtype == KDA_ID_I64, V, desc->ignore_index, dev_status};
+        p.y = y;
         p.lse = lse;
         p.d_loss = d_loss;
         p.dz = dz;

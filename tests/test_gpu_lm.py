@@ -493,3 +493,43 @@ def test_calls_are_captured_in_a_graph():
     torch.cuda.synchronize()
     for a, b in zip(got, want):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D", [(200, 300, 64), (7, 1000, 72), (300, 129, 31)])
+def test_cross_entropy_of_rows_with_nan_where_ignored(dtype, T, V, D):
+    """Padding may hold anything: an ignored row of NaN and infinities changes nothing."""
+    g, dt = _gen(11), DT[dtype]
+    x, w = _randn((T, D), g, dt), _randn((V, D), g, dt, 0.1)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    y[::3] = -100
+    d = torch.rand(T, generator=g, device="cuda")
+    bad = x.clone()
+    bad[::3] = float("nan")
+    bad[3::6] = float("inf")
+    clean = x.clone()
+    clean[::3] = 0
+    kept = y != -100
+    loss, lse, mean = kda.linear_cross_entropy(bad, w, y)
+    ref, ref_lse, ref_mean = kda.linear_cross_entropy(clean, w, y)
+    assert torch.equal(loss, ref) and torch.equal(mean, ref_mean)
+    assert torch.equal(lse[kept], ref_lse[kept])
+    dx, dw = kda.linear_cross_entropy_backward(bad, w, y, lse, d)
+    ref_dx, ref_dw = kda.linear_cross_entropy_backward(clean, w, y, ref_lse, d)
+    assert torch.equal(dw, ref_dw) and torch.equal(dx, ref_dx)
+    assert not dx[::3].any()
+
+
+def test_workspaces_on_another_stream():
+    """A call on a stream of its own keeps its workspace until its kernels are done."""
+    g = _gen(12)
+    x, w = _randn((2000, 512), g, torch.bfloat16), _randn((20000, 512), g, torch.bfloat16, 0.1)
+    y = torch.randint(0, 20000, (2000,), generator=g, device="cuda")
+    want, _, _ = kda.linear_cross_entropy(x, w, y)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for _ in range(20):
+        got, _, _ = kda.linear_cross_entropy(x, w, y, stream=s)
+        torch.full((1_000_000,), 7.0, device="cuda")  # would land in a freed workspace
+        s.synchronize()
+        assert torch.equal(got, want)
