@@ -242,6 +242,18 @@ __device__ __forceinline__ int merged_tokens(const SumArgs &a, long long d, int 
 // columns of wide rows that are not whole 16-byte pieces), and eight tokens in flight.
 constexpr int kSumThreads = 128, kAhead = 8;
 
+// Zeros for n elements: 16-byte stores between the ends, by all threads of the block.
+template <typename T>
+__device__ __forceinline__ void fill_zero(T *p, long long n) {
+    const int lead = (int)((16 - ((uintptr_t)p & 15u)) & 15u) / (int)sizeof(T);
+    const long long head = lead < n ? lead : n, pieces = (n - head) * (long long)sizeof(T) / 16;
+    const long long tail = head + pieces * (16 / (int)sizeof(T));
+    if (threadIdx.x < head) act_st(p, threadIdx.x, 0.f);
+    for (long long k = threadIdx.x; k < pieces; k += blockDim.x)
+        *(uint4 *)(p + head + k * (16 / (int)sizeof(T))) = make_uint4(0u, 0u, 0u, 0u);
+    if (threadIdx.x < n - tail) act_st(p, (size_t)tail + threadIdx.x, 0.f);
+}
+
 template <typename T, int VEC, int NC>
 __global__ void __launch_bounds__(kSumThreads)
     segment_sum_kernel(const __grid_constant__ SumArgs a, const T *d_out, T *d_table) {
@@ -258,7 +270,7 @@ __global__ void __launch_bounds__(kSumThreads)
     __syncthreads();
     if (threadIdx.x == 0 && blockIdx.y == 0) a.cut[blockIdx.x] = cut[0];
     const int c0 = (blockIdx.y * NC * blockDim.x + threadIdx.x) * VEC, step = blockDim.x * VEC;
-    if (c0 >= a.D) return;
+    if (VEC > 1 && c0 >= a.D) return;
     int j = cut[0];
     const int j1 = cut[1];
     int i = (int)(d0 - j);
@@ -296,6 +308,19 @@ __global__ void __launch_bounds__(kSumThreads)
         clear();
         ++i;
     };
+    // Rows up to `to` end here: the one that is summed, then rows without tokens.  Those
+    // are contiguous memory whatever the width, so where rows are not whole pieces the
+    // column blocks share it out as such.
+    auto end_rows = [&](int to) {
+        if (i < to) end_row();
+        if (VEC == 1 && i + 1 < to) {
+            const long long n = (long long)(to - i) * a.D, y = blockIdx.y, ny = gridDim.y;
+            const long long from = n * y / ny;
+            fill_zero(d_table + (size_t)i * a.D + from, n * (y + 1) / ny - from);
+            i = to;
+        }
+        while (i < to) end_row();
+    };
     clear();
     while (j < j1) {
         P p[kAhead][NC];
@@ -313,7 +338,7 @@ __global__ void __launch_bounds__(kSumThreads)
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
             if (id[u] < 0) continue;
-            while (i < id[u] && i < i1) end_row();
+            end_rows(id[u] < i1 ? id[u] : i1);
 #pragma unroll
             for (int n = 0; n < NC; ++n) {
                 float v[VEC];
@@ -324,7 +349,7 @@ __global__ void __launch_bounds__(kSumThreads)
         }
         j += kAhead;
     }
-    while (i < i1) end_row();
+    end_rows(i1);
     // what is left belongs to a row that ends in a later part
     if (j1 > cut[0] && a.key[j1 - 1] == i1) keep(a.carry);
 }
