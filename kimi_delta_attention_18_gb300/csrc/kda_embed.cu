@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(256)
 
 // --------------------------------------------------------------------- sort
 constexpr int kTile = 4096, kSortThreads = 1024, kItems = kTile / kSortThreads;
-constexpr int kSortWarps = kSortThreads / 32, kFewTiles = 4;
+constexpr int kSortWarps = kSortThreads / 32, kFewTiles = 2;
 constexpr int kMaxBits = 10, kMaxDigits = 1 << kMaxBits;
 static_assert(kMaxDigits <= kSortThreads, "a thread per digit");
 
@@ -86,6 +86,7 @@ struct SortArgs {
     const int *in_key, *in_pos;  // NULL: the first pass reads ids
     int *out_key, *out_pos;
     int *hist;                   // [tiles][digits]
+    int *todo;                   // first pass: cleared for the sums
     int shift, bits, tiles;
     int32_t *status;
 };
@@ -114,8 +115,10 @@ __global__ void __launch_bounds__(kSortThreads) sort_hist_kernel(const __grid_co
 // Moves a tile's tokens to their places: all smaller digits, then the same digit
 // in earlier tiles, then in earlier warps of this tile, then earlier in the warp
 // (a warp holds consecutive tokens, 32 at a time).  With up to kFewTiles tiles each block
-// counts the other tiles itself, so up to 16,384 tokens take one launch per pass.  The
-// pass is all latency; large tiles keep the loop over the tiles' counts short.
+// counts the other tiles itself, so up to 8,192 tokens take one launch per pass (a
+// frequent id makes the counting slow: at 30,000 tokens 88 us that way, 78 with a launch
+// for the counts).  The pass is all latency; large tiles keep the loop over the tiles'
+// counts short.
 __global__ void __launch_bounds__(kSortThreads)
     sort_scatter_kernel(const __grid_constant__ SortArgs a) {
     extern __shared__ unsigned short cnt[];  // [warps][digits]: tokens, then those before
@@ -129,6 +132,7 @@ __global__ void __launch_bounds__(kSortThreads)
     first[threadIdx.x] = others[threadIdx.x] = 0;
     griddep_wait();
     griddep_launch_dependents();
+    if (!a.in_key && blockIdx.x == 0 && threadIdx.x == 0) *a.todo = 0;
     __syncthreads();
     const int base = blockIdx.x * kTile + warp * (kTile / kSortWarps);
     int key[kItems], pos[kItems], rank[kItems];
@@ -219,6 +223,7 @@ struct SumArgs {
     long long per;         // entries of the merged list per part
     float *carry, *head;   // [parts][D] fp32
     int *cut;              // [parts]: tokens before the part
+    int *todo;             // their number, then the parts in which a row begun earlier ends
     float scale;
 };
 
@@ -277,6 +282,8 @@ __global__ void __launch_bounds__(kSumThreads)
     const int i1 = (int)(d1 - j1);
     // a row that an earlier part began
     bool begun = j > 0 && i < a.rows && a.key[j - 1] == i;
+    if (begun && i < i1 && threadIdx.x == 0 && blockIdx.y == 0)
+        a.todo[1 + atomicAdd(a.todo, 1)] = blockIdx.x;  // in any order: each is joined by itself
     float acc[NC][VEC];
     auto clear = [&]() {
 #pragma unroll
@@ -354,48 +361,72 @@ __global__ void __launch_bounds__(kSumThreads)
     if (j1 > cut[0] && a.key[j1 - 1] == i1) keep(a.carry);
 }
 
-// Rows that span parts: the part in which the row ends adds the remainders of the
-// parts from the row's first token on, in order, and its own head.
-template <typename T, int VEC, int NC>
-__global__ void __launch_bounds__(kSumThreads)
-    segment_join_kernel(const __grid_constant__ SumArgs a, T *d_table) {
+// Rows that span parts: for each part on the list, the remainders of the parts from the
+// row's first token on, in order, and the part's own head.  `lanes` threads x 4 columns;
+// narrow rows leave room for several slices of the parts (a frequent id of a small
+// vocabulary spans a hundred).
+constexpr int kJoinThreads = 256;
+int join_lanes(int D) { return D >= 1024 ? 256 : 64; }
+
+template <typename T>
+__global__ void __launch_bounds__(kJoinThreads)
+    segment_join_kernel(const __grid_constant__ SumArgs a, T *d_table, int lanes, bool fours) {
     __shared__ int from;
+    __shared__ float4 sh[kJoinThreads];
     griddep_wait();
     griddep_launch_dependents();
-    const long long d0 = blockIdx.x * a.per;
-    const int j0 = a.cut[blockIdx.x], i = (int)(d0 - j0);
-    const int i1 = blockIdx.x + 1 < (unsigned)a.parts
-                       ? (int)(d0 + a.per - a.cut[blockIdx.x + 1]) : a.rows;
-    if (j0 == 0 || i >= i1 || a.key[j0 - 1] != i) return;
-    if (threadIdx.x < 32) {  // back to the part in which the row begins, 32 at a time
-        int q = blockIdx.x - 1;
-        while (true) {
-            const int at = q - (int)threadIdx.x, n = at >= 0 ? a.cut[at] : 0;
-            const unsigned in = __ballot_sync(0xffffffffu, n > 0 && a.key[n > 0 ? n - 1 : 0] == i);
-            if (in != 0xffffffffu) {  // part `at` continues the row for the lowest lanes
-                q -= __ffs(~in) - 1;
-                break;
+    const int slices = kJoinThreads / lanes, slice = threadIdx.x / lanes;
+    const int lane = threadIdx.x - slice * lanes;
+    const int blocks = (a.D + 4 * lanes - 1) / (4 * lanes), n_todo = *a.todo;
+    for (long long w = blockIdx.x; w < (long long)n_todo * blocks; w += gridDim.x) {
+        const int part = a.todo[1 + w / blocks], block = (int)(w % blocks);
+        const int i = (int)(part * a.per - a.cut[part]);
+        if (threadIdx.x < 32) {  // back to the part in which the row begins, 32 at a time
+            int q = part - 1;
+            while (true) {
+                const int at = q - (int)threadIdx.x, n = at >= 0 ? a.cut[at] : 0;
+                const unsigned in = __ballot_sync(0xffffffffu, n > 0 && a.key[n > 0 ? n - 1 : 0] == i);
+                if (in != 0xffffffffu) {  // part `at` continues the row for the lowest lanes
+                    q -= __ffs(~in) - 1;
+                    break;
+                }
+                q -= 32;
             }
-            q -= 32;
+            if (threadIdx.x == 0) from = q;
         }
-        if (threadIdx.x == 0) from = q;
-    }
-    __syncthreads();
+        __syncthreads();
+        // four columns together, or `lanes` apart where rows are not whole fours
+        const int c = block * 4 * lanes + lane * (fours ? 4 : 1), step = fours ? 1 : lanes;
+        auto get = [&](const float *p, int q) {
+            const float *r = p + (size_t)q * a.D + c;
+            if (fours) return c < a.D ? *(const float4 *)r : make_float4(0.f, 0.f, 0.f, 0.f);
+            return make_float4(c < a.D ? r[0] : 0.f, c + step < a.D ? r[step] : 0.f,
+                               c + 2 * step < a.D ? r[2 * step] : 0.f,
+                               c + 3 * step < a.D ? r[3 * step] : 0.f);
+        };
+        const long long n = part - from;
+        const int q0 = from + (int)(n * slice / slices);
+        const int q1 = from + (int)(n * (slice + 1) / slices);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int q = q0; q < q1; ++q) {
+            const float4 v = get(a.carry, q);
+            acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+        }
+        sh[threadIdx.x] = acc;
+        __syncthreads();
+        if (slice == 0) {
+            for (int k = 1; k <= slices; ++k) {
+                const float4 v = k < slices ? sh[k * lanes + lane] : get(a.head, part);
+                acc = make_float4(acc.x + v.x, acc.y + v.y, acc.z + v.z, acc.w + v.w);
+            }
+            T *r = d_table + (size_t)i * a.D;
+            const float v[4] = {acc.x, acc.y, acc.z, acc.w};
 #pragma unroll
-    for (int n = 0; n < NC; ++n) {
-        const int c = ((blockIdx.y * NC + n) * blockDim.x + threadIdx.x) * VEC;
-        if (c >= a.D) return;
-        float acc[VEC];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k) acc[k] = 0.f;
-#pragma unroll 8
-        for (int q = from; q < (int)blockIdx.x; ++q)
-#pragma unroll
-            for (int k = 0; k < VEC; ++k) acc[k] += a.carry[(size_t)q * a.D + c + k];
-#pragma unroll
-        for (int k = 0; k < VEC; ++k)
-            acc[k] = (acc[k] + a.head[(size_t)blockIdx.x * a.D + c + k]) * a.scale;
-        Piece<T, VEC>::store(d_table + (size_t)i * a.D + c, acc);
+            for (int k = 0; k < 4; ++k)
+                if (c + k * step < a.D) act_st(r, c + k * step, v[k] * a.scale);
+        }
+        __syncthreads();
     }
 }
 
@@ -451,7 +482,7 @@ Plan plan_for(int tokens, int rows, int D, int size) {
     p.pairs = round256((size_t)tokens * 4);
     p.hist = round256((size_t)p.tiles * ((size_t)1 << p.bits) * 4);
     p.rem = round256((size_t)p.parts * D * 4);
-    p.cut = round256((size_t)p.parts * 4);
+    p.cut = round256((size_t)(2 * p.parts + 1) * 4);  // cut, todo
     p.total = 4 * p.pairs + p.hist + 2 * p.rem + p.cut;
     return p;
 }
@@ -482,7 +513,11 @@ cudaError_t run_sums(const SumArgs &a, const Columns &c, const void *d_out, void
     cudaError_t e = launch_dependent(segment_sum_kernel<T, VEC, NC>, grid, block, 0, st, a,
                                      (const T *)d_out, (T *)d_table);
     if (e != cudaSuccess || a.tokens == 0) return e;
-    return launch_dependent(segment_join_kernel<T, VEC, NC>, grid, block, 0, st, a, (T *)d_table);
+    const int lanes = join_lanes(a.D);
+    const long long joins = (long long)a.parts * ((a.D + 4 * lanes - 1) / (4 * lanes));
+    const long long most = 8ll * device_sms();
+    return launch_dependent(segment_join_kernel<T>, dim3((unsigned)(joins < most ? joins : most)),
+                            dim3(kJoinThreads), 0, st, a, (T *)d_table, lanes, a.D % 4 == 0);
 }
 
 template <typename T>
@@ -558,6 +593,7 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
     uint8_t *w = (uint8_t *)workspace;
     int *keys[2] = {(int *)w, (int *)(w + p.pairs)};
     int *poss[2] = {(int *)(w + 2 * p.pairs), (int *)(w + 3 * p.pairs)};
+    int *cut = (int *)(w + 4 * p.pairs + p.hist + 2 * p.rem);
     int last = 0;
     if (desc->tokens > 0) {
         SortArgs a = {};
@@ -569,6 +605,7 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
         a.bits = p.bits;
         a.tiles = p.tiles;
         a.status = dev_status;
+        a.todo = cut + p.parts;
         const size_t scatter_smem = ((size_t)2 * kSortWarps) << p.bits;
         if (set_max_dynamic_smem((const void *)sort_scatter_kernel, (2 * kSortWarps) << kMaxBits) !=
             cudaSuccess)
@@ -597,7 +634,8 @@ kda_status_t kda_embedding_backward(const kda_embed_desc_t *desc, const void *d_
     s.per = p.per;
     s.carry = (float *)(w + 4 * p.pairs + p.hist);
     s.head = (float *)(w + 4 * p.pairs + p.hist + p.rem);
-    s.cut = (int *)(w + 4 * p.pairs + p.hist + 2 * p.rem);
+    s.cut = cut;
+    s.todo = cut + p.parts;
     s.scale = desc->scale;
     const bool vec = wide_rows(desc->width, size, d_out, d_table);
     const cudaError_t e = size == 2 ? run_sums<__nv_bfloat16>(s, vec, d_out, d_table, st)
