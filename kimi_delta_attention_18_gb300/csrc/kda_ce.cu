@@ -15,6 +15,12 @@
 // products of terms whose weight is 2^-16 or more are accumulated, smallest first.
 // They are stored as such terms first; only W, where there are few tokens, is split on
 // its way through shared memory instead (kda_ce_w32.cu).
+//
+// Measured on GB300: gradient of 8,192 x 131,072 x 4,096 BF16 15.2 ms = 1.74 PFLOP/s of
+// its 6 T V D, in a loop under the power cap (cuBLAS sustains 1.73 there; each product
+// alone takes 1.14-1.17 ms per 32,768 columns, 1.89-1.93 PFLOP/s); losses of 256 x
+// 131,072 x 7,168 325 us (5.8 TB/s of W, 1.48 PFLOP/s: near both bounds); fp32 gradient
+// of 777 x 10,007 x 515 208 us.
 #include <math.h>
 
 #include "kda_ce_gemm.cuh"

@@ -2,6 +2,12 @@
 // ring of stages), so the bytes in flight do not depend on the registers that the
 // arithmetic takes, and rows of odd widths need no aligned access of their own: a tile
 // of eight (BF16) or four (fp32) of them, or a multiple, starts on a 16-byte boundary.
+//
+// Measured on GB300 (BF16; a copy of this size runs at 6.4-6.7 TB/s): gradient of the
+// gated norm of 81,920 x 56 x 128 865-920 us (6.4-6.8 TB/s; with rows loaded straight
+// into registers 1,083, bound by the loads that 25 % of the warps can have in flight);
+// of the residual norm of 40,960 x 7,168 477 us (6.2 TB/s; 505 without the ring, 498
+// with a barrier per row); 72,896 x 281 84 us (121 in shifted pieces).
 #include "kda_norm_math.cuh"
 #include "kda_sm100.cuh"
 
