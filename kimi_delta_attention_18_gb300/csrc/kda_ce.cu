@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             bool ok = true;
             for (int w = w0; w < work && ok; w += wstep) {
                 const Tile t = tile_at<CTAS>(p, w);
-                const int ar = (t.m * CTAS + rank) * BM + p.a_row0;
+                const int ar = (t.m * CTAS + rank) * BM;
                 const int br = t.n * p.bn + rank * (p.bn / CTAS) + p.b_row0;
                 for (int pr = 0; pr < p.pairs && ok; ++pr) {
                     const int pa = term_a(pr, p.pairs), pb = term_b(pr, p.pairs);
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < BM / 64; ++i)
                                 tma_load_3d<CTAS>(a + i * kBox, ta, ar + 64 * i,
-                                                  kb * BK + p.ak_row0, pa, full);
+                                                  kb * BK, pa, full);
                         } else {
                             tma_load_3d<CTAS>(a, ta, kb * BK, ar, pa, full);
                         }

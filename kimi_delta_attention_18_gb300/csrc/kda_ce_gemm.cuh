@@ -42,8 +42,8 @@ struct GemmArgs {
     int k_blocks, splits, pairs;
     int chunk;                 // FINE: stages per accumulator
     int m_tiles, n_tiles, bn;  // set at the launch; bn: columns per tile, a multiple of 64
-    int a_row0, b_row0;        // added to the operands' non-contraction coordinate
-    int ak_row0, bk_row0;      // added to the contraction coordinate of MN-major operands
+    int b_row0;                // B's first row (of the vocabulary's piece)
+    int bk_row0;               // the same where the contraction is along B's rows
     // EPI_STATS, EPI_DZ
     Targets y;
     float2 *part;              // [2 n_tiles][M] (maximum, sum)
