@@ -174,8 +174,8 @@ def test_cross_entropy_workspace_follows_the_piece():
     """The backward's workspace holds dz for one piece of the vocabulary, not for all."""
     size = lambda **kw: kda.lib().kda_linear_ce_workspace_size(  # noqa: E731
         _ce(tokens=4096, vocab=100000, width=512, **kw), 1)
-    one, four = size(piece=1024), size(piece=4096)
-    assert four - one == 4096 * 3072 * 2
+    one, two = size(piece=2048), size(piece=4096)
+    assert two - one == 4096 * 2048 * 2
     assert size() < 4096 * 100000 * 2
 
 
