@@ -286,14 +286,14 @@ cudaError_t launch_op(const NormArgs &a, int size, const Shape &s, cudaStream_t 
 // The kernel for these rows and, in a backward pass, its number of blocks (the rows
 // of `partial`).
 int norm_blocks(const NormArgs &a, int op, bool bwd, int size, int move) {
-    const int ring = move != BY_ELEMENT && !a.strided
+    const int ring = move != BY_ELEMENT
                          ? norm_ring_blocks(a, op, bwd, size, move == SHIFTED) : 0;
     return ring ? ring : norm_shape(a.D, size, move, a.rows, bwd).blocks;
 }
 
 template <bool BWD>
 cudaError_t launch_norm(NormArgs a, int op, int size, int move, cudaStream_t st) {
-    if (move != BY_ELEMENT && !a.strided && norm_ring_blocks(a, op, BWD, size, move == SHIFTED))
+    if (move != BY_ELEMENT && norm_ring_blocks(a, op, BWD, size, move == SHIFTED))
         return launch_norm_ring(a, op, BWD, size, move == SHIFTED, st);
     const Shape s = norm_shape(a.D, size, move, a.rows, BWD);
     a.tpr = s.tpr;

@@ -1,13 +1,14 @@
-// The norms of many contiguous rows: rows stream through shared memory (bulk copies, a
+// The norms of many rows: rows stream through shared memory (bulk copies, a
 // ring of stages), so the bytes in flight do not depend on the registers that the
 // arithmetic takes, and rows of odd widths need no aligned access of their own: a tile
 // of eight (BF16) or four (fp32) of them, or a multiple, starts on a 16-byte boundary.
 //
-// Measured on GB300 (BF16; a copy of this size runs at 6.4-6.7 TB/s): gradient of the
-// gated norm of 81,920 x 56 x 128 865-920 us (6.4-6.8 TB/s; with rows loaded straight
-// into registers 1,083, bound by the loads that 25 % of the warps can have in flight);
-// of the residual norm of 40,960 x 7,168 477 us (6.2 TB/s; 505 without the ring, 498
-// with a barrier per row); 72,896 x 281 84 us (121 in shifted pieces).
+// Measured on GB300 (BF16; a copy of this size runs at 6.4-6.8 TB/s): gradient of the
+// gated norm of 81,920 x 56 x 128 865-873 us (6.7 TB/s; with rows loaded straight into
+// registers 1,083, bound by the loads that 25 % of the warps can have in flight); of the
+// residual norm of 40,960 x 7,168 423-433 us (6.8 TB/s; 505 without the ring).  Rows of
+// 5,120 leave 3 of 8 threads idle and are bound by the latency of a row (52,428 rows,
+// forward: 408 us; a copy 317).
 #include "kda_norm_math.cuh"
 #include "kda_sm100.cuh"
 
@@ -25,9 +26,23 @@ constexpr int kRingBytes = 208 * 1024, kMaxStages = 8;
 
 struct Ring {
     int tpr, rows, arrays, stages;  // threads per row, rows per tile, arrays read
-    int array_bytes, stage_bytes;
+    int array_bytes, stage_bytes, skew;
     long long tiles;
 };
+
+// The stages, as bytes in flight in an SM.  Few are faster where the arithmetic keeps up:
+// 256 M elements of BF16 (gated norm forward, 8 x 128: 270 us with 192 KB, 233 with 96;
+// the norm alone 190 with 128 KB, 162 with 64; residual norm, 512: forward 363 with 192,
+// 350 with 96, 318 with 64; 7,168: 334 with 57, 316 with 86; its gradient, 512: 454 with
+// 144, 419 with 96; fp32, gated norm forward, 4 x 100: 254 with 154, 232 with 102).  The
+// gradient of the gated norm (404 +- 3 either way) and rows as pairs (residual norm
+// forward, 125: 403 with 64 KB, 360 with 160; backward, 33: 635 with 76, 598 with 152,
+// 663 with 203) are bound by more than the copies.
+int bytes_in_flight(int op, bool bwd, int size, bool pairs) {
+    if (pairs || (bwd && size == 2 && (op == OP_SIGMOID || op == OP_SILU))) return 160 * 1024;
+    if (bwd || size == 4 || op == OP_SIGMOID || op == OP_SILU) return 96 * 1024;
+    return op == OP_NORM ? 64 * 1024 : 88 * 1024;  // as many bytes written as read
+}
 
 // A thread holds 16 elements: 16-byte pieces (two of BF16, four of fp32), or eight pairs
 // where rows are not whole pieces (`pairs`).  A tile is one row per group of tpr
@@ -42,18 +57,29 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
     if (pairs && r.rows % (16 / size) != 0) return r;  // tiles would start anywhere
     r.tiles = (a.rows + r.rows - 1) / r.rows;
     r.arrays = 1 + (bwd ? 1 : 0);
-    if (op == OP_SIGMOID || op == OP_SILU || (op == OP_RESIDUAL && (bwd ? a.d_res : a.gate))) ++r.arrays;
+    if (op == OP_SIGMOID || op == OP_SILU || (op == OP_RESIDUAL && (bwd ? a.d_res : a.gate)))
+        ++r.arrays;
     r.array_bytes = r.rows * a.D * size;
     r.stage_bytes = r.arrays * r.array_bytes;
-    r.stages = kRingBytes / r.stage_bytes;
+    // SKEW pays where all threads have work and three arrays are read (BF16 gradients of
+    // 65,536 x 4,096: residual norm 404 us, 421 without; 37,449 x 7,168 with idle threads
+    // 438 and 398; of the norm alone, two arrays, 32,768 x 8 x 1,024: 313 and 258)
+    r.skew = size == 2 && bwd && !pairs && r.arrays == 3 && r.tpr > 32 && r.tpr * nv == pieces;
+    const int most = kRingBytes / r.stage_bytes;
+    r.stages = r.skew ? most : bytes_in_flight(op, bwd, size, pairs) / r.stage_bytes;
+    if (r.stages < 2) r.stages = 2;
+    if (r.stages > most) r.stages = most;
     if (r.stages > kMaxStages) r.stages = kMaxStages;
     return r;
 }
 
-// SKEW, for rows of more than a warp: a row's outputs come after the next row's sums,
-// so no warp waits at a barrier for its row's other warps.  The pieces are then read
-// from shared memory twice and the stage is released after the outputs.
-template <int OP, bool BWD, typename T, bool SKEW, bool PAIRS>
+// SKEW, for rows of more than a warp (it needs four stages): a row's outputs come after
+// the next row's sums, so no warp waits at a barrier for its row's other warps.  The
+// pieces are then read from shared memory twice and the stage is released after the
+// outputs.
+// APART: x's and the gate's tokens lie apart, one copy for each token's part of a tile,
+// issued by the producer's whole warp.
+template <int OP, bool BWD, typename T, bool SKEW, bool PAIRS, bool APART>
 __global__ void __launch_bounds__(kThreads, 1)
     norm_ring_kernel(const __grid_constant__ NormArgs p, const __grid_constant__ Ring r) {
     constexpr int VEC = PAIRS ? 2 : 16 / sizeof(T), NV = 16 / VEC, VP = kPairs<VEC>;
@@ -85,34 +111,54 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp >= kWarps) {  // producer
         regs_dealloc<24>();
-        if (threadIdx.x == kWork) {
-            const uint8_t *src[3] = {(const uint8_t *)p.x, nullptr, nullptr};
-            int n = 1;
-            const void *second = OP == OP_RESIDUAL && BWD ? p.d_res : p.gate;
-            if (OP != OP_NORM && second) src[n++] = (const uint8_t *)second;
-            if (BWD) src[n++] = (const uint8_t *)p.d_out;
-            int i = 0;
-            for (long long t = blockIdx.x; t < r.tiles; t += gridDim.x, ++i) {
-                const int s = i % r.stages;
-                if (!mbar_wait(empty(s), ((i / r.stages) & 1) ^ 1, abort, kWaitLimit)) break;
-                const long long row = t * r.rows, left = p.rows - row;
-                const uint32_t bytes =
-                    (uint32_t)((left < r.rows ? left : r.rows) * p.D * (long long)sizeof(T));
-                const uint32_t whole = bytes & ~15u;  // the last tile may end inside a piece
+        if (APART ? warp > kWarps : threadIdx.x != kWork) return;
+        const uint8_t *src[3] = {(const uint8_t *)p.x, nullptr, nullptr};
+        int n = 1;
+        const void *second = OP == OP_RESIDUAL && BWD ? p.d_res : p.gate;
+        if (OP != OP_NORM && second) src[n++] = (const uint8_t *)second;
+        if (BWD) src[n++] = (const uint8_t *)p.d_out;
+        const long long row_bytes = p.D * (long long)sizeof(T);
+        int i = 0;
+        for (long long t = blockIdx.x; t < r.tiles; t += gridDim.x, ++i) {
+            const int s = i % r.stages;
+            int ok = 1;
+            if (wl == 0) ok = mbar_wait(empty(s), ((i / r.stages) & 1) ^ 1, abort, kWaitLimit);
+            if (APART) ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            const long long row = t * r.rows, left = p.rows - row;
+            const long long rows = left < r.rows ? left : r.rows;
+            const uint32_t bytes = (uint32_t)(rows * row_bytes), at = sb + s * r.stage_bytes;
+            const uint32_t whole = bytes & ~15u;  // the last tile may end inside a piece
+            if (wl == 0) {
                 for (int k = 0; PAIRS && k < n && whole < bytes; ++k)
                     for (uint32_t b = whole; b < bytes; b += sizeof(T))
                         *(T *)(sm + s * r.stage_bytes + k * r.array_bytes + b) =
-                            *(const T *)(src[k] + row * p.D * (long long)sizeof(T) + b);
+                            *(const T *)(src[k] + row * row_bytes + b);
                 mbar_arrive_expect_tx(full(s), n * whole);
-                for (int k = 0; k < n && whole > 0; ++k)
-                    bulk_g2s(sb + s * r.stage_bytes + k * r.array_bytes,
-                             src[k] + row * p.D * (long long)sizeof(T), whole, full(s));
+                for (int k = APART ? 2 : 0; k < n && whole > 0; ++k)
+                    bulk_g2s(at + k * r.array_bytes, src[k] + row * row_bytes, whole, full(s));
             }
-            if (*abort) {  // let the copies in flight land before the block exits
-                volatile int never = 0;
-                for (int k = i > r.stages ? i - r.stages : 0; k < i; ++k)
-                    mbar_wait(full(k % r.stages), (k / r.stages) & 1, &never, kWaitLimit);
+            if constexpr (APART) {
+                __syncwarp();
+                const long long last = (row + rows - 1) / p.heads;
+                for (long long tok = row / p.heads + wl; tok <= last; tok += 32) {
+                    const long long first = tok * p.heads, next = first + p.heads;
+                    const long long r0 = first > row ? first : row;
+                    const long long r1 = next < row + rows ? next : row + rows;
+#pragma unroll 1  // unrolled it would spill with 24 registers
+                    for (int k = 0; k < 2; ++k) {
+                        const long long from = tok * (k ? p.gate_stride : p.x_stride);
+                        bulk_g2s(at + k * r.array_bytes + (uint32_t)((r0 - row) * row_bytes),
+                                 src[k] + from * (long long)sizeof(T) + (r0 - first) * row_bytes,
+                                 (uint32_t)((r1 - r0) * row_bytes), full(s));
+                    }
+                }
             }
+        }
+        if (wl == 0 && *abort) {  // let the copies in flight land before the block exits
+            volatile int never = 0;
+            for (int k = i > r.stages ? i - r.stages : 0; k < i; ++k)
+                mbar_wait(full(k % r.stages), (k / r.stages) & 1, &never, kWaitLimit);
         }
         return;
     }
@@ -256,9 +302,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-template <int OP, bool BWD, typename T, bool SKEW, bool PAIRS>
+template <int OP, bool BWD, typename T, bool SKEW, bool PAIRS, bool APART>
 cudaError_t launch_k(const NormArgs &a, const Ring &r, int blocks, cudaStream_t st) {
-    const auto kernel = norm_ring_kernel<OP, BWD, T, SKEW, PAIRS>;
+    const auto kernel = norm_ring_kernel<OP, BWD, T, SKEW, PAIRS, APART>;
     cudaError_t e = set_max_dynamic_smem((const void *)kernel, kRingBytes);
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, dim3(blocks), dim3(kThreads), r.stages * r.stage_bytes, st, a, r);
@@ -266,13 +312,12 @@ cudaError_t launch_k(const NormArgs &a, const Ring &r, int blocks, cudaStream_t 
 
 template <int OP, bool BWD, typename T>
 cudaError_t launch_t(const NormArgs &a, const Ring &r, bool pairs, int blocks, cudaStream_t st) {
-    // two stages are in use at a time with SKEW
-    const bool skew = r.tpr > 32 && r.stages >= 4;
-    if (pairs)
-        return skew ? launch_k<OP, BWD, T, true, true>(a, r, blocks, st)
-                    : launch_k<OP, BWD, T, false, true>(a, r, blocks, st);
-    return skew ? launch_k<OP, BWD, T, true, false>(a, r, blocks, st)
-                : launch_k<OP, BWD, T, false, false>(a, r, blocks, st);
+    if constexpr (sizeof(T) == 2 && (OP == OP_SIGMOID || OP == OP_SILU))
+        if (a.strided) return launch_k<OP, BWD, T, false, false, true>(a, r, blocks, st);
+    if constexpr (sizeof(T) == 2 && BWD && OP != OP_NORM)
+        if (r.skew) return launch_k<OP, BWD, T, true, false, false>(a, r, blocks, st);
+    return pairs ? launch_k<OP, BWD, T, false, true, false>(a, r, blocks, st)
+                 : launch_k<OP, BWD, T, false, false, false>(a, r, blocks, st);
 }
 
 template <int OP, bool BWD>
@@ -297,12 +342,30 @@ cudaError_t launch_b(const NormArgs &a, const Ring &r, int op, int size, bool pa
 
 int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
     const Ring r = ring_for(a, op, bwd, size, pairs);
+    const bool gated = op == OP_SIGMOID || op == OP_SILU;
     const int sms = device_sms();
     // fewer than a few tiles per SM: the ring would not fill, and its start costs more
+    if (!r.arrays || r.stages < 2 || r.tiles < 4ll * sms) return 0;
     // forward passes with more than a warp per row are faster as shifted pieces (fp32,
     // 20,011 x 1,001: 51 us, and 57 this way; BF16, 72,896 x 281: 81, and 57 this way)
     if (pairs && !bwd && r.tpr > 32) return 0;
-    return r.arrays && r.stages >= 2 && r.tiles >= 4ll * sms ? sms : 0;
+    // fp32 needs half as many threads for the same bytes in flight, and is often faster
+    // straight into registers (128 M elements): residual norm forward, 4,096 308 us, and
+    // 329 this way, 3,200 306 and 344; backward where all threads have work, 128 399 and
+    // 418, 4,096 414 and 447, but 8,192 451 and 419, 3,200 446 and 438, 96 463 and 432;
+    // gated norm of 4 x 128, forward 260 and 241, backward 404 and 432.
+    if (size == 4 && !pairs) {
+        const bool full = a.D == r.tpr * 16;
+        if (bwd ? full && r.tpr <= 256 : !gated && (full || r.tpr > 32)) return 0;
+    }
+    // Tokens apart: a copy moves a token, and copies of less than 2 KB are too slow (BF16
+    // forward, 160,000 x 1 x 128: 30 us without the ring, 78 this way; 40,000 x 8 x 128:
+    // 55 and 49; 20,000 x 56 x 128: 184 and 126, backward 280 and 231).  Not for fp32
+    // (backward, 10,000 x 32 x 128: 130 and 141) nor rows of more than a warp (forward,
+    // 160,000 x 1 x 1,024: 172 and 190).
+    if (a.strided && (size != 2 || !gated || r.tpr > 32 || a.heads * (long long)a.D * size < 2048))
+        return 0;
+    return sms;
 }
 
 cudaError_t launch_norm_ring(const NormArgs &a, int op, bool bwd, int size, bool pairs,

@@ -74,6 +74,10 @@ def _gated64(x, z, w, act, eps):
     (5, 1, 16384, "sigmoid", True, False),
     (2, 1, 16383, "sigmoid", True, False),
     (4000, 8, 64, "sigmoid", True, False),
+    (1500, 56, 128, "silu", True, True),
+    (50001, 1, 128, "sigmoid", True, True),
+    (20000, 3, 64, "none", True, True),
+    (9000, 5, 100, "silu", True, False),
 ])
 def test_gated_norm(dtype, T, H, D, act, weight, strided):
     g, dt = _gen(T + D), DT[dtype]
@@ -161,6 +165,11 @@ def test_norms_without_tokens():
     (64, 4096, 1.0, True, False),
     (1, 33, 1.0, False, False),
     (2049, 192, 0.5, True, True),
+    (5003, 1024, 0.5, True, True),
+    (5001, 1001, 1.0, True, True),
+    (2501, 2560, 0.5, True, False),
+    (700, 7168, 0.5, True, True),
+    (700, 8192, 1.0, False, True),
 ])
 def test_residual_norm(dtype, T, D, scale, weight, with_y):
     g, dt = _gen(T + D), DT[dtype]
