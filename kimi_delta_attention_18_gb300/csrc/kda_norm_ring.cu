@@ -6,9 +6,9 @@
 // Measured on GB300 (BF16; a copy of this size runs at 6.4-6.8 TB/s): gradient of the
 // gated norm of 81,920 x 56 x 128 865-873 us (6.7 TB/s; with rows loaded straight into
 // registers 1,083, bound by the loads that 25 % of the warps can have in flight); of the
-// residual norm of 40,960 x 7,168 423-433 us (6.8 TB/s; 505 without the ring).  Rows of
-// 5,120 leave 3 of 8 threads idle and are bound by the latency of a row (52,428 rows,
-// forward: 408 us; a copy 317).
+// residual norm of 40,960 x 7,168 423-433 us (6.8 TB/s; 505 without the ring).  A row of
+// 5,120 in a tile by itself is bound by its latency (26,214 rows, forward: 189 us, a copy
+// 159; with 512 threads instead of the 384 that it needs 209).
 #include "kda_norm_math.cuh"
 #include "kda_sm100.cuh"
 
@@ -26,6 +26,7 @@ constexpr int kRingBytes = 208 * 1024, kMaxStages = 8;
 
 struct Ring {
     int tpr, rows, arrays, stages;  // threads per row, rows per tile, arrays read
+    int work, warps, join;  // threads with a row; a row's warps, and a power of two for them
     int array_bytes, stage_bytes, skew;
     long long tiles;
 };
@@ -52,8 +53,19 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
     const int vec = pairs ? 2 : 16 / size, pieces = (a.D + vec - 1) / vec, nv = 16 / vec;
     r.tpr = 1;
     while (r.tpr * nv < pieces) r.tpr *= 2;
+    if (!pairs && r.tpr > (size == 2 ? 32 : 256)) {
+        // whole warps, and as many on each scheduler where a tile is one row (BF16 forward,
+        // 1,280: 190 -> 162 us, 5,120: 209 -> 189; not for shorter rows of fp32: more rows
+        // in a tile are more bytes in flight, backward, 2,560: 415 -> 453)
+        const int unit = r.tpr > 256 ? 128 : 32;
+        r.tpr = ((pieces + nv - 1) / nv + unit - 1) / unit * unit;
+    }
     if (pieces < nv || r.tpr > kWork) return r;  // arrays = 0: does not apply
+    r.warps = r.tpr / 32;
+    r.join = 1;
+    while (r.join < r.warps) r.join *= 2;
     r.rows = kWork / r.tpr;
+    r.work = r.rows * r.tpr;
     if (pairs && r.rows % (16 / size) != 0) return r;  // tiles would start anywhere
     r.tiles = (a.rows + r.rows - 1) / r.rows;
     r.arrays = 1 + (bwd ? 1 : 0);
@@ -61,10 +73,12 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
         ++r.arrays;
     r.array_bytes = r.rows * a.D * size;
     r.stage_bytes = r.arrays * r.array_bytes;
-    // SKEW pays where all threads have work and three arrays are read (BF16 gradients of
-    // 65,536 x 4,096: residual norm 404 us, 421 without; 37,449 x 7,168 with idle threads
-    // 438 and 398; of the norm alone, two arrays, 32,768 x 8 x 1,024: 313 and 258)
-    r.skew = size == 2 && bwd && !pairs && r.arrays == 3 && r.tpr > 32 && r.tpr * nv == pieces;
+    // SKEW pays in BF16 gradients of three arrays: gated norm (SiLU, 1,170 x 8 x 7,168) 154
+    // us, 185 without; residual norm where all threads have work on several rows (32,768 x
+    // 4,096 212 and 217; 18,724 x 7,168 231 and 208); of the norm alone, two arrays,
+    // 32,768 x 8 x 1,024 it is 313 and 258.
+    r.skew = size == 2 && bwd && !pairs && r.arrays == 3 && r.tpr > 32 &&
+             (op != OP_RESIDUAL || (a.D == r.tpr * 16 && r.work == kWork && r.rows > 1));
     const int most = kRingBytes / r.stage_bytes;
     r.stages = r.skew ? most : bytes_in_flight(op, bwd, size, pairs) / r.stage_bytes;
     if (r.stages < 2) r.stages = 2;
@@ -88,17 +102,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ __align__(128) uint8_t sm[];
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
     __shared__ __align__(8) uint64_t sum_bars[kRed][kWarps / 2];
-    __shared__ float2 red[kRed][kWarps];
+    __shared__ float2 red[kRed][2 * kWarps];  // r.join for a row, those beyond r.warps zero
     __shared__ int abort_flag;
     volatile int *abort = &abort_flag;
     const uint32_t sb = smem_addr(sm), bb = smem_addr(bars);
     auto full = [&](int s) { return bb + 8 * s; };
     auto empty = [&](int s) { return bb + 8 * (kMaxStages + s); };
     const int warp = threadIdx.x >> 5, wl = threadIdx.x & 31;
+    for (int k = threadIdx.x; k < kRed * 2 * kWarps; k += kThreads)
+        red[k / (2 * kWarps)][k % (2 * kWarps)] = make_float2(0.f, 0.f);
     if (threadIdx.x == 0) {
         for (int s = 0; s < r.stages; ++s) {
             mbar_init(full(s), 1);
-            mbar_init(empty(s), kWarps);
+            mbar_init(empty(s), r.work / 32);
         }
         if (SKEW)
             for (int k = 0; k < kRed; ++k)
@@ -164,7 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 
     regs_alloc<112>();
+    if (threadIdx.x >= r.work) return;  // beyond the tile's last row
     const int group = threadIdx.x / r.tpr, lane = threadIdx.x - group * r.tpr;
+    const int slot = group * r.join + (lane >> 5);
     auto column = [&](int i) { return (lane + i * r.tpr) * VEC; };
     auto load_w = [&](int i, f2 (&w)[VP]) {
 #pragma unroll
@@ -218,12 +236,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (BWD) se += __shfl_xor_sync(0xffffffffu, se, o);
         }
     };
-    const int nw = r.tpr >> 5;  // warps of a row
     auto row_sums = [&](int buf, float &ss, float &se) {
-        const float2 u = red[buf][group * nw + (wl & (nw - 1))];
+        const float2 u = red[buf][group * r.join + (wl & (r.join - 1))];
         ss = u.x;
         se = u.y;
-        warp_sums(ss, se, nw);
+        warp_sums(ss, se, r.join);
     };
     auto outputs = [&](long long t, float ss, float se) {
         const long long row = row_of(t);
@@ -249,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             math.sums(p, px, pg, pd, load_w, ss, se);
             warp_sums(ss, se, 32);
             if (wl == 0) {
-                red[i % kRed][warp] = make_float2(ss, se);
+                red[i % kRed][slot] = make_float2(ss, se);
                 mbar_arrive(smem_addr(&sum_bars[i % kRed][group]));
             }
         };
@@ -272,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             math.sums(p, px, pg, pd, load_w, ss, se);
             warp_sums(ss, se, r.tpr < 32 ? r.tpr : 32);
             if (r.tpr > 32) {
-                if (wl == 0) red[i % kRed][warp] = make_float2(ss, se);
+                if (wl == 0) red[i % kRed][slot] = make_float2(ss, se);
                 named_bar_sync(1 + group, r.tpr);
                 row_sums(i % kRed, ss, se);
             }
@@ -283,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (threadIdx.x == 0 && *abort) dev_fail(p.status, KDA_ERR_TIMEOUT);
     if (!BWD || !p.partial) return;
     // dw: the block's groups in group order, in the ring (every copy has been used)
-    named_bar_sync(15, kWork);
+    named_bar_sync(15, r.work);
     if (*abort) return;
     float *sh = (float *)sm;
 #pragma unroll
@@ -294,8 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < VEC; ++j)
             if (column(k) + j < p.D) sh[group * p.D + column(k) + j] = v[j];
     }
-    named_bar_sync(15, kWork);
-    for (int c = threadIdx.x; c < p.D; c += kWork) {
+    named_bar_sync(15, r.work);
+    for (int c = threadIdx.x; c < p.D; c += r.work) {
         float s = 0.f;
         for (int g = 0; g < r.rows; ++g) s += sh[g * p.D + c];
         p.partial[(size_t)blockIdx.x * p.D + c] = s;
@@ -352,11 +369,14 @@ int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size, bool pairs) 
     // fp32 needs half as many threads for the same bytes in flight, and is often faster
     // straight into registers (128 M elements): residual norm forward, 4,096 308 us, and
     // 329 this way, 3,200 306 and 344; backward where all threads have work, 128 399 and
-    // 418, 4,096 414 and 447, but 8,192 451 and 419, 3,200 446 and 438, 96 463 and 432;
-    // gated norm of 4 x 128, forward 260 and 241, backward 404 and 432.
+    // 418, 4,096 414 and 447, but 8,192 451 and 419, 2,560 480 and 455, 96 463 and 432;
+    // gated norm of 4 x 128, forward 260 and 241, backward with a sigmoid 404 and 432, of
+    // 8 x 1,024 with SiLU 460 and 453.
     if (size == 4 && !pairs) {
         const bool full = a.D == r.tpr * 16;
-        if (bwd ? full && r.tpr <= 256 : !gated && (full || r.tpr > 32)) return 0;
+        if (bwd ? full && r.work == kWork && r.tpr <= 256 && op != OP_SILU
+                : !gated && (full || r.tpr > 32))
+            return 0;
     }
     // Tokens apart: a copy moves a token, and copies of less than 2 KB are too slow (BF16
     // forward, 160,000 x 1 x 128: 30 us without the ring, 78 this way; 40,000 x 8 x 128:
