@@ -358,6 +358,28 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
     if (threadIdx.x == 0) *mean = flat[0].y > 0.f ? flat[0].x / flat[0].y : 0.f;  // none counts: 0
 }
 
+// The eight BF16 values from element e of p (a 16-byte base, n elements).
+__device__ __forceinline__ uint4 eight_from(const __nv_bfloat16 *p, long long e, long long n) {
+    uint32_t v[8] = {};
+    const long long a = e & ~7ll;
+    if (a + 16 <= n) {
+        *(uint4 *)v = *(const uint4 *)(p + a);
+        *(uint4 *)(v + 4) = *(const uint4 *)(p + a + 8);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (a + j < n) v[j / 2] |= (uint32_t)((const uint16_t *)p)[a + j] << (16 * (j & 1));
+    }
+    const int by = (int)(e & 7);
+#pragma unroll
+    for (int k = 0; k < 6; ++k) v[k] = by & 4 ? v[k + 2] : v[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) v[k] = by & 2 ? v[k + 1] : v[k];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = by & 1 ? __funnelshift_r(v[k], v[k + 1], 16) : v[k];
+    return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
 // Rows of x and, if w_rows, of W as `planes` BF16 terms with a pitch of whole 128-byte
 // lines (zeros past the width): fp32 operands, and BF16 rows whose width is no multiple
 // of the 16 bytes that a tensor map needs.  With targets, rows of x whose target is
@@ -379,6 +401,20 @@ __global__ void __launch_bounds__(256)
         const T *src = second ? w : x;
         __nv_bfloat16 *dst = second ? wp : xp;
         const long long rows = second ? w_rows : x_rows;
+        if constexpr (sizeof(T) == 2) {
+            uint4 u = make_uint4(0, 0, 0, 0);
+            if (c < D && !(!second && y.ids && y.at(r, false) < 0)) {
+                u = eight_from(src, r * D + c, rows * D);
+                uint32_t *word = &u.x;
+                if (D - c < 8) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        word[k] &= D - c >= 2 * k + 2 ? 0xffffffffu : D - c > 2 * k ? 0xffffu : 0u;
+                }
+            }
+            *(uint4 *)(dst + r * pitch + c) = u;
+            continue;
+        }
         float v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[j] = c + j < D ? act_ld(src, (size_t)(r * D + c + j)) : 0.f;
@@ -434,9 +470,16 @@ int piece_cols(const kda_ce_desc_t *d, int planes) {
 
 struct Layout {
     bool f32, w32, pack_x, pack_w;
-    int planes, pairs, chunk, x_pitch, w_pitch, piece, pieces, dx_splits;
-    size_t xp, wp, part, zy, sums, dz, acc, total;
+    int planes, pairs, chunk, x_pitch, w_pitch, piece, pieces, dx_splits, dw_splits;
+    size_t xp, wp, part, zy, sums, dz, acc, dw_acc, total;
 };
+
+// In how many parts a contraction of k_blocks is taken so that every SM has a share;
+// each has at least four steps.
+int splits_for(int tiles, int k_blocks) {
+    const int n = device_sms(), most = k_blocks / 4, want = n / tiles;
+    return want <= 1 || most <= 1 ? 1 : want < most ? want : most;
+}
 
 // Pieces of the workspace.
 Layout layout_for(const kda_ce_desc_t *d, bool backward) {
@@ -467,18 +510,15 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
         l.piece = piece_cols(d, l.planes);
         l.pieces = cdiv(V, l.piece);
         l.dz = round256(T * l.piece * l.planes * 2);
-        // dx has few tiles when T and D are small: its contraction over the
-        // vocabulary is then split so that every SM has a share
-        const int tiles = cdiv(T, BM) * cdiv(D, l.w32 ? kW32Cols : BN), n = device_sms();
-        l.dx_splits = 1;
-        if (l.pieces == 1 && tiles > 0 && tiles < n) {
-            l.dx_splits = n / tiles;
-            const int most = l.piece / BK / 4;  // at least four steps each
-            if (l.dx_splits > most) l.dx_splits = most < 1 ? 1 : most;
-        }
+        // dx has few tiles when T and D are small, d_weight when V and D are (fp32, 3,200 x
+        // 116,608 x 120: 670 us for a piece's part of dx on the 26 SMs of its tiles)
+        const int last = (int)V - (l.pieces - 1) * l.piece;
+        l.dx_splits = splits_for(cdiv(T, BM) * cdiv(D, l.w32 ? kW32Cols : BN), last / BK);
+        l.dw_splits = splits_for(cdiv(l.piece, BM) * cdiv(D, BN), cdiv(T, BK));
         if (l.pieces > 1 || l.dx_splits > 1) l.acc = round256((size_t)l.dx_splits * T * D * 4);
+        if (l.dw_splits > 1) l.dw_acc = round256((size_t)l.dw_splits * l.piece * D * 4);
     }
-    l.total = l.xp + l.wp + l.part + l.zy + l.sums + l.dz + l.acc;
+    l.total = l.xp + l.wp + l.part + l.zy + l.sums + l.dz + l.acc + l.dw_acc;
     return l;
 }
 
@@ -553,6 +593,18 @@ cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap
     return use_pairs(p, n) ? start_gemm<EPI, A_MN, B_MN, FINE, 2>(p, ta, tb, n, st)
                            : start_gemm<EPI, A_MN, B_MN, FINE, 1>(p, ta, tb, n, st);
 }
+
+// dst = the sum of `splits` parts of n values.
+cudaError_t sum_splits(const float *acc, void *dst, long long n, int splits, bool bf16,
+                       cudaStream_t st) {
+    const long long need = (n + 255) / 256, most = 16ll * device_sms();
+    const dim3 grid((unsigned)(need < most ? need : most));
+    return bf16 ? launch_dependent(split_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0, st, acc,
+                                   (__nv_bfloat16 *)dst, n, splits)
+                : launch_dependent(split_sum_kernel<float>, grid, dim3(256), 0, st, acc,
+                                   (float *)dst, n, splits);
+}
+
 // Copies x and W where the layout wants them; xp, wp are what the products read.
 cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *x, const void *w,
                      const Targets &y, uint8_t *ws, const void *&xp, const void *&wp,
@@ -676,7 +728,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         return KDA_ERR_WORKSPACE;
     uint8_t *ws = (uint8_t *)workspace;
     __nv_bfloat16 *dz = (__nv_bfloat16 *)(ws + l.xp + l.wp);
-    float *acc = (float *)(ws + l.xp + l.wp + l.dz);
+    float *acc = (float *)(ws + l.xp + l.wp + l.dz), *dw_acc = acc + l.acc / 4;
     const void *xp, *wp;
     const Targets y = {targets, desc->id_dtype == KDA_ID_I64, desc->vocab, desc->ignore_index,
                        dev_status};
@@ -736,32 +788,29 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
                  : l.f32 ? run_gemm<EPI_OUT, false, true, true>(q, zk, wm, st)
                          : run_gemm<EPI_OUT, false, true, false>(q, zk, wm, st)) != cudaSuccess)
                 return KDA_ERR_CUDA;
-            if (l.dx_splits > 1) {
-                const long long n = (long long)T * D, need = (n + 255) / 256, most = 16ll * device_sms();
-                const dim3 grid((unsigned)(need < most ? need : most));
-                const cudaError_t e =
-                    size == 2 ? launch_dependent(split_sum_kernel<__nv_bfloat16>, grid, dim3(256), 0,
-                                                 st, (const float *)acc, (__nv_bfloat16 *)dx, n,
-                                                 l.dx_splits)
-                              : launch_dependent(split_sum_kernel<float>, grid, dim3(256), 0, st,
-                                                 (const float *)acc, (float *)dx, n, l.dx_splits);
-                if (e != cudaSuccess) return KDA_ERR_CUDA;
-            }
+            if (l.dx_splits > 1 && k == l.pieces - 1 &&
+                sum_splits(acc, dx, (long long)T * D, l.dx_splits, size == 2, st) != cudaSuccess)
+                return KDA_ERR_CUDA;
         }
         if (d_weight) {
             GemmArgs q = {};
             q.status = dev_status;
             q.pairs = l.pairs;
             q.chunk = l.chunk;
-            q.splits = 1;
+            q.splits = l.dw_splits;
             q.M = cols;
             q.N = D;
             q.k_blocks = cdiv(T, BK);
-            q.out = (uint8_t *)d_weight + (size_t)v0 * D * size;
+            void *to = (uint8_t *)d_weight + (size_t)v0 * D * size;
+            if (l.dw_splits > 1) q.acc_out = dw_acc;
+            else q.out = to;
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)d_weight & 15u) == 0;
             if ((l.f32 ? run_gemm<EPI_OUT, true, true, true>(q, zm, xm, st)
                        : run_gemm<EPI_OUT, true, true, false>(q, zm, xm, st)) != cudaSuccess)
+                return KDA_ERR_CUDA;
+            if (l.dw_splits > 1 && sum_splits(dw_acc, to, (long long)cols * D, l.dw_splits,
+                                              size == 2, st) != cudaSuccess)
                 return KDA_ERR_CUDA;
         }
     }

@@ -52,7 +52,7 @@ struct GemmArgs {
     const float *lse, *d_loss;
     __nv_bfloat16 *dz;         // [planes][M][pitch]
     int pitch, planes;
-    // EPI_OUT: value (+ acc_in) to acc_out [splits][M][N] fp32, or to out
+    // EPI_OUT: value (+ acc_in) to acc_out, both [splits][M][N] fp32, or to out
     const float *acc_in;
     float *acc_out;
     void *out;
@@ -196,6 +196,26 @@ struct Row {
         __syncwarp();
     }
 
+    // The same to rows of any width, n of the 64 columns: words aligned in memory, and a
+    // row's odd ends by themselves (107 x 58,219 x 6,404: d_weight 819 us column by column)
+    __device__ __forceinline__ void ragged(const GemmArgs &p, const Turn &turn, __nv_bfloat16 *base,
+                                           size_t pitch, int n) {
+        __syncwarp();
+        const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32), l = turn.lane;
+#pragma unroll 4
+        for (int r = 0; r < rows; ++r) {
+            const uint32_t w = __float_as_uint(turn.word(r));
+            const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
+            __nv_bfloat16 *to = base + (size_t)(row0 + r) * pitch;
+            const int odd = ((uintptr_t)to >> 1) & 1, c = 2 * l + odd;
+            const uint32_t v = odd ? __funnelshift_r(w, next, 16) : w;
+            if (c + 1 < n) *(uint32_t *)(to + c) = v;
+            else if (c < n) *(uint16_t *)(to + c) = (uint16_t)v;
+            if (odd && l == 0) *(uint16_t *)to = (uint16_t)w;
+        }
+        __syncwarp();
+    }
+
     // v -> d_loss (softmax - onehot) for columns c .. c + 31
     __device__ __forceinline__ void dz_of(const GemmArgs &p, int c, float (&v)[32]) {
 #pragma unroll
@@ -242,7 +262,9 @@ struct Row {
                                    __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
         __syncwarp();
         const bool narrow = p.out && p.out_bf16;
-        float *o32 = p.out ? (float *)p.out : p.acc_out + (size_t)t.split * p.M * p.N;
+        const size_t part = (size_t)t.split * p.M * p.N;
+        float *o32 = p.out ? (float *)p.out : p.acc_out + part;
+        const float *in = p.acc_in ? p.acc_in + part : nullptr;
         __nv_bfloat16 *o16 = (__nv_bfloat16 *)p.out;
         if (p.vec) {  // widths and bases of whole pieces: four columns are in or out together
             const int col = c + 4 * (turn.lane & 7);
@@ -254,8 +276,8 @@ struct Row {
                 const size_t at = (size_t)r * p.N + col;
                 float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
                                        __uint_as_float(u.z), __uint_as_float(u.w));
-                if (p.acc_in) {
-                    const float4 a = *(const float4 *)(p.acc_in + at);
+                if (in) {
+                    const float4 a = *(const float4 *)(in + at);
                     f = make_float4(f.x + a.x, f.y + a.y, f.z + a.z, f.w + a.w);
                 }
                 if (narrow)
@@ -270,7 +292,7 @@ struct Row {
                 float f = turn.word(r);
                 if (c + turn.lane >= p.N) continue;
                 const size_t at = (size_t)(row0 + r) * p.N + c + turn.lane;
-                if (p.acc_in) f += p.acc_in[at];
+                if (in) f += in[at];
                 if (narrow) o16[at] = __float2bfloat16_rn(f);
                 else o32[at] = f;
             }
@@ -297,6 +319,11 @@ struct Row {
             put_bf16<false>(turn, 0, a);
             put_bf16<false>(turn, 1, b);
             lines(p, turn, (__nv_bfloat16 *)p.out + c, p.N);
+        } else if (p.out && p.out_bf16 && !p.acc_in && !p.vec) {
+            if (c >= p.N) return;
+            put_bf16<false>(turn, 0, a);
+            put_bf16<false>(turn, 1, b);
+            ragged(p, turn, (__nv_bfloat16 *)p.out + c, p.N, p.N - c < 64 ? p.N - c : 64);
         } else {
             if (c < p.N) out32(p, t, turn, c, a);
             if (c + 32 < p.N) out32(p, t, turn, c + 32, b);

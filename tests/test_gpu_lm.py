@@ -327,6 +327,11 @@ def _check_ce(dtype, x, w, y, d_loss, ignore=-100, piece=0):
     (77, 5003, 100, 0),
     (1000, 700, 1024, 256),
     (2500, 4000, 256, 0),
+    (300, 20011, 120, 4096),
+    (70, 9000, 643, 4096),
+    (6000, 50, 102, 0),
+    (3001, 300, 77, 256),
+    (513, 1537, 1001, 0),
 ])
 def test_cross_entropy(dtype, T, V, D, piece):
     g, dt = _gen(T + V + D), DT[dtype]
