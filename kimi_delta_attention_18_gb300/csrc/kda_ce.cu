@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int w = w0; w < work && ok; w += wstep) {
             const Tile t = tile_at<CTAS>(p, w);
-            Row<EPI> r;
+            Row<EPI, !FINE> r;
             r.begin(p, t, (t.m * CTAS + rank) * BM + 32 * quarter, lane, half, 128);
             __syncwarp();
             if constexpr (FINE) {
@@ -474,11 +474,24 @@ struct Layout {
     size_t xp, wp, part, zy, sums, dz, acc, dw_acc, total;
 };
 
-// In how many parts a contraction of k_blocks is taken so that every SM has a share;
-// each has at least four steps.
-int splits_for(int tiles, int k_blocks) {
-    const int n = device_sms(), most = k_blocks / 4, want = n / tiles;
-    return want <= 1 || most <= 1 ? 1 : want < most ? want : most;
+// In how many parts the contraction of an M x N product is taken so that its tiles fill
+// the rounds over the SMs: a stage of a tile is about a third of a microsecond, and the
+// parts are written and read once more (fp32, 1,000 x 58,219 x 2,502: dx has 80 tiles).
+int splits_for(long long M, int N, int cols, int k_blocks, int pairs) {
+    const int n = device_sms();
+    const long long tiles = (long long)cdiv(M, BM) * cdiv(N, cols);
+    int best = 1;
+    double least = 0.;
+    for (int s = 1; s == 1 || (s <= k_blocks / 4 && tiles * s <= 12ll * n); ++s) {
+        const double stages = (double)cdiv(k_blocks, s) * pairs;
+        double us = (double)cdiv(tiles * s, n) * (stages / 3. + 1.);
+        if (s > 1) us += 5. + (double)s * M * N * 8. / 6.5e6;
+        if (s == 1 || us < 0.97 * least) {
+            best = s;
+            least = us;
+        }
+    }
+    return best;
 }
 
 // Pieces of the workspace.
@@ -510,11 +523,10 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
         l.piece = piece_cols(d, l.planes);
         l.pieces = cdiv(V, l.piece);
         l.dz = round256(T * l.piece * l.planes * 2);
-        // dx has few tiles when T and D are small, d_weight when V and D are (fp32, 3,200 x
-        // 116,608 x 120: 670 us for a piece's part of dx on the 26 SMs of its tiles)
+        // dx has few tiles when T and D are small, d_weight when V and D are
         const int last = (int)V - (l.pieces - 1) * l.piece;
-        l.dx_splits = splits_for(cdiv(T, BM) * cdiv(D, l.w32 ? kW32Cols : BN), last / BK);
-        l.dw_splits = splits_for(cdiv(l.piece, BM) * cdiv(D, BN), cdiv(T, BK));
+        l.dx_splits = splits_for(T, D, l.w32 ? kW32Cols : BN, last / BK, l.pairs);
+        l.dw_splits = splits_for(l.piece, D, BN, cdiv(T, BK), l.pairs);
         if (l.pieces > 1 || l.dx_splits > 1) l.acc = round256((size_t)l.dx_splits * T * D * 4);
         if (l.dw_splits > 1) l.dw_acc = round256((size_t)l.dw_splits * l.piece * D * 4);
     }

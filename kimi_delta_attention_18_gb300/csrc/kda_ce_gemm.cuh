@@ -135,9 +135,11 @@ struct Turn {
     }
 };
 
+constexpr int kBatch = 8;  // rows whose words are read before any is stored
+
 // One thread's part of the epilogue: a row and up to 128 of the tile's columns, taken
-// 32 at a time.
-template <int EPI>
+// 32 at a time.  BF16: the product may be stored so.
+template <int EPI, bool BF16>
 struct Row {
     int row0;       // the warp's first row
     long long row;  // this thread's
@@ -202,16 +204,22 @@ struct Row {
                                            size_t pitch, int n) {
         __syncwarp();
         const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32), l = turn.lane;
-#pragma unroll 4
-        for (int r = 0; r < rows; ++r) {
-            const uint32_t w = __float_as_uint(turn.word(r));
-            const uint32_t next = __shfl_down_sync(0xffffffffu, w, 1);
-            __nv_bfloat16 *to = base + (size_t)(row0 + r) * pitch;
-            const int odd = ((uintptr_t)to >> 1) & 1, c = 2 * l + odd;
-            const uint32_t v = odd ? __funnelshift_r(w, next, 16) : w;
-            if (c + 1 < n) *(uint32_t *)(to + c) = v;
-            else if (c < n) *(uint16_t *)(to + c) = (uint16_t)v;
-            if (odd && l == 0) *(uint16_t *)to = (uint16_t)w;
+        for (int r0 = 0; r0 < rows; r0 += kBatch) {
+            uint32_t w[kBatch], next[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) w[k] = __float_as_uint(turn.word(r0 + k));
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) next[k] = __shfl_down_sync(0xffffffffu, w[k], 1);
+            __nv_bfloat16 *to = base + (size_t)(row0 + r0) * pitch;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k, to += pitch) {
+                if (r0 + k >= rows) break;
+                const int odd = ((uintptr_t)to >> 1) & 1, c = 2 * l + odd;
+                const uint32_t v = odd ? __funnelshift_r(w[k], next[k], 16) : w[k];
+                if (c + 1 < n) *(uint32_t *)(to + c) = v;
+                if (c + 1 == n) *(uint16_t *)(to + c) = (uint16_t)v;
+                if (odd && l == 0) *(uint16_t *)to = (uint16_t)w[k];
+            }
         }
         __syncwarp();
     }
@@ -261,7 +269,7 @@ struct Row {
             turn.put(i, make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
                                    __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
         __syncwarp();
-        const bool narrow = p.out && p.out_bf16;
+        const bool narrow = BF16 && p.out && p.out_bf16;
         const size_t part = (size_t)t.split * p.M * p.N;
         float *o32 = p.out ? (float *)p.out : p.acc_out + part;
         const float *in = p.acc_in ? p.acc_in + part : nullptr;
@@ -315,11 +323,11 @@ struct Row {
                 put_bf16<true>(turn, 1, b);
                 lines(p, turn, p.dz + (size_t)pl * p.M * p.pitch + c, p.pitch);
             }
-        } else if (p.out && p.out_bf16 && !p.acc_in && p.vec && c + 64 <= p.N) {
+        } else if (BF16 && p.out && p.out_bf16 && !p.acc_in && p.vec && c + 64 <= p.N) {
             put_bf16<false>(turn, 0, a);
             put_bf16<false>(turn, 1, b);
             lines(p, turn, (__nv_bfloat16 *)p.out + c, p.N);
-        } else if (p.out && p.out_bf16 && !p.acc_in && !p.vec) {
+        } else if (BF16 && p.out && p.out_bf16 && !p.acc_in && !p.vec) {
             if (c >= p.N) return;
             put_bf16<false>(turn, 0, a);
             put_bf16<false>(turn, 1, b);

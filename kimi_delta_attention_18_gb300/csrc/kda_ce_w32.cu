@@ -240,7 +240,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
         bool ok = true;
         for (int w = blockIdx.x; w < work && ok; w += gridDim.x) {
             const Tile t = tile_at<1>(p, w);
-            Row<EPI> r;
+            Row<EPI, false> r;
             r.begin(p, t, t.m * BM + 32 * quarter, lane, half, 64);
             __syncwarp();
             float acc[2][32];
