@@ -279,20 +279,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the row statistics: 8 rows per block and 128 slices of the partial sums, each
-// slice in order, then the slices pairwise.  Writes lse and the loss (0 where the
-// target is ignored), and the mean over the others: per block (sum, count), added up
-// in block order by the block that finishes last.
-constexpr int kJoinRows = 8, kJoinSlices = 128;
-__global__ void __launch_bounds__(kJoinRows * kJoinSlices)
+// Joins the row statistics: ROWS rows per block, the partial sums in as many slices as
+// its 1,024 threads allow, each slice in order, then the slices pairwise.  Writes lse and
+// the loss (0 where the target is ignored), and the mean over the others: per block (sum,
+// count), added up in block order by the block that finishes last.
+constexpr int kJoinThreads = 1024, kJoinFew = 8, kJoinMany = 32;
+template <int ROWS>
+__global__ void __launch_bounds__(kJoinThreads)
     ce_join_kernel(const float2 *part, int parts, int M, Targets y, const float *z_y, float *loss,
                    float *lse, float *mean, float2 *sums, unsigned *ticket) {
-    __shared__ float2 sh[kJoinSlices][kJoinRows + 1];
+    constexpr int kSlices = kJoinThreads / ROWS;
+    __shared__ float2 sh[kSlices][ROWS + 1];
     __shared__ bool last;
     griddep_wait();
     griddep_launch_dependents();
-    const int r = threadIdx.x % kJoinRows, sl = threadIdx.x / kJoinRows, lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * kJoinRows + r;
+    const int r = threadIdx.x % ROWS, sl = threadIdx.x / ROWS, lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * ROWS + r;
     auto join = [](float2 a, float2 b) {
         const float m = fmaxf(a.x, b.x);
         if (m == -INFINITY) return make_float2(m, a.y + b.y);
@@ -301,11 +303,11 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
     float2 v = make_float2(-INFINITY, 0.f);
     if (row < M) {
 #pragma unroll 8
-        for (int q = sl; q < parts; q += kJoinSlices) v = join(v, part[(size_t)q * M + row]);
+        for (int q = sl; q < parts; q += kSlices) v = join(v, part[(size_t)q * M + row]);
     }
     sh[sl][r] = v;
     __syncthreads();
-    for (int o = kJoinSlices / 2; o > 0; o >>= 1) {
+    for (int o = kSlices / 2; o > 0; o >>= 1) {
         if (sl < o) sh[sl][r] = join(sh[sl][r], sh[sl + o][r]);
         __syncthreads();
     }
@@ -323,7 +325,7 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
         }
         if (mean) {
 #pragma unroll
-            for (int o = kJoinRows / 2; o > 0; o >>= 1) {
+            for (int o = ROWS / 2; o > 0; o >>= 1) {
                 l += __shfl_xor_sync(0xffffffffu, l, o);
                 n += __shfl_xor_sync(0xffffffffu, n, o);
             }
@@ -339,16 +341,16 @@ __global__ void __launch_bounds__(kJoinRows * kJoinSlices)
     if (!last) return;
     __threadfence();
     float2 s = make_float2(0.f, 0.f);
-    for (int b = threadIdx.x; b < (int)gridDim.x; b += kJoinRows * kJoinSlices) {
+    for (int b = threadIdx.x; b < (int)gridDim.x; b += kJoinThreads) {
         const float2 u = __ldcg(&sums[b]);
         s.x += u.x;
         s.y += u.y;
     }
-    float2 *flat = &sh[0][0];  // kJoinSlices (kJoinRows + 1) entries
+    float2 *flat = &sh[0][0];  // kSlices (ROWS + 1) entries
     __syncthreads();
     flat[threadIdx.x] = s;
     __syncthreads();
-    for (int o = kJoinRows * kJoinSlices / 2; o > 0; o >>= 1) {
+    for (int o = kJoinThreads / 2; o > 0; o >>= 1) {
         if (threadIdx.x < o) {
             flat[threadIdx.x].x += flat[threadIdx.x + o].x;
             flat[threadIdx.x].y += flat[threadIdx.x + o].y;
@@ -518,7 +520,7 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
     if (!backward) {
         l.part = round256((size_t)2 * cdiv(V, l.w32 ? kW32Cols : BN) * T * sizeof(float2));
         l.zy = round256(T * 4);
-        l.sums = round256((T / kJoinRows + 1) * sizeof(float2)) + 256;
+        l.sums = round256((T / kJoinFew + 1) * sizeof(float2)) + 256;
     } else {
         l.piece = piece_cols(d, l.planes);
         l.pieces = cdiv(V, l.piece);
@@ -707,9 +709,13 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
         e = run_gemm<EPI_STATS, false, false, true>(p, ta, tb, st);
     }
     if (e != cudaSuccess) return KDA_ERR_CUDA;
-    if (launch_dependent(ce_join_kernel, dim3(cdiv(p.M, kJoinRows)), dim3(kJoinRows * kJoinSlices), 0, st,
-                         (const float2 *)part, 2 * cdiv(p.N, tile_cols), p.M, p.y, (const float *)zy, loss, lse,
-                         mean, sums, ticket) != cudaSuccess)
+    // 8 rows to a block while all blocks are resident (8 rows and 32: 1,024 x 131,072 9.0
+    // us and 13.6; 4,992 x 36,995 19.1 and 10.7; 8,128 x 277 18.2 and 7.8)
+    const bool many = cdiv(p.M, kJoinFew) > 2 * device_sms();
+    if (launch_dependent(many ? ce_join_kernel<kJoinMany> : ce_join_kernel<kJoinFew>,
+                         dim3(cdiv(p.M, many ? kJoinMany : kJoinFew)), dim3(kJoinThreads), 0, st,
+                         (const float2 *)part, 2 * cdiv(p.N, tile_cols), p.M, p.y,
+                         (const float *)zy, loss, lse, mean, sums, ticket) != cudaSuccess)
         return KDA_ERR_CUDA;
     return KDA_OK;
 }
