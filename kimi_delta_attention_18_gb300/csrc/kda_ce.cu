@@ -528,7 +528,10 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
         // dx has few tiles when T and D are small, d_weight when V and D are
         const int last = (int)V - (l.pieces - 1) * l.piece;
         l.dx_splits = splits_for(T, D, l.w32 ? kW32Cols : BN, last / BK, l.pairs);
-        l.dw_splits = splits_for(l.piece, D, BN, cdiv(T, BK), l.pairs);
+        // (not where the caller bounds the workspace with pieces: d_weight's parts would
+        // outgrow a small piece's dz)
+        l.dw_splits = d->piece > 0 && l.pieces > 1
+                          ? 1 : splits_for(l.piece, D, BN, cdiv(T, BK), l.pairs);
         if (l.pieces > 1 || l.dx_splits > 1) l.acc = round256((size_t)l.dx_splits * T * D * 4);
         if (l.dw_splits > 1) l.dw_acc = round256((size_t)l.dw_splits * l.piece * D * 4);
     }
