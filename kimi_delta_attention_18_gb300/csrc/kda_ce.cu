@@ -20,7 +20,7 @@
 // its 6 T V D, in a loop under the power cap (cuBLAS sustains 1.73 there; each product
 // alone takes 1.14-1.17 ms per 32,768 columns, 1.89-1.93 PFLOP/s); losses of 256 x
 // 131,072 x 7,168 325 us (5.8 TB/s of W, 1.48 PFLOP/s: near both bounds); fp32 gradient
-// of 777 x 10,007 x 515 208 us.
+// of 777 x 10,007 x 515 203 us.
 #include <math.h>
 
 #include "kda_ce_gemm.cuh"
@@ -509,8 +509,9 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
     l.planes = l.f32 ? 3 : 1;
     l.pairs = l.f32 ? 6 : 1;
     l.chunk = l.f32 ? kChunkF32 : kChunkBf16;
-    // Copies: x in a backward pass (ignored rows become zeros); whole 128-byte lines where x and W are copied as BF16 (with rows of 1,040
-    // bytes the copies of 128-byte boxes ran at half the rate)
+    // Copies: x in a backward pass (ignored rows become zeros); whole 128-byte lines where
+    // x and W are copied as BF16 (with rows of 1,040 bytes the copies of 128-byte boxes ran
+    // at half the rate)
     l.pack_x = l.f32 || D % 8 != 0 || backward;
     l.pack_w = l.f32 ? !l.w32 : D % 8 != 0;
     l.x_pitch = l.pack_x ? (D + 63) / 64 * 64 : D;

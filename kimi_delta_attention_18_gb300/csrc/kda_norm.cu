@@ -15,7 +15,8 @@
 // row needs are one reduction (sum e n = r sum e x needs no r first) and nothing
 // is read twice.  dw is summed per thread in fp32 over the block's rows, then per
 // block in shared memory, then by a second kernel over the blocks in block order:
-// no atomics, the same result every time.  Many contiguous rows take kda_norm_ring.cu.
+// no atomics, the same result every time.  Many rows take kda_norm_ring.cu, but for fp32
+// ones that fill their threads.
 //
 // Measured on GB300: decode's 256 x 56 x 128 BF16 gate 3.6 us and 256 x 7,168 residual
 // norm 5.7 us (a launch and one round of loads; their bytes are 1.6 and 2.2 us); fp32,
