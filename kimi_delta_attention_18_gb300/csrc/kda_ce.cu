@@ -480,15 +480,21 @@ struct Layout {
 // the rounds over the SMs: a stage of a tile is about a third of a microsecond, and the
 // parts are written and read once more (fp32, 1,000 x 58,219 x 2,502: dx has 80 tiles).
 int splits_for(long long M, int N, int cols, int k_blocks, int pairs) {
-    const int n = device_sms();
+    const int n = device_sms(), most = k_blocks / 4;  // at least four steps each
     const long long tiles = (long long)cdiv(M, BM) * cdiv(N, cols);
-    int best = 1;
-    double least = 0.;
-    for (int s = 1; s == 1 || (s <= k_blocks / 4 && tiles * s <= 12ll * n); ++s) {
+    auto microseconds = [&](int s) {
         const double stages = (double)cdiv(k_blocks, s) * pairs;
-        double us = (double)cdiv(tiles * s, n) * (stages / 3. + 1.);
-        if (s > 1) us += 5. + (double)s * M * N * 8. / 6.5e6;
-        if (s == 1 || us < 0.97 * least) {
+        const double parts = s > 1 ? 5. + (double)s * M * N * 8. / 6.5e6 : 0.;
+        return cdiv(tiles * s, n) * (stages / 3. + 1.) + parts;
+    };
+    int best = 1;
+    double least = microseconds(1);
+    for (int rounds = 1; rounds <= 12; ++rounds) {  // as many parts as fit in them
+        const long long fit = (long long)rounds * n / tiles;
+        const int s = (int)(fit < most ? fit : most);
+        if (s < 2 || s == best) continue;
+        const double us = microseconds(s);
+        if (us < 0.97 * least) {
             best = s;
             least = us;
         }
