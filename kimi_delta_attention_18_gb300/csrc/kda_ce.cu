@@ -21,6 +21,7 @@
 // alone takes 1.14-1.17 ms per 32,768 columns, 1.89-1.93 PFLOP/s); losses of 256 x
 // 131,072 x 7,168 325 us (5.8 TB/s of W, 1.48 PFLOP/s: near both bounds); fp32 gradient
 // of 777 x 10,007 x 515 203 us.
+#include <float.h>
 #include <math.h>
 
 #include "kda_ce_gemm.cuh"
@@ -386,16 +387,37 @@ __device__ __forceinline__ uint4 eight_from(const __nv_bfloat16 *p, long long e,
 // lines (zeros past the width): fp32 operands, and BF16 rows whose width is no multiple
 // of the 16 bytes that a tensor map needs.  With targets, rows of x whose target is
 // ignored become zeros: dW is a sum over all rows, and what a padded position holds
-// (NaN perhaps) has no part in it.
+// (NaN perhaps) has no part in it.  With d_loss the first block only finds the
+// largest of its magnitudes that counts (1 if none does).
 template <typename T>
 __global__ void __launch_bounds__(256)
     pack_kernel(const T *x, long long x_rows, __nv_bfloat16 *xp, const T *w, long long w_rows,
-                __nv_bfloat16 *wp, int D, int pitch, int planes, Targets y) {
+                __nv_bfloat16 *wp, int D, int pitch, int planes, Targets y, const float *d_loss,
+                float *unit) {
     griddep_wait();
     griddep_launch_dependents();
+    if (d_loss && blockIdx.x == 0) {
+        __shared__ float sh[8];
+        float m = 0.f;
+#pragma unroll 4
+        for (long long r = threadIdx.x; r < x_rows; r += 256) {
+            const float g = fabsf(d_loss[r]);
+            m = g <= FLT_MAX && y.at(r, false) >= 0 ? fmaxf(m, g) : m;
+        }
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        if (threadIdx.x % 32 == 0) sh[threadIdx.x / 32] = m;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int k = 1; k < 8; ++k) m = fmaxf(m, sh[k]);
+            *unit = m >= FLT_MIN ? m : 1.f;
+        }
+        return;
+    }
+    const int first = d_loss ? 1 : 0;  // the block that copies first
     const int pieces = pitch / 8;
     const long long total = (x_rows + w_rows) * pieces;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const long long step = (gridDim.x - first) * 256ll;
+    for (long long i = (blockIdx.x - first) * 256ll + threadIdx.x; i < total; i += step) {
         long long r = i / pieces;
         const int c = (int)(i - r * pieces) * 8;
         const bool second = r >= x_rows;
@@ -473,7 +495,7 @@ int piece_cols(const kda_ce_desc_t *d, int planes) {
 struct Layout {
     bool f32, w32, pack_x, pack_w;
     int planes, pairs, chunk, x_pitch, w_pitch, piece, pieces, dx_splits, dw_splits;
-    size_t xp, wp, part, zy, sums, dz, acc, dw_acc, total;
+    size_t xp, wp, part, zy, sums, dz, acc, dw_acc, unit, total;
 };
 
 // In how many parts the contraction of an M x N product is taken so that its tiles fill
@@ -541,8 +563,9 @@ Layout layout_for(const kda_ce_desc_t *d, bool backward) {
                           ? 1 : splits_for(l.piece, D, BN, cdiv(T, BK), l.pairs);
         if (l.pieces > 1 || l.dx_splits > 1) l.acc = round256((size_t)l.dx_splits * T * D * 4);
         if (l.dw_splits > 1) l.dw_acc = round256((size_t)l.dw_splits * l.piece * D * 4);
+        l.unit = 256;
     }
-    l.total = l.xp + l.wp + l.part + l.zy + l.sums + l.dz + l.acc + l.dw_acc;
+    l.total = l.xp + l.wp + l.part + l.zy + l.sums + l.dz + l.acc + l.dw_acc + l.unit;
     return l;
 }
 
@@ -631,21 +654,21 @@ cudaError_t sum_splits(const float *acc, void *dst, long long n, int splits, boo
 
 // Copies x and W where the layout wants them; xp, wp are what the products read.
 cudaError_t run_pack(const kda_ce_desc_t *d, const Layout &l, const void *x, const void *w,
-                     const Targets &y, uint8_t *ws, const void *&xp, const void *&wp,
-                     cudaStream_t st) {
+                     const Targets &y, const float *d_loss, float *unit, uint8_t *ws,
+                     const void *&xp, const void *&wp, cudaStream_t st) {
     xp = l.pack_x ? ws : x;
     wp = l.pack_w ? ws + l.xp : w;
     if (!l.pack_x) return cudaSuccess;
     const long long T = d->tokens, V = l.pack_w ? d->vocab : 0, most = 16ll * device_sms();
     const long long need = ((T + V) * (l.x_pitch / 8) + 255) / 256;
-    const dim3 grid((unsigned)(need < most ? need : most));
+    const dim3 grid((unsigned)(need < most ? need : most) + (d_loss ? 1 : 0));
     __nv_bfloat16 *to = (__nv_bfloat16 *)ws, *to_w = (__nv_bfloat16 *)(ws + l.xp);
     if (l.f32)
         return launch_dependent(pack_kernel<float>, grid, dim3(256), 0, st, (const float *)x, T, to,
-                                (const float *)w, V, to_w, d->width, l.x_pitch, l.planes, y);
+                                (const float *)w, V, to_w, d->width, l.x_pitch, l.planes, y, d_loss, unit);
     return launch_dependent(pack_kernel<__nv_bfloat16>, grid, dim3(256), 0, st,
                             (const __nv_bfloat16 *)x, T, to, (const __nv_bfloat16 *)w, V, to_w,
-                            d->width, l.x_pitch, l.planes, y);
+                            d->width, l.x_pitch, l.planes, y, d_loss, unit);
 }
 
 bool bad_ids(const kda_ce_desc_t *d, const void *ids) {
@@ -693,7 +716,8 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
     float2 *sums = (float2 *)(ws + l.xp + l.wp + l.part + l.zy);
     unsigned *ticket = (unsigned *)(ws + l.total - 256);
     const void *xp, *wp;
-    if (run_pack(desc, l, x, weight, Targets{}, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
+    if (run_pack(desc, l, x, weight, Targets{}, nullptr, nullptr, ws, xp, wp, st) != cudaSuccess)
+        return KDA_ERR_CUDA;
     GemmArgs p = {};
     p.M = desc->tokens;
     p.N = desc->vocab;
@@ -760,7 +784,14 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
     const void *xp, *wp;
     const Targets y = {targets, desc->id_dtype == KDA_ID_I64, desc->vocab, desc->ignore_index,
                        dev_status};
-    if (run_pack(desc, l, x, weight, y, ws, xp, wp, st) != cudaSuccess) return KDA_ERR_CUDA;
+    // BF16: dz is kept in units of the largest d_loss and dx and d_weight are multiplied by
+    // it.  A mean's 1 / N, the same for every row, rounded into dz would move the whole
+    // gradient by up to 2^-8 (34 rows: error 2.6e-3 of the gradient, 1.7e-3 of it the
+    // output's rounding).
+    float *unit = l.f32 ? nullptr : (float *)(ws + l.total - 256);
+    if (run_pack(desc, l, x, weight, y, l.f32 ? nullptr : d_loss, unit, ws, xp, wp, st) !=
+        cudaSuccess)
+        return KDA_ERR_CUDA;
     const int T = desc->tokens, V = desc->vocab, D = desc->width;
     const int step = l.w32 ? kW32Step : BK;
     // as K-major and MN-major operands
@@ -789,6 +820,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.y = y;
         p.lse = lse;
         p.d_loss = d_loss;
+        p.unit = unit;
         p.dz = dz;
         p.pitch = l.piece;
         p.planes = l.planes;
@@ -800,6 +832,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             GemmArgs q = {};
             q.status = dev_status;
             q.pairs = l.pairs;
+            q.unit = unit;
             q.chunk = l.chunk;
             q.splits = l.dx_splits;
             q.M = T;
@@ -824,6 +857,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             GemmArgs q = {};
             q.status = dev_status;
             q.pairs = l.pairs;
+            q.unit = unit;
             q.chunk = l.chunk;
             q.splits = l.dw_splits;
             q.M = cols;

@@ -52,6 +52,8 @@ struct GemmArgs {
     const float *lse, *d_loss;
     __nv_bfloat16 *dz;         // [planes][M][pitch]
     int pitch, planes;
+    // BF16: the largest |d_loss|, in whose units dz is; EPI_OUT multiplies by it
+    const float *unit;
     // EPI_OUT: value (+ acc_in) to acc_out, both [splits][M][N] fp32, or to out
     const float *acc_in;
     float *acc_out;
@@ -162,9 +164,11 @@ struct Row {
             if (EPI == EPI_DZ) {
                 lse2 = p.lse[row] * kLog2e;
                 g = y >= 0 ? p.d_loss[row] : 0.f;
+                if (p.unit) g /= *p.unit;
             }
             y = y >= 0 ? y - p.b_row0 : -1;
         }
+        if (EPI == EPI_OUT && BF16) g = *p.unit;
     }
 
     // 32 values as BF16 into half `h` of the warp's lines; what the rounding left stays
@@ -312,6 +316,13 @@ struct Row {
     __device__ __forceinline__ void pair(const GemmArgs &p, const Tile &t, const Turn &turn, int q,
                                          float (&a)[32], float (&b)[32]) {
         const int c = c0 + 64 * q;
+        if (EPI == EPI_OUT && BF16) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+                a[i] *= g;
+                b[i] *= g;
+            }
+        }
         if (EPI == EPI_STATS) {
             stats(p, c, a);
             stats(p, c + 32, b);

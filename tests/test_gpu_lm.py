@@ -351,6 +351,22 @@ def test_cross_entropy_of_large_logits(dtype):
     _check_ce(dtype, x, w, y, torch.ones(40, device="cuda"))
 
 
+def test_cross_entropy_gradient_of_a_mean_is_not_scaled_by_rounding():
+    """d_loss halfway between two BF16 values and equal in all rows: rounded into dz it would
+    move every gradient by 2^-8.  The output's own rounding is at most 2^-8 of an element,
+    evenly spread at worst: 2^-8 / sqrt 3 of the norm; a tenth more for the softmax's."""
+    g = _gen(11)
+    x, w = _randn((40, 256), g, torch.bfloat16), _randn((3000, 256), g, torch.bfloat16, 0.1)
+    y = torch.randint(0, 3000, (40,), generator=g, device="cuda")
+    d = torch.full((40,), 2.0 ** -5 * (1 + 2.0 ** -8), device="cuda")
+    _, lse, _ = kda.linear_cross_entropy(x, w, y)
+    got = kda.linear_cross_entropy_backward(x, w, y, lse, d)
+    z = x.double() @ w.double().T
+    dz = (torch.softmax(z, 1) - torch.nn.functional.one_hot(y, 3000)) * d.double()[:, None]
+    for a, ref in zip(got, (dz @ w.double(), dz.T @ x.double())):
+        assert (a.double() - ref).norm() <= 1.1 * 2.0 ** -8 / math.sqrt(3) * ref.norm()
+
+
 def test_cross_entropy_with_nothing_to_predict():
     x, w = torch.ones((6, 16), device="cuda"), torch.ones((50, 16), device="cuda")
     y = torch.full((6,), 7, device="cuda")
