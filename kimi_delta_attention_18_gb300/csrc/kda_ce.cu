@@ -54,17 +54,24 @@ struct Smem {
 // index contiguous: W and x in dx = dz W, dz and x in dW = dz^T x), so nothing is
 // transposed in memory.
 //
-// FINE, for results that are held in fp32 (lse, loss, and all of an fp32 problem):
-// the tensor core adds each step of 16 to its accumulator with truncation, about
-// 2^-24 of the sum per step and always towards zero, so a long contraction loses
-// bits (at 7,168 measured 2.3e-6 of lse, against 1.4e-7 with fp32 arithmetic).  The
-// accumulator is then handed over every `chunk` stages and added up, rounded to
-// nearest, in the epilogue's registers, while the other accumulator fills.  16
+// FINE, for results that are held in fp32 (lse, loss, and all of an fp32 problem) and for
+// long contractions: the tensor core adds each step of 16 to its accumulator with
+// truncation, up to 2^-23 of the sum per step and always towards zero, so bits are lost
+// (at 7,168 measured 2.3e-6 of lse, against 1.4e-7 with fp32 arithmetic).  The accumulator
+// is then handed over every `chunk` stages and added up, rounded to nearest, in the
+// epilogue's registers, while the other accumulator fills.  16
 // stages for BF16 operands (lse within 3e-7, no slower than one accumulator for
 // all: 1.93 ms at 2,048 x 131,072 x 7,168), 8 for fp32 ones (gradients within 6e-7).
 constexpr int kChunkBf16 = 16, kChunkF32 = 8;
+// BF16 gradients: one accumulator up to so many stages (32,768 elements), which leaves the
+// sum 2e-4 short at worst (4e-7 a stage where all terms have one sign; the output's own
+// rounding is 1.7e-3 of the norm); FINE beyond (d_weight over 2^20 tokens was 6.5e-3 short).
+// FINE for all is 4-7 % slower (8,192 x 131,072 x 4,096: 15.2 and 15.8 ms; its epilogue has a
+// whole tile in registers), but not for long sums (d_weight of 81,920 x 8,192 x 2,048, 1,280
+// stages: 3.60 ms with one accumulator, 3.52 FINE).
+constexpr int kLongStages = 512;
 
-template <int EPI, bool A_MN, bool B_MN, bool FINE, int CTAS>
+template <int EPI, bool A_MN, bool B_MN, bool FINE, bool BF16, int CTAS>
 __global__ void __launch_bounds__(kThreads, 1)
     gemm_kernel(const __grid_constant__ GemmArgs p, const __grid_constant__ CUtensorMap tm_a,
                 const __grid_constant__ CUtensorMap tm_b) {
@@ -224,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         for (int w = w0; w < work && ok; w += wstep) {
             const Tile t = tile_at<CTAS>(p, w);
-            Row<EPI, !FINE> r;
+            Row<EPI, BF16> r;
             r.begin(p, t, (t.m * CTAS + rank) * BM + 32 * quarter, lane, half, 128);
             __syncwarp();
             if constexpr (FINE) {
@@ -597,10 +604,10 @@ bool encode(CUtensorMap *tm, const void *base, int inner, long long rows, int pl
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool FINE, int CTAS>
+template <int EPI, bool A_MN, bool B_MN, bool FINE, bool BF16, int CTAS>
 cudaError_t start_gemm(GemmArgs p, const CUtensorMap &ta, const CUtensorMap &tb, int n,
                        cudaStream_t st) {
-    const auto kernel = gemm_kernel<EPI, A_MN, B_MN, FINE, CTAS>;
+    const auto kernel = gemm_kernel<EPI, A_MN, B_MN, FINE, BF16, CTAS>;
     cudaError_t e = set_max_dynamic_smem((const void *)kernel, Smem<CTAS>::bytes);
     if (e != cudaSuccess) return e;
     p.m_tiles = cdiv(p.M, BM * CTAS);
@@ -633,12 +640,23 @@ bool use_pairs(const GemmArgs &p, int n) {
     return n >= 2 && two <= one;
 }
 
-template <int EPI, bool A_MN, bool B_MN, bool FINE>
+template <int EPI, bool A_MN, bool B_MN, bool FINE, bool BF16>
 cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap &tb,
                      cudaStream_t st) {
     const int n = device_sms();
-    return use_pairs(p, n) ? start_gemm<EPI, A_MN, B_MN, FINE, 2>(p, ta, tb, n, st)
-                           : start_gemm<EPI, A_MN, B_MN, FINE, 1>(p, ta, tb, n, st);
+    return use_pairs(p, n) ? start_gemm<EPI, A_MN, B_MN, FINE, BF16, 2>(p, ta, tb, n, st)
+                           : start_gemm<EPI, A_MN, B_MN, FINE, BF16, 1>(p, ta, tb, n, st);
+}
+
+// A backward pass's product: FINE for fp32 operands and for long contractions.
+template <int EPI, bool A_MN, bool B_MN>
+cudaError_t run_backward(const GemmArgs &p, bool f32, const CUtensorMap &ta, const CUtensorMap &tb,
+                         cudaStream_t st) {
+    constexpr bool BF16 = EPI == EPI_OUT;
+    if (f32) return run_gemm<EPI, A_MN, B_MN, true, false>(p, ta, tb, st);
+    return cdiv(p.k_blocks, p.splits) > kLongStages
+               ? run_gemm<EPI, A_MN, B_MN, true, BF16>(p, ta, tb, st)
+               : run_gemm<EPI, A_MN, B_MN, false, BF16>(p, ta, tb, st);
 }
 
 // dst = the sum of `splits` parts of n values.
@@ -740,7 +758,7 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
         if (!encode(&ta, xp, l.x_pitch, p.M, l.planes, kMajor) ||
             !encode(&tb, wp, l.w_pitch, p.N, l.planes, kMajor))
             return KDA_ERR_CUDA;
-        e = run_gemm<EPI_STATS, false, false, true>(p, ta, tb, st);
+        e = run_gemm<EPI_STATS, false, false, true, false>(p, ta, tb, st);
     }
     if (e != cudaSuccess) return KDA_ERR_CUDA;
     // 8 rows to a block while all blocks are resident (8 rows and 32: 1,024 x 131,072 9.0
@@ -824,9 +842,8 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
         p.dz = dz;
         p.pitch = l.piece;
         p.planes = l.planes;
-        if ((l.w32   ? launch_w32(EPI_DZ, p, logits, st)
-             : l.f32 ? run_gemm<EPI_DZ, false, false, true>(p, xk, wk, st)
-                     : run_gemm<EPI_DZ, false, false, false>(p, xk, wk, st)) != cudaSuccess)
+        if ((l.w32 ? launch_w32(EPI_DZ, p, logits, st)
+                   : run_backward<EPI_DZ, false, false>(p, l.f32, xk, wk, st)) != cudaSuccess)
             return KDA_ERR_CUDA;
         if (dx) {
             GemmArgs q = {};
@@ -845,9 +862,8 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)dx & 15u) == 0;
             if (q.splits > q.k_blocks) return KDA_ERR_CUDA;
-            if ((l.w32   ? launch_w32(EPI_OUT, q, back, st)
-                 : l.f32 ? run_gemm<EPI_OUT, false, true, true>(q, zk, wm, st)
-                         : run_gemm<EPI_OUT, false, true, false>(q, zk, wm, st)) != cudaSuccess)
+            if ((l.w32 ? launch_w32(EPI_OUT, q, back, st)
+                       : run_backward<EPI_OUT, false, true>(q, l.f32, zk, wm, st)) != cudaSuccess)
                 return KDA_ERR_CUDA;
             if (l.dx_splits > 1 && k == l.pieces - 1 &&
                 sum_splits(acc, dx, (long long)T * D, l.dx_splits, size == 2, st) != cudaSuccess)
@@ -868,8 +884,7 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
             else q.out = to;
             q.out_bf16 = size == 2;
             q.vec = D % 8 == 0 && ((uintptr_t)d_weight & 15u) == 0;
-            if ((l.f32 ? run_gemm<EPI_OUT, true, true, true>(q, zm, xm, st)
-                       : run_gemm<EPI_OUT, true, true, false>(q, zm, xm, st)) != cudaSuccess)
+            if (run_backward<EPI_OUT, true, true>(q, l.f32, zm, xm, st) != cudaSuccess)
                 return KDA_ERR_CUDA;
             if (l.dw_splits > 1 && sum_splits(dw_acc, to, (long long)cols * D, l.dw_splits,
                                               size == 2, st) != cudaSuccess)

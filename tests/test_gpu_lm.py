@@ -563,3 +563,48 @@ def test_workspaces_on_another_stream():
         torch.full((1_000_000,), 7.0, device="cuda")  # would land in a freed workspace
         s.synchronize()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("T,V,D,piece", [
+    (1 << 20, 512, 64, 256),     # d_weight over 2^20 tokens
+    (64, 256, 1 << 17, 0),       # logits of 2^17 channels
+    (1216, 131072, 4096, 0),     # dx over 131,072 columns
+])
+def test_cross_entropy_gradient_of_long_sums(T, V, D, piece):
+    """BF16 gradients whose sums are long and of one sign (the targets are elsewhere): the
+    tensor core's truncation at every step would add up to 0.6 % of d_weight, 0.8 % of the
+    logits here.  Bounds: one rounding to BF16 of dz and one of the result, each at most
+    2^-8 and evenly spread, so 2^-8 / sqrt 3 of the norm each; a tenth more for the rest."""
+    g = _gen(T + D)
+    scale = 1.0 + torch.rand(D, generator=g, device="cuda")
+    if T > V:  # logits about 1 / 64
+        x = ((1.0 + 0.1 * torch.randn((T, D), generator=g, device="cuda")) * scale).bfloat16()
+        w = _randn((V, D), g, torch.bfloat16, 1.0 / D)
+    elif D > V:  # logits between 10 and 11
+        x = ((1.0 + 0.1 * torch.randn((T, D), generator=g, device="cuda")) * scale).bfloat16()
+        rows = 10.0 + torch.rand(V, generator=g, device="cuda")
+        w = (rows[:, None] / (1.5 * D) * torch.ones(D, device="cuda")).bfloat16()
+    else:  # a softmax over many rows of one sign
+        x = _randn((T, D), g, torch.bfloat16, 10.0 / math.sqrt(D))
+        w = ((1.0 + 0.1 * torch.randn((V, D), generator=g, device="cuda")) * scale).bfloat16()
+        w[V - 1] = 0.0
+    y = torch.randint(V // 2, V, (T,), generator=g, device="cuda")
+    if V > T:
+        y.fill_(V - 1)
+    d = torch.ones(T, device="cuda")
+    _, lse, _ = kda.linear_cross_entropy(x, w, y)
+    dx, dw = kda.linear_cross_entropy_backward(x, w, y, lse, d, piece=piece)
+    if T < V and V > D:
+        rows = torch.arange(16, device="cuda") * (T // 16)
+        p = torch.exp(x[rows].double() @ w.double().T - lse[rows, None].double())
+        got, ref = dx[rows], p @ w.double()  # the target's row of w is zero
+    else:
+        cols = torch.arange(32, device="cuda") * (V // 64)
+        ref = torch.zeros((32, D), dtype=torch.float64, device="cuda")
+        for i in range(0, T, 131072):
+            part = x[i:i + 131072].double()
+            p = torch.exp(part @ w[cols].double().T - lse[i:i + 131072, None].double())
+            ref += p.T @ part
+        got = dw[cols]
+    bound = 1.1 * math.sqrt(2.0) * 2.0 ** -8 / math.sqrt(3.0)
+    assert (got.double() - ref).norm() <= bound * ref.norm()
