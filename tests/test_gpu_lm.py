@@ -608,3 +608,23 @@ def test_cross_entropy_gradient_of_long_sums(T, V, D, piece):
         got = dw[cols]
     bound = 1.1 * math.sqrt(2.0) * 2.0 ** -8 / math.sqrt(3.0)
     assert (got.double() - ref).norm() <= bound * ref.norm()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,D,act,strided", [
+    (1500, 56, 128, "sigmoid", False),
+    (1500, 56, 128, "silu", False),
+    (1500, 56, 128, "none", False),
+    (1500, 56, 128, "sigmoid", True),    # tokens apart, more than 2 KB each
+    (3200, 1, 1032, "sigmoid", False),   # BF16: 96 threads a row
+    (5200, 1, 1024, "silu", False),      # 64 threads a row, 8 rows a tile
+    (700, 1, 5120, "sigmoid", False),    # a row a tile, 384 threads
+    (700, 1, 7168, "silu", False),       # 512 threads
+    (2000, 56, 33, "sigmoid", False),    # rows as pairs
+    (25000, 3, 65, "none", False),
+])
+def test_gated_norm_of_rows_through_shared_memory(dtype, T, H, D, act, strided):
+    """Rows enough for the ring in shared memory (four tiles for each of 152 SMs), in each of
+    its forms: a row in part of a warp, in several warps, alone in its tile; with the next
+    row's sums before this row's outputs (BF16 gradients of rows wider than a warp)."""
+    test_gated_norm(dtype, T, H, D, act, True, strided)
