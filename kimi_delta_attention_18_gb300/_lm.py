@@ -2,7 +2,9 @@
 gate and residual, the token embedding, and softmax cross entropy over the
 vocabulary.  As in ``_native``: argument marshalling only; outputs the caller did
 not pass are allocated with torch, launches go to the current stream (or
-``stream``), and every library error raises ``KDAError``.
+``stream``: the caller makes it wait for the inputs and waits for it before it uses the
+outputs; the tensors' memory is kept for both streams), and every library error raises
+``KDAError``.
 """
 from __future__ import annotations
 
@@ -62,7 +64,8 @@ def bind(L):
 # These calls are as short as a decode step's (a few microseconds on the device), so
 # the host's part is kept short: one combined test per tensor (_need, and with it
 # the precise error, only when that fails), plain integers instead of ctypes
-# objects, and the current stream's handle without a Stream object around it.
+# objects, and the current stream's handle without a Stream object around it.  A call
+# with a stream of its own is the same call inside that stream's context.
 
 def _lib():
     return _k._lib or _k.lib()
@@ -81,10 +84,8 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream, dev):
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev.index)
-    return stream.cuda_stream
+def _stream(dev):
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _first(t, name, dims):
@@ -101,12 +102,9 @@ def _first(t, name, dims):
     raise ValueError("%s must be float32 or bfloat16" % name)
 
 
-def _workspace(workspace, need, dev, stream):
+def _workspace(workspace, need, dev):
     if workspace is None:
-        workspace = torch.empty(need or 16, dtype=torch.uint8, device=dev)
-        if stream is not None:  # it must outlive the kernels on a stream not its own
-            workspace.record_stream(stream)
-        return workspace, need or 16
+        return torch.empty(need or 16, dtype=torch.uint8, device=dev), need or 16
     if not isinstance(workspace, torch.Tensor) or workspace.device != dev:
         raise ValueError("workspace must be a tensor on %s" % dev)
     return workspace, workspace.numel() * workspace.element_size()
@@ -171,12 +169,15 @@ def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, 
     act(gate)`` (see kda_gated_norm_forward in kda.h).  x, gate ``[T, H, D]`` in one
     activation dtype, tokens possibly strided; weight ``[D]`` fp32 or None; act
     "sigmoid", "silu" or "none" (gate None).  Returns out ``[T, H, D]``."""
+    if stream is not None:
+        return _k._on(stream, gated_norm, x, gate, weight, act=act, eps=eps, out=out,
+                      dev_status=dev_status)
     dev, desc = _gated(x, gate, weight, act, eps)
     out = _out(out, "out", x)
     _check("kda_gated_norm_forward",
            _lib().kda_gated_norm_forward(desc, x.data_ptr(), _ptr(gate), _ptr(weight),
                                          out.data_ptr(), _status(dev_status, dev),
-                                         _stream(stream, dev)))
+                                         _stream(dev)))
     return out
 
 
@@ -185,6 +186,9 @@ def gated_norm_backward(d_out, x, gate=None, weight=None, *, act="sigmoid", eps=
     """Gradients of ``gated_norm`` for the adjoint d_out ``[T, H, D]`` of its output:
     ``(dx, d_gate, d_weight)``, d_gate None without a gate, d_weight fp32 ``[D]`` (see
     kda_gated_norm_backward in kda.h)."""
+    if stream is not None:
+        return _k._on(stream, gated_norm_backward, d_out, x, gate, weight, act=act, eps=eps,
+                      want_d_weight=want_d_weight, workspace=workspace, dev_status=dev_status)
     dev, desc = _gated(x, gate, weight, act, eps)
     _is(d_out, "d_out", x.dtype, x.shape, dev)
     L = _lib()
@@ -193,13 +197,12 @@ def gated_norm_backward(d_out, x, gate=None, weight=None, *, act="sigmoid", eps=
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(x.shape[2], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev,
-                                       stream)
+        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
     _check("kda_gated_norm_backward",
            L.kda_gated_norm_backward(desc, d_out.data_ptr(), x.data_ptr(), _ptr(gate),
                                      _ptr(weight), dx.data_ptr(), _ptr(d_gate), _ptr(d_weight),
                                      _ptr(workspace), ws_len, _status(dev_status, dev),
-                                     _stream(stream, dev)))
+                                     _stream(dev)))
     return dx, d_gate, d_weight
 
 
@@ -219,6 +222,9 @@ def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, ou
     """The residual stream's update and the next block's norm: ``h_out = h + scale y``
     and the RMS norm of it times weight (see kda_residual_norm_forward in kda.h).
     h, y ``[T, D]``; without y, h_out is h.  Returns ``(h_out, out)``."""
+    if stream is not None:
+        return _k._on(stream, residual_norm, h, y, weight, scale=scale, eps=eps, h_out=h_out, out=out,
+                      dev_status=dev_status)
     dev, desc = _residual(h, weight, eps, "h")
     new_h = None
     if y is not None:
@@ -230,7 +236,7 @@ def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, ou
     _check("kda_residual_norm_forward",
            _lib().kda_residual_norm_forward(desc, h.data_ptr(), _ptr(y), _ptr(weight), scale,
                                             _ptr(new_h), out.data_ptr(),
-                                            _status(dev_status, dev), _stream(stream, dev)))
+                                            _status(dev_status, dev), _stream(dev)))
     return (h if y is None else new_h), out
 
 
@@ -240,6 +246,10 @@ def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0
     """Gradients of ``residual_norm`` from its h_out, for the adjoints d_out of the
     norm and d_h_out (None: zero) of h_out: ``(dh, dy, d_weight)`` (see
     kda_residual_norm_backward in kda.h).  With scale 1, dy is dh itself."""
+    if stream is not None:
+        return _k._on(stream, residual_norm_backward, d_out, h_out, weight, d_h_out, scale=scale,
+                      eps=eps, want_dy=want_dy, want_d_weight=want_d_weight, workspace=workspace,
+                      dev_status=dev_status)
     dev, desc = _residual(h_out, weight, eps, "h_out")
     _is(d_out, "d_out", h_out.dtype, h_out.shape, dev)
     if d_h_out is not None:
@@ -250,13 +260,12 @@ def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(h_out.shape[1], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev,
-                                       stream)
+        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
     _check("kda_residual_norm_backward",
            L.kda_residual_norm_backward(desc, d_out.data_ptr(), _ptr(d_h_out), h_out.data_ptr(),
                                         _ptr(weight), scale, dh.data_ptr(), _ptr(dy),
                                         _ptr(d_weight), _ptr(workspace), ws_len,
-                                        _status(dev_status, dev), _stream(stream, dev)))
+                                        _status(dev_status, dev), _stream(dev)))
     return dh, (dh if want_dy and scale == 1.0 else dy), d_weight
 
 
@@ -279,6 +288,8 @@ def embedding(table, ids, *, scale=1.0, out=None, dev_status=None, stream=None):
     """``out[t] = scale table[ids[t]]`` (see kda_embedding_forward in kda.h): table
     ``[V, D]``, ids ``[T]`` int32 or int64.  An id outside the table gives a zero row
     and status 1 in dev_status (a device int32)."""
+    if stream is not None:
+        return _k._on(stream, embedding, table, ids, scale=scale, out=out, dev_status=dev_status)
     dev, dtype = _first(table, "table", 2)
     _is(table, "table", table.dtype, table.shape, dev)
     kind = _ids(ids, "ids", dev)
@@ -290,7 +301,7 @@ def embedding(table, ids, *, scale=1.0, out=None, dev_status=None, stream=None):
     _check("kda_embedding_forward",
            _lib().kda_embedding_forward(EmbedDesc(T, V, D, dtype, kind, scale), table.data_ptr(),
                                         ids.data_ptr(), out.data_ptr(), _status(dev_status, dev),
-                                        _stream(stream, dev)))
+                                        _stream(dev)))
     return out
 
 
@@ -298,6 +309,9 @@ def embedding_backward(d_out, ids, num_rows, *, scale=1.0, d_table=None, workspa
                        dev_status=None, stream=None):
     """The gradient ``[num_rows, D]`` of ``embedding``'s table for the adjoint d_out
     ``[T, D]``, in d_out's dtype (see kda_embedding_backward in kda.h)."""
+    if stream is not None:
+        return _k._on(stream, embedding_backward, d_out, ids, num_rows, scale=scale, d_table=d_table,
+                      workspace=workspace, dev_status=dev_status)
     dev, dtype = _first(d_out, "d_out", 2)
     _is(d_out, "d_out", d_out.dtype, d_out.shape, dev)
     T, D = d_out.shape
@@ -307,12 +321,11 @@ def embedding_backward(d_out, ids, num_rows, *, scale=1.0, d_table=None, workspa
     else:
         _is(d_table, "d_table", d_out.dtype, (num_rows, D), dev)
     L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_embedding_backward_workspace_size(desc), dev,
-                                   stream)
+    workspace, ws_len = _workspace(workspace, L.kda_embedding_backward_workspace_size(desc), dev)
     _check("kda_embedding_backward",
            L.kda_embedding_backward(desc, d_out.data_ptr(), ids.data_ptr(), d_table.data_ptr(),
                                     workspace.data_ptr(), ws_len, _status(dev_status, dev),
-                                    _stream(stream, dev)))
+                                    _stream(dev)))
     return d_table
 
 
@@ -341,17 +354,20 @@ def linear_cross_entropy(x, weight, targets, *, ignore_index=-100, loss=None, ls
     kda_linear_ce_forward in kda.h): x ``[T, D]``, weight ``[V, D]``, targets ``[T]``
     int32 or int64.  Returns ``(loss [T], lse [T], mean)`` in fp32, mean over the rows
     whose target is not ignore_index."""
+    if stream is not None:
+        return _k._on(stream, linear_cross_entropy, x, weight, targets, ignore_index=ignore_index,
+                      loss=loss, lse=lse, workspace=workspace, dev_status=dev_status)
     dev, desc = _ce(x, weight, targets, ignore_index, 0)
     T = x.shape[0]
     loss, lse = _vector(loss, "loss", T, dev), _vector(lse, "lse", T, dev)
     mean = torch.empty((), dtype=torch.float32, device=dev)
     L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 0), dev, stream)
+    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 0), dev)
     _check("kda_linear_ce_forward",
            L.kda_linear_ce_forward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
                                    loss.data_ptr(), lse.data_ptr(), mean.data_ptr(),
                                    workspace.data_ptr(), ws_len, _status(dev_status, dev),
-                                   _stream(stream, dev)))
+                                   _stream(dev)))
     return loss, lse, mean
 
 
@@ -361,6 +377,10 @@ def linear_cross_entropy_backward(x, weight, targets, lse, d_loss, *, ignore_ind
     """Gradients ``(dx, d_weight)`` of ``linear_cross_entropy`` for the adjoint d_loss
     ``[T]`` fp32 of its per-row loss (see kda_linear_ce_backward in kda.h); ``piece``
     vocabulary columns at a time (0: the library's choice)."""
+    if stream is not None:
+        return _k._on(stream, linear_cross_entropy_backward, x, weight, targets, lse, d_loss,
+                      ignore_index=ignore_index, piece=piece, want_dx=want_dx,
+                      want_d_weight=want_d_weight, workspace=workspace, dev_status=dev_status)
     dev, desc = _ce(x, weight, targets, ignore_index, piece)
     T = x.shape[0]
     _is(lse, "lse", torch.float32, (T,), dev)
@@ -368,10 +388,10 @@ def linear_cross_entropy_backward(x, weight, targets, lse, d_loss, *, ignore_ind
     dx = _out(None, "dx", x) if want_dx else None
     d_weight = _out(None, "d_weight", weight) if want_d_weight else None
     L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 1), dev, stream)
+    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 1), dev)
     _check("kda_linear_ce_backward",
            L.kda_linear_ce_backward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
                                     lse.data_ptr(), d_loss.data_ptr(), _ptr(dx), _ptr(d_weight),
                                     workspace.data_ptr(), ws_len, _status(dev_status, dev),
-                                    _stream(stream, dev)))
+                                    _stream(dev)))
     return dx, d_weight

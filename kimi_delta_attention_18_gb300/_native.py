@@ -114,6 +114,24 @@ def _stream(stream, device):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on(stream, fn, *args, **kw):
+    """``fn(*args, **kw)`` on ``stream``, with every tensor of the call kept for it: what the
+    call allocates comes from that stream's memory, so that neither work queued on the
+    current stream nor a tensor that the caller drops early can share it; the results are
+    kept for the current stream too, where the caller uses them next, and the arguments for
+    ``stream``."""
+    here = torch.cuda.current_stream(stream.device)
+    for t in (*args, *kw.values()):
+        if isinstance(t, torch.Tensor) and t.is_cuda:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        result = fn(*args, **kw)
+    for t in result if isinstance(result, tuple) else (result,):
+        if t is not None:
+            t.record_stream(here)
+    return result
+
+
 def _need(t, name, dtype=None, shape=None, device=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a torch.Tensor" % name)

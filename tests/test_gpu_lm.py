@@ -628,3 +628,57 @@ def test_gated_norm_of_rows_through_shared_memory(dtype, T, H, D, act, strided):
     its forms: a row in part of a warp, in several warps, alone in its tile; with the next
     row's sums before this row's outputs (BF16 gradients of rows wider than a warp)."""
     test_gated_norm(dtype, T, H, D, act, True, strided)
+
+
+def test_tensors_of_calls_on_another_stream_are_kept():
+    """With stream=, neither an output that the caller drops before the call's kernels have
+    run nor memory that the current stream still writes is shared with anything else."""
+    g = _gen(13)
+    T, V, D = 1500, 4000, 256
+    x, w = _randn((T, D), g, torch.bfloat16), _randn((V, D), g, torch.bfloat16, 0.1)
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    d = torch.rand(T, generator=g, device="cuda")
+    _, lse, _ = kda.linear_cross_entropy(x, w, y)
+    h, wn = x.view(T, 2, 128), torch.ones(128, device="cuda")
+    calls = [lambda s: kda.linear_cross_entropy(x, w, y, stream=s),
+             lambda s: kda.linear_cross_entropy_backward(x, w, y, lse, d, stream=s),
+             lambda s: kda.gated_norm_backward(h, h, h, wn, stream=s),
+             lambda s: kda.residual_norm(x, x, None, stream=s),
+             lambda s: kda.residual_norm_backward(x, x, None, x, scale=0.5, stream=s),
+             lambda s: (kda.embedding(w, y, stream=s), kda.embedding_backward(x, y, V, stream=s))]
+    s = torch.cuda.Stream()
+    for call in calls:
+        want = [t.clone() for t in call(None)]
+        sizes = [t.numel() * t.element_size() for t in want] + [1 << 16, 1 << 20, 1 << 22, 1 << 24]
+        torch.cuda.synchronize()
+        for kept in range(len(want)):
+            torch.cuda._sleep(20_000_000)  # late writes of the current stream to memory it gave back
+            for n in sizes:
+                torch.full((n,), 7, dtype=torch.uint8, device="cuda")
+            with torch.cuda.stream(s):
+                torch.cuda._sleep(40_000_000)  # the call's kernels come later than what follows
+            out = call(s)[kept]  # the others are dropped
+            others = [torch.full((n,), 9, dtype=torch.uint8, device="cuda") for n in sizes for _ in (0, 1)]
+            torch.cuda.synchronize()
+            assert torch.equal(out, want[kept])
+            assert all(bool((t == 9).all()) for t in others)
+            del out, others
+
+
+def test_arguments_of_calls_on_another_stream_are_kept():
+    """An argument that the caller drops at once (a copy made for the call) stays whole until
+    the call's kernels have read it."""
+    x = torch.randn((3000, 512), device="cuda")
+    want = kda.residual_norm(x, x, scale=0.0)[1]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(40_000_000)
+    s.wait_stream(torch.cuda.current_stream())
+    copy = x.clone()
+    s.wait_stream(torch.cuda.current_stream())
+    _, out = kda.residual_norm(copy, copy, stream=s, scale=0.0)
+    del copy
+    torch.full((3000, 512), 9.0, device="cuda")
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
