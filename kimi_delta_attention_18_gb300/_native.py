@@ -3,7 +3,9 @@
 Every function takes torch CUDA tensors, checks their dtype / shape / layout,
 allocates the outputs the caller did not pass (with torch, on the tensors'
 device), and calls the C entry point of the same name on the current CUDA
-stream.  All arithmetic runs in the library's kernels; there is no fallback.
+stream, or on ``stream``: the caller makes it wait for the inputs and waits for it
+before it uses the outputs; the tensors' memory is kept for both streams.  All
+arithmetic runs in the library's kernels; there is no fallback.
 """
 from __future__ import annotations
 
@@ -108,10 +110,8 @@ def _ptr(t):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream, device):
-    if stream is None:
-        stream = torch.cuda.current_stream(device)
-    return ctypes.c_void_p(stream.cuda_stream)
+def _stream(device):
+    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
 
 
 def _on(stream, fn, *args, **kw):
@@ -176,6 +176,11 @@ def prefill_chunked(q, k, v, g, beta, S0=None, cu_seqlens=None, *, num_segments=
     ``stage_events`` (four ``torch.cuda.Event``) calls kda_prefill_chunked_timed
     instead, which records them around the call's launches (measurement only).
     """
+    if stream is not None:
+        return _on(stream, prefill_chunked, q, k, v, g, beta, S0, cu_seqlens,
+                   num_segments=num_segments, out=out, S_final=S_final,
+                   want_final_state=want_final_state, workspace=workspace, dev_status=dev_status,
+                   stage_events=stage_events)
     dev = q.device
     T, H, dk = q.shape
     dv = v.shape[2]
@@ -211,12 +216,12 @@ def prefill_chunked(q, k, v, g, beta, S0=None, cu_seqlens=None, *, num_segments=
         rc = lib().kda_prefill_chunked(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v), _ptr(g),
                                        _ptr(beta), _ptr(S0), _ptr(cu_seqlens), _ptr(out),
                                        _ptr(S_final), _ptr(workspace), ws_len, _ptr(dev_status),
-                                       _stream(stream, dev))
+                                       _stream(dev))
         _check("kda_prefill_chunked", rc)
         return out, S_final
     if len(stage_events) != 4:
         raise ValueError("stage_events must be four torch.cuda.Event")
-    st = torch.cuda.current_stream(dev) if stream is None else stream
+    st = torch.cuda.current_stream(dev)
     for e in stage_events:  # torch creates an event's handle at its first record
         if not e.cuda_event:
             e.record(st)
@@ -225,7 +230,7 @@ def prefill_chunked(q, k, v, g, beta, S0=None, cu_seqlens=None, *, num_segments=
                                          _ptr(beta), _ptr(S0), _ptr(cu_seqlens), _ptr(out),
                                          _ptr(S_final), _ptr(workspace), ws_len,
                                          _ptr(dev_status), ctypes.cast(evs, ctypes.c_void_p),
-                                         _stream(st, dev))
+                                         _stream(dev))
     _check("kda_prefill_chunked_timed", rc)
     return out, S_final
 
@@ -237,6 +242,10 @@ def prefill_chunked_gated(q, k, v, x_g, x_beta, S0=None, cu_seqlens=None, *, num
     q, k ``[T, H, 128]`` BF16 not normalised, v ``[T, H, 128]`` BF16, x_g ``[T, H,
     128]`` BF16, x_beta ``[T, H]`` fp32; the kernels form g = -5 sigmoid(x_g), beta =
     sigmoid(x_beta) and the normalised q, k.  Returns ``(out, S_final)``."""
+    if stream is not None:
+        return _on(stream, prefill_chunked_gated, q, k, v, x_g, x_beta, S0, cu_seqlens,
+                   num_segments=num_segments, out=out, S_final=S_final,
+                   want_final_state=want_final_state, workspace=workspace, dev_status=dev_status)
     dev = q.device
     T, H, dk = q.shape
     dv = v.shape[2]
@@ -271,7 +280,7 @@ def prefill_chunked_gated(q, k, v, x_g, x_beta, S0=None, cu_seqlens=None, *, num
     rc = lib().kda_prefill_chunked_gated(ctypes.byref(desc), _ptr(q), _ptr(k), _ptr(v),
                                          _ptr(x_g), _ptr(x_beta), _ptr(S0), _ptr(cu_seqlens),
                                          _ptr(out), _ptr(S_final), _ptr(workspace), ws_len,
-                                         _ptr(dev_status), _stream(stream, dev))
+                                         _ptr(dev_status), _stream(dev))
     _check("kda_prefill_chunked_gated", rc)
     return out, S_final
 
@@ -294,6 +303,11 @@ def prefill_chunked_ckpt(q, k, v, g, beta, S0=None, cu_seqlens=None, *, ckpt_int
     of each sequence (see kda_prefill_chunked_ckpt in kda.h).  ckpt_states
     ``[K, H, dk, dv]`` fp32 with K >= num_checkpoints(cu_seqlens, ckpt_interval)
     (allocated when None).  Returns ``(out, S_final, ckpt_states)``."""
+    if stream is not None:
+        return _on(stream, prefill_chunked_ckpt, q, k, v, g, beta, S0, cu_seqlens,
+                   ckpt_interval=ckpt_interval, ckpt_states=ckpt_states,
+                   num_segments=num_segments, out=out, S_final=S_final,
+                   want_final_state=want_final_state, workspace=workspace, dev_status=dev_status)
     dev = q.device
     T, H, dk = q.shape
     dv = v.shape[2]
@@ -339,7 +353,7 @@ def prefill_chunked_ckpt(q, k, v, g, beta, S0=None, cu_seqlens=None, *, ckpt_int
                                         _ptr(beta), _ptr(S0), _ptr(cu_seqlens), _ptr(out),
                                         _ptr(S_final), int(ckpt_interval), _ptr(ckpt_buf),
                                         _ptr(workspace), ws_len, _ptr(dev_status),
-                                        _stream(stream, dev))
+                                        _stream(dev))
     _check("kda_prefill_chunked_ckpt", rc)
     return out, S_final, ckpt_states
 
@@ -362,6 +376,10 @@ def prefill_backward(q, k, v, g, beta, S0, cu_seqlens, d_out, d_S_final=None, *,
     activation dtype, d_S_final ``[N, H, dk, dv]`` fp32 or None; num_segments
     splits each sequence (0: the library's choice).  Returns fp32
     ``(dq, dk, dv, dg, dbeta, dS0)`` (dS0 None unless want_dS0)."""
+    if stream is not None:
+        return _on(stream, prefill_backward, q, k, v, g, beta, S0, cu_seqlens, d_out, d_S_final,
+                   want_dS0=want_dS0, num_segments=num_segments, workspace=workspace,
+                   dev_status=dev_status)
     dev = q.device
     T, H, dk = q.shape
     dv = v.shape[2]
@@ -400,7 +418,7 @@ def prefill_backward(q, k, v, g, beta, S0, cu_seqlens, d_out, d_S_final=None, *,
                                     _ptr(beta), _ptr(S0), _ptr(cu_seqlens), _ptr(d_out),
                                     _ptr(d_S_final), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dg),
                                     _ptr(dbeta), _ptr(dS0), _ptr(workspace), ws_len,
-                                    _ptr(dev_status), _stream(stream, dev))
+                                    _ptr(dev_status), _stream(dev))
     _check("kda_prefill_backward", rc)
     return dq, dk_, dv_, dg, dbeta, dS0
 
@@ -411,6 +429,10 @@ def prefill_segments(q, k, v, g, beta, seg_init_states, cu_seqlens, num_segments
     """Run segments [seg_begin, seg_end) from their given start states (see
     kda_prefill_segments in kda.h).  seg_init_states ``[N, H, S, dk, dv]`` fp32
     (None = zeros for every segment).  Returns ``(out, S_final)``."""
+    if stream is not None:
+        return _on(stream, prefill_segments, q, k, v, g, beta, seg_init_states, cu_seqlens,
+                   num_segments, seg_begin=seg_begin, seg_end=seg_end, out=out, S_final=S_final,
+                   want_final_state=want_final_state, dev_status=dev_status)
     dev = q.device
     T, H, dk = q.shape
     dv = v.shape[2]
@@ -440,7 +462,7 @@ def prefill_segments(q, k, v, g, beta, seg_init_states, cu_seqlens, num_segments
                                     _ptr(v), _ptr(g),
                                     _ptr(beta), _ptr(seg_init_states), _ptr(cu_seqlens),
                                     _ptr(out), _ptr(S_final), _ptr(dev_status),
-                                    _stream(stream, dev))
+                                    _stream(dev))
     _check("kda_prefill_segments", rc)
     return out, S_final
 
@@ -448,6 +470,8 @@ def prefill_segments(q, k, v, g, beta, seg_init_states, cu_seqlens, num_segments
 def decode_step(q, k, v, g, beta, S, *, out=None, dev_status=None, stream=None):
     """One decode token per sequence; updates S ``[B, H, dk, dv]`` in place and
     returns out ``[B, H, dv]`` (see kda_decode_step in kda.h)."""
+    if stream is not None:
+        return _on(stream, decode_step, q, k, v, g, beta, S, out=out, dev_status=dev_status)
     dev = S.device
     B, H, dk, dv = S.shape
     act = _ACT.get(q.dtype)
@@ -465,7 +489,7 @@ def decode_step(q, k, v, g, beta, S, *, out=None, dev_status=None, stream=None):
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32, None, dev)
     rc = lib().kda_decode_step(B, H, dk, dv, act, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta),
-                               _ptr(S), _ptr(out), _ptr(dev_status), _stream(stream, dev))
+                               _ptr(S), _ptr(out), _ptr(dev_status), _stream(dev))
     _check("kda_decode_step", rc)
     return out
 
@@ -478,6 +502,10 @@ def state_transfer(k, v, g, beta, cu_seqlens, num_segments, *, seg_begin=0, seg_
     it also writes the zero-start outputs and A_t^T q_t (allocated if not passed).
     Returns ``(A [N,H,S,dk,dk], B [N,H,S,dk,dv])``, plus ``(out_zero [T,H,dv],
     out_transfer [T,H,dk])`` when q is given."""
+    if stream is not None:
+        return _on(stream, state_transfer, k, v, g, beta, cu_seqlens, num_segments,
+                   seg_begin=seg_begin, seg_end=seg_end, transfer=transfer, zero_init_state=zero_init_state, q=q,
+                   out_zero=out_zero, out_transfer=out_transfer, dev_status=dev_status)
     dev = k.device
     T, H, dk = k.shape
     dv = v.shape[2]
@@ -510,7 +538,7 @@ def state_transfer(k, v, g, beta, cu_seqlens, num_segments, *, seg_begin=0, seg_
     rc = lib().kda_state_transfer(ctypes.byref(desc), int(seg_begin), seg_end, _ptr(q), _ptr(k),
                                   _ptr(v), _ptr(g), _ptr(beta), _ptr(cu_seqlens), _ptr(transfer),
                                   _ptr(zero_init_state), _ptr(out_zero), _ptr(out_transfer),
-                                  _ptr(dev_status), _stream(stream, dev))
+                                  _ptr(dev_status), _stream(dev))
     _check("kda_state_transfer", rc)
     if q is not None:
         return transfer, zero_init_state, out_zero, out_transfer
@@ -523,6 +551,10 @@ def prefill_combine(out, out_transfer, seg_init_states, cu_seqlens, *, first_seg
     see kda_prefill_combine in kda.h.  ``start_images`` (from state_compose) selects
     the tcgen05 path; ``seg_init_states`` may then be None, with ``num_segments``
     given.  Returns ``out``."""
+    if stream is not None:
+        return _on(stream, prefill_combine, out, out_transfer, seg_init_states, cu_seqlens,
+                   first_segment=first_segment, start_images=start_images,
+                   num_segments=num_segments, dev_status=dev_status)
     dev = out.device
     T, H, dv = out.shape
     dk = out_transfer.shape[2]
@@ -545,7 +577,7 @@ def prefill_combine(out, out_transfer, seg_init_states, cu_seqlens, *, first_seg
     desc = _desc(N, T, H, dk, dv, act, Sg)
     rc = lib().kda_prefill_combine(ctypes.byref(desc), int(first_segment), _ptr(seg_init_states),
                                    _ptr(start_images), _ptr(out_transfer), _ptr(cu_seqlens),
-                                   _ptr(out), _ptr(dev_status), _stream(stream, dev))
+                                   _ptr(out), _ptr(dev_status), _stream(dev))
     _check("kda_prefill_combine", rc)
     return out
 
@@ -559,6 +591,10 @@ def state_compose(transfer, zero_init_state, S0=None, *, seg_init_states=None, S
     without a final state the last pair is never read.  ``start_images`` (BF16
     ``[U, S, 128 * 128]``, dk = dv = 128) also receives each start state as the
     operand image prefill_combine's tcgen05 path reads."""
+    if stream is not None:
+        return _on(stream, state_compose, transfer, zero_init_state, S0,
+                   seg_init_states=seg_init_states, S_final=S_final, want_starts=want_starts, want_final_state=want_final_state,
+                   start_images=start_images, dev_status=dev_status)
     dev = transfer.device
     U, Sg, dk, _ = transfer.shape
     dv = zero_init_state.shape[-1]
@@ -576,7 +612,7 @@ def state_compose(transfer, zero_init_state, S0=None, *, seg_init_states=None, S
         _need(dev_status, "dev_status", torch.int32, None, dev)
     rc = lib().kda_state_compose(U, Sg, dk, dv, _ptr(transfer), _ptr(zero_init_state), _ptr(S0),
                                  _ptr(seg_init_states), _ptr(S_final), _ptr(start_images),
-                                 _ptr(dev_status), _stream(stream, dev))
+                                 _ptr(dev_status), _stream(dev))
     _check("kda_state_compose", rc)
     return seg_init_states, S_final
 
@@ -585,7 +621,9 @@ def selftest_wait_timeout(limit_us, dev_status, stream=None):
     """Run the bounded-wait self-test (see kda_selftest_wait_timeout in kda.h): a
     wait that nothing completes gives up after ~limit_us and writes status 5
     (KDA_ERR_TIMEOUT) to dev_status (a device int32 tensor)."""
+    if stream is not None:
+        return _on(stream, selftest_wait_timeout, limit_us, dev_status)
     _need(dev_status, "dev_status", torch.int32, None)
     rc = lib().kda_selftest_wait_timeout(int(limit_us), _ptr(dev_status),
-                                         _stream(stream, dev_status.device))
+                                         _stream(dev_status.device))
     _check("kda_selftest_wait_timeout", rc)
