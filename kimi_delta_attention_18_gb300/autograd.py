@@ -10,10 +10,14 @@ Around the mixer: ``kda_gated_norm`` (x, gate, weight), ``kda_residual_norm`` (h
 weight), ``kda_embedding`` (the table) and ``kda_linear_cross_entropy`` (x, weight),
 each with its library forward and backward; gradients have their inputs' dtypes
 (norm weights fp32).
+
+The gradients are not differentiable themselves: a second derivative through one of
+these operations raises an error.
 """
 from __future__ import annotations
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lm
 from . import _native as _k
@@ -29,6 +33,7 @@ class KDAPrefill(torch.autograd.Function):
         return out, S_final
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out, d_S_final):
         q, k, v, g, beta, S0, cu_seqlens = ctx.saved_tensors
         if d_out is None:
@@ -59,6 +64,7 @@ class GatedNorm(torch.autograd.Function):
         return _lm.gated_norm(x, gate, weight, act=act, eps=eps)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out):
         x, gate, weight = ctx.saved_tensors
         dx, d_gate, d_weight = _lm.gated_norm_backward(
@@ -81,6 +87,7 @@ class ResidualNorm(torch.autograd.Function):
         return (h_out, out) if ctx.has_y else out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, *grads):
         h_out, weight = ctx.saved_tensors
         d_h, d_out = grads if ctx.has_y else (None, grads[0])
@@ -106,6 +113,7 @@ class Embedding(torch.autograd.Function):
         return _lm.embedding(table, ids, scale=scale)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out):
         ids, = ctx.saved_tensors
         return _lm.embedding_backward(d_out.contiguous(), ids, ctx.rows, scale=ctx.scale), None, None
@@ -125,6 +133,7 @@ class LinearCrossEntropy(torch.autograd.Function):
         return total if mean else loss
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_loss):
         x, weight, targets, lse = ctx.saved_tensors
         if ctx.mean:  # over the rows that have a loss

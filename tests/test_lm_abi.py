@@ -202,3 +202,43 @@ def test_descriptors_match_the_header():
     assert ctypes.sizeof(NormDesc) == 48 and NormDesc.eps.offset == 40
     assert ctypes.sizeof(EmbedDesc) == 24 and EmbedDesc.scale.offset == 20
     assert ctypes.sizeof(CrossEntropyDesc) == 32 and CrossEntropyDesc.piece.offset == 28
+
+
+def _stand_ins(monkeypatch):
+    """The library's calls, each as a tensor of the right shape (no GPU here)."""
+    def like(*ts):
+        return tuple(None if t is None else t.detach() * 0 for t in ts)
+
+    for name, fn in dict(
+            gated_norm=lambda x, *a, **k: x * 1.0,
+            gated_norm_backward=lambda d, x, gate, w, **k: like(x, gate, w),
+            residual_norm=lambda h, y, w, **k: (h * 1.0, h * 1.0),
+            residual_norm_backward=lambda d, h, w, dh, want_dy, **k: like(h, h if want_dy else None, w),
+            embedding=lambda t, ids, **k: t[ids] * 1.0,
+            embedding_backward=lambda d, ids, n, **k: d.new_zeros((n, d.shape[1])),
+            linear_cross_entropy=lambda x, w, y, **k: (x.sum(1), x.sum(1), x.sum()),
+            linear_cross_entropy_backward=lambda x, w, *a, **k: like(x, w)).items():
+        monkeypatch.setattr(autograd._lm, name, fn)
+    monkeypatch.setattr(autograd._k, "prefill_chunked", lambda q, k, v, *a, **kw: (v * 1.0, v.sum()))
+    monkeypatch.setattr(autograd._k, "prefill_backward",
+                        lambda q, k, v, g, beta, *a, **kw: like(q, k, v, g, beta) + (None,))
+
+
+@pytest.mark.parametrize("op", [
+    lambda x, w: autograd.kda_gated_norm(x[:, None], x[:, None] * 2.0, w),
+    lambda x, w: autograd.kda_residual_norm(x, x * 2.0, w)[1],
+    lambda x, w: autograd.kda_residual_norm(x, None, w)[1],
+    lambda x, w: autograd.kda_embedding(x, torch.tensor([1, 0, 1])),
+    lambda x, w: autograd.kda_linear_cross_entropy(x, x * 2.0, torch.tensor([1, 0])),
+    lambda x, w: autograd.kda_linear_cross_entropy(x, x * 2.0, torch.tensor([1, 0]), reduction="sum"),
+    lambda x, w: autograd.kda_prefill(x[:, None], x[:, None], x[:, None], x[:, None], x[:, :1])[0],
+])
+def test_second_derivatives_are_refused(monkeypatch, op):
+    """A gradient of a gradient (a gradient penalty) raises: without the refusal its terms
+    through the operation would be dropped and the rest returned as if it were all."""
+    _stand_ins(monkeypatch)
+    x = torch.randn(2, 4, requires_grad=True)
+    y = op(x, torch.ones(4, requires_grad=True))
+    grad, = torch.autograd.grad((y * y).sum() + (x * x * x).sum(), x, create_graph=True)
+    with pytest.raises(RuntimeError, match="once_differentiable"):
+        grad.pow(2).sum().backward()
