@@ -71,6 +71,12 @@ def _lib():
     return _k._lib or _k.lib()
 
 
+def _fit(n):
+    """n for a 32-bit field, which would keep n's low bits only: the nearest value that it
+    holds, which is beyond the library's limits wherever n is."""
+    return n if -0x80000000 <= n <= 0x7fffffff else 0x7fffffff if n > 0 else -0x80000000
+
+
 def _is(t, name, dtype, shape, dev):
     try:
         if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
@@ -159,8 +165,8 @@ def _gated(x, gate, weight, act, eps):
     T, H, D = x.shape
     if weight is not None:
         _is(weight, "weight", torch.float32, (D,), dev)
-    return dev, NormDesc(T, _rows(x, "x", x), 0 if gate is None else _rows(gate, "gate", x), H, D,
-                         dtype, kind, eps)
+    return dev, NormDesc(T, _rows(x, "x", x), 0 if gate is None else _rows(gate, "gate", x),
+                         _fit(H), _fit(D), dtype, kind, eps)
 
 
 def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, dev_status=None,
@@ -214,7 +220,7 @@ def _residual(h, weight, eps, name):
     T, D = h.shape
     if weight is not None:
         _is(weight, "weight", torch.float32, (D,), dev)
-    return dev, NormDesc(T, 0, 0, 1, D, dtype, 0, eps)
+    return dev, NormDesc(T, 0, 0, 1, _fit(D), dtype, 0, eps)
 
 
 def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, out=None,
@@ -299,9 +305,9 @@ def embedding(table, ids, *, scale=1.0, out=None, dev_status=None, stream=None):
     else:
         _is(out, "out", table.dtype, (T, D), dev)
     _check("kda_embedding_forward",
-           _lib().kda_embedding_forward(EmbedDesc(T, V, D, dtype, kind, scale), table.data_ptr(),
-                                        ids.data_ptr(), out.data_ptr(), _status(dev_status, dev),
-                                        _stream(dev)))
+           _lib().kda_embedding_forward(EmbedDesc(_fit(T), _fit(V), _fit(D), dtype, kind, scale),
+                                        table.data_ptr(), ids.data_ptr(), out.data_ptr(),
+                                        _status(dev_status, dev), _stream(dev)))
     return out
 
 
@@ -315,7 +321,7 @@ def embedding_backward(d_out, ids, num_rows, *, scale=1.0, d_table=None, workspa
     dev, dtype = _first(d_out, "d_out", 2)
     _is(d_out, "d_out", d_out.dtype, d_out.shape, dev)
     T, D = d_out.shape
-    desc = EmbedDesc(T, num_rows, D, dtype, _ids(ids, "ids", dev, T), scale)
+    desc = EmbedDesc(_fit(T), _fit(num_rows), _fit(D), dtype, _ids(ids, "ids", dev, T), scale)
     if d_table is None:
         d_table = torch.empty((num_rows, D), dtype=d_out.dtype, device=dev)
     else:
@@ -337,8 +343,8 @@ def _ce(x, weight, targets, ignore_index, piece):
     T, D = x.shape
     _is(x, "x", x.dtype, x.shape, dev)
     _is(weight, "weight", x.dtype, (weight.shape[0], D), dev)
-    return dev, CrossEntropyDesc(ignore_index, T, weight.shape[0], D, dtype,
-                                 _ids(targets, "targets", dev, T), piece)
+    return dev, CrossEntropyDesc(ignore_index, _fit(T), _fit(weight.shape[0]), _fit(D), dtype,
+                                 _ids(targets, "targets", dev, T), _fit(piece))
 
 
 def _vector(t, name, T, dev):

@@ -242,3 +242,52 @@ def test_second_derivatives_are_refused(monkeypatch, op):
     grad, = torch.autograd.grad((y * y).sum() + (x * x * x).sum(), x, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         grad.pow(2).sum().backward()
+
+
+class _OnDevice:
+    """What the binding looks at of a contiguous tensor on the GPU."""
+    is_cuda, device = True, torch.device("cpu")
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return A
+
+
+@pytest.mark.parametrize("n", [1 << 32, (1 << 32) + 3, (1 << 31) + 1])
+def test_sizes_beyond_32_bits_are_refused(monkeypatch, n):
+    """A length, width or vocabulary whose low 32 bits are a small number is not taken for
+    that number (most of the output would stay unwritten)."""
+    from kimi_delta_attention_18_gb300 import _lm
+    monkeypatch.setattr(_lm, "_stream", lambda dev: None)
+    monkeypatch.setattr(_lm, "_workspace", lambda *a: (_OnDevice(16), 1 << 60))
+    t, ids = _OnDevice, lambda k: _OnDevice(k, dtype=torch.int32)  # noqa: E731
+    vec = dict(loss=t(4), lse=t(4))
+    for call in (lambda: kda.gated_norm(t(1, n, 8), t(1, n, 8), out=t(1, n, 8)),
+                 lambda: kda.gated_norm(t(1, 1, n), t(1, 1, n), out=t(1, 1, n)),
+                 lambda: kda.residual_norm(t(1, n), t(1, n), h_out=t(1, n), out=t(1, n)),
+                 lambda: kda.embedding(t(7, 1), ids(n), out=t(n, 1)),
+                 lambda: kda.embedding(t(n, 1), ids(7), out=t(7, 1)),
+                 lambda: kda.embedding(t(7, n), ids(1), out=t(1, n)),
+                 lambda: kda.embedding_backward(t(n, 1), ids(n), 7, d_table=t(7, 1)),
+                 lambda: kda.embedding_backward(t(7, 1), ids(7), n, d_table=t(n, 1)),
+                 lambda: kda.embedding_backward(t(1, n), ids(1), 7, d_table=t(7, n)),
+                 lambda: kda.linear_cross_entropy(t(4, 8), t(n, 8), ids(4), **vec),
+                 lambda: kda.linear_cross_entropy(t(4, n), t(9, n), ids(4), **vec),
+                 lambda: kda.linear_cross_entropy(t(n, 8), t(9, 8), ids(n), loss=t(n), lse=t(n)),
+                 lambda: kda.linear_cross_entropy_backward(t(4, 8), t(n, 8), ids(4), t(4), t(4),
+                                                           want_dx=False, want_d_weight=False)):
+        with pytest.raises(kda.KDAError) as e:
+            call()
+        assert e.value.status == UNSUPPORTED
+
+
+def test_a_piece_beyond_32_bits_is_the_whole_vocabulary(monkeypatch):
+    from kimi_delta_attention_18_gb300 import _lm
+    desc = _lm._ce(_OnDevice(4, 8), _OnDevice(9, 8), _OnDevice(4, dtype=torch.int32), -100,
+                   (1 << 32) + 256)[1]
+    assert desc.piece == 0x7fffffff
