@@ -394,8 +394,8 @@ __device__ __forceinline__ uint4 eight_from(const __nv_bfloat16 *p, long long e,
 // lines (zeros past the width): fp32 operands, and BF16 rows whose width is no multiple
 // of the 16 bytes that a tensor map needs.  With targets, rows of x whose target is
 // ignored become zeros: dW is a sum over all rows, and what a padded position holds
-// (NaN perhaps) has no part in it.  With d_loss the first block only finds the
-// largest of its magnitudes that counts (1 if none does).
+// (NaN perhaps) has no part in it.  With d_loss the first block only finds dz's unit, from
+// the largest of its magnitudes that counts (1 if none does).
 template <typename T>
 __global__ void __launch_bounds__(256)
     pack_kernel(const T *x, long long x_rows, __nv_bfloat16 *xp, const T *w, long long w_rows,
@@ -416,6 +416,9 @@ __global__ void __launch_bounds__(256)
         __syncthreads();
         if (threadIdx.x == 0) {
             for (int k = 1; k < 8; ++k) m = fmaxf(m, sh[k]);
+            // from 2 on its significand alone: dz then keeps d_loss's own exponents (a row of
+            // 1e-20 next to one of 1e30 would be zero in units of 1e30)
+            if (m >= 2.f) m = __int_as_float((__float_as_int(m) & 0x7fffff) | 0x3f800000);
             *unit = m >= FLT_MIN ? m : 1.f;
         }
         return;
@@ -802,10 +805,10 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
     const void *xp, *wp;
     const Targets y = {targets, desc->id_dtype == KDA_ID_I64, desc->vocab, desc->ignore_index,
                        dev_status};
-    // BF16: dz is kept in units of the largest d_loss and dx and d_weight are multiplied by
-    // it.  A mean's 1 / N, the same for every row, rounded into dz would move the whole
-    // gradient by up to 2^-8 (34 rows: error 2.6e-3 of the gradient, 1.7e-3 of it the
-    // output's rounding).
+    // BF16: dz is kept in units of the largest d_loss (or its significand) and dx and
+    // d_weight are multiplied by the unit.  A mean's 1 / N, the same for every row, rounded
+    // into dz would move the whole gradient by up to 2^-8 (34 rows: error 2.6e-3 of the
+    // gradient, 1.7e-3 of it the output's rounding).
     float *unit = l.f32 ? nullptr : (float *)(ws + l.total - 256);
     if (run_pack(desc, l, x, weight, y, l.f32 ? nullptr : d_loss, unit, ws, xp, wp, st) !=
         cudaSuccess)

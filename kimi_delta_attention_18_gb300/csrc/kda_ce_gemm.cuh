@@ -52,7 +52,7 @@ struct GemmArgs {
     const float *lse, *d_loss;
     __nv_bfloat16 *dz;         // [planes][M][pitch]
     int pitch, planes;
-    // BF16: the largest |d_loss|, in whose units dz is; EPI_OUT multiplies by it
+    // BF16: the unit of dz (the largest |d_loss|, or its significand); EPI_OUT multiplies by it
     const float *unit;
     // EPI_OUT: value (+ acc_in) to acc_out, both [splits][M][N] fp32, or to out
     const float *acc_in;

@@ -682,3 +682,23 @@ def test_arguments_of_calls_on_another_stream_are_kept():
     torch.full((3000, 512), 9.0, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("large,small", [(1e30, 1e-20), (1.0, 1e-30), (1.7e38, 1e-3), (3e-36, 1e-36)])
+def test_cross_entropy_gradient_of_rows_of_unequal_weight(large, small):
+    """BF16: a row's dx does not depend on how large the other rows' d_loss is.  Bound: a
+    rounding to BF16 of each term and of the result, 2^-8 each at most."""
+    g = _gen(14)
+    x, w = _randn((48, 128), g, torch.bfloat16), _randn((300, 128), g, torch.bfloat16, 0.1)
+    y = torch.randint(0, 300, (48,), generator=g, device="cuda")
+    d = torch.where(torch.arange(48, device="cuda") % 2 == 0, large, small)
+    _, lse, _ = kda.linear_cross_entropy(x, w, y)
+    dx, dw = kda.linear_cross_entropy_backward(x, w, y, lse, d)
+    p = torch.softmax(x.double() @ w.double().T, 1)
+    dz = (p - torch.nn.functional.one_hot(y, 300)) * d.double()[:, None]
+    for got, ref, terms in ((dx, dz @ w.double(), dz.abs() @ w.double().abs()),
+                            (dw, dz.T @ x.double(), dz.T.abs() @ x.double().abs())):
+        beyond = ref.abs() > torch.finfo(torch.bfloat16).max  # no BF16 value: infinite
+        assert torch.equal(got[beyond].double(), ref[beyond].sign() * math.inf)
+        err = torch.where(beyond, 0.0, got.double() - ref).norm(dim=1)
+        assert (err <= 2.0 ** -8 * (terms.norm(dim=1) + ref.norm(dim=1)) * 1.01).all()
