@@ -41,15 +41,15 @@ class Layer(torch.nn.Module):
         self.norm = torch.nn.Parameter(torch.ones(width, device="cuda"))
         self.out_norm = torch.nn.Parameter(torch.ones(HEAD, device="cuda"))
 
-    def forward(self, x, cu_seqlens):
+    def forward(self, x, cu_seqlens, status):
         T, H = x.shape[0], self.heads
         p = (x @ self.qkvz.T).view(T, 4, H, HEAD)
         q, k = (torch.nn.functional.normalize(p[:, i].float(), dim=-1).to(x.dtype) for i in (0, 1))
         g = -5.0 * torch.sigmoid((x @ self.decay.T).float() - 4.0).view(T, H, HEAD)
         beta = torch.sigmoid((x @ self.beta.T).float())
         o, _ = kda_prefill(q.contiguous(), k.contiguous(), p[:, 2].contiguous(), g, beta, None,
-                           cu_seqlens)
-        u = kda_gated_norm(o, p[:, 3], self.out_norm)  # the gate: a slice of the projection
+                           cu_seqlens, dev_status=status)
+        u = kda_gated_norm(o, p[:, 3], self.out_norm, dev_status=status)  # the gate: a slice of the projection
         return u.view(T, H * HEAD) @ self.out.T
 
 
@@ -64,13 +64,15 @@ class Model(torch.nn.Module):
         self.embed_scale = width ** 0.5
         self.residual_scale = layers ** -0.5
 
-    def forward(self, ids, targets, cu_seqlens):
-        h, y = kda_embedding(self.table, ids, scale=self.embed_scale), None
+    def forward(self, ids, targets, cu_seqlens, status):
+        """``status`` gets the first error of any kernel of the step (see train)."""
+        h = kda_embedding(self.table, ids, scale=self.embed_scale, dev_status=status)
+        y, norm = None, dict(scale=self.residual_scale, dev_status=status)
         for layer in self.layers:
-            h, x = kda_residual_norm(h, y, layer.norm, scale=self.residual_scale)
-            y = layer(x, cu_seqlens)
-        _, x = kda_residual_norm(h, y, self.norm, scale=self.residual_scale)
-        return kda_linear_cross_entropy(x, self.head, targets)
+            h, x = kda_residual_norm(h, y, layer.norm, **norm)
+            y = layer(x, cu_seqlens, status)
+        _, x = kda_residual_norm(h, y, self.norm, **norm)
+        return kda_linear_cross_entropy(x, self.head, targets, dev_status=status)
 
 
 def batch(vocab, lengths, gen):
@@ -94,13 +96,16 @@ def train(steps=40, vocab=199, width=256, heads=2, layers=2, lengths=(96, 64, 31
     gen = torch.Generator(device="cuda").manual_seed(seed)
     model = Model(vocab, width, heads, layers)
     opt = torch.optim.Adam(model.parameters(), lr=3e-3)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
     losses = []
     for i in range(steps):
-        loss = model(*batch(vocab, lengths, gen))
+        loss = model(*batch(vocab, lengths, gen), status)
         opt.zero_grad()
         loss.backward()
         opt.step()
         losses.append(float(loss.detach()))
+        if int(status):  # the host waits for the loss anyway
+            raise RuntimeError("step %d: a kernel reported status %d" % (i, int(status)))
         if i % 10 == 0 or i == steps - 1:
             log("step %d: loss %.3f" % (i, losses[-1]))
     return losses

@@ -702,3 +702,20 @@ def test_cross_entropy_gradient_of_rows_of_unequal_weight(large, small):
         assert torch.equal(got[beyond].double(), ref[beyond].sign() * math.inf)
         err = torch.where(beyond, 0.0, got.double() - ref).norm(dim=1)
         assert (err <= 2.0 ** -8 * (terms.norm(dim=1) + ref.norm(dim=1)) * 1.01).all()
+
+
+def test_differentiable_forms_report_errors():
+    """An id outside the table, a target outside the vocabulary: in dev_status, from the
+    forward pass and again from the backward pass."""
+    from kimi_delta_attention_18_gb300 import autograd as ag
+    table = torch.ones((4, 8), device="cuda", requires_grad=True)
+    bad, good = torch.tensor([0, 4], device="cuda"), torch.tensor([0, 3], device="cuda")
+    for f in (lambda ids, s: ag.kda_embedding(table, ids, dev_status=s),
+              lambda ids, s: ag.kda_linear_cross_entropy(table[:2], table, ids, dev_status=s)):
+        for ids, code in ((bad, 1), (good, 0)):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            out = f(ids, status)
+            assert int(status) == code
+            status.zero_()
+            out.sum().backward()
+            assert int(status) == code

@@ -291,3 +291,27 @@ def test_a_piece_beyond_32_bits_is_the_whole_vocabulary(monkeypatch):
     desc = _lm._ce(_OnDevice(4, 8), _OnDevice(9, 8), _OnDevice(4, dtype=torch.int32), -100,
                    (1 << 32) + 256)[1]
     assert desc.piece == 0x7fffffff
+
+
+def test_differentiable_forms_pass_the_status_on(monkeypatch):
+    """Forward and backward of each operation give the library the caller's dev_status."""
+    _stand_ins(monkeypatch)
+    seen = []
+    for module, names in ((autograd._lm, ("gated_norm", "residual_norm", "embedding", "linear_cross_entropy",
+                                          "gated_norm_backward", "residual_norm_backward",
+                                          "embedding_backward", "linear_cross_entropy_backward")),
+                          (autograd._k, ("prefill_chunked", "prefill_backward"))):
+        for name in names:
+            def call(*a, fn=getattr(module, name), name=name, **kw):
+                seen.append((name, kw["dev_status"]))
+                return fn(*a, **kw)
+            monkeypatch.setattr(module, name, call)
+    x, w = torch.randn(2, 4, requires_grad=True), torch.ones(4, requires_grad=True)
+    ids, status = torch.tensor([1, 0]), torch.zeros(1, dtype=torch.int32)
+    s = dict(dev_status=status)
+    for out in (autograd.kda_gated_norm(x[:, None], x[:, None], w, **s), autograd.kda_residual_norm(x, x, w, **s)[1],
+                autograd.kda_residual_norm(x, None, w, **s)[1], autograd.kda_embedding(x, ids, **s),
+                autograd.kda_linear_cross_entropy(x, x, ids, **s),
+                autograd.kda_prefill(x[:, None], x[:, None], x[:, None], x[:, None], x[:, :1], **s)[0]):
+        out.sum().backward()
+    assert len(seen) == 12 and all(t is status for _, t in seen), seen
