@@ -719,3 +719,56 @@ def test_differentiable_forms_report_errors():
             status.zero_()
             out.sum().backward()
             assert int(status) == code
+
+
+@pytest.mark.parametrize("T,V,D,piece", [
+    (96, 4000, 1024, 0),      # the fp32 weight split on its way (up to 128 tokens, whole fours)
+    (100, 1500, 256, 256),    # the same in pieces of the vocabulary
+    (300, 3001, 515, 0),      # operands stored as terms
+    (300, 3001, 515, 512),
+])
+def test_cross_entropy_of_fp32_is_accurate(T, V, D, piece):
+    """fp32 operands are three BF16 terms each and six products.  With the rounding of exp's
+    argument (up to 3e-7 of a term) the gradients are within about 6e-7 of the norm; five
+    products would be 2.6e-6 off, three 4.5e-6 (in 64 bits, these sizes).  lse: 3e-7 and
+    fp32's spacing."""
+    g = _gen(T + V)
+    x, w = _randn((T, D), g, torch.float32), _randn((V, D), g, torch.float32, 2.0 / math.sqrt(D))
+    y = torch.randint(0, V, (T,), generator=g, device="cuda")
+    d = torch.rand(T, generator=g, device="cuda") - 0.3
+    z = x.double() @ w.double().T
+    lse = torch.logsumexp(z, 1)
+    _, got, _ = kda.linear_cross_entropy(x, w, y)
+    assert ((got.double() - lse) / lse).pow(2).mean().sqrt() <= 1e-6
+    lse = lse.float()
+    dz = (torch.exp(z - lse.double()[:, None]) - torch.nn.functional.one_hot(y, V)) * d.double()[:, None]
+    dx, dw = kda.linear_cross_entropy_backward(x, w, y, lse, d, piece=piece)
+    for got, ref in ((dx, dz @ w.double()), (dw, dz.T @ x.double())):
+        assert (got.double() - ref).norm() <= 2e-6 * ref.norm()
+
+
+def test_cross_entropy_row_statistics_of_a_wide_row_are_accurate():
+    """BF16, 7,168 channels: lse within 3e-7 (2.3e-6 if one accumulator took the whole sum,
+    which the tensor core truncates at every step)."""
+    g = _gen(15)
+    x, w = _randn((64, 7168), g, torch.bfloat16), _randn((2000, 7168), g, torch.bfloat16, 2.0 / math.sqrt(7168))
+    y = torch.randint(0, 2000, (64,), generator=g, device="cuda")
+    lse = torch.logsumexp(x.double() @ w.double().T, 1)
+    got = kda.linear_cross_entropy(x, w, y)[1]
+    assert ((got.double() - lse) / lse).pow(2).mean().sqrt() <= 1e-6
+
+
+@pytest.mark.parametrize("dtype,T,V,D,piece", [
+    ("f32", 100, 1000, 64, 256),     # an fp32 weight read in pieces, dx added up over them
+    ("f32", 128, 700, 132, 512),
+    ("bf16", 4100, 131072, 72, 0),   # more than one piece by default
+])
+def test_cross_entropy_in_pieces(dtype, T, V, D, piece):
+    test_cross_entropy(dtype, T, V, D, piece)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,D", [(3000, 500, 701), (700, 9000, 517)])
+def test_embedding_of_wide_rows_that_are_not_whole_pieces(dtype, T, V, D):
+    """Four single columns per thread; frequent ids, and runs of absent ones."""
+    test_embedding(dtype, T, V, D, "text", torch.int32)
