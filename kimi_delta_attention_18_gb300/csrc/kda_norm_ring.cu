@@ -4,11 +4,11 @@
 // of eight (BF16) or four (fp32) of them, or a multiple, starts on a 16-byte boundary.
 //
 // Measured on GB300 (BF16; a copy of this size runs at 6.4-6.8 TB/s): gradient of the
-// gated norm of 81,920 x 56 x 128 865-873 us (6.7 TB/s; with rows loaded straight into
-// registers 1,083, bound by the loads that 25 % of the warps can have in flight); of the
-// residual norm of 40,960 x 7,168 423-433 us (6.8 TB/s; 505 without the ring).  A row of
-// 5,120 in a tile by itself is bound by its latency (26,214 rows, forward: 189 us, a copy
-// 159; with 512 threads instead of the 384 that it needs 209).
+// gated norm of 81,920 x 56 x 128 876-880 us (6.7 TB/s; with rows loaded straight into
+// registers 1,026, bound by the loads that 25 % of the warps can have in flight); of the
+// residual norm of 40,960 x 7,168 440-442 us (6.7 TB/s; 518 without the ring).  A row of
+// 5,120 in a tile by itself is bound by its latency (26,214 rows, forward: 175 us, a copy
+// 159; with 512 threads instead of the 384 that it needs 194).
 #include "kda_norm_math.cuh"
 #include "kda_sm100.cuh"
 
@@ -32,13 +32,13 @@ struct Ring {
 };
 
 // The stages, as bytes in flight in an SM.  Few are faster where the arithmetic keeps up:
-// 256 M elements of BF16 (gated norm forward, 8 x 128: 270 us with 192 KB, 233 with 96;
-// the norm alone 190 with 128 KB, 162 with 64; residual norm, 512: forward 363 with 192,
-// 350 with 96, 318 with 64; 7,168: 334 with 57, 316 with 86; its gradient, 512: 454 with
-// 144, 419 with 96; fp32, gated norm forward, 4 x 100: 254 with 154, 232 with 102).  The
-// gradient of the gated norm (404 +- 3 either way) and rows as pairs (residual norm
-// forward, 125: 403 with 64 KB, 360 with 160; backward, 33: 635 with 76, 598 with 152,
-// 663 with 203) are bound by more than the copies.
+// 256 M elements of BF16 (gated norm forward, 8 x 128: 277 us with 192 KB, 230 with 96;
+// the norm alone 188 with 128 KB, 168 with 64; residual norm, 512: forward 356 with 192,
+// 350 with 96, 313 with 64; 7,168: 335 with 115, 318 with 86; its gradient, 512: 456 with
+// 144, 426 with 96; 128 M of fp32, gated norm forward, 4 x 100: 250 with 154, 229 with 102).
+// The gradient of the gated norm (400-411 from 96 to 200) and rows as pairs (residual norm
+// forward, 125: 798 with 64 KB, 702 with 160; backward, 33: 1,250 with 76, 1,212 with 152,
+// 1,292 with 203) are bound by more than the copies.
 int bytes_in_flight(int op, bool bwd, int size, bool pairs) {
     if (pairs || (bwd && size == 2 && (op == OP_SIGMOID || op == OP_SILU))) return 160 * 1024;
     if (bwd || size == 4 || op == OP_SIGMOID || op == OP_SILU) return 96 * 1024;
@@ -54,9 +54,9 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
     r.tpr = 1;
     while (r.tpr * nv < pieces) r.tpr *= 2;
     if (!pairs && r.tpr > (size == 2 ? 32 : 256)) {
-        // whole warps, and as many on each scheduler where a tile is one row (BF16 forward,
-        // 1,280: 190 -> 162 us, 5,120: 209 -> 189; not for shorter rows of fp32: more rows
-        // in a tile are more bytes in flight, backward, 2,560: 415 -> 453)
+        // whole warps, and as many on each scheduler where a tile is one row (128 M elements,
+        // BF16 forward, 1,280: 180 -> 166 us, 5,120: 194 -> 175; not for shorter rows of fp32:
+        // more rows in a tile are more bytes in flight, backward, 2,560: 437 -> 444)
         const int unit = r.tpr > 256 ? 128 : 32;
         r.tpr = ((pieces + nv - 1) / nv + unit - 1) / unit * unit;
     }
@@ -73,12 +73,11 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
         ++r.arrays;
     r.array_bytes = r.rows * a.D * size;
     r.stage_bytes = r.arrays * r.array_bytes;
-    // SKEW pays in BF16 gradients of three arrays: gated norm (SiLU, 1,170 x 8 x 7,168) 154
-    // us, 185 without; residual norm where all threads have work on several rows (32,768 x
-    // 4,096 212 and 217; 18,724 x 7,168 231 and 208); of the norm alone, two arrays,
-    // 32,768 x 8 x 1,024 it is 313 and 258.
-    r.skew = size == 2 && bwd && !pairs && r.arrays == 3 && r.tpr > 32 &&
-             (op != OP_RESIDUAL || (a.D == r.tpr * 16 && r.work == kWork && r.rows > 1));
+    // SKEW pays in BF16 gradients of the gated norm, whose arithmetic is the longest (SiLU,
+    // 1,170 x 8 x 7,168 145 us, 187 without, 8,190 x 8 x 1,024 120 and 134; sigmoid, 65,536 x
+    // 2,048 225 and 244), not of the residual norm (32,768 x 4,096 225 and 219, 131,072 x
+    // 1,024 230 and 220, 16,384 x 8,192 225 and 206).
+    r.skew = size == 2 && bwd && !pairs && r.tpr > 32 && (op == OP_SIGMOID || op == OP_SILU);
     const int most = kRingBytes / r.stage_bytes;
     r.stages = r.skew ? most : bytes_in_flight(op, bwd, size, pairs) / r.stage_bytes;
     if (r.stages < 2) r.stages = 2;
@@ -334,7 +333,7 @@ template <int OP, bool BWD, typename T>
 cudaError_t launch_t(const NormArgs &a, const Ring &r, bool pairs, int blocks, cudaStream_t st) {
     if constexpr (sizeof(T) == 2 && (OP == OP_SIGMOID || OP == OP_SILU))
         if (a.strided) return launch_k<OP, BWD, T, false, false, true>(a, r, blocks, st);
-    if constexpr (sizeof(T) == 2 && BWD && OP != OP_NORM)
+    if constexpr (sizeof(T) == 2 && BWD && (OP == OP_SIGMOID || OP == OP_SILU))
         if (r.skew) return launch_k<OP, BWD, T, true, false, false>(a, r, blocks, st);
     return pairs ? launch_k<OP, BWD, T, false, true, false>(a, r, blocks, st)
                  : launch_k<OP, BWD, T, false, false, false>(a, r, blocks, st);
@@ -366,15 +365,16 @@ int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size, bool pairs) 
     const int sms = device_sms();
     // fewer than a few tiles per SM: the ring would not fill, and its start costs more
     if (!r.arrays || r.stages < 2 || r.tiles < 4ll * sms) return 0;
-    // forward passes with more than a warp per row are faster as shifted pieces (fp32,
-    // 20,011 x 1,001: 51 us, and 57 this way; BF16, 72,896 x 281: 81, and 57 this way)
+    // forward passes with more than a warp per row go as shifted pieces (fp32, 20,011 x
+    // 1,001: 49 us, and 55 this way; but BF16 52 and 41), those with a warp this way (BF16,
+    // 72,896 x 281: 54, and 79 as shifted pieces)
     if (pairs && !bwd && r.tpr > 32) return 0;
     // fp32 needs half as many threads for the same bytes in flight, and is often faster
-    // straight into registers (128 M elements): residual norm forward, 4,096 308 us, and
-    // 329 this way, 3,200 306 and 344; backward where all threads have work, 128 399 and
-    // 418, 4,096 414 and 447, but 8,192 451 and 419, 2,560 480 and 455, 96 463 and 432;
-    // gated norm of 4 x 128, forward 260 and 241, backward with a sigmoid 404 and 432, of
-    // 8 x 1,024 with SiLU 460 and 453.
+    // straight into registers (128 M elements): residual norm forward, 4,096 304 us, and
+    // 337 this way, 3,200 303 and 345; backward where all threads have work, 128 396 and
+    // 429, 4,096 408 and 444, but 8,192 446 and 428, 2,560 465 and 435, 96 457 and 435;
+    // gated norm of 4 x 128, forward 255 and 244, backward with a sigmoid 404 and 428, of
+    // 8 x 1,024 with SiLU 452 and 447.
     if (size == 4 && !pairs) {
         const bool full = a.D == r.tpr * 16;
         if (bwd ? full && r.work == kWork && r.tpr <= 256 && op != OP_SILU
@@ -382,10 +382,10 @@ int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size, bool pairs) 
             return 0;
     }
     // Tokens apart: a copy moves a token, and copies of less than 2 KB are too slow (BF16
-    // forward, 160,000 x 1 x 128: 30 us without the ring, 78 this way; 40,000 x 8 x 128:
-    // 55 and 49; 20,000 x 56 x 128: 184 and 126, backward 280 and 231).  Not for fp32
+    // forward, 160,000 x 1 x 128: 28 us without the ring, 79 this way; 40,000 x 8 x 128:
+    // 54 and 50; 20,000 x 56 x 128: 182 and 134, backward 278 and 229).  Not for fp32
     // (backward, 10,000 x 32 x 128: 130 and 141) nor rows of more than a warp (forward,
-    // 160,000 x 1 x 1,024: 172 and 190).
+    // 160,000 x 1 x 1,024: 170 and 190).
     if (a.strided && (size != 2 || !gated || r.tpr > 32 || a.heads * (long long)a.D * size < 2048))
         return 0;
     return sms;
