@@ -511,11 +511,15 @@ kda_status_t kda_linear_ce_forward(const kda_ce_desc_t *desc, const void *x, con
 /*
  * Its gradients for the adjoint d_loss [T] fp32 of loss (lse as the forward gave
  * it): dx [T, D] and d_weight [V, D] (either may be NULL), both overwritten.  Works
- * through the vocabulary in pieces of desc->piece columns (rounded up to 256): the
- * piece's logits are computed again, dz = d_loss (softmax - onehot) of the piece is
- * held in BF16 (F32: three BF16 terms), and both products read it.  Rows whose target is
- * ignored have no part in d_weight whatever x holds there (NaN, say), and dx 0.
- * Workspace: kda_linear_ce_workspace_size(desc, 1), 16-byte aligned.
+ * through the vocabulary in pieces of desc->piece columns (rounded up to 256; 0: 512 MiB
+ * of dz, 4,096 columns at least): the piece's logits are computed again, dz = d_loss
+ * (softmax - onehot) of the piece is held in BF16 (F32: three BF16 terms), and both
+ * products read it.  BF16: dz's rounding is up to 2^-8 of a term; a factor that all rows'
+ * d_loss share is not rounded.  Rows whose target is ignored have no part in d_weight
+ * whatever x holds there (NaN, say), and dx 0.
+ * Workspace: kda_linear_ce_workspace_size(desc, 1), 16-byte aligned: dz of a piece, a copy
+ * of x and, whatever the piece, one of all of W where a tensor map cannot read it as it is
+ * (F32 of more than 128 tokens, BF16 widths that are no multiples of 8).
  */
 kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, const void *weight,
                                     const void *targets, const float *lse, const float *d_loss,

@@ -485,8 +485,9 @@ __global__ void __launch_bounds__(256) split_sum_kernel(const float *acc, T *out
 
 // ------------------------------------------------------------------ host side
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-// Width of dz's buffer: at most 512 MiB of BF16 (or three fp32 terms) in whole
-// column tiles, unless the caller says.
+// Width of dz's buffer, unless the caller says: 512 MiB of BF16 (or three fp32 terms), but
+// 4,096 columns at least (from 65,536 tokens of BF16 on more bytes than that: 8 GiB at
+// 2^20), in equal pieces of whole column tiles.
 int piece_cols(const kda_ce_desc_t *d, int planes) {
     const long long all = (long long)cdiv(d->vocab, BN) * BN;
     long long cols = d->piece;

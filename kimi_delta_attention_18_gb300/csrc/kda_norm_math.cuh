@@ -30,8 +30,8 @@ enum { OP_NORM = 0, OP_SIGMOID = 1, OP_SILU = 2, OP_RESIDUAL = 3 };  // the firs
 
 // Rows streamed through shared memory (from 16-byte bases, enough of them; whole 16-byte
 // pieces, at most 8,192 channels, and with a gate in BF16 tokens apart too; or `pairs`:
-// contiguous, any width up to 1,024): its number of blocks, 0 where it does not apply,
-// and the launch.
+// contiguous, any width up to 512 forward, 1,024 (BF16) or 2,048 (fp32) backward): its
+// number of blocks, 0 where it does not apply, and the launch.
 int norm_ring_blocks(const NormArgs &a, int op, bool bwd, int size, bool pairs);
 cudaError_t launch_norm_ring(const NormArgs &a, int op, bool bwd, int size, bool pairs,
                              cudaStream_t st);
