@@ -526,6 +526,75 @@ kda_status_t kda_linear_ce_backward(const kda_ce_desc_t *desc, const void *x, co
                                     void *dx, void *d_weight, void *workspace,
                                     size_t workspace_bytes, int32_t *dev_status, void *stream);
 
+/* ------------------------------------------------------------------------
+ * A recurrent layer's parts beside the mixer: a linear recurrence whose state is
+ * a vector, the gated feed-forward block, dropout.  Same rules as above.
+ * ------------------------------------------------------------------------ */
+
+/* What a token writes into the state: x itself, or (1 - e^g) x (a mean of the past
+ * with weights that sum to 1, a GRU's update). */
+typedef enum { KDA_WRITE_ADD = 0, KDA_WRITE_MIX = 1 } kda_write_t;
+
+/* Problem description of the gated linear recurrence. */
+typedef struct {
+    int64_t x_stride;  /* elements from one token's x to the next's, 0 = channels: at   */
+    int64_t g_stride;  /* least channels, at most 2^30.  The same for g                 */
+    int32_t num_seqs;  /* N, 1..2^24                                                    */
+    int32_t tokens;    /* T, 0..2^30                                                    */
+    int32_t channels;  /* C, 1..2^20                                                    */
+    int32_t act_dtype; /* kda_dtype_t of x, h and their adjoints                        */
+    int32_t write;     /* kda_write_t                                                   */
+} kda_recurrence_desc_t;
+
+/*
+ * The gated linear recurrence over packed sequences: every channel has a state,
+ *     h_t = e^{g_t} h_{t-1} + w_t x_t,   w = 1 (KDA_WRITE_ADD) or 1 - e^{g_t} (KDA_WRITE_MIX),
+ * from the sequence's h0 on.
+ *   x           [T, C] act_dtype, tokens x_stride elements apart (a slice of a wider
+ *               projection's output).
+ *   g           [T, C] fp32 log-decays, normally <= 0 (-inf: the state starts anew).
+ *   h0          [N, C] fp32, or NULL (zero).
+ *   cu_seqlens  int32 [N+1] as for the prefill (sequences may be empty), or NULL with
+ *               N = 1: one sequence.
+ *   h           [T, C] act_dtype: the state after every token, rounded once; the
+ *               recurrence runs on in fp32.
+ *   h_final     [N, C] fp32, or NULL: the state after each sequence's last token (h0
+ *               where it has none); may equal h0.
+ * A malformed cu_seqlens is reported in dev_status (KDA_ERR_INVALID_ARG) and nothing or
+ * only part of the outputs is written; KDA_ERR_TIMEOUT there: a bounded wait gave up.
+ * The results do not depend on how the work was spread over the GPU.
+ * Workspace: kda_recurrence_workspace_size(desc), 16-byte aligned (0 up to 1,024 tokens and
+ * on invalid arguments).
+ * Pointers aligned to their element; C, strides and bases that are even (in elements) are
+ * the fast case.
+ */
+size_t kda_recurrence_workspace_size(const kda_recurrence_desc_t *desc);
+kda_status_t kda_recurrence_forward(const kda_recurrence_desc_t *desc, const void *x, const float *g,
+                                    const float *h0, const int32_t *cu_seqlens, void *h,
+                                    float *h_final, void *workspace, size_t workspace_bytes,
+                                    int32_t *dev_status, void *stream);
+
+/*
+ * Its gradients for the adjoints d_h [T, C] (act_dtype) and d_h_final [N, C] fp32 (NULL:
+ * zero), from x (read for KDA_WRITE_MIX only, may be NULL for KDA_WRITE_ADD), g, h0 and the
+ * forward's h [T, C] (h_{t-1} is taken as it was rounded there), all but x and g contiguous:
+ *     dx [T, C] act_dtype,  dg [T, C] fp32,  d_h0 [N, C] fp32 (NULL: skipped; may equal
+ *     d_h_final).
+ * Workspace as kda_recurrence_forward.
+ */
+kda_status_t kda_recurrence_backward(const kda_recurrence_desc_t *desc, const void *d_h,
+                                     const void *x, const float *g, const void *h, const float *h0,
+                                     const int32_t *cu_seqlens, const float *d_h_final, void *dx,
+                                     float *dg, float *d_h0, void *workspace, size_t workspace_bytes,
+                                     int32_t *dev_status, void *stream);
+
+/*
+ * One token of each of N sequences (desc->tokens = N): state_out = e^g state + w x [N, C]
+ * fp32, h [N, C] the same in act_dtype.  state_out may equal state (in place).
+ */
+kda_status_t kda_recurrence_step(const kda_recurrence_desc_t *desc, const void *x, const float *g,
+                                 const float *state, float *state_out, void *h, void *stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char *kda_status_string(kda_status_t status);
 

@@ -27,6 +27,11 @@ from ._native import (  # noqa: F401
     state_compose,
     state_transfer,
 )
+from ._layer import (  # noqa: F401
+    linear_recurrence,
+    linear_recurrence_backward,
+    linear_recurrence_step,
+)
 from ._lm import (  # noqa: F401
     embedding,
     embedding_backward,
@@ -40,7 +45,8 @@ from ._lm import (  # noqa: F401
 
 __all__ = ["KDAError", "PrefillDesc", "decode_step", "embedding", "embedding_backward", "gated_norm",
            "gated_norm_backward", "lib", "library_path", "linear_cross_entropy",
-           "linear_cross_entropy_backward", "num_checkpoints",
+           "linear_cross_entropy_backward", "linear_recurrence",
+           "linear_recurrence_backward", "linear_recurrence_step", "num_checkpoints",
            "prefill_backward",
            "prefill_backward_num_segments", "prefill_backward_workspace_size", "prefill_chunked", "prefill_chunked_ckpt", "prefill_chunked_gated",
            "prefill_ckpt_workspace_size", "prefill_combine", "prefill_desc",

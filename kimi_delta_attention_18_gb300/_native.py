@@ -91,8 +91,9 @@ def lib():
             L.kda_status_string.argtypes = [ctypes.c_int]
             L.kda_build_info.restype = ctypes.c_char_p
             L.kda_build_info.argtypes = []
-            from . import _lm
+            from . import _layer, _lm
             _lm.bind(L)
+            _layer.bind(L)
             _lib = L
     return _lib
 

@@ -1,0 +1,318 @@
+"""A recurrent layer's parts beside the mixer against their formulas in 64 bits: the gated
+linear recurrence, the gated feed-forward block and dropout, forward and backward.
+
+Bounds.  A rounding to BF16 is up to 2^-8 of the value, to fp32 2^-24.  What an operator
+sums in fp32 is held to a number of fp32 roundings of the terms' magnitudes, derived at
+each test's reference.
+"""
+import math
+
+import pytest
+import torch
+
+import kimi_delta_attention_18_gb300 as kda
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+ROUND = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+U = 2.0 ** -24
+
+
+def _gen(seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return g
+
+
+def _randn(shape, g, dt=torch.float32, std=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * std).to(dt)
+
+
+def _within(got, ref, bound, what=""):
+    assert got.shape == ref.shape
+    bad = ~((got.double() - ref).abs() <= bound)
+    assert not bad.any(), "%s: %d of %d off, worst %g, first at %s" % (
+        what, int(bad.sum()), bad.numel(), float((got.double() - ref).abs().max()),
+        bad.nonzero()[0].tolist())
+
+
+# ------------------------------------------------------------ linear recurrence
+#
+# A step in fp32 multiplies by a factor that is up to 2^-22 of itself off where it comes
+# from ex2.approx (its argument's rounding adds |g| e^g 2^-24 < 2^-25; slow decays are off
+# by one rounding), adds and rounds; a map's factor and term carry the same errors as the
+# steps they stand for, plus one rounding each per join.  Sixteen roundings a step of the
+# state that the terms' magnitudes would give (S below) cover it:
+#     E_t = e^g E_{t-1} + 16 2^-24 S_t.
+STEP = 16 * U
+
+
+def _recurrence64(x, g, h0, cu, write):
+    """h, h_final, and how far they may be off."""
+    x, a = x.double(), torch.exp(g.double())
+    if write == "mix":
+        x = x * -torch.expm1(g.double())
+    h, err = torch.empty_like(x), torch.empty_like(x)
+    N, C = len(cu) - 1, x.shape[1]
+    final = torch.zeros((N, C), device="cuda", dtype=torch.float64)
+    final_err = torch.zeros_like(final)
+    for n in range(N):
+        s = torch.zeros(C, device="cuda", dtype=torch.float64) if h0 is None else h0[n].double()
+        size, e = s.abs(), torch.zeros_like(s)
+        for t in range(cu[n], cu[n + 1]):
+            s = a[t] * s + x[t]
+            size = a[t] * size + x[t].abs()
+            e = a[t] * e + STEP * size
+            h[t], err[t] = s, e
+        final[n], final_err[n] = s, e
+    return h, err, final, final_err
+
+
+def _recurrence_grad64(d_h, x, g, h, h0, cu, d_final, write):
+    x, h, d, a = x.double(), h.double(), d_h.double(), torch.exp(g.double())
+    w = -torch.expm1(g.double()) if write == "mix" else torch.ones_like(a)
+    dx, dg, dx_err, dg_err = (torch.empty_like(x) for _ in range(4))
+    N, C = len(cu) - 1, x.shape[1]
+    d0 = torch.zeros((N, C), device="cuda", dtype=torch.float64)
+    d0_err = torch.zeros_like(d0)
+    for n in range(N):
+        u = torch.zeros(C, device="cuda", dtype=torch.float64) if d_final is None else d_final[n].double()
+        size, e = u.abs(), torch.zeros_like(u)
+        for t in range(cu[n + 1] - 1, cu[n] - 1, -1):
+            dh, size = d[t] + u, d[t].abs() + size
+            dx[t], dx_err[t] = w[t] * dh, w[t] * (e + STEP * size)
+            u, size = a[t] * dh, a[t] * size
+            e = a[t] * e + STEP * size
+            before = h[t - 1] if t > cu[n] else h[t] * 0 if h0 is None else h0[n].double()
+            dg[t] = u * (before - x[t] if write == "mix" else before)
+            dg_err[t] = (e + 2 * U * u.abs()) * (before.abs() + (x[t].abs() if write == "mix" else 0))
+        d0[n], d0_err[n] = u, e
+    return dx, dx_err, dg, dg_err, d0, d0_err
+
+
+def _gates(T, C, g, slow=True):
+    """Log-decays from a thousand tokens to one, some that keep or drop everything."""
+    rate = torch.exp(torch.rand(C, generator=g, device="cuda") * 6.9 - (6.9 if slow else 0.0))
+    v = -rate * torch.exp(0.5 * torch.randn((T, C), generator=g, device="cuda"))
+    pick = torch.rand((T, C), generator=g, device="cuda")
+    v = torch.where(pick < 0.01, torch.zeros_like(v), v)
+    return torch.where(pick > 0.99, torch.full_like(v, -math.inf), v)
+
+
+def _cu(lengths):
+    return torch.tensor([0] + list(lengths), device="cuda").cumsum(0).to(torch.int32)
+
+
+CASES = [  # lengths, channels
+    ([1], 1), ([0, 3, 0], 2), ([7], 3), ([127, 1], 64), ([128], 65), ([129], 63), ([300, 0, 724], 66),
+    ([1024], 2), ([1025], 130), ([0, 1200, 0, 0, 1, 127, 128, 129, 0], 67), ([400] * 5, 4),
+    ([4993], 5), ([2100, 37, 2600], 128), ([1] * 1300, 3), ([0] * 40 + [1500] + [0] * 40, 64),
+]
+
+
+@pytest.mark.parametrize("write", ["add", "mix"])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("lengths,C", CASES, ids=lambda v: str(v) if isinstance(v, int) else "n%d-t%d" % (len(v), sum(v)))
+def test_recurrence(lengths, C, act, write):
+    g = _gen(sum(lengths) + C)
+    T, N, dt = sum(lengths), len(lengths), DT[act]
+    cu = _cu(lengths)
+    x, gate = _randn((T, C), g, dt), _gates(T, C, g)
+    h0 = _randn((N, C), g) if C % 3 else None
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    h, h_final = kda.linear_recurrence(x, gate, h0, cu, write=write, dev_status=status)
+    ref, err, final, final_err = _recurrence64(x, gate, h0, cu.tolist(), write)
+    _within(h, ref, ROUND[act] * ref.abs() * (1 + 2 * U) + 2 * err, "h")
+    _within(h_final, final, final_err + U * final.abs(), "h_final")
+
+    d_h, d_final = _randn((T, C), g, dt), _randn((N, C), g) if C % 2 else None
+    got = kda.linear_recurrence_backward(d_h, x, gate, h, h0, cu, d_final, write=write,
+                                         dev_status=status)
+    dx, dx_err, dg, dg_err, d0, d0_err = _recurrence_grad64(d_h, x, gate, h, h0, cu.tolist(),
+                                                            d_final, write)
+    _within(got[0], dx, ROUND[act] * dx.abs() + 2 * dx_err, "dx")
+    _within(got[1], dg, U * dg.abs() + 2 * dg_err, "dg")
+    _within(got[2], d0, U * d0.abs() + d0_err, "d_h0")
+    assert int(status) == 0
+    # the same bits again, whatever order the tiles were worked in
+    again = kda.linear_recurrence(x, gate, h0, cu, write=write)
+    assert torch.equal(again[0], h) and torch.equal(again[1], h_final)
+    more = kda.linear_recurrence_backward(d_h, x, gate, h, h0, cu, d_final, write=write)
+    assert all(torch.equal(p, q) for p, q in zip(more, got))
+
+
+def test_recurrence_gradient_against_differences():
+    """Central differences of the library's own forward (fp32; h0, x and g moved by 2^-7: the
+    forward is linear in x and h0, and in g the third derivative adds 2^-14 / 6 of it)."""
+    g = _gen(3)
+    lengths, C = [5, 0, 9], 2
+    cu, T = _cu(lengths), 14
+    x, h0 = _randn((T, C), g), _randn((3, C), g)
+    gate = -torch.rand((T, C), generator=g, device="cuda") - 0.05
+    d_h, d_final = _randn((T, C), g), _randn((3, C), g)
+    for write in ("add", "mix"):
+        def value(x, gate, h0):
+            h, last = kda.linear_recurrence(x, gate, h0, cu, write=write)
+            return float((h.double() * d_h).sum() + (last.double() * d_final).sum())
+        h = kda.linear_recurrence(x, gate, h0, cu, write=write)[0]
+        dx, dg, d0 = kda.linear_recurrence_backward(d_h, x, gate, h, h0, cu, d_final, write=write)
+        step = 2.0 ** -7
+        # a difference divides the forward's fp32 errors (up to 2^-20 of a sum of about 40) by
+        # 2 step: 2.5e-3; the gradients are of order 1
+        for which, grad in (("x", dx), ("g", dg), ("h0", d0)):
+            src = {"x": x, "g": gate, "h0": h0}
+            for i in range(0, src[which].numel(), 3):
+                moved = []
+                for sign in (1, -1):
+                    m = dict(src)
+                    m[which] = src[which].clone()
+                    m[which].view(-1)[i] += sign * step
+                    moved.append(value(m["x"], m["g"], m["h0"]))
+                slope = (moved[0] - moved[1]) / (2 * step)
+                assert abs(slope - float(grad.view(-1)[i])) < 5e-3, (write, which, i)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [700, 3000])
+def test_recurrence_strided_and_odd_bases(T, act):
+    g, dt, C = _gen(T), DT[act], 70
+    wide, wide_g = _randn((T, 3, C), g, dt), _gates(T, 2 * C, g).view(T, 2, C)
+    for x, gate in ((wide[:, 1], wide_g[:, 1]), (wide.view(T, 3 * C)[:, 1:C + 1], wide_g[:, 0])):
+        h, last = kda.linear_recurrence(x, gate, write="mix")
+        plain, plain_last = kda.linear_recurrence(x.contiguous(), gate.contiguous(), write="mix")
+        assert torch.equal(h, plain) and torch.equal(last, plain_last)
+        got = kda.linear_recurrence_backward(h, x, gate, h, write="mix")
+        ref = kda.linear_recurrence_backward(h, x.contiguous(), gate.contiguous(), h, write="mix")
+        assert all(torch.equal(p, q) for p, q in zip(got, ref))
+
+
+def test_recurrence_of_growing_factors_and_infinities():
+    """Factors whose product overflows do not turn a zero state into NaN; a NaN and an infinity
+    stay in their channel and sequence, and g = -inf starts anew."""
+    T, C = 2600, 4
+    x, g = torch.zeros((T, C), device="cuda"), torch.full((T, C), 3.0, device="cuda")
+    cu = _cu([1300, 1300])
+    h, last = kda.linear_recurrence(x, g, None, cu)
+    assert bool((h == 0).all()) and bool((last == 0).all())
+    g.fill_(-0.5)
+    x.fill_(1.0)
+    x[100, 1] = math.nan
+    x[200, 2] = math.inf
+    g[700, 1] = g[700, 2] = -math.inf
+    h, last = kda.linear_recurrence(x, g, None, cu)
+    assert bool(torch.isfinite(h[:, [0, 3]]).all()) and bool(torch.isfinite(h[1300:]).all())
+    assert bool(torch.isnan(h[100:700, 1]).all()) and bool(torch.isinf(h[200:205, 2]).all())
+    # past the reset 0 * NaN and 0 * inf are NaN, as the formula says
+    assert bool(torch.isnan(h[700:1300, 1:3]).all())
+
+
+def test_recurrence_past_32_bits():
+    """More elements than 32 bits count; with e^-1 a step, 64 tokens decide the last ones."""
+    T, C = 70001, 65536
+    x = torch.empty((T, C), device="cuda", dtype=torch.bfloat16).normal_()
+    g = torch.full((T, C), -1.0, device="cuda")
+    h, last = kda.linear_recurrence(x, g)
+    tail = slice(T - 80, T)
+    ref, err, final, final_err = _recurrence64(x[tail], g[tail], None, [0, 80], "add")
+    _within(h[T - 16:], ref[64:], ROUND["bf16"] * ref[64:].abs() + 2 * err[64:] + 1e-26, "h")
+    _within(last, final, final_err + 1e-26, "h_final")
+    del last
+    dx, dg, d0 = kda.linear_recurrence_backward(h, x, g, h)
+    start = slice(0, 80)
+    ref = _recurrence_grad64(h[start], x[start], g[start], h[start], None, [0, 80], None, "add")
+    _within(dx[:16], ref[0][:16], ROUND["bf16"] * ref[0][:16].abs() + 2 * ref[1][:16] + 1e-24, "dx")
+    _within(dg[:16], ref[2][:16], U * ref[2][:16].abs() + 2 * ref[3][:16] + 1e-24, "dg")
+    ref = _recurrence_grad64(h[tail], x[tail], g[tail], h[tail], None, [0, 80], None, "add")
+    _within(dx[T - 79:], ref[0][1:], ROUND["bf16"] * ref[0][1:].abs() + 2 * ref[1][1:], "dx")
+    _within(dg[T - 79:], ref[2][1:], U * ref[2][1:].abs() + 2 * ref[3][1:], "dg")
+
+
+@pytest.mark.parametrize("write", ["add", "mix"])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("N,C", [(1, 1), (3, 7), (5, 64), (256, 1001), (33, 4096)])
+def test_recurrence_step(N, C, act, write):
+    g, dt = _gen(N + C), DT[act]
+    wide = _randn((N, 2, C), g, dt)
+    for x in (wide[:, 0].contiguous(), wide[:, 1]):
+        gate, state = _gates(N, C, g), _randn((N, C), g)
+        ref, err, final, final_err = _recurrence64(x, gate, state, list(range(N + 1)), write)
+        new = torch.full_like(state, math.nan)
+        h, got = kda.linear_recurrence_step(x, gate, state, write=write, state_out=new)
+        assert got is new
+        _within(got, final, final_err + U * final.abs(), "state")
+        _within(h, ref, ROUND[act] * ref.abs() * (1 + 2 * U) + 2 * err, "h")
+        h2, same = kda.linear_recurrence_step(x, gate, state, write=write)  # in place
+        assert same is state and torch.equal(state, new) and torch.equal(h2, h)
+
+
+def test_recurrence_steps_continue_a_prefill():
+    g, C = _gen(5), 96
+    lengths = [37, 1500, 4]
+    cu, T = _cu(lengths), sum(lengths)
+    x, gate = _randn((T, C), g), _gates(T, C, g)
+    h, last = kda.linear_recurrence(x, gate, None, cu, write="mix")
+    more, more_gate = _randn((6, 3, C), g), _gates(18, C, g).view(6, 3, C)
+    state = last.clone()
+    steps = [kda.linear_recurrence_step(more[i], more_gate[i], state, write="mix")[0] for i in range(6)]
+    one = torch.cat([torch.cat([x[cu[n]:cu[n + 1]], more[:, n]]) for n in range(3)])
+    one_gate = torch.cat([torch.cat([gate[cu[n]:cu[n + 1]], more_gate[:, n]]) for n in range(3)])
+    cu2 = _cu([n + 6 for n in lengths])
+    ref, err, final, final_err = _recurrence64(one, one_gate, None, cu2.tolist(), "mix")
+    _within(state, final, final_err, "state")
+    for n in range(3):
+        at = slice(int(cu2[n + 1]) - 6, int(cu2[n + 1]))
+        _within(torch.stack([s[n] for s in steps]), ref[at], err[at] + U * ref[at].abs(), "h")
+
+
+@pytest.mark.parametrize("T", [900, 5000])
+def test_recurrence_bad_sequences_are_reported(T):
+    """A malformed cu_seqlens: a status, no access outside the arrays."""
+    x, g = torch.zeros((T, 8), device="cuda"), torch.zeros((T, 8), device="cuda")
+    for cu in ([0, T - 1], [1, T], [0, 500, 400, T], [0, -3, T], [0, T + 7, T], [0, 2 ** 30, T]):
+        for backward in (False, True):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            seqs = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            if backward:
+                kda.linear_recurrence_backward(x, x, g, x, None, seqs, dev_status=status)
+            else:
+                kda.linear_recurrence(x, g, None, seqs, dev_status=status)
+            assert int(status) == 1, (cu, backward)
+
+
+def test_recurrence_states_may_be_updated_in_place():
+    g, C = _gen(8), 64
+    for lengths in ([300, 0, 5], [3000, 0, 41, 900]):
+        cu, T, N = _cu(lengths), sum(lengths), len(lengths)
+        x, gate, h0 = _randn((T, C), g), _gates(T, C, g), _randn((N, C), g)
+        h, last = kda.linear_recurrence(x, gate, h0, cu)
+        state = h0.clone()
+        h2, same = kda.linear_recurrence(x, gate, state, cu, h_final=state)
+        assert same is state and torch.equal(state, last) and torch.equal(h2, h)
+
+
+def test_recurrence_captured_and_on_another_stream():
+    g, C, T = _gen(9), 192, 6000
+    cu = _cu([2500, 0, 3500])
+    x, gate, h0 = _randn((T, C), g, torch.bfloat16), _gates(T, C, g), _randn((3, C), g)
+    d_h = _randn((T, C), g, torch.bfloat16)
+
+    def both():
+        h, last = kda.linear_recurrence(x, gate, h0, cu, write="mix")
+        return (h, last) + kda.linear_recurrence_backward(d_h, x, gate, h, h0, cu, last, write="mix")
+    want = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    h, last = kda.linear_recurrence(x, gate, h0, cu, write="mix", stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(h, want[0]) and torch.equal(last, want[1])
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = both()
+    for seed in (1, 2):
+        x.copy_(_randn((T, C), _gen(seed), torch.bfloat16))
+        want = both()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
