@@ -595,6 +595,44 @@ kda_status_t kda_recurrence_backward(const kda_recurrence_desc_t *desc, const vo
 kda_status_t kda_recurrence_step(const kda_recurrence_desc_t *desc, const void *x, const float *g,
                                  const float *state, float *state_out, void *h, void *stream);
 
+typedef enum { KDA_FFN_SIGMOID = 1, KDA_FFN_SILU = 2, KDA_FFN_GELU = 3 } kda_ffn_act_t;
+
+/* Problem description of the gated feed-forward block. */
+typedef struct {
+    int32_t tokens;    /* T, 0..2^24                                              */
+    int32_t width;     /* D, 1..2^17: the channels that it reads                  */
+    int32_t hidden;    /* F, 1..2^20: the channels that it writes                 */
+    int32_t act_dtype; /* kda_dtype_t of x, weight, h and their gradients         */
+    int32_t act;       /* kda_ffn_act_t: sigmoid, silu, or gelu (with the error   */
+                       /* function)                                               */
+} kda_ffn_desc_t;
+
+/*
+ * The gated feed-forward block up to its last projection: with weight [2, F, D] (the
+ * gate's projection, then the other one),
+ *     h = act(x weight[0]^T) * (x weight[1]^T),   x [T, D], h [T, F];
+ * the projections are never stored.  BF16: products of BF16 on tensor cores with fp32
+ * accumulation; F32: each operand as three BF16 terms, six products, to about fp32's
+ * own accuracy.  x and weight 16-byte aligned (tensor-map copies).  Workspace:
+ * kda_gated_ffn_workspace_size(desc, 0), 16-byte aligned (may be NULL when that is 0).
+ * dev_status, here and below: KDA_ERR_TIMEOUT if a bounded wait gave up.
+ */
+size_t kda_gated_ffn_workspace_size(const kda_ffn_desc_t *desc, int32_t backward);
+kda_status_t kda_gated_ffn_forward(const kda_ffn_desc_t *desc, const void *x, const void *weight,
+                                   void *h, void *workspace, size_t workspace_bytes,
+                                   int32_t *dev_status, void *stream);
+
+/*
+ * Its gradients for the adjoint d_h [T, F]: dx [T, D] and d_weight [2, F, D] (either may
+ * be NULL; d_weight zeros when T = 0).  The projections are computed again, in pieces of
+ * the F channels whose adjoints (BF16; F32: three BF16 terms) take 1 GiB at most, or 512
+ * channels.  BF16: those adjoints' rounding is up to 2^-8 of a term of dx and d_weight.
+ * Workspace: kda_gated_ffn_workspace_size(desc, 1), 16-byte aligned.
+ */
+kda_status_t kda_gated_ffn_backward(const kda_ffn_desc_t *desc, const void *d_h, const void *x,
+                                    const void *weight, void *dx, void *d_weight, void *workspace,
+                                    size_t workspace_bytes, int32_t *dev_status, void *stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char *kda_status_string(kda_status_t status);
 

@@ -16,6 +16,7 @@ from ._lm import _first, _fit, _is, _lib, _out, _ptr, _status, _stream, _workspa
 from ._native import _check
 
 WRITES = {"add": 0, "mix": 1}
+FFN_ACTS = {"sigmoid": 1, "silu": 2, "gelu": 3}
 
 
 class RecurrenceDesc(ctypes.Structure):
@@ -25,17 +26,25 @@ class RecurrenceDesc(ctypes.Structure):
                 ("write", ctypes.c_int32)]
 
 
+class FFNDesc(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int32), ("width", ctypes.c_int32), ("hidden", ctypes.c_int32),
+                ("act_dtype", ctypes.c_int32), ("act", ctypes.c_int32)]
+
+
 def bind(L):
     """Declare the C signatures of this module's entry points on the loaded library."""
-    P, Z = ctypes.c_void_p, ctypes.c_size_t
-    R = ctypes.POINTER(RecurrenceDesc)
+    P, I, Z = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    R, F = ctypes.POINTER(RecurrenceDesc), ctypes.POINTER(FFNDesc)
     for name, args in (
             ("kda_recurrence_forward", [R] + [P] * 7 + [Z, P, P]),
             ("kda_recurrence_backward", [R] + [P] * 11 + [Z, P, P]),
-            ("kda_recurrence_step", [R] + [P] * 6)):
+            ("kda_recurrence_step", [R] + [P] * 6),
+            ("kda_gated_ffn_forward", [F] + [P] * 4 + [Z, P, P]),
+            ("kda_gated_ffn_backward", [F] + [P] * 6 + [Z, P, P])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = ctypes.c_int, args
-    for name, args in (("kda_recurrence_workspace_size", [R]),):
+    for name, args in (("kda_recurrence_workspace_size", [R]),
+                       ("kda_gated_ffn_workspace_size", [F, I])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = Z, args
 
@@ -47,6 +56,15 @@ def _call(dev, name, *args):
         return _check(name, fn(*args, _stream(dev)))
     with torch.cuda.device(dev):
         _check(name, fn(*args, _stream(dev)))
+
+
+def _size(dev, name, *args):
+    """A workspace's size, which can depend on the device's SMs."""
+    fn = getattr(_lib(), name)
+    if torch._C._cuda_getDevice() == dev.index:
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
 
 # ------------------------------------------------------------ linear recurrence
@@ -165,3 +183,55 @@ def linear_recurrence_step(x, g, state, *, write="add", state_out=None, h=None, 
         _call(dev, "kda_recurrence_step", desc, x.data_ptr(), g.data_ptr(), state.data_ptr(),
               state_out.data_ptr(), h.data_ptr())
     return h, state_out
+
+
+# ------------------------------------------------------ gated feed-forward block
+
+def _ffn(x, weight, act):
+    dev, dtype = _first(x, "x", 2)
+    kind = FFN_ACTS.get(act)
+    if kind is None:
+        raise ValueError("act must be one of %s" % ", ".join(sorted(FFN_ACTS)))
+    _first(weight, "weight", 3)
+    T, D = x.shape
+    F = weight.shape[1]
+    _is(x, "x", x.dtype, x.shape, dev)
+    _is(weight, "weight", x.dtype, (2, F, D), dev)
+    return dev, FFNDesc(_fit(T), _fit(D), _fit(F), dtype, kind)
+
+
+def gated_ffn(x, weight, *, act="silu", h=None, workspace=None, dev_status=None, stream=None):
+    """The gated feed-forward block up to its last projection: ``act(x weight[0]^T) *
+    (x weight[1]^T)`` without storing the projections (see kda_gated_ffn_forward in kda.h):
+    x ``[T, D]``, weight ``[2, F, D]`` in x's dtype; act "silu", "gelu" or "sigmoid".
+    Returns h ``[T, F]``."""
+    if stream is not None:
+        return _k._on(stream, gated_ffn, x, weight, act=act, h=h, workspace=workspace,
+                      dev_status=dev_status)
+    dev, desc = _ffn(x, weight, act)
+    T, F = x.shape[0], weight.shape[1]
+    if h is None:
+        h = torch.empty((T, F), dtype=x.dtype, device=dev)
+    else:
+        _is(h, "h", x.dtype, (T, F), dev)
+    workspace, ws_len = _workspace(workspace, _size(dev, "kda_gated_ffn_workspace_size", desc, 0), dev)
+    _call(dev, "kda_gated_ffn_forward", desc, x.data_ptr(), weight.data_ptr(), h.data_ptr(),
+          workspace.data_ptr(), ws_len, _status(dev_status, dev))
+    return h
+
+
+def gated_ffn_backward(d_h, x, weight, *, act="silu", want_dx=True, want_d_weight=True,
+                       workspace=None, dev_status=None, stream=None):
+    """Gradients ``(dx [T, D], d_weight [2, F, D])`` of ``gated_ffn`` for the adjoint d_h
+    ``[T, F]``, from its inputs alone (see kda_gated_ffn_backward in kda.h)."""
+    if stream is not None:
+        return _k._on(stream, gated_ffn_backward, d_h, x, weight, act=act, want_dx=want_dx,
+                      want_d_weight=want_d_weight, workspace=workspace, dev_status=dev_status)
+    dev, desc = _ffn(x, weight, act)
+    _is(d_h, "d_h", x.dtype, (x.shape[0], weight.shape[1]), dev)
+    dx = _out(None, "dx", x) if want_dx else None
+    d_weight = _out(None, "d_weight", weight) if want_d_weight else None
+    workspace, ws_len = _workspace(workspace, _size(dev, "kda_gated_ffn_workspace_size", desc, 1), dev)
+    _call(dev, "kda_gated_ffn_backward", desc, d_h.data_ptr(), x.data_ptr(), weight.data_ptr(),
+          _ptr(dx), _ptr(d_weight), workspace.data_ptr(), ws_len, _status(dev_status, dev))
+    return dx, d_weight

@@ -18,7 +18,7 @@
 //               truncates), 64 columns per thread.
 // A is K-major with 128-byte swizzle, B (along W's channels) K-major with 64-byte
 // swizzle or (along the vocabulary) MN-major with 128-byte swizzle.
-#include "kda_ce_gemm.cuh"
+#include "kda_gemm.cuh"
 
 namespace kda {
 namespace {

@@ -1,5 +1,6 @@
-// What the cross entropy's products share: their arguments, tiles and epilogues.  The
-// kernels are in kda_ce.cu (BF16 operands) and kda_ce_w32.cu (an fp32 weight, few tokens).
+// What the products of the cross entropy and of the gated feed-forward block share: their
+// arguments, tiles and epilogues.  The kernels are in kda_gemm_kernel.cuh (BF16 operands)
+// and kda_ce_w32.cu (an fp32 weight, few tokens).
 #pragma once
 
 #include "kda_internal.cuh"
@@ -17,7 +18,10 @@ constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr uint32_t kTmemCols = 512;  // two 256-column accumulators
 
-enum { EPI_STATS = 0, EPI_DZ = 1, EPI_OUT = 2 };
+// EPI_GLU, EPI_DGLU: B's rows are taken from two matrices in turn, 32 of the first and 32 of
+// the second, so 64 accumulator columns are both projections of 32 of the block's channels.
+enum { EPI_STATS = 0, EPI_DZ = 1, EPI_OUT = 2, EPI_GLU = 3, EPI_DGLU = 4 };
+enum { ACT_SIGMOID = 1, ACT_SILU = 2, ACT_GELU = 3 };  // kda_ffn_act_t
 
 struct Targets {
     const void *ids;
@@ -39,7 +43,12 @@ struct Targets {
 
 struct GemmArgs {
     int M, N;                  // rows and columns of the product that exist
+    int cols;                  // columns of the outputs: N, or of one of EPI_GLU's matrices
     int k_blocks, splits, pairs;
+    // Operands of more than one matrix, [planes][groups][rows][pitch]: groups > 1 adds the
+    // matrices' products up (dx = da Wg + db Wu), batches > 1 keeps them apart (dWg, dWu).
+    int groups, batches;
+    int a_group, b_group;      // matrices in A's and B's planes
     int chunk;                 // FINE: stages per accumulator
     int m_tiles, n_tiles, bn;  // set at the launch; bn: columns per tile, a multiple of 64
     int b_row0;                // B's first row (of the vocabulary's piece)
@@ -54,13 +63,44 @@ struct GemmArgs {
     int pitch, planes;
     // BF16: the unit of dz (the largest |d_loss|, or its significand); EPI_OUT multiplies by it
     const float *unit;
-    // EPI_OUT: value (+ acc_in) to acc_out, both [splits][M][N] fp32, or to out
+    // EPI_OUT: value (+ acc_in) to acc_out, both [splits][batches][M][cols] fp32, or to out
+    // (batches out_batch elements apart)
+    long long out_batch;
     const float *acc_in;
     float *acc_out;
     void *out;
     int out_bf16, vec;
+    // EPI_GLU: act(a) b to out [M][out_ld].  EPI_DGLU: from d_h [M][out_ld] the adjoints of
+    // a and b to dz's first and second matrix.
+    int act, out_ld;
+    const void *d_h;
     int32_t *status;
 };
+
+// Arguments of a product of one matrix by another.
+inline GemmArgs one_product() {
+    GemmArgs p = {};
+    p.splits = p.groups = p.batches = p.a_group = p.b_group = 1;
+    return p;
+}
+
+// The activation of a gated block and its derivative.  ex2.approx and rcp.approx are within
+// 2^-22; the exponent's rounding adds |a| 2^-24 of it, where |a| is large a vanishing value.
+__device__ __forceinline__ void glu_act(int act, float a, float &f, float &df) {
+    if (act == ACT_GELU) {
+        const float cdf = 0.5f * erfcf(a * -0.70710678118654752f);
+        f = a * cdf;
+        df = fmaf(a * 0.39894228040143268f, exp2f(a * a * (-0.5f * kLog2e)), cdf);
+        return;
+    }
+    float e, p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-a * kLog2e));
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(p) : "f"(1.f + e));
+    // 1 - p = e p; e may have overflowed where p is 0
+    const float q = 1.f - p;
+    f = act == ACT_SILU ? a * p : p;
+    df = act == ACT_SILU ? p * fmaf(a, q, 1.f) : p * q;
+}
 
 // MN-major operand with 128-byte swizzle, as boxes of 64 elements x `rows` rows lay it
 // down: 8 rows (along K) of 128 bytes form an atom, atoms follow each other along
@@ -76,7 +116,7 @@ __device__ __forceinline__ uint64_t umma_desc_mn_sw128(uint32_t saddr, int rows)
 }
 
 struct Tile {
-    int m, n, split, kb0, kb1;
+    int m, n, split, batch, kb0, kb1;
 };
 template <int CTAS>
 __device__ __forceinline__ Tile tile_at(const GemmArgs &p, int w) {
@@ -84,7 +124,13 @@ __device__ __forceinline__ Tile tile_at(const GemmArgs &p, int w) {
     Tile t;
     const int per = p.m_tiles * p.n_tiles;
     t.split = w / per;
-    const int r = w - t.split * per, g = r / (G * p.n_tiles), q = r - g * G * p.n_tiles;
+    const int r = w - t.split * per;
+    t.batch = 0;
+    if (p.batches > 1) {
+        t.batch = t.split % p.batches;
+        t.split /= p.batches;
+    }
+    const int g = r / (G * p.n_tiles), q = r - g * G * p.n_tiles;
     const int gm = min(G, p.m_tiles - g * G);
     t.n = q / gm;
     t.m = g * G + (q - t.n * gm);
@@ -159,7 +205,7 @@ struct Row {
         y = -1;
         mx = -INFINITY;
         sum = lse2 = g = 0.f;
-        if (EPI != EPI_OUT && live) {
+        if ((EPI == EPI_STATS || EPI == EPI_DZ) && live) {
             y = p.y.at(row, t.n == 0 && half == 0);
             if (EPI == EPI_DZ) {
                 lse2 = p.lse[row] * kLog2e;
@@ -168,7 +214,7 @@ struct Row {
             }
             y = y >= 0 ? y - p.b_row0 : -1;
         }
-        if (EPI == EPI_OUT && BF16) g = *p.unit;
+        if (EPI == EPI_OUT && BF16) g = p.unit ? *p.unit : 1.f;
     }
 
     // 32 values as BF16 into half `h` of the warp's lines; what the rounding left stays
@@ -274,18 +320,19 @@ struct Row {
                                    __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
         __syncwarp();
         const bool narrow = BF16 && p.out && p.out_bf16;
-        const size_t part = (size_t)t.split * p.M * p.N;
-        float *o32 = p.out ? (float *)p.out : p.acc_out + part;
+        const size_t part = ((size_t)t.split * p.batches + t.batch) * p.M * p.cols;
+        const size_t ld = EPI == EPI_GLU ? p.out_ld : p.cols;
+        float *o32 = p.out ? (float *)p.out + t.batch * p.out_batch : p.acc_out + part;
         const float *in = p.acc_in ? p.acc_in + part : nullptr;
-        __nv_bfloat16 *o16 = (__nv_bfloat16 *)p.out;
+        __nv_bfloat16 *o16 = (__nv_bfloat16 *)p.out + t.batch * p.out_batch;
         if (p.vec) {  // widths and bases of whole pieces: four columns are in or out together
             const int col = c + 4 * (turn.lane & 7);
 #pragma unroll
             for (int it = 0; it < 8; ++it) {
                 const long long r = row0 + turn.row(it);
                 const uint4 u = turn.get(it);
-                if (r >= p.M || col >= p.N) continue;
-                const size_t at = (size_t)r * p.N + col;
+                if (r >= p.M || col >= p.cols) continue;
+                const size_t at = (size_t)r * ld + col;
                 float4 f = make_float4(__uint_as_float(u.x), __uint_as_float(u.y),
                                        __uint_as_float(u.z), __uint_as_float(u.w));
                 if (in) {
@@ -302,14 +349,101 @@ struct Row {
 #pragma unroll 4
             for (int r = 0; r < rows; ++r) {
                 float f = turn.word(r);
-                if (c + turn.lane >= p.N) continue;
-                const size_t at = (size_t)(row0 + r) * p.N + c + turn.lane;
+                if (c + turn.lane >= p.cols) continue;
+                const size_t at = (size_t)(row0 + r) * ld + c + turn.lane;
                 if (in) f += in[at];
                 if (narrow) o16[at] = __float2bfloat16_rn(f);
                 else o32[at] = f;
             }
         }
         __syncwarp();
+    }
+
+    // The warp's half lines (pieces 0-3) to `first` and, if given, pieces 4-7 to `second`: 32
+    // columns of each, 64 contiguous bytes of a row.
+    __device__ __forceinline__ void half_lines(const GemmArgs &p, const Turn &turn,
+                                               __nv_bfloat16 *first, __nv_bfloat16 *second,
+                                               size_t pitch) {
+        __syncwarp();
+#pragma unroll
+        for (int it = 0; it < 8; ++it) {
+            const int piece = turn.lane & 7;
+            const long long r = row0 + turn.row(it);
+            const uint4 u = turn.get(it);
+            __nv_bfloat16 *to = piece < 4 ? first : second;
+            if (r < p.M && to) *(uint4 *)(to + (size_t)r * pitch + 8 * (piece & 3)) = u;
+        }
+        __syncwarp();
+    }
+
+    // act(a) b of channels f .. f + 31
+    __device__ __forceinline__ void glu(const GemmArgs &p, const Tile &t, const Turn &turn, int f,
+                                        float (&a)[32], float (&b)[32]) {
+        if (f >= p.cols) return;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            float v, dv;
+            glu_act(p.act, a[i], v, dv);
+            a[i] = v * b[i];
+        }
+        if (!BF16) {
+            out32(p, t, turn, f, a);
+            return;
+        }
+        __nv_bfloat16 *out = (__nv_bfloat16 *)p.out + f;
+        put_bf16<false>(turn, 0, a);
+        if (p.vec && f + 32 <= p.cols) half_lines(p, turn, out, nullptr, p.out_ld);
+        else ragged(p, turn, out, p.out_ld, p.cols - f < 32 ? p.cols - f : 32);
+    }
+
+    // dz of channels f .. f + 31: d_h b act'(a) and d_h act(a), zeros past the last channel
+    // (dz's pitch is a multiple of 64, and the next products read whole steps of 64)
+    __device__ __forceinline__ void dglu(const GemmArgs &p, const Turn &turn, int f,
+                                         float (&a)[32], float (&b)[32]) {
+        if (f >= (p.cols + 63) / 64 * 64) return;
+        const int n = p.cols - f;
+        const size_t at = (size_t)row * p.out_ld + f;
+#pragma unroll
+        for (int i0 = 0; i0 < 32; i0 += 8) {
+            float d[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = 0.f;
+            if (live && p.vec && i0 < n) {  // pieces of eight are in or out together
+                if (p.planes == 1) {
+                    const uint4 u = *(const uint4 *)((const __nv_bfloat16 *)p.d_h + at + i0);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        d[2 * k] = __uint_as_float(w[k] << 16);
+                        d[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                    }
+                } else {
+                    *(float4 *)d = *(const float4 *)((const float *)p.d_h + at + i0);
+                    *(float4 *)(d + 4) = *(const float4 *)((const float *)p.d_h + at + i0 + 4);
+                }
+            } else if (live) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (i0 + k < n)
+                        d[k] = p.planes == 1 ? act_ld((const __nv_bfloat16 *)p.d_h, at + i0 + k)
+                                             : act_ld((const float *)p.d_h, at + i0 + k);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float v, dv;
+                glu_act(p.act, a[i0 + k], v, dv);
+                a[i0 + k] = d[k] * b[i0 + k] * dv;
+                b[i0 + k] = d[k] * v;
+            }
+        }
+        // One plane (BF16): dz is rounded to the products' operand type, 2^-8 of a term at
+        // most and at random, as large an error as the outputs' own rounding.
+        for (int pl = 0; pl < p.planes; ++pl) {
+            put_bf16<true>(turn, 0, a);
+            put_bf16<true>(turn, 1, b);
+            __nv_bfloat16 *to = p.dz + (size_t)(2 * pl) * p.M * p.pitch + f;
+            half_lines(p, turn, to, to + (size_t)p.M * p.pitch, p.pitch);
+        }
     }
 
     // Columns c0 + 64 q .. + 63 as two halves a, b.
@@ -323,7 +457,11 @@ struct Row {
                 b[i] *= g;
             }
         }
-        if (EPI == EPI_STATS) {
+        if (EPI == EPI_GLU) {
+            glu(p, t, turn, c / 2, a, b);
+        } else if (EPI == EPI_DGLU) {
+            dglu(p, turn, c / 2, a, b);
+        } else if (EPI == EPI_STATS) {
             stats(p, c, a);
             stats(p, c + 32, b);
         } else if (EPI == EPI_DZ) {
@@ -341,12 +479,13 @@ struct Row {
         } else if (BF16 && p.out && p.out_bf16 && !p.acc_in && p.vec && c + 64 <= p.N) {
             put_bf16<false>(turn, 0, a);
             put_bf16<false>(turn, 1, b);
-            lines(p, turn, (__nv_bfloat16 *)p.out + c, p.N);
+            lines(p, turn, (__nv_bfloat16 *)p.out + t.batch * p.out_batch + c, p.N);
         } else if (BF16 && p.out && p.out_bf16 && !p.acc_in && !p.vec) {
             if (c >= p.N) return;
             put_bf16<false>(turn, 0, a);
             put_bf16<false>(turn, 1, b);
-            ragged(p, turn, (__nv_bfloat16 *)p.out + c, p.N, p.N - c < 64 ? p.N - c : 64);
+            ragged(p, turn, (__nv_bfloat16 *)p.out + t.batch * p.out_batch + c, p.N,
+                   p.N - c < 64 ? p.N - c : 64);
         } else {
             if (c < p.N) out32(p, t, turn, c, a);
             if (c + 32 < p.N) out32(p, t, turn, c + 32, b);

@@ -316,3 +316,200 @@ def test_recurrence_captured_and_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+# ------------------------------------------------------ gated feed-forward block
+#
+# A projection a = sum x w: the tensor core adds steps of 16 terms with truncation, 2^-23 of
+# the running sum each; fp32 operands as three BF16 terms leave 2^-22 of a term, and their
+# accumulators of 32 steps are added up with a rounding each:
+#     |a - a64| <= (D / 16 + 40) 2^-23 sum |x w|.
+# The activation: exp and the reciprocal are within 2^-21, the exponent's rounding adds
+# |a| 2^-23, 1 - p is off by 2^-24 of 1; gelu's error function and its density (argument
+# a^2 / 2) the same with a^2.  Slopes: |f'| < 1.2, |f''| < 0.8.
+
+def _act64(a, act):
+    if act == "gelu":
+        cdf = 0.5 * torch.erfc(a * -math.sqrt(0.5))
+        return a * cdf, cdf + a * torch.exp(-0.5 * a * a) / math.sqrt(2 * math.pi)
+    p, q = torch.sigmoid(a), torch.sigmoid(-a)
+    return (p, p * q) if act == "sigmoid" else (a * p, p * (1 + a * q))
+
+
+def _ffn64(x, w, act, d_h=None, kind="f32"):
+    """(h, bound) or, with d_h, (dx, bound, dw, bound)."""
+    x, w, rnd = x.double(), w.double(), ROUND[kind]
+    D, F = x.shape[1], w.shape[1]
+    a, b = x @ w[0].T, x @ w[1].T
+    acc = (D / 16 + 40) * 2 * U
+    ea, eb = acc * (x.abs() @ w[0].abs().T), acc * (x.abs() @ w[1].abs().T)
+    f, df = _act64(a, act)
+    fuzz = 2.0 ** -20 + (a.abs() + a * a) * 2 * U
+    ef = 1.2 * ea + fuzz * torch.maximum(f.abs(), torch.ones_like(f) * 2.0 ** -4)
+    if d_h is None:
+        ref = f * b
+        return ref, b.abs() * ef + f.abs() * eb + ef * eb + (rnd + 2 * U) * ref.abs() + 1e-30
+    d = d_h.double()
+    da, db = d * b * df, d * f
+    eda = d.abs() * (b.abs() * (0.8 * ea + fuzz) + df.abs() * eb + ea * eb) + (rnd + 4 * U) * da.abs()
+    edb = d.abs() * ef + (rnd + 4 * U) * db.abs()
+    dx = da @ w[0] + db @ w[1]
+    sx = da.abs() @ w[0].abs() + db.abs() @ w[1].abs()
+    ex = eda @ w[0].abs() + edb @ w[1].abs() + (2 * F / 16 + 40) * 2 * U * sx + (rnd + U) * dx.abs()
+    dw = torch.stack([da.T @ x, db.T @ x])
+    sw = torch.stack([da.abs().T @ x.abs(), db.abs().T @ x.abs()])
+    ew = torch.stack([eda.T @ x.abs(), edb.T @ x.abs()]) + \
+        (len(x) / 16 + 40) * 2 * U * sw + (rnd + U) * dw.abs()
+    return dx, ex + 1e-30, dw, ew + 1e-30
+
+
+def _norm_error(got, ref):
+    return float((got.double() - ref).norm() / ref.norm())
+
+
+FFN = [  # T, D, F
+    (1, 1, 1), (1, 64, 64), (2, 7, 31), (3, 100, 33), (7, 515, 200), (8, 128, 1003), (9, 129, 65),
+    (16, 1000, 300), (31, 72, 257), (65, 64, 8), (128, 256, 640), (129, 520, 96), (256, 264, 1100),
+    (300, 90, 513), (700, 448, 2050), (1030, 100, 100),
+]
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "sigmoid"])
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D,F", FFN)
+def test_gated_ffn(T, D, F, kind, act):
+    g, dt = _gen(T + D + F), DT[kind]
+    x, w, d_h = _randn((T, D), g, dt), _randn((2, F, D), g, dt, 1.5 / math.sqrt(D)), _randn((T, F), g, dt)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    room = torch.full((T + 3, F), 7.0, device="cuda", dtype=dt)
+    h = kda.gated_ffn(x, w, act=act, h=room[:T], dev_status=status)
+    assert bool((room[T:] == 7).all())
+    ref, bound = _ffn64(x, w, act, kind=kind)
+    _within(h, ref, bound, "h")
+    dx, dw = kda.gated_ffn_backward(d_h, x, w, act=act, dev_status=status)
+    rx, bx, rw, bw = _ffn64(x, w, act, d_h, kind)
+    _within(dx, rx, bx, "dx")
+    _within(dw, rw, bw, "d_weight")
+    assert int(status) == 0
+    if T * F > 1000:
+        # errors at random: the outputs' rounding and, in the gradients, the adjoints' too,
+        # each 2^-9 of a value in the mean at most; fp32 a few units of 2^-24
+        most = {"bf16": 2.0 ** -8, "f32": 2.0 ** -19}[kind]
+        assert max(_norm_error(h, ref), _norm_error(dx, rx), _norm_error(dw, rw)) < most
+    only_x = kda.gated_ffn_backward(d_h, x, w, act=act, want_d_weight=False)
+    only_w = kda.gated_ffn_backward(d_h, x, w, act=act, want_dx=False)
+    assert torch.equal(only_x[0], dx) and only_x[1] is None
+    assert torch.equal(only_w[1], dw) and only_w[0] is None
+
+
+def test_gated_ffn_gradient_against_differences():
+    """Central differences of the library's own fp32 forward with steps of 2^-6: the third
+    derivative adds about 2^-13, the forward's errors (2^-20 of a sum of about 30) 2^-10."""
+    g = _gen(4)
+    T, D, F = 5, 12, 9
+    x, w, d_h = _randn((T, D), g), _randn((2, F, D), g, std=0.3), _randn((T, F), g)
+    for act in ("silu", "gelu", "sigmoid"):
+        dx, dw = kda.gated_ffn_backward(d_h, x, w, act=act)
+        for src, grad, other in ((x, dx, lambda m: (m, w)), (w, dw, lambda m: (x, m))):
+            for i in range(0, src.numel(), 7):
+                value = []
+                for sign in (1, -1):
+                    m = src.clone()
+                    m.view(-1)[i] += sign * 2.0 ** -6
+                    value.append(float((kda.gated_ffn(*other(m), act=act).double() * d_h).sum()))
+                slope = (value[0] - value[1]) * 2.0 ** 5
+                assert abs(slope - float(grad.view(-1)[i])) < 4e-3
+
+
+def test_gated_ffn_of_no_tokens_and_odd_outputs():
+    w = torch.randn(2, 24, 16, device="cuda").bfloat16()
+    x = torch.randn(40, 16, device="cuda").bfloat16()
+    assert kda.gated_ffn(x[:0], w).shape == (0, 24)
+    dx, dw = kda.gated_ffn_backward(x.new_empty(0, 24), x[:0], w)
+    assert dx.shape == (0, 16) and bool((dw == 0).all())
+    room = torch.zeros(40 * 24 + 8, device="cuda", dtype=torch.bfloat16)
+    for by in (0, 1, 4):  # an output that starts anywhere
+        h = kda.gated_ffn(x, w, h=room[by:by + 960].view(40, 24))
+        assert torch.equal(h, kda.gated_ffn(x, w))
+        d = room[by:by + 960].view(40, 24)
+        assert all(torch.equal(p, q) for p, q in zip(kda.gated_ffn_backward(d, x, w),
+                                                     kda.gated_ffn_backward(d.clone(), x, w)))
+
+
+@pytest.mark.parametrize("T", [1, 5, 40, 300])
+def test_gated_ffn_rows_stay_apart(T):
+    """NaN and infinity in a token's x or d_h reach no other token's h or dx."""
+    g = _gen(T)
+    x, w, d_h = (_randn(s, g, torch.bfloat16) for s in ((T, 64), (2, 96, 64), (T, 96)))
+    h, dx = kda.gated_ffn(x, w), kda.gated_ffn_backward(d_h, x, w)[0]
+    bad = T // 2
+    x2, d2 = x.clone(), d_h.clone()
+    x2[bad, 3], d2[bad, 5] = math.nan, math.inf
+    h2, dx2 = kda.gated_ffn(x2, w), kda.gated_ffn_backward(d2, x2, w)[0]
+    keep = torch.arange(T, device="cuda") != bad
+    assert torch.equal(h2[keep], h[keep]) and torch.equal(dx2[keep], dx[keep])
+    assert bool(torch.isnan(h2[bad]).all()) and bool(torch.isnan(dx2[bad]).all())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+def test_gated_ffn_in_pieces(kind):
+    """More tokens than 1 GiB of adjoints holds: dx adds up over pieces of the channels."""
+    g, dt = _gen(6), DT[kind]
+    T, D, F = 66000 if kind == "bf16" else 23000, 72, 8200
+    x, w = _randn((T, D), g, dt), _randn((2, F, D), g, dt, 0.12)
+    d_h = _randn((T, F), g, dt, 0.1)
+    dx, dw = kda.gated_ffn_backward(d_h, x, w)
+    most = {"bf16": 2.0 ** -8, "f32": 2.0 ** -19}[kind]
+    x6, w6, sum_w = x.double(), w.double(), 0
+    for i in range(0, T, 8192):
+        at = slice(i, i + 8192)
+        a, b = x6[at] @ w6[0].T, x6[at] @ w6[1].T
+        f, df = _act64(a, "silu")
+        da, db = d_h[at].double() * b * df, d_h[at].double() * f
+        assert _norm_error(dx[at], da @ w6[0] + db @ w6[1]) < most
+        sum_w = sum_w + torch.stack([da.T @ x6[at], db.T @ x6[at]])
+    assert _norm_error(dw, sum_w) < most
+
+
+def test_gated_ffn_past_32_bits():
+    """More elements of h than 32 bits count."""
+    g = _gen(7)
+    T, D, F = 2 ** 20 + 5, 64, 4104
+    x, w = _randn((T, D), g, torch.bfloat16), _randn((2, F, D), g, torch.bfloat16, 0.15)
+    h = kda.gated_ffn(x, w)
+    for at in (slice(0, 64), slice(T - 64, T)):
+        ref, bound = _ffn64(x[at], w, "silu", kind="bf16")
+        _within(h[at], ref, bound, "h")
+    h[:-64] = 0  # as d_h: only the last tokens have a part in d_weight
+    dx, dw = kda.gated_ffn_backward(h, x, w)
+    at = slice(T - 64, T)
+    rx, bx, rw, bw = _ffn64(x[at], w, "silu", h[at], "bf16")
+    _within(dx[at], rx, bx, "dx")
+    # the accumulators' truncation over the other tokens adds nothing to zeros
+    _within(dw, rw, bw, "d_weight")
+    assert bool((dx[:1000] == 0).all())
+
+
+def test_gated_ffn_captured_and_on_another_stream():
+    g, T, D, F = _gen(9), 200, 136, 300
+    x, w, d_h = (_randn(s, g, torch.bfloat16) for s in ((T, D), (2, F, D), (T, F)))
+
+    def both():
+        return (kda.gated_ffn(x, w), kda.gated_ffn(x[:3], w)) + kda.gated_ffn_backward(d_h, x, w)
+    want = both()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    h = kda.gated_ffn(x, w, stream=side)
+    dx, dw = kda.gated_ffn_backward(d_h, x, w, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert all(torch.equal(p, q) for p, q in zip((h, dx, dw), (want[0],) + want[2:]))
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = both()
+    for seed in (1, 2):
+        x.copy_(_randn((T, D), _gen(seed), torch.bfloat16))
+        want = both()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import kimi_delta_attention_18_gb300 as kda
-from kimi_delta_attention_18_gb300._layer import RecurrenceDesc
+from kimi_delta_attention_18_gb300._layer import FFNDesc, RecurrenceDesc
 
 OK, INVALID, UNSUPPORTED, WORKSPACE = range(4)
 A = 0x10000  # an address that is never touched
@@ -105,3 +105,64 @@ def test_recurrence_binding_refuses_tensors():
         kda.linear_recurrence_backward(x, x, g, x)
     with pytest.raises(ValueError, match="CUDA"):
         kda.linear_recurrence_step(x, g, g)
+
+
+def _ffn(**kw):
+    return _make(FFNDesc, dict(tokens=4, width=64, hidden=96, act_dtype=1, act=2), kw)
+
+
+BAD_FFN = [
+    (dict(tokens=-1), INVALID), (dict(width=0), INVALID), (dict(hidden=0), INVALID),
+    (dict(act_dtype=2), UNSUPPORTED), (dict(act=0), UNSUPPORTED), (dict(act=4), UNSUPPORTED),
+    (dict(tokens=2 ** 24 + 1), UNSUPPORTED), (dict(width=2 ** 17 + 1), UNSUPPORTED),
+    (dict(hidden=2 ** 20 + 1), UNSUPPORTED),
+]
+
+
+@pytest.mark.parametrize("kw,status", BAD_FFN, ids=str)
+def test_gated_ffn_refuses_descriptors(kw, status):
+    L, d = kda.lib(), _ffn(**kw)
+    assert L.kda_gated_ffn_workspace_size(d, 0) == 0 and L.kda_gated_ffn_workspace_size(d, 1) == 0
+    assert L.kda_gated_ffn_forward(d, A, A, A, A, 2 ** 40, None, None) == status
+    assert L.kda_gated_ffn_backward(d, A, A, A, A, A, A, 2 ** 40, None, None) == status
+
+
+def test_gated_ffn_refuses_pointers():
+    L = kda.lib()
+    for i, bad in ((0, None), (0, A + 8), (1, None), (1, A + 8), (2, None), (2, A + 1), (3, A + 2)):
+        p = [A, A, A, None]
+        p[i] = bad
+        assert L.kda_gated_ffn_forward(_ffn(), p[0], p[1], p[2], None, 0, p[3], None) == INVALID
+    for i, bad in ((0, None), (0, A + 1), (1, None), (1, A + 2), (2, None), (2, A + 4), (3, A + 1),
+                   (4, A + 1), (5, A + 2)):
+        p = [A, A, A, A, A, None]
+        p[i] = bad
+        assert L.kda_gated_ffn_backward(_ffn(), *p[:5], A, 2 ** 40, p[5], None) == INVALID
+    assert L.kda_gated_ffn_backward(_ffn(), A, A, A, None, None, None, 0, None, None) == OK  # nothing wanted
+    assert L.kda_gated_ffn_forward(_ffn(tokens=0), None, None, None, None, 0, None, None) == OK
+
+
+def test_gated_ffn_workspace():
+    L = kda.lib()
+    size = L.kda_gated_ffn_workspace_size
+    assert size(_ffn(), 0) == 0  # BF16 rows of whole 16-byte pieces are read as they are
+    d = _ffn(width=63)
+    assert size(d, 0) == 4 * 64 * 2 + 2 * 96 * 64 * 2
+    assert L.kda_gated_ffn_forward(d, A, A, A, None, 0, None, None) == WORKSPACE
+    assert L.kda_gated_ffn_forward(d, A, A, A, A, size(d, 0) - 1, None, None) == WORKSPACE
+    assert L.kda_gated_ffn_forward(d, A, A, A, A + 8, 2 ** 40, None, None) == WORKSPACE
+    assert size(_ffn(act_dtype=0), 0) == 3 * (4 + 2 * 96) * 64 * 2
+    assert L.kda_gated_ffn_backward(_ffn(), A, A, A, A, A, A, size(_ffn(), 1) - 1, None, None) == WORKSPACE
+    # the adjoints of a piece: 1 GiB at most, or 512 channels
+    assert size(_ffn(tokens=2 ** 18, hidden=2 ** 16), 1) < 2 ** 30 + 2 ** 18 * 64 * 4 + 2 ** 12
+    assert size(_ffn(tokens=2 ** 22, hidden=2 ** 16), 1) < 2 ** 22 * 512 * 4 + 2 ** 22 * 64 * 4 + 2 ** 12
+
+
+def test_gated_ffn_binding_refuses_tensors():
+    x, w = torch.zeros(4, 6), torch.zeros(2, 8, 6)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.gated_ffn(x, w)
+    with pytest.raises(ValueError, match="dimensions"):
+        kda.gated_ffn(x[0], w)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.gated_ffn_backward(x, x, w)
