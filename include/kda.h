@@ -633,6 +633,43 @@ kda_status_t kda_gated_ffn_backward(const kda_ffn_desc_t *desc, const void *d_h,
                                     const void *weight, void *dx, void *d_weight, void *workspace,
                                     size_t workspace_bytes, int32_t *dev_status, void *stream);
 
+/* Dropout whose mask is never stored: element (t, c) of a [T, D] array is kept where word
+ * c mod 4 of Philox 4x32-10 (counter ((t ceil(D / 4) + c / 4) + site 2^48, offset), key
+ * seed) is at least round(p 2^32), and kept values are divided by 1 - p (p as rounded). */
+typedef struct {
+    const int64_t *rng; /* device [2]: seed, offset; read when the kernel runs, so a captured */
+                        /* graph drops other elements once they have changed                  */
+    double p;           /* 0 <= p, and round(p 2^32) < 2^32                                   */
+    int32_t site;       /* 0..65535: which of the dropouts that share rng this is             */
+} kda_dropout_t;
+
+/*
+ * out = dropout of x, both [tokens, width] contiguous in act_dtype (tokens x width up to
+ * 2^42); out may equal x.  Dropped elements are 0 whatever x holds there.  The gradient is
+ * the same call on the adjoint of out.
+ */
+kda_status_t kda_dropout(const kda_dropout_t *dropout, int64_t tokens, int32_t width,
+                         int32_t act_dtype, const void *x, void *out, void *stream);
+
+/*
+ * kda_residual_norm_forward with y (required) dropped out before it is added:
+ *     h_out = h + scale dropout(y),   out = h_out r weight,
+ * and kda_residual_norm_backward with the mask again: dy (required) = scale dropout(dh).
+ * With p = 0 they give what the calls without dropout give.
+ */
+kda_status_t kda_residual_norm_dropout_forward(const kda_norm_desc_t *desc,
+                                               const kda_dropout_t *dropout, const void *h,
+                                               const void *y, const float *weight, float scale,
+                                               void *h_out, void *out, int32_t *dev_status,
+                                               void *stream);
+kda_status_t kda_residual_norm_dropout_backward(const kda_norm_desc_t *desc,
+                                                const kda_dropout_t *dropout, const void *d_out,
+                                                const void *d_h_out, const void *h_out,
+                                                const float *weight, float scale, void *dh, void *dy,
+                                                float *d_weight, void *workspace,
+                                                size_t workspace_bytes, int32_t *dev_status,
+                                                void *stream);
+
 /* Human-readable name of a status. Never NULL. */
 const char *kda_status_string(kda_status_t status);
 

@@ -28,6 +28,7 @@ from ._native import (  # noqa: F401
     state_transfer,
 )
 from ._layer import (  # noqa: F401
+    dropout,
     gated_ffn,
     gated_ffn_backward,
     linear_recurrence,
@@ -45,7 +46,7 @@ from ._lm import (  # noqa: F401
     residual_norm_backward,
 )
 
-__all__ = ["KDAError", "PrefillDesc", "decode_step", "embedding", "embedding_backward", "gated_ffn",
+__all__ = ["KDAError", "PrefillDesc", "decode_step", "dropout", "embedding", "embedding_backward", "gated_ffn",
            "gated_ffn_backward", "gated_norm",
            "gated_norm_backward", "lib", "library_path", "linear_cross_entropy",
            "linear_cross_entropy_backward", "linear_recurrence",

@@ -12,7 +12,8 @@ import ctypes
 import torch
 
 from . import _native as _k
-from ._lm import _first, _fit, _is, _lib, _out, _ptr, _status, _stream, _workspace
+from ._lm import (DropoutDesc, _dropout, _first, _fit, _is, _lib, _out, _ptr, _status, _stream,
+                  _workspace)
 from ._native import _check
 
 WRITES = {"add": 0, "mix": 1}
@@ -39,6 +40,7 @@ def bind(L):
             ("kda_recurrence_forward", [R] + [P] * 7 + [Z, P, P]),
             ("kda_recurrence_backward", [R] + [P] * 11 + [Z, P, P]),
             ("kda_recurrence_step", [R] + [P] * 6),
+            ("kda_dropout", [ctypes.POINTER(DropoutDesc), ctypes.c_int64, I, I] + [P] * 3),
             ("kda_gated_ffn_forward", [F] + [P] * 4 + [Z, P, P]),
             ("kda_gated_ffn_backward", [F] + [P] * 6 + [Z, P, P])):
         fn = getattr(L, name)
@@ -235,3 +237,22 @@ def gated_ffn_backward(d_h, x, weight, *, act="silu", want_dx=True, want_d_weigh
     _call(dev, "kda_gated_ffn_backward", desc, d_h.data_ptr(), x.data_ptr(), weight.data_ptr(),
           _ptr(dx), _ptr(d_weight), workspace.data_ptr(), ws_len, _status(dev_status, dev))
     return dx, d_weight
+
+
+# ------------------------------------------------------------------------ dropout
+
+def dropout(x, p, rng, *, site=0, out=None, stream=None):
+    """x ``[T, D]`` with each element kept (and divided by 1 - p) or, with probability p, 0;
+    the mask comes from a counter and is never stored (see kda_dropout in kda.h).  rng: a
+    device int64 tensor (seed, offset) that the kernel reads; ``site`` (0..65535) tells a
+    step's dropouts apart.  The gradient is the same call on the output's adjoint, with rng
+    holding what it held here.  ``out`` may be x."""
+    if stream is not None:
+        return _k._on(stream, dropout, x, p, rng, site=site, out=out)
+    dev, dtype = _first(x, "x", 2)
+    _is(x, "x", x.dtype, x.shape, dev)
+    desc = _dropout(p, rng, site, dev)
+    out = _out(out, "out", x)
+    T, D = x.shape
+    _call(dev, "kda_dropout", desc, T, _fit(D), dtype, x.data_ptr(), out.data_ptr())
+    return out

@@ -26,6 +26,10 @@ class NormDesc(ctypes.Structure):
                 ("gate", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class DropoutDesc(ctypes.Structure):
+    _fields_ = [("rng", ctypes.c_void_p), ("p", ctypes.c_double), ("site", ctypes.c_int32)]
+
+
 class EmbedDesc(ctypes.Structure):
     _fields_ = [("tokens", ctypes.c_int32), ("rows", ctypes.c_int32), ("width", ctypes.c_int32),
                 ("act_dtype", ctypes.c_int32), ("id_dtype", ctypes.c_int32),
@@ -42,12 +46,14 @@ class CrossEntropyDesc(ctypes.Structure):
 def bind(L):
     """Declare the C signatures of this module's entry points on the loaded library."""
     P, I, Z, F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t, ctypes.c_float
-    N, E, C = (ctypes.POINTER(t) for t in (NormDesc, EmbedDesc, CrossEntropyDesc))
+    N, E, C, K = (ctypes.POINTER(t) for t in (NormDesc, EmbedDesc, CrossEntropyDesc, DropoutDesc))
     for name, args in (
             ("kda_gated_norm_forward", [N] + [P] * 6),
             ("kda_gated_norm_backward", [N] + [P] * 8 + [Z, P, P]),
             ("kda_residual_norm_forward", [N] + [P] * 3 + [F] + [P] * 4),
             ("kda_residual_norm_backward", [N] + [P] * 4 + [F] + [P] * 4 + [Z, P, P]),
+            ("kda_residual_norm_dropout_forward", [N, K] + [P] * 3 + [F] + [P] * 4),
+            ("kda_residual_norm_dropout_backward", [N, K] + [P] * 4 + [F] + [P] * 4 + [Z, P, P]),
             ("kda_embedding_forward", [E] + [P] * 5),
             ("kda_embedding_backward", [E] + [P] * 4 + [Z, P, P]),
             ("kda_linear_ce_forward", [C] + [P] * 7 + [Z, P, P]),
@@ -223,14 +229,22 @@ def _residual(h, weight, eps, name):
     return dev, NormDesc(T, 0, 0, 1, _fit(D), dtype, 0, eps)
 
 
-def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, out=None,
-                  dev_status=None, stream=None):
+def _dropout(p, rng, site, dev):
+    """The descriptor of a dropout with probability p by the device's (seed, offset)."""
+    _is(rng, "rng", torch.int64, (2,), dev)
+    return DropoutDesc(rng.data_ptr(), p, _fit(site))
+
+
+def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, dropout=0.0, rng=None, site=0,
+                  h_out=None, out=None, dev_status=None, stream=None):
     """The residual stream's update and the next block's norm: ``h_out = h + scale y``
     and the RMS norm of it times weight (see kda_residual_norm_forward in kda.h).
-    h, y ``[T, D]``; without y, h_out is h.  Returns ``(h_out, out)``."""
+    h, y ``[T, D]``; without y, h_out is h.  With ``dropout`` > 0 y is dropped out first, by
+    rng and site as in ``dropout`` (see kda_residual_norm_dropout_forward in kda.h).  Returns
+    ``(h_out, out)``."""
     if stream is not None:
-        return _k._on(stream, residual_norm, h, y, weight, scale=scale, eps=eps, h_out=h_out, out=out,
-                      dev_status=dev_status)
+        return _k._on(stream, residual_norm, h, y, weight, scale=scale, eps=eps, dropout=dropout,
+                      rng=rng, site=site, h_out=h_out, out=out, dev_status=dev_status)
     dev, desc = _residual(h, weight, eps, "h")
     new_h = None
     if y is not None:
@@ -239,6 +253,15 @@ def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, ou
     elif h_out is not None:
         raise ValueError("h_out needs y")
     out = _out(out, "out", h)
+    if dropout:
+        if y is None:
+            raise ValueError("dropout needs y")
+        _check("kda_residual_norm_dropout_forward",
+               _lib().kda_residual_norm_dropout_forward(
+                   desc, _dropout(dropout, rng, site, dev), h.data_ptr(), y.data_ptr(),
+                   _ptr(weight), scale, new_h.data_ptr(), out.data_ptr(),
+                   _status(dev_status, dev), _stream(dev)))
+        return new_h, out
     _check("kda_residual_norm_forward",
            _lib().kda_residual_norm_forward(desc, h.data_ptr(), _ptr(y), _ptr(weight), scale,
                                             _ptr(new_h), out.data_ptr(),
@@ -247,14 +270,15 @@ def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, h_out=None, ou
 
 
 def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0, eps=1e-6,
-                           want_dy=True, want_d_weight=True, workspace=None, dev_status=None,
-                           stream=None):
+                           dropout=0.0, rng=None, site=0, want_dy=True, want_d_weight=True,
+                           workspace=None, dev_status=None, stream=None):
     """Gradients of ``residual_norm`` from its h_out, for the adjoints d_out of the
     norm and d_h_out (None: zero) of h_out: ``(dh, dy, d_weight)`` (see
-    kda_residual_norm_backward in kda.h).  With scale 1, dy is dh itself."""
+    kda_residual_norm_backward in kda.h).  With scale 1 and no dropout, dy is dh itself.  With
+    ``dropout``, rng and site as in the forward call (rng holding what it held then)."""
     if stream is not None:
         return _k._on(stream, residual_norm_backward, d_out, h_out, weight, d_h_out, scale=scale,
-                      eps=eps, want_dy=want_dy, want_d_weight=want_d_weight, workspace=workspace,
+                      eps=eps, dropout=dropout, rng=rng, site=site, want_dy=want_dy, want_d_weight=want_d_weight, workspace=workspace,
                       dev_status=dev_status)
     dev, desc = _residual(h_out, weight, eps, "h_out")
     _is(d_out, "d_out", h_out.dtype, h_out.shape, dev)
@@ -262,11 +286,20 @@ def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0
         _is(d_h_out, "d_h_out", h_out.dtype, h_out.shape, dev)
     L = _lib()
     dh = _out(None, "dh", h_out)
-    dy = _out(None, "dy", h_out) if want_dy and scale != 1.0 else None
+    dropped = bool(dropout) and want_dy
+    dy = _out(None, "dy", h_out) if dropped or (want_dy and scale != 1.0) else None
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(h_out.shape[1], dtype=torch.float32, device=dev)
         workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
+    if dropped:
+        _check("kda_residual_norm_dropout_backward",
+               L.kda_residual_norm_dropout_backward(
+                   desc, _dropout(dropout, rng, site, dev), d_out.data_ptr(), _ptr(d_h_out),
+                   h_out.data_ptr(), _ptr(weight), scale, dh.data_ptr(), dy.data_ptr(),
+                   _ptr(d_weight), _ptr(workspace), ws_len, _status(dev_status, dev),
+                   _stream(dev)))
+        return dh, dy, d_weight
     _check("kda_residual_norm_backward",
            L.kda_residual_norm_backward(desc, d_out.data_ptr(), _ptr(d_h_out), h_out.data_ptr(),
                                         _ptr(weight), scale, dh.data_ptr(), _ptr(dy),

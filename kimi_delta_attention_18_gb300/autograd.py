@@ -9,7 +9,10 @@ are fp32; they are cast to each input's dtype (BF16 q, k, v get BF16 gradients).
 Around the mixer: ``kda_gated_norm`` (x, gate, weight), ``kda_residual_norm`` (h, y,
 weight), ``kda_embedding`` (the table) and ``kda_linear_cross_entropy`` (x, weight),
 each with its library forward and backward; gradients have their inputs' dtypes
-(norm weights fp32).
+(norm weights fp32).  Of a recurrent layer: ``kda_linear_recurrence`` (x, g, h0),
+``kda_gated_ffn`` (x, weight) and ``kda_dropout`` (x); the residual norm drops y out too.
+A dropout keeps a copy of ``rng`` (seed, offset), so the program may move it on before
+the backward pass.
 
 The gradients are not differentiable themselves: a second derivative through one of
 these operations raises an error.
@@ -25,7 +28,7 @@ from __future__ import annotations
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import _lm
+from . import _layer, _lm
 from . import _native as _k
 
 
@@ -87,30 +90,36 @@ def kda_gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, dev_st
 
 class ResidualNorm(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, h, y, weight, scale, eps, dev_status):
-        h_out, out = _lm.residual_norm(h, y, weight, scale=scale, eps=eps, dev_status=dev_status)
-        ctx.save_for_backward(h_out, weight)
+    def forward(ctx, h, y, weight, scale, eps, dropout, rng, site, dev_status):
+        rng = rng.clone() if dropout and isinstance(rng, torch.Tensor) else rng
+        h_out, out = _lm.residual_norm(h, y, weight, scale=scale, eps=eps, dropout=dropout, rng=rng,
+                                       site=site, dev_status=dev_status)
+        ctx.save_for_backward(h_out, weight, rng)
         ctx.scale, ctx.eps, ctx.has_y, ctx.dev_status = scale, eps, y is not None, dev_status
+        ctx.dropout, ctx.site = dropout, site
         return (h_out, out) if ctx.has_y else out
 
     @staticmethod
     @once_differentiable
     def backward(ctx, *grads):
-        h_out, weight = ctx.saved_tensors
+        h_out, weight, rng = ctx.saved_tensors
         d_h, d_out = grads if ctx.has_y else (None, grads[0])
         d_out = torch.zeros_like(h_out) if d_out is None else d_out.contiguous()
         dh, dy, d_weight = _lm.residual_norm_backward(
             d_out, h_out, weight, None if d_h is None else d_h.contiguous(), scale=ctx.scale,
-            eps=ctx.eps, want_dy=ctx.has_y, want_d_weight=ctx.needs_input_grad[2],
-            dev_status=ctx.dev_status)
-        return dh, dy, d_weight, None, None, None
+            eps=ctx.eps, dropout=ctx.dropout, rng=rng, site=ctx.site, want_dy=ctx.has_y,
+            want_d_weight=ctx.needs_input_grad[2], dev_status=ctx.dev_status)
+        return dh, dy, d_weight, None, None, None, None, None, None
 
 
-def kda_residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, dev_status=None):
+def kda_residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, dropout=0.0, rng=None, site=0,
+                      dev_status=None):
     """Differentiable ``residual_norm``; returns ``(h_out, out)``."""
     if y is None:
-        return h, ResidualNorm.apply(h, None, weight, scale, eps, dev_status)
-    return ResidualNorm.apply(h, y, weight, scale, eps, dev_status)
+        if dropout:
+            raise ValueError("dropout needs y")
+        return h, ResidualNorm.apply(h, None, weight, scale, eps, 0.0, None, 0, dev_status)
+    return ResidualNorm.apply(h, y, weight, scale, eps, dropout, rng, site, dev_status)
 
 
 class Embedding(torch.autograd.Function):
@@ -166,3 +175,70 @@ def kda_linear_cross_entropy(x, weight, targets, *, ignore_index=-100, reduction
     loss = LinearCrossEntropy.apply(x, weight, targets, ignore_index, reduction == "mean",
                                     dev_status)
     return loss.sum() if reduction == "sum" else loss
+
+
+class LinearRecurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, h0, cu_seqlens, write, dev_status):
+        h, h_final = _layer.linear_recurrence(x, g, h0, cu_seqlens, write=write,
+                                              dev_status=dev_status)
+        ctx.save_for_backward(x, g, h0, cu_seqlens, h)
+        ctx.write, ctx.dev_status = write, dev_status
+        return h, h_final
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_h, d_h_final):
+        x, g, h0, cu_seqlens, h = ctx.saved_tensors
+        d_h = torch.zeros_like(h) if d_h is None else d_h.contiguous()
+        dx, dg, d_h0 = _layer.linear_recurrence_backward(
+            d_h, x, g, h, h0, cu_seqlens, None if d_h_final is None else d_h_final.contiguous(),
+            write=ctx.write, want_d_h0=ctx.needs_input_grad[2], dev_status=ctx.dev_status)
+        return dx, dg, d_h0, None, None, None
+
+
+def kda_linear_recurrence(x, g, h0=None, cu_seqlens=None, *, write="add", dev_status=None):
+    """Differentiable ``linear_recurrence``; returns ``(h, h_final)``."""
+    return LinearRecurrence.apply(x, g, h0, cu_seqlens, write, dev_status)
+
+
+class GatedFFN(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, act, dev_status):
+        ctx.save_for_backward(x, weight)
+        ctx.act, ctx.dev_status = act, dev_status
+        return _layer.gated_ffn(x, weight, act=act, dev_status=dev_status)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_h):
+        x, weight = ctx.saved_tensors
+        dx, d_weight = _layer.gated_ffn_backward(
+            d_h.contiguous(), x, weight, act=ctx.act, want_dx=ctx.needs_input_grad[0],
+            want_d_weight=ctx.needs_input_grad[1], dev_status=ctx.dev_status)
+        return dx, d_weight, None, None
+
+
+def kda_gated_ffn(x, weight, *, act="silu", dev_status=None):
+    """Differentiable ``gated_ffn``."""
+    return GatedFFN.apply(x, weight, act, dev_status)
+
+
+class Dropout(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, p, rng, site):
+        rng = rng.clone() if isinstance(rng, torch.Tensor) else rng
+        ctx.save_for_backward(rng)
+        ctx.p, ctx.site = p, site
+        return _layer.dropout(x, p, rng, site=site)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, d_out):
+        rng, = ctx.saved_tensors
+        return _layer.dropout(d_out.contiguous(), ctx.p, rng, site=ctx.site), None, None, None
+
+
+def kda_dropout(x, p, rng, *, site=0):
+    """Differentiable ``dropout``."""
+    return Dropout.apply(x, p, rng, site)

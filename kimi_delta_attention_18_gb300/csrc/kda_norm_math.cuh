@@ -10,6 +10,7 @@
 #pragma once
 
 #include "kda_internal.cuh"
+#include "kda_philox.cuh"
 #include "kda_vec.cuh"
 
 namespace kda {
@@ -24,9 +25,14 @@ struct NormArgs {
     long long x_stride, gate_stride;  // elements between tokens
     int heads, D, tpr, strided;
     float eps, scale, inv_d;
+    Drop drop;  // OP_DROP
 };
 
-enum { OP_NORM = 0, OP_SIGMOID = 1, OP_SILU = 2, OP_RESIDUAL = 3 };  // the first three: kda_gate_t
+// OP_DROP: the residual norm with y dropped out (its scale includes 1 / (1 - p)).  A kernel
+// clears y's dropped elements on the way in, dy's on the way out; between them it is
+// OP_RESIDUAL.
+enum { OP_NORM = 0, OP_SIGMOID = 1, OP_SILU = 2, OP_RESIDUAL = 3, OP_DROP = 4 };  // first: kda_gate_t
+constexpr bool is_residual(int op) { return op == OP_RESIDUAL || op == OP_DROP; }
 
 // Rows streamed through shared memory (from 16-byte bases, enough of them; whole 16-byte
 // pieces, at most 8,192 channels, and with a gate in BF16 tokens apart too; or `pairs`:
@@ -142,7 +148,7 @@ struct RowMath {
         for (int i = 0; i < NV; ++i) {
             f2 v[VP], g[VP], d[VP], w[VP];
             get2<T, VEC>(px[i], v);
-            if (GATED ? BWD : OP == OP_RESIDUAL && !BWD) get2<T, VEC>(pg[i], g);
+            if (GATED ? BWD : is_residual(OP) && !BWD) get2<T, VEC>(pg[i], g);
             if (BWD) {
                 get2<T, VEC>(pd[i], d);
                 if (KEEP) {
@@ -154,7 +160,7 @@ struct RowMath {
             }
 #pragma unroll
             for (int j = 0; j < VP; ++j) {
-                if (OP == OP_RESIDUAL && !BWD) v[j] = fma2(scale, g[j], v[j]);
+                if (is_residual(OP) && !BWD) v[j] = fma2(scale, g[j], v[j]);
                 a2[j & 1] = fma2(mul2(v[j], inv), v[j], a2[j & 1]);
                 if (BWD) {
                     f2 e = d[j];
@@ -187,7 +193,7 @@ struct RowMath {
         for (int i = 0; i < NV; ++i) {
             f2 v[VP], g[VP], d[VP], w[VP], o1[VP], o2[VP];
             get2<T, VEC>(px[i], v);
-            if (GATED || OP == OP_RESIDUAL) get2<T, VEC>(pg[i], g);
+            if (GATED || is_residual(OP)) get2<T, VEC>(pg[i], g);
             if (BWD) get2<T, VEC>(pd[i], d);
             if (KEEP) {
 #pragma unroll
@@ -198,7 +204,7 @@ struct RowMath {
 #pragma unroll
             for (int j = 0; j < VP; ++j) {
                 o2[j] = 0;
-                if (OP == OP_RESIDUAL && !BWD) {
+                if (is_residual(OP) && !BWD) {
                     o1[j] = fma2(scale, g[j], v[j]);
                     o2[j] = mul2(mul2(o1[j], rs), w[j]);
                 } else if (!BWD) {
@@ -221,7 +227,7 @@ struct RowMath {
                     }
                     dw[i][j] = fma2(e, n, dw[i][j]);
                     const f2 ew = mul2(e, w[j]);
-                    if (OP == OP_RESIDUAL) {
+                    if (is_residual(OP)) {
                         o1[j] = fma2(rk, v[j], fma2(ew, rs, g[j]));
                         o2[j] = mul2(scale, o1[j]);
                     } else {

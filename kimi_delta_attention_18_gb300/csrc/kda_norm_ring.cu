@@ -69,7 +69,7 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
     if (pairs && r.rows % (16 / size) != 0) return r;  // tiles would start anywhere
     r.tiles = (a.rows + r.rows - 1) / r.rows;
     r.arrays = 1 + (bwd ? 1 : 0);
-    if (op == OP_SIGMOID || op == OP_SILU || (op == OP_RESIDUAL && (bwd ? a.d_res : a.gate)))
+    if (op == OP_SIGMOID || op == OP_SILU || (is_residual(op) && (bwd ? a.d_res : a.gate)))
         ++r.arrays;
     r.array_bytes = r.rows * a.D * size;
     r.stage_bytes = r.arrays * r.array_bytes;
@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (APART ? warp > kWarps : threadIdx.x != kWork) return;
         const uint8_t *src[3] = {(const uint8_t *)p.x, nullptr, nullptr};
         int n = 1;
-        const void *second = OP == OP_RESIDUAL && BWD ? p.d_res : p.gate;
+        const void *second = is_residual(OP) && BWD ? p.d_res : p.gate;
         if (OP != OP_NORM && second) src[n++] = (const uint8_t *)second;
         if (BWD) src[n++] = (const uint8_t *)p.d_out;
         const long long row_bytes = p.D * (long long)sizeof(T);
@@ -194,8 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     };
-    RowMath<OP, BWD, T, VEC, NV, !SKEW> math;
+    RowMath<is_residual(OP) ? OP_RESIDUAL : OP, BWD, T, VEC, NV, !SKEW> math;
     math.begin(load_w);
+    const Keep keep(OP == OP_DROP ? p.drop : Drop{});
     bool failed = false;  // a wait gave up: go through the motions, store nothing
     P px[NV], pg[NV], pd[NV];
     auto row_of = [&](long long t) { return t * r.rows + group; };
@@ -252,11 +253,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             auto put = [&](void *to, f2 (&o)[VP]) {
                 float v[VEC];
                 floats<VEC>(o, v);
+                if constexpr (OP == OP_DROP && BWD)
+                    if (to == p.o2) keep_floats(v, keep.bits<VEC, false>(row, c));
                 if constexpr (PAIRS) P::store((T *)to + row * p.D + c, v, c + 1 < p.D);
                 else P::store((T *)to + row * p.D + c, v);
             };
             if (p.o1) put(p.o1, a1);
-            if ((BWD || OP == OP_RESIDUAL) && p.o2) put(p.o2, a2);
+            if ((BWD || is_residual(OP)) && p.o2) put(p.o2, a2);
         });
     };
     int i = 0;
@@ -287,6 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             wait(full(i % r.stages), (i / r.stages) & 1);
             load(t, i);
             release(i);  // the stage is in registers
+            if constexpr (OP == OP_DROP && !BWD) {
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    keep_piece(pg[k], keep.bits<VEC, false>(row_of(t), column(k)));
+            }
             float ss, se;
             math.sums(p, px, pg, pd, load_w, ss, se);
             warp_sums(ss, se, r.tpr < 32 ? r.tpr : 32);
@@ -353,6 +361,7 @@ cudaError_t launch_b(const NormArgs &a, const Ring &r, int op, int size, bool pa
         case OP_NORM: return launch_op<OP_NORM, BWD>(a, r, size, pairs, blocks, st);
         case OP_SIGMOID: return launch_op<OP_SIGMOID, BWD>(a, r, size, pairs, blocks, st);
         case OP_SILU: return launch_op<OP_SILU, BWD>(a, r, size, pairs, blocks, st);
+        case OP_DROP: return launch_op<OP_DROP, BWD>(a, r, size, pairs, blocks, st);
     }
     return launch_op<OP_RESIDUAL, BWD>(a, r, size, pairs, blocks, st);
 }

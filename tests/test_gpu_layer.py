@@ -11,6 +11,8 @@ import pytest
 import torch
 
 import kimi_delta_attention_18_gb300 as kda
+from kimi_delta_attention_18_gb300 import autograd
+from oracle.philox import keep_mask
 
 pytestmark = pytest.mark.gpu
 
@@ -513,3 +515,257 @@ def test_gated_ffn_captured_and_on_another_stream():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(out, want))
+
+
+# ------------------------------------------------------------------------ dropout
+
+def _mask(rows, D, p, rng, site):
+    """The mask and its factor from the oracle's generator, as 64-bit tensors."""
+    seed, offset = rng.tolist()
+    rows = range(rows) if isinstance(rows, int) else rows
+    mask, factor = keep_mask(rows, D, p, seed, offset, site)
+    return torch.from_numpy(mask).cuda(), factor
+
+
+def _rng(seed, offset=None):
+    return torch.tensor([seed, 3 * seed + 1 if offset is None else offset], device="cuda")
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D", [(1, 1), (1, 5), (3, 64), (7, 1001), (33, 250), (257, 4096), (5, 20003)])
+def test_dropout(T, D, kind):
+    g, dt = _gen(T * D), DT[kind]
+    for p, rng, site in ((0.1, _rng(D), 0), (0.5, _rng(-T, 2 ** 62 + 5), 65535), (0.0, _rng(1), 3)):
+        x = _randn((T, D), g, dt)
+        mask, factor = _mask(T, D, p, rng, site)
+        x[~mask] = math.nan  # a dropped element is 0 whatever it was
+        room = torch.full((T * D + 9,), 7.0, device="cuda", dtype=dt)
+        for by in (0, 1):  # an aligned output and one that is not
+            out = kda.dropout(x, p, rng, site=site, out=room[by:by + T * D].view(T, D))
+            ref = torch.where(mask, x.double() * factor, 0.0)
+            # the factor is rounded to fp32, the product too
+            _within(out, ref, (ROUND[kind] + 2 * U) * ref.abs(), "dropout")
+            assert bool((room[by + T * D:] == 7).all()) and (by == 0 or float(room[0]) == float(out0))
+            out0 = out.view(-1)[0].clone()
+        if p == 0:
+            assert torch.equal(out, x)
+        same = kda.dropout(x, p, rng, site=site, out=x)
+        assert same is x and torch.equal(x, out)
+
+
+def test_dropout_of_almost_everything_and_of_no_rows():
+    x = torch.ones((500, 1000), device="cuda")
+    assert bool((kda.dropout(x, 1 - 2.0 ** -32, _rng(4)) == 0).all())  # 2^-32 x 5e5 are kept
+    assert kda.dropout(x[:0], 0.3, _rng(4)).shape == (0, 1000)
+
+
+def test_dropout_masks_are_apart():
+    """Another seed, offset or site is another mask, whose share of kept elements is as told
+    (five deviations)."""
+    x = torch.ones((1000, 1000), device="cuda")
+    calls = [(_rng(1, 2), 0), (_rng(2, 2), 0), (_rng(1, 3), 0), (_rng(1, 2), 1),
+             (_rng(1 + 2 ** 40, 2), 0), (_rng(1, 2 + 2 ** 40), 0)]
+    masks = [kda.dropout(x, 0.25, r, site=s) != 0 for r, s in calls]
+    for i, m in enumerate(masks):
+        assert abs(float(m.double().mean()) - 0.75) < 5 * math.sqrt(0.25 * 0.75 / 1e6)
+        for n in masks[:i]:  # both kept: 0.75^2
+            assert abs(float((m & n).double().mean()) - 0.5625) < 5 * math.sqrt(0.5625 * 0.4375 / 1e6)
+
+
+def test_dropout_past_32_bits():
+    T, D = 70001, 65540
+    x = torch.ones((T, D), device="cuda", dtype=torch.bfloat16)
+    out = kda.dropout(x, 0.5, _rng(11), site=9)
+    rows = [0, 1, 65535, 65536, 65537, T - 1]
+    mask, _ = _mask(rows, D, 0.5, _rng(11), 9)
+    assert torch.equal(out[rows], mask.bfloat16() * 2)
+
+
+NORMS = [  # T, D, elements off the 16-byte boundary
+    (1, 1, 0), (5, 64, 0), (3, 250, 0), (6, 1001, 0), (4, 7168, 0), (2, 16384, 0), (9, 100, 1),
+    (3, 2000, 1), (10000, 512, 0), (40000, 125, 0), (90000, 33, 0), (5000, 2048, 0), (3000, 7168, 0),
+    (1500, 5120, 0), (2600, 1001, 0),
+]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D,by", NORMS)
+def test_residual_norm_with_dropout(T, D, by, kind):
+    """Rows in pieces, shifted pieces, pairs and elements, streamed and not.  Bounds: an output's
+    rounding, and 2^-18 of the terms behind it for fp32 sums over a row and rsqrt."""
+    g, dt, p, scale, site, eps = _gen(T + D), DT[kind], 0.3, 0.5, 7, 1e-5
+    rng = _rng(T + D)
+    mask, factor = _mask(T, D, p, rng, site)
+
+    def array(std=1.0):
+        t = torch.empty(T * D + by, device="cuda", dtype=dt)[by:].view(T, D)
+        return t.copy_(_randn((T, D), g, dt, std))
+    h, y, d_out, d_h = array(2.0), array(), array(), array()
+    y[~mask] = math.nan
+    w = 1 + 0.1 * _randn((D,), g)
+    drop = dict(dropout=p, rng=rng, site=site, scale=scale, eps=eps)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    h_out, out = kda.residual_norm(h, y, w, dev_status=status, h_out=array(), out=array(), **drop)
+    add = torch.where(mask, y.double() * (scale * factor), 0.0)
+    ref = h.double() + add
+    terms = h.double().abs() + add.abs()
+    _within(h_out, ref, ROUND[kind] * ref.abs() + 2.0 ** -21 * terms, "h_out")
+    r = (ref.pow(2).mean(-1, keepdim=True) + eps).rsqrt()
+    ref = ref * r * w.double()
+    _within(out, ref, ROUND[kind] * ref.abs() + 2.0 ** -18 * terms * r * w.abs(), "out")
+
+    dh, dy, dw = kda.residual_norm_backward(d_out, h_out, w, d_h, dev_status=status, **drop)
+    v = h_out.double()
+    r = (v.pow(2).mean(-1, keepdim=True) + eps).rsqrt()
+    n, e = v * r, d_out.double() * w.double()
+    ref = d_h.double() + r * (e - n * (e * n).mean(-1, keepdim=True))
+    terms = d_h.double().abs() + r * (e.abs() + n.abs() * (e * n).abs().mean(-1, keepdim=True))
+    _within(dh, ref, ROUND[kind] * ref.abs() + 2.0 ** -18 * terms, "dh")
+    ref = torch.where(mask, ref * (scale * factor), 0.0)
+    _within(dy, ref, ROUND[kind] * ref.abs() + 2.0 ** -18 * terms * scale * factor * mask, "dy")
+    ref, terms = (d_out.double() * n).sum(0), (d_out.double() * n).abs().sum(0)
+    _within(dw, ref, 2.0 ** -18 * terms, "d_weight")
+    assert int(status) == 0
+    # without dy the mask has no part
+    plain = kda.residual_norm_backward(d_out, h_out, w, d_h, want_dy=False, **drop)
+    assert torch.equal(plain[0], dh) and plain[1] is None
+    # the same norm without dropout: p = 0 through the calls' C form
+    zero = kda._lm.DropoutDesc(rng.data_ptr(), 0.0, 0)
+    desc = kda._lm.NormDesc(T, 0, 0, 1, D, kda._lm._ACT[dt], 0, eps)
+    y = array()
+    a, b = kda.residual_norm(h, y, w, scale=scale, eps=eps)
+    a2, b2 = torch.empty_like(a), torch.empty_like(b)
+    assert kda.lib().kda_residual_norm_dropout_forward(
+        desc, zero, h.data_ptr(), y.data_ptr(), w.data_ptr(), scale, a2.data_ptr(), b2.data_ptr(),
+        None, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(a, a2) and torch.equal(b, b2)
+
+
+def test_dropout_captured_with_a_generator_that_moves_on():
+    """A graph reads seed and offset when it runs: the captured step moves the offset on."""
+    g, T, D = _gen(12), 300, 136
+    x, y = _randn((T, D), g, torch.bfloat16), _randn((T, D), g, torch.bfloat16)
+    rng = _rng(77, 0)
+
+    def step():
+        d = kda.dropout(x, 0.2, rng, site=1)
+        h, n = kda.residual_norm(x, y, None, dropout=0.4, rng=rng, site=2)
+        return (d, h, n) + kda.residual_norm_backward(y, h, None, x, dropout=0.4, rng=rng, site=2)[:2]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    d = kda.dropout(x, 0.2, rng, site=1, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(d, step()[0])
+    with torch.cuda.stream(side):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            out = step()
+            rng[1] += 1
+    rng[1] = 0
+    seen = []
+    for i in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        seen.append(out[0].clone())
+        now = rng.clone()
+        rng[1] = i
+        want = step()
+        rng.copy_(now)
+        assert int(now[1]) == i + 1 and all(torch.equal(p, q) for p, q in zip(out, want))
+    assert not torch.equal(seen[0], seen[1])
+
+
+# --------------------------------------------------------- differentiable forms
+
+def test_differentiable_forms_of_a_layer():
+    """A layer as it is trained, residual norm with dropout -> recurrence -> residual norm with
+    dropout -> feed-forward block -> norm, against the same layer in 64 bits (masks from the
+    oracle).  fp32: a chain of operators each within about 2^-20 of its outputs' size."""
+    g, T, D, F = _gen(15), 61, 40, 56
+    cu = _cu([20, 0, 41])
+    rng, p = _rng(5), 0.25
+    leaf = lambda *shape, std=1.0: _randn(shape, g, std=std).requires_grad_()  # noqa: E731
+    h, y, gate_x = leaf(T, D), leaf(T, D), leaf(T, D)
+    w1, w2, ffn, down = leaf(D), leaf(D), leaf(2, F, D, std=0.2), leaf(D, F, std=0.2)
+    h0 = leaf(3, D)
+    leaves = [h, y, gate_x, w1, w2, ffn, down, h0]
+    d_end, d_last = _randn((T, D), g), _randn((3, D), g)
+
+    keep = rng.clone()
+    a, n = autograd.kda_residual_norm(h, y, w1, scale=0.5, dropout=p, rng=rng, site=1)
+    s, last = autograd.kda_linear_recurrence(n, -torch.nn.functional.softplus(gate_x), h0, cu, write="mix")
+    b, n = autograd.kda_residual_norm(a, s, w2, dropout=p, rng=rng, site=2)
+    f = autograd.kda_gated_ffn(n, ffn, act="gelu")
+    end = b + autograd.kda_dropout(f @ down.T, p, rng, site=3)
+    rng += 1  # the program moves on; the backward pass needs what was
+    ((end * d_end).sum() + (last * d_last).sum()).backward()
+    got = [t.grad.clone() for t in leaves]
+
+    ref = [t.detach().double().requires_grad_() for t in leaves]
+    h, y, gate_x, w1, w2, ffn, down, h0 = ref
+    m = [torch.where(mask, factor, 0.0) for mask, factor in (_mask(T, D, p, keep, s) for s in (1, 2, 3))]
+    norm = lambda v, w: v * (v.pow(2).mean(-1, keepdim=True) + 1e-6).rsqrt() * w  # noqa: E731
+    a = h + 0.5 * m[0] * y
+    n, decay = norm(a, w1), -torch.nn.functional.softplus(gate_x)
+    rows, ends = [], []
+    for i in range(3):
+        state = h0[i]
+        for t in range(int(cu[i]), int(cu[i + 1])):
+            state = torch.exp(decay[t]) * state - torch.expm1(decay[t]) * n[t]
+            rows.append(state)
+        ends.append(state)
+    b = a + m[1] * torch.stack(rows)
+    n = norm(b, w2)
+    f = torch.nn.functional.gelu(n @ ffn[0].T) * (n @ ffn[1].T)
+    want = b + m[2] * (f @ down.T)
+    ((want * d_end).sum() + (torch.stack(ends) * d_last).sum()).backward()
+    assert _norm_error(end.detach(), want.detach()) < 2.0 ** -17
+    for name, x, r in zip("h y gate w1 w2 ffn down h0".split(), got, ref):
+        assert _norm_error(x, r.grad) < 2.0 ** -16, (name, _norm_error(x, r.grad))
+
+
+def test_second_derivatives_are_refused():
+    x = torch.ones((4, 8), device="cuda", requires_grad=True)
+    w = torch.ones((2, 8, 8), device="cuda")
+    for y in (autograd.kda_gated_ffn(x, w), autograd.kda_dropout(x, 0.5, _rng(1)),
+              autograd.kda_linear_recurrence(x, -torch.ones_like(x))[0]):
+        d, = torch.autograd.grad(y.pow(2).sum(), x, create_graph=True)
+        with pytest.raises(RuntimeError):
+            d.sum().backward()
+
+
+def test_wrong_tensors_are_refused():
+    """The binding's checks beside a GPU: types, shapes, layouts, places."""
+    x, g = torch.zeros((6, 8), device="cuda"), torch.zeros((6, 8), device="cuda")
+    w, rng = torch.zeros((2, 5, 8), device="cuda"), _rng(1)
+    cu = torch.tensor([0, 6], dtype=torch.int32, device="cuda")
+    bad = [
+        lambda: kda.linear_recurrence(x.double(), g), lambda: kda.linear_recurrence(x, g.bfloat16()),
+        lambda: kda.linear_recurrence(x, g[:5]), lambda: kda.linear_recurrence(x.T, g.T),
+        lambda: kda.linear_recurrence(x, g, write="x"), lambda: kda.linear_recurrence(x, g, x),
+        lambda: kda.linear_recurrence(x, g, None, cu.long()), lambda: kda.linear_recurrence(x, g, None, cu[:1]),
+        lambda: kda.linear_recurrence(x, g, None, cu.cpu()), lambda: kda.linear_recurrence(x, g, h=x[:5]),
+        lambda: kda.linear_recurrence(x[:1].expand(6, 8), g),
+        lambda: kda.linear_recurrence(x, g, h_final=torch.zeros(2, 8, device="cuda")),
+        lambda: kda.linear_recurrence(x, g, dev_status=cu.long()),
+        lambda: kda.linear_recurrence_backward(x.bfloat16(), x, g, x),
+        lambda: kda.linear_recurrence_backward(x, x, g, x[:5]),
+        lambda: kda.linear_recurrence_backward(x, x, g, x, None, None, x),
+        lambda: kda.linear_recurrence_step(x, g, x[:5]), lambda: kda.linear_recurrence_step(x, g, x.bfloat16()),
+        lambda: kda.linear_recurrence_step(x, g, x, write="x"),
+        lambda: kda.gated_ffn(x, w.bfloat16()), lambda: kda.gated_ffn(x, w[:1]),
+        lambda: kda.gated_ffn(x, w[:, :, :7]), lambda: kda.gated_ffn(x.T, w), lambda: kda.gated_ffn(x, w, act="x"),
+        lambda: kda.gated_ffn(x, w, h=x), lambda: kda.gated_ffn_backward(x, x, w),
+        lambda: kda.dropout(x, 0.1, rng.int()), lambda: kda.dropout(x, 0.1, rng.cpu()),
+        lambda: kda.dropout(x, 0.1, rng[:1]), lambda: kda.dropout(x.T, 0.1, rng),
+        lambda: kda.residual_norm(x, None, dropout=0.1, rng=rng), lambda: kda.residual_norm(x, x, dropout=0.1, rng=cu),
+    ]
+    for i, call in enumerate(bad):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        kda.residual_norm(x, x, dropout=0.1)
+    for call in (lambda: kda.dropout(x, 1.0, rng), lambda: kda.dropout(x, 0.1, rng, site=1 << 16),
+                 lambda: kda.dropout(x, -0.5, rng), lambda: kda.residual_norm(x, x, dropout=1.5, rng=rng)):
+        with pytest.raises(kda.KDAError):
+            call()

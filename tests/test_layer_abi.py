@@ -8,6 +8,8 @@ import torch
 
 import kimi_delta_attention_18_gb300 as kda
 from kimi_delta_attention_18_gb300._layer import FFNDesc, RecurrenceDesc
+from kimi_delta_attention_18_gb300._lm import DropoutDesc, NormDesc
+from oracle.philox import keep_mask, philox
 
 OK, INVALID, UNSUPPORTED, WORKSPACE = range(4)
 A = 0x10000  # an address that is never touched
@@ -166,3 +168,64 @@ def test_gated_ffn_binding_refuses_tensors():
         kda.gated_ffn(x[0], w)
     with pytest.raises(ValueError, match="CUDA"):
         kda.gated_ffn_backward(x, x, w)
+
+
+def test_the_generator_gives_its_published_values():
+    """The known answers that its authors publish for ten rounds."""
+    for counter, key, words in (
+            ([0] * 4, [0] * 2, "6627e8d5 e169c58d bc57ac4c 9b00dbd8"),
+            ([0xffffffff] * 4, [0xffffffff] * 2, "408f276d 41c83b0e a20bc7c6 6d5451fd"),
+            ([0x243f6a88, 0x85a308d3, 0x13198a2e, 0x03707344], [0xa4093822, 0x299f31d0],
+             "d16cfe09 94fdcceb 5001e420 24126ea1")):
+        assert [int(w) for w in philox(counter, key)] == [int(w, 16) for w in words.split()]
+    mask, factor = keep_mask(range(1000), 37, 0.3, 5, 6)
+    assert abs(mask.mean() - 0.7) < 0.01 and abs(factor - 1 / 0.7) < 1e-9
+
+
+def _drop(**kw):
+    return _make(DropoutDesc, dict(rng=A, p=0.1, site=0), kw)
+
+
+BAD_DROPOUT = [dict(rng=None), dict(rng=A + 4), dict(p=-0.1), dict(p=1.0), dict(p=math.nan),
+               dict(p=1 - 2.0 ** -34), dict(site=-1), dict(site=65536)]
+
+
+@pytest.mark.parametrize("kw", BAD_DROPOUT, ids=str)
+def test_dropout_refuses_descriptors(kw):
+    L, n = kda.lib(), NormDesc(4, 0, 0, 1, 64, 1, 0, 1e-6)
+    assert L.kda_dropout(_drop(**kw), 4, 64, 1, A, A, None) == INVALID
+    assert L.kda_residual_norm_dropout_forward(n, _drop(**kw), A, A, A, 1.0, A, A, None, None) == INVALID
+    assert L.kda_residual_norm_dropout_backward(n, _drop(**kw), A, A, A, A, 1.0, A, A, A, A, 2 ** 30,
+                                                None, None) == INVALID
+
+
+def test_dropout_refuses_arguments():
+    L, n, d = kda.lib(), NormDesc(4, 0, 0, 1, 64, 1, 0, 1e-6), _drop()
+    assert L.kda_dropout(None, 4, 64, 1, A, A, None) == INVALID
+    for args, status in (((-1, 64, 1, A, A), INVALID), ((4, 0, 1, A, A), INVALID),
+                         ((4, 64, 2, A, A), UNSUPPORTED), ((2 ** 42, 64, 1, A, A), UNSUPPORTED),
+                         ((4, 2 ** 30 + 1, 1, A, A), UNSUPPORTED), ((4, 64, 1, None, A), INVALID),
+                         ((4, 64, 1, A, None), INVALID), ((4, 64, 1, A + 1, A), INVALID),
+                         ((4, 64, 0, A, A + 2), INVALID), ((0, 64, 1, None, None), OK)):
+        assert L.kda_dropout(d, *args, None) == status, args
+    fwd, bwd = L.kda_residual_norm_dropout_forward, L.kda_residual_norm_dropout_backward
+    assert fwd(n, None, A, A, A, 1.0, A, A, None, None) == INVALID
+    assert fwd(n, d, A, None, A, 1.0, None, A, None, None) == INVALID  # nothing to drop
+    assert fwd(n, d, A, A, A, math.inf, A, A, None, None) == INVALID
+    assert fwd(n, _drop(p=0.999), A, A, A, 3e38, A, A, None, None) == INVALID
+    assert bwd(n, None, A, A, A, A, 1.0, A, A, A, A, 2 ** 30, None, None) == INVALID
+    assert bwd(n, d, A, A, A, A, 1.0, A, None, A, A, 2 ** 30, None, None) == INVALID
+    assert bwd(n, d, A, A, A, A, 1.0, A, A, A, None, 0, None, None) == WORKSPACE
+    bad = NormDesc(4, 0, 0, 2, 64, 1, 0, 1e-6)  # heads
+    assert fwd(bad, d, A, A, A, 1.0, A, A, None, None) == INVALID
+
+
+def test_dropout_binding_refuses_tensors():
+    x, rng = torch.zeros(4, 6), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA"):
+        kda.dropout(x, 0.1, rng)
+    with pytest.raises(ValueError, match="dimensions"):
+        kda.dropout(x[0], 0.1, rng)
+    from kimi_delta_attention_18_gb300 import autograd
+    with pytest.raises(ValueError, match="needs y"):
+        autograd.kda_residual_norm(x, dropout=0.5, rng=rng)
