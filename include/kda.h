@@ -563,12 +563,12 @@ typedef struct {
  * A malformed cu_seqlens is reported in dev_status (KDA_ERR_INVALID_ARG) and nothing or
  * only part of the outputs is written; KDA_ERR_TIMEOUT there: a bounded wait gave up.
  * The results do not depend on how the work was spread over the GPU.
- * Workspace: kda_recurrence_workspace_size(desc), 16-byte aligned (0 up to 1,024 tokens and
+ * Workspace: kda_recurrence_workspace_size(desc, 0), 16-byte aligned (0 up to 512 tokens and
  * on invalid arguments).
- * Pointers aligned to their element; C, strides and bases that are even (in elements) are
- * the fast case.
+ * Pointers aligned to their element; 64 channels or more, with strides and bases of whole 16
+ * bytes, are the fast case.
  */
-size_t kda_recurrence_workspace_size(const kda_recurrence_desc_t *desc);
+size_t kda_recurrence_workspace_size(const kda_recurrence_desc_t *desc, int32_t backward);
 kda_status_t kda_recurrence_forward(const kda_recurrence_desc_t *desc, const void *x, const float *g,
                                     const float *h0, const int32_t *cu_seqlens, void *h,
                                     float *h_final, void *workspace, size_t workspace_bytes,
@@ -580,7 +580,7 @@ kda_status_t kda_recurrence_forward(const kda_recurrence_desc_t *desc, const voi
  * forward's h [T, C] (h_{t-1} is taken as it was rounded there), all but x and g contiguous:
  *     dx [T, C] act_dtype,  dg [T, C] fp32,  d_h0 [N, C] fp32 (NULL: skipped; may equal
  *     d_h_final).
- * Workspace as kda_recurrence_forward.
+ * Workspace: kda_recurrence_workspace_size(desc, 1), as above.
  */
 kda_status_t kda_recurrence_backward(const kda_recurrence_desc_t *desc, const void *d_h,
                                      const void *x, const float *g, const void *h, const float *h0,

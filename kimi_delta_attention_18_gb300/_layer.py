@@ -45,7 +45,7 @@ def bind(L):
             ("kda_gated_ffn_backward", [F] + [P] * 6 + [Z, P, P])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = ctypes.c_int, args
-    for name, args in (("kda_recurrence_workspace_size", [R]),
+    for name, args in (("kda_recurrence_workspace_size", [R, I]),
                        ("kda_gated_ffn_workspace_size", [F, I])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = Z, args
@@ -126,7 +126,7 @@ def linear_recurrence(x, g, h0=None, cu_seqlens=None, *, write="add", h=None, h_
     _state(h0, "h0", N, C, dev)
     h = _out(h, "h", x)
     h_final = _state(h_final, "h_final", N, C, dev, want_final_state)
-    workspace, ws_len = _workspace(workspace, _lib().kda_recurrence_workspace_size(desc), dev)
+    workspace, ws_len = _workspace(workspace, _lib().kda_recurrence_workspace_size(desc, 0), dev)
     _call(dev, "kda_recurrence_forward", desc, x.data_ptr(), g.data_ptr(), _ptr(h0),
           _ptr(cu_seqlens), h.data_ptr(), _ptr(h_final), workspace.data_ptr(), ws_len,
           _status(dev_status, dev))
@@ -153,7 +153,7 @@ def linear_recurrence_backward(d_h, x, g, h, h0=None, cu_seqlens=None, d_h_final
     dx = _out(None, "dx", x)
     dg = torch.empty(x.shape, dtype=torch.float32, device=dev)
     d_h0 = _state(None, "d_h0", N, C, dev, want_d_h0)
-    workspace, ws_len = _workspace(workspace, _lib().kda_recurrence_workspace_size(desc), dev)
+    workspace, ws_len = _workspace(workspace, _lib().kda_recurrence_workspace_size(desc, 1), dev)
     _call(dev, "kda_recurrence_backward", desc, d_h.data_ptr(), x.data_ptr(), g.data_ptr(),
           h.data_ptr(), _ptr(h0), _ptr(cu_seqlens), _ptr(d_h_final), dx.data_ptr(), dg.data_ptr(),
           _ptr(d_h0), workspace.data_ptr(), ws_len, _status(dev_status, dev))

@@ -54,7 +54,7 @@ BAD_RECURRENCE = [
 @pytest.mark.parametrize("kw,status", BAD_RECURRENCE, ids=str)
 def test_recurrence_refuses_descriptors(kw, status):
     d = _rec(**kw)
-    assert kda.lib().kda_recurrence_workspace_size(d) == 0
+    assert kda.lib().kda_recurrence_workspace_size(d, 0) == kda.lib().kda_recurrence_workspace_size(d, 1) == 0
     assert _forward(d) == status and _backward(d) == status
     assert kda.lib().kda_recurrence_step(d, A, A, A, A, A, None) == status
 
@@ -84,17 +84,20 @@ def test_recurrence_refuses_pointers():
 
 def test_recurrence_workspace():
     size = kda.lib().kda_recurrence_workspace_size
-    assert size(_rec(tokens=1024)) == 0 and size(_rec(tokens=0)) == 0
-    d = _rec(tokens=1025, channels=100)
-    need = size(d)
-    # tiles of 128 tokens (one more for each sequence) x 64 channels: a flag, maps and ends
-    tiles = 1025 // 128 + 2
-    assert tiles * (16 + 2 * 4 + 128 * 12) <= need <= tiles * (16 + 2 * 4 + 128 * 12) + 5 * 256
-    assert _forward(d) == WORKSPACE and _backward(d) == WORKSPACE
-    assert _forward(d, ws=A, ws_len=need - 1) == WORKSPACE
-    assert _forward(d, ws=A + 8, ws_len=need) == WORKSPACE
-    # sequences of one token each: never more tiles than tokens
-    assert size(_rec(tokens=1025, num_seqs=2 ** 20, channels=100)) < 1025 * (16 + 8 + 128 * 12) + 5 * 256
+    for backward, tile in ((0, 128), (1, 64)):
+        assert size(_rec(tokens=512), backward) == 0 and size(_rec(tokens=0), backward) == 0
+        d = _rec(tokens=1025, channels=100)
+        need = size(d, backward)
+        # tiles (one more for each sequence) x 64 channels: maps and ends
+        tiles = 1025 // tile + 2
+        assert tiles * (16 + 128 * 12) <= need <= tiles * (16 + 128 * 12) + 2 * 256
+        call = _backward if backward else _forward
+        assert call(d) == WORKSPACE
+        assert call(d, ws=A, ws_len=need - 1) == WORKSPACE
+        assert call(d, ws=A + 8, ws_len=need) == WORKSPACE
+        # sequences of one token each: never more tiles than tokens
+        d = _rec(tokens=1025, num_seqs=2 ** 20, channels=100)
+        assert size(d, backward) < 1025 * (16 + 128 * 12) + 3 * 256
 
 
 def test_recurrence_binding_refuses_tensors():
