@@ -6,20 +6,27 @@
 //
 // Both are scans of maps s -> A s + B (A the product of the factors e^g, B the result from a
 // zero start), which compose: a tile of some tokens x 64 channels is one map per channel.
-// Every element should be read and written once, so the scan takes one pass: the four warps of
-// a block each run a quarter of a tile's tokens (a lane has two channels) and join their maps;
-// the block publishes the tile's map, looks back along the sequence for the nearest tile whose
-// end state is known, carries that state through the maps in between, publishes its own end
-// state and writes its tokens.  Tiles are handed out in order by a counter, so a tile that is
-// waited for is already being worked on.  A state always goes through one tile's map at a time
-// and in order, whoever computes it, so the results do not depend on where a look back ended.
+// Every element should be read and written once, so the scan takes one pass: the warps of a
+// block each run some of a tile's tokens (a lane has two channels) and join their maps; the
+// block publishes the tile's map, looks back along the chain for what enters it, and writes its
+// tokens.  Tiles are handed out by a counter so that a tile follows those that it waits for,
+// which are then already being worked on; of few sequences they take turns, so that they are
+// done, too.
 //
-// The look back's latency is what the pass must hide: without it 81,920 x 7,168 BF16 (mix)
-// takes 0.65 ms, the time of its bytes.  So maps and ends are words that a NaN of their own
-// marks as absent (no flag beside the data, no fence between the two, one trip to L2 for both),
-// a look back reads its whole window at once, and a block has the next tile's tokens on their
-// way (TMA) while it works; with flags, and the maps read four at a time, it took 1.62 ms.
-// Tiles by 16 warps with loads straight into registers, two such blocks to an SM, took 2.38.
+// Eight tiles along a chain are a group.  The last of them publishes the group's map and, once
+// it knows it, the group's end: the state that leaves it.  A tile's state comes from the nearest
+// end that is there, through the maps of the groups after it and of its own group's earlier
+// tiles, one at a time and in this order whoever computes it, so the results do not depend on
+// how far a look back went.
+//
+// Without its look back the pass takes the time of its bytes, so that is what the layout hides:
+// maps and ends are words that a NaN of their own marks as absent (no flag beside the data, no
+// fence between the two, one trip to L2 for both); the window is asked for while the tile's
+// tokens come; the forward pass holds a tile in registers while the next one's tokens come
+// (TMA); tiles are large and few are in flight.  Measured, in ms (forward 81,920 x 7,168 and
+// gradient of 81,920 x 4,096, BF16, mix: their bytes take 0.69 and 0.79; forward 1,048,576 x
+// 512, add, 0.63): flags, and maps read four at a time, 1.62, 2.36, 3.75; words that mark
+// themselves 0.82, 1.06, 3.39; as it is now @@.
 //
 // Batches of few tokens have no look back: a block takes all tiles of a sequence's 64
 // channels one after another.
@@ -34,10 +41,17 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kWarps = 4, kChan = 64, kThreads = 32 * kWarps;
-// Tokens of a warp in a tile: the forward pass holds them in registers, the backward pass
-// reads them from shared memory twice.
-constexpr int tok_of(bool bwd) { return bwd ? 16 : 32; }
+constexpr int kChan = 64;
+// A tile: so many warps and tokens of each, by how the tokens come (TMA, or lane by lane).
+// With TMA one block of 256 tokens to an SM has all of its registers in use (a warp holds its
+// 32 tokens' factors and terms), and a chain has few steps: 81,920 x 7,168 BF16 takes 823 us,
+// two blocks of 128 810, three 950; 1,048,576 x 512 1.22, 1.76 and 2.51 ms; 81,920 x 2,048
+// fp32 297 us, 311, 311.  Loads of single lanes want warps: 81,920 x 2,047 BF16 790 us with
+// three blocks of eight warps, 1,414 as with TMA.  The backward pass holds nothing: with TMA
+// 128 tokens 834 us (81,920 x 4,096), 64 872; lane by lane 147 and 116 (20,011 x 1,001 fp32).
+constexpr int warps_of(bool bwd, bool tma) { return bwd && !tma ? 4 : 8; }
+constexpr int tok_of(bool bwd, bool tma) { return !bwd && tma ? 32 : 16; }
+constexpr int tile_of(bool bwd, bool tma) { return warps_of(bwd, tma) * tok_of(bwd, tma); }
 constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
 // Up to so many tokens one block walks a sequence; beyond, a launch lays out the tiles of a
 // batch first.
@@ -57,7 +71,8 @@ struct RecArgs {
     int N, T, C, groups;
     int32_t *status;
     // the look back
-    int4 *tiles;         // [tiles] sequence, first token, end, 2 (place in the chain) + last
+    int4 *tiles;         // [tiles] in the order of work: row of maps and ends, first token, 256
+                         // sequence + tokens - 1, 2 (place in the chain) + last
     float2 *maps;        // [tiles][64 groups]
     float *ends;         // [tiles][64 groups], behind maps
     unsigned *control;   // next tile, tiles, a wait gave up
@@ -145,32 +160,22 @@ __device__ __forceinline__ void tell(void *p, float a, float b) {  // two words 
 }
 
 struct TileAt {
-    int seq, t0, t1, place, group;
+    int seq, t0, t1, place, group, index;
     bool last;
 };
 
 // A tile's entry in a look back's window: maps of 64 channels, then their ends.
 constexpr int kEntry = kChan * 12;
 
-// The state that enters the tile in this lane's two channels from the window's `n` entries,
-// nearest first; false if it does not reach an end yet.
-__device__ __forceinline__ bool look_back(const uint8_t *window, int n, int lane, float2 &state) {
-    int q = 0;
-    bool found = false;
-    for (; q < n; ++q) {
-        const float2 e = *(const float2 *)(window + q * kEntry + kChan * 8 + 8 * lane);
-        if (there(e.x) && there(e.y)) {
-            state = e;
-            found = true;
-            break;
-        }
-        const float4 m = *(const float4 *)(window + q * kEntry + 16 * lane);
-        if (!there(m.x) || !there(m.z)) break;
-    }
-    if (!__all_sync(0xffffffffu, found)) return false;
-    for (--q; q >= 0; --q) state = through(*(const float4 *)(window + q * kEntry + 16 * lane), state);
-    return true;
-}
+// Tiles go in groups of eight along a chain.  A tile of a group publishes its map, the group's
+// last one the group's map instead, and its end: with one step for eight tiles, a chain of
+// few channels and many tokens is not bound by the look back's latency (1,048,576 x 512: 1.73
+// ms where every tile was a step).
+constexpr int kGroup = 8;
+// A look back reads so many groups at first, and twice as many when all their maps are there
+// and no end.
+constexpr int kFirstRead = 2;
+constexpr int kUsualWindow = 10;  // entries, of a batch of many channels
 
 // 8-byte asynchronous copy global -> shared (zero fill when !pred).
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, bool pred) {
@@ -209,34 +214,36 @@ struct No {
 // How a tile's tokens come: by TMA, or lane by lane, pairs of channels or single ones.
 enum { BY_TMA = 0, BY_PAIRS = 1, BY_ONE = 2 };
 
-template <typename T, bool BWD, bool MIX>
+template <typename T, bool BWD, bool MIX, bool TMA>
 struct Stage {  // a warp's part of a tile in shared memory
-    static constexpr int tok = tok_of(BWD);
+    static constexpr int tok = tok_of(BWD, TMA), warps = warps_of(BWD, TMA);
     static constexpr int g = 0, v = tok * kChan * 4, one = tok * kChan * (int)sizeof(T);
     static constexpr int h = v + one, x = h + (BWD ? one : 0), bytes = x + (BWD && MIX ? one : 0);
-    static constexpr int block = kWarps * bytes;
-    // blocks to an SM: by registers (the forward pass holds a tile) or shared memory
-    static constexpr int most = BWD ? 5 : 3;
+    static constexpr int block = warps * bytes;
+    // blocks to an SM, with a window of so many entries
+    static constexpr int most = BWD ? 6 : TMA ? 1 : 3;
     static constexpr int fit(int window) {
-        const int n = 227 * 1024 / (block + window * kEntry + 7 * 1024);
+        const int n = 227 * 1024 / (block + (BWD ? 1 : 2) * window * kEntry + 10 * 1024);
         return n < 1 ? 1 : n < most ? n : most;
     }
 };
 
 template <typename T, bool BWD, bool MIX, int BY, bool SPLIT>
-__global__ void __launch_bounds__(kThreads, Stage<T, BWD, MIX>::fit(4))
+__global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
+                                  Stage<T, BWD, MIX, BY == BY_TMA>::fit(kUsualWindow))
     recurrence_kernel(const __grid_constant__ RecArgs p, const __grid_constant__ CUtensorMap tm_g,
                       const __grid_constant__ CUtensorMap tm_v,
                       const __grid_constant__ CUtensorMap tm_h,
                       const __grid_constant__ CUtensorMap tm_x) {
-    using S = Stage<T, BWD, MIX>;
-    constexpr int TOK = S::tok, kTile = TOK * kWarps;
+    using S = Stage<T, BWD, MIX, BY == BY_TMA>;
+    constexpr int TOK = S::tok, kWarps = S::warps, kTile = TOK * kWarps;
     constexpr bool PAIRS = BY != BY_ONE;
     extern __shared__ __align__(128) uint8_t sm_raw[];
     __shared__ float4 maps[2][kWarps][32];  // (A, B) of two channels
-    __shared__ float2 carry[2][32];  // without a look back
-    __shared__ int4 next_tile[2];
-    __shared__ int next_ticket[2];
+    __shared__ float2 carry[2][32];         // without a look back
+    __shared__ uint2 seen[2][kWarps];       // a warp's entries of the window: maps, ends
+    __shared__ int4 tile_at[2];             // this block's tiles, in turn
+    __shared__ int ticket_at[2];
     __shared__ __align__(8) uint64_t bars[kWarps];
     __shared__ int abort_flag;
     __shared__ bool failed;
@@ -244,9 +251,8 @@ __global__ void __launch_bounds__(kThreads, Stage<T, BWD, MIX>::fit(4))
     const T *x = (const T *)p.x, *d = (const T *)p.d, *hs = (const T *)p.hs;
     const float *first = BWD ? p.d_final : p.h0;
     float *final_out = BWD ? p.d_h0 : p.h_final;
-    const uint32_t bar = smem_addr(&bars[warp]);
     uint8_t *sm = sm_raw + ((128u - (smem_addr(sm_raw) & 127u)) & 127u);
-    uint8_t *window = sm + S::block;
+    uint8_t *windows = sm + S::block;
     if (threadIdx.x == 0) {
         abort_flag = 0;
         failed = false;
@@ -258,22 +264,21 @@ __global__ void __launch_bounds__(kThreads, Stage<T, BWD, MIX>::fit(4))
     griddep_wait();
     griddep_launch_dependents();
 
-    TileAt t = {};
-    int total = 0, begin = 0, end = 0;
+    int total = 0, begin = 0, end = 0, walk_seq = 0, walk_group = 0;
     auto take = [&](int &ticket, int4 &tile) {  // one thread
         ticket = (int)atomicAdd(p.control + NEXT, 1u);
         const int k = ticket / p.groups;
         tile = make_int4(0, 0, 0, 0);
-        if (k < total) tile = p.tiles[BWD ? total - 1 - k : k];
+        if (k < total) tile = p.tiles[k];
     };
     if (SPLIT) {
         total = (int)p.control[TILES];
-        if (threadIdx.x == 0) take(next_ticket[0], next_tile[0]);
+        if (threadIdx.x == 0) take(ticket_at[0], tile_at[0]);
     } else {
-        t.seq = blockIdx.x / p.groups;
-        t.group = blockIdx.x - t.seq * p.groups;
-        begin = begin_of(p, t.seq);
-        end = end_of(p, t.seq);
+        walk_seq = blockIdx.x / p.groups;
+        walk_group = blockIdx.x - walk_seq * p.groups;
+        begin = begin_of(p, walk_seq);
+        end = end_of(p, walk_seq);
         const bool good = !p.cu || (begin >= 0 && begin <= end && end <= p.T && p.cu[0] == 0 &&
                                     p.cu[p.N] == p.T);
         if (!good) {
@@ -281,33 +286,62 @@ __global__ void __launch_bounds__(kThreads, Stage<T, BWD, MIX>::fit(4))
             return;
         }
         if (warp == 0) {
-            const int c = t.group * kChan + 2 * lane;
-            const f2 s = first ? load2<false>(first + (size_t)t.seq * p.C + c, p.C - c) : pk(0.f, 0.f);
+            const int c = walk_group * kChan + 2 * lane;
+            const f2 s = first ? load2<false>(first + (size_t)walk_seq * p.C + c, p.C - c) : pk(0.f, 0.f);
             carry[0][lane] = un(s);
             if (begin == end && final_out)
-                store2<false>(final_out + (size_t)t.seq * p.C + c, p.C - c, s);
+                store2<false>(final_out + (size_t)walk_seq * p.C + c, p.C - c, s);
         }
     }
     __syncthreads();
 
-    // this warp's copies of the tile of tokens t0 .. t1 - 1
-    const uint32_t stage = smem_addr(sm) + warp * S::bytes;
-    auto copy = [&](int t0, int t1, int group) {
-        const int y = t0 + warp * TOK;
+    // This block's k-th tile; false beyond its last.
+    auto turn = [&](int k, TileAt &t) {
+        int4 v;
+        if (SPLIT) {
+            const int ticket = ticket_at[k & 1], row = ticket / p.groups;
+            if (row >= total) return false;
+            v = tile_at[k & 1];
+            t.index = v.x;
+            t.seq = (int)((unsigned)v.z >> 8);
+            t.t1 = v.y + (v.z & 255) + 1;
+            t.group = ticket - row * p.groups;
+        } else {
+            const int n = (end - begin + kTile - 1) / kTile;
+            if (k >= n) return false;
+            const int t0 = begin + (BWD ? n - 1 - k : k) * kTile;
+            v = make_int4(0, t0, 0, 2 * k + (k == n - 1));
+            t.index = 0;
+            t.seq = walk_seq;
+            t.t1 = min(t0 + kTile, end);
+            t.group = walk_group;
+        }
+        t.t0 = v.y;
+        t.place = v.w >> 1;
+        t.last = v.w & 1;
+        return true;
+    };
+    // This warp's copies of its part of the k-th tile.
+    auto start = [&](int k) {
+        TileAt t;
+        if (!turn(k, t)) return;
+        const uint32_t stage = smem_addr(sm) + warp * S::bytes;
+        const int y = t.t0 + warp * TOK;
         if constexpr (BY == BY_TMA) {
             if (lane != 0) return;
-            const int c = group * kChan;
+            const int c = t.group * kChan;
+            const uint32_t bar = smem_addr(&bars[warp]);
             mbar_arrive_expect_tx(bar, S::bytes);
             tma_load_2d(stage + S::g, reinterpret_cast<uint64_t>(&tm_g), c, y, bar);
             tma_load_2d(stage + S::v, reinterpret_cast<uint64_t>(&tm_v), c, y, bar);
             if (BWD) tma_load_2d(stage + S::h, reinterpret_cast<uint64_t>(&tm_h), c, y - 1, bar);
             if (BWD && MIX) tma_load_2d(stage + S::x, reinterpret_cast<uint64_t>(&tm_x), c, y, bar);
         } else {
-            const int c = group * kChan + 2 * lane, left = p.C - c;
+            const int c = t.group * kChan + 2 * lane, left = p.C - c;
             const uint32_t to = stage + 8 * lane, to_t = stage + 2 * (int)sizeof(T) * lane;
 #pragma unroll 8
             for (int j = 0; j < TOK; ++j) {
-                const int n = y + j < t1 ? left : 0;
+                const int n = y + j < t.t1 ? left : 0;
                 const size_t row = (size_t)(y + j), at = row * p.C + c;
                 constexpr int step = kChan * (int)sizeof(T);
                 fetch<PAIRS>(to + S::g + j * kChan * 4, p.g + row * p.g_stride + c, p.g, n);
@@ -316,69 +350,29 @@ __global__ void __launch_bounds__(kThreads, Stage<T, BWD, MIX>::fit(4))
                 if (BWD && MIX)
                     fetch<PAIRS>(to_t + S::x + j * step, x + row * p.x_stride + c, p.g, n);
             }
+            cp_async_commit();
         }
     };
-    const uint8_t *mine = sm + warp * S::bytes + 8 * lane;  // of g
-    const uint8_t *mine_t = sm + warp * S::bytes + 2 * sizeof(T) * lane;
-    bool pending = false;  // this warp's copies are on their way
-    auto tile_of_walk = [&](int walk) {  // without a look back
-        const int n = (end - begin + kTile - 1) / kTile;
-        const int t0 = begin + (BWD ? n - 1 - walk : walk) * kTile;
-        return make_int4(t.seq, t0, min(t0 + kTile, end), walk >= n ? -1 : 2 * walk + (walk == n - 1));
+    // Two channels of token j of an array of the tile.
+    auto gate = [&](int j) {
+        return get2((const float *)(sm + warp * S::bytes + S::g + j * kChan * 4 + 8 * lane));
     };
-    auto start = [&](int walk) {  // of the tile after the next barrier, or the first
-        if (SPLIT) {
-            const int ticket = next_ticket[walk & 1], k = ticket / p.groups;
-            const int4 tile = next_tile[walk & 1];
-            pending = k < total;
-            if (pending) copy(tile.y, tile.z, ticket - k * p.groups);
-        } else {
-            const int4 tile = tile_of_walk(walk);
-            pending = tile.w >= 0;
-            if (pending) copy(tile.y, tile.z, t.group);
-        }
+    auto item = [&](int array, int j) {
+        return get2((const T *)(sm + warp * S::bytes + array + (j * kChan + 2 * lane) * (int)sizeof(T)));
     };
-    start(0);
-
-    for (int walk = 0;; ++walk) {
-        const int par = walk & 1;
-        int index = 0, ahead_ticket = 0;
-        int4 tile, ahead;
-        if (SPLIT) {
-            const int ticket = next_ticket[par], k = ticket / p.groups;
-            if (k >= total) return;
-            tile = next_tile[par];
-            index = BWD ? total - 1 - k : k;
-            t.group = ticket - k * p.groups;
-            if (threadIdx.x == 0) take(ahead_ticket, ahead);
-        } else {
-            tile = tile_of_walk(walk);
-            if (tile.w < 0) return;
-        }
-        t.seq = tile.x;
-        t.t0 = tile.y;
-        t.t1 = tile.z;
-        t.place = tile.w >> 1;
-        t.last = tile.w & 1;
-        const int c = t.group * kChan + 2 * lane, left = p.C - c;
-        const int tok = t.t0 + warp * TOK;  // this warp's first token
-        const int n = max(0, min(TOK, t.t1 - tok));
-        const bool starts = BWD ? t.last : t.place == 0;  // the tile has the sequence's first token
+    auto tokens = [&](const TileAt &t) { return max(0, min(TOK, t.t1 - t.t0 - warp * TOK)); };
+    f2 fa[BWD ? 1 : TOK], fb[BWD ? 1 : TOK];  // forward: the tile's factors and terms
+    // The map of this warp's tokens of the k-th tile; false if they did not come.
+    auto reduce = [&](int k, const TileAt &t, auto hold) {
         bool landed = true;
         if (BY == BY_TMA) {
-            landed = __all_sync(0xffffffffu, mbar_wait(bar, par, &abort_flag, kWaitLimit));
+            landed = __all_sync(0xffffffffu, mbar_wait(smem_addr(&bars[warp]), k & 1, &abort_flag,
+                                                       kWaitLimit));
             if (!landed) failed = true;
         } else {
             cp_async_wait_all();  // every lane reads what it copied itself
         }
-        pending = !landed;
-        auto gate = [&](int j) { return get2((const float *)(mine + S::g + j * kChan * 4)); };
-        auto item = [&](int array, int j) {
-            return get2((const T *)(mine_t + array + j * kChan * sizeof(T)));
-        };
-
-        // the map of this warp's tokens
-        f2 a[BWD ? 1 : TOK], b[BWD ? 1 : TOK];  // forward: factors and terms
+        const int n = tokens(t);
         f2 A = both(1.f), B = both(0.f);
         auto run = [&](auto whole) {
 #pragma unroll
@@ -387,117 +381,204 @@ __global__ void __launch_bounds__(kThreads, Stage<T, BWD, MIX>::fit(4))
                 f2 f = both(1.f), w, v = both(0.f);
                 if (whole.value || j < n) {
                     decay2(gate(j), f, w);
-                    v = item(S::v, j);  // x, or backward d
+                    v = item(S::v, j);
                     if (!BWD && MIX) v = mul2(w, v);
                 }
-                if (BWD) {
-                    B = mul2(f, add2(B, v));
-                } else {
-                    a[BWD ? 0 : j] = f;
-                    b[BWD ? 0 : j] = v;
-                    B = fma2(f, B, v);
-                }
+                B = BWD ? mul2(f, add2(B, v)) : fma2(f, B, v);
                 A = mul2(A, f);
+                if constexpr (hold.value) {
+                    fa[j] = f;
+                    fb[j] = v;
+                }
             }
         };
         if (n == TOK) run(Yes{});
         else run(No{});
         const float2 ua = un(A), ub = un(B);
-        maps[par][warp][lane] = make_float4(ua.x, ub.x, ua.y, ub.y);
-        if (SPLIT && threadIdx.x == 0) {
-            next_ticket[par ^ 1] = ahead_ticket;
-            next_tile[par ^ 1] = ahead;
-        }
-        __syncthreads();
-        if (!BWD && landed) start(walk + 1);  // this tile is in registers
-
-        // the tile's map, published by one warp
+        maps[k & 1][warp][lane] = make_float4(ua.x, ub.x, ua.y, ub.y);
+        return landed;
+    };
+    // After a barrier: the map of the warps before this one, and (of use in the warp that
+    // publishes it) of the tile.
+    auto join = [&](int k, const TileAt &t, float4 &before, float4 &whole) {
         float4 m = make_float4(1.f, 0.f, 1.f, 0.f);
-        const size_t slot = (size_t)index * p.groups * kChan + c;
-        if (warp == 0) {
 #pragma unroll
-            for (int i = 0; i < kWarps; ++i) {
-                const float4 v = maps[par][BWD ? kWarps - 1 - i : i][lane];
-                const float2 to = through(v, make_float2(m.y, m.w));
-                m = make_float4(m.x * v.x, to.x, m.z * v.z, to.y);
-            }
-            if (SPLIT && t.place > 0 && !t.last) {
-                tell(p.maps + slot, m.x, m.y);
-                tell(p.maps + slot + 1, m.z, m.w);
-            }
+        for (int i = 0; i < kWarps; ++i) {
+            const int w = BWD ? kWarps - 1 - i : i;
+            if (w == warp) before = m;
+            const float4 v = maps[k & 1][w][lane];
+            const float2 to = through(v, make_float2(m.y, m.w));
+            m = make_float4(m.x * v.x, to.x, m.z * v.z, to.y);
         }
-        // the state that enters the tile, in every warp
-        float2 in;
-        if (!SPLIT) {
-            in = carry[par][lane];
-        } else if (t.place == 0) {
-            in = un(first ? load2<false>(first + (size_t)t.seq * p.C + c, left) : pk(0.f, 0.f));
-        } else {
-            const int n = min(p.window, t.place), step = BWD ? 1 : -1;
+        whole = m;
+        if (SPLIT && warp == 0 && !t.last && t.place % kGroup != kGroup - 1) {
+            const size_t slot = ((size_t)t.index * p.groups + t.group) * kChan + 2 * lane;
+            tell(p.maps + slot, m.x, m.y);
+            tell(p.maps + slot + 1, m.z, m.w);
+        }
+    };
+
+    start(0);
+    unsigned polls = 0;
+    TileAt t;
+    for (int k = 0; turn(k, t); ++k) {
+        int ahead_ticket = 0;
+        int4 ahead;
+        if (!BWD && SPLIT && threadIdx.x == 0) take(ahead_ticket, ahead);
+        const int c = t.group * kChan + 2 * lane, left = p.C - c;
+        // The look back's window: the maps of the group's earlier tiles, then of earlier groups
+        // their maps and ends, all nearest first; a warp reads every fourth entry, for the
+        // first time while the tile's tokens come, and again while it is not there.
+        const int inside = t.place % kGroup, groups = t.place / kGroup;
+        uint8_t *window = windows + (BWD ? 0 : (k & 1) * (p.window + kGroup - 1) * kEntry);
+        const int most = inside + min(p.window, groups);
+        int asked = min(inside + kFirstRead, most);
+        unsigned have_maps = 0, have_ends = 0;
+        auto ask = [&]() {
             const size_t pitch = (size_t)p.groups * kChan;
-            const long long since = clock64();
-            while (true) {
-                for (int k = threadIdx.x; k < n * (kEntry / 16); k += kThreads) {
-                    const int q = k / (kEntry / 16), part = k - q * (kEntry / 16);
-                    const size_t at = (size_t)(index + step * (q + 1)) * pitch + t.group * kChan;
-                    cp_async16(smem_addr(window) + 16 * k,
-                               part < kChan / 2 ? (const void *)(p.maps + at + 2 * part)
-                                                : (const void *)(p.ends + at + 4 * (part - kChan / 2)),
-                               true);
+            for (int q = warp; q < asked; q += kWarps) {
+                const int back = q < inside ? q + 1 : inside + 1 + kGroup * (q - inside);
+                const size_t at = (size_t)(t.index + (BWD ? back : -back)) * pitch + t.group * kChan;
+                const uint32_t to = smem_addr(window) + q * kEntry;
+                if (!(have_maps >> q & 1)) cp_async16(to + 16 * lane, p.maps + at + 2 * lane, true);
+                if (q >= inside && !(have_ends >> q & 1) && lane < 16)
+                    cp_async16(to + kChan * 8 + 16 * lane, p.ends + at + 4 * lane, true);
+            }
+        };
+        auto look = [&]() {
+            cp_async_wait_all();
+            __syncwarp();
+            for (int q = warp; q < asked; q += kWarps) {
+                const uint8_t *at = window + q * kEntry;
+                if (!(have_maps >> q & 1)) {
+                    const float4 v = *(const float4 *)(at + 16 * lane);
+                    if (__all_sync(0xffffffffu, there(v.x) && there(v.z))) have_maps |= 1u << q;
                 }
-                cp_async_wait_all();
-                __syncthreads();
-                if (failed || look_back(window, n, lane, in)) break;  // the same in every warp
-                __syncthreads();
-                if (threadIdx.x == 0 && (clock64() - since > kWaitLimit ||
-                                         *(volatile unsigned *)(p.control + ABORT))) {
+                if (q >= inside && !(have_ends >> q & 1)) {
+                    const float2 v = *(const float2 *)(at + kChan * 8 + 8 * lane);
+                    if (__all_sync(0xffffffffu, there(v.x) && there(v.y))) have_ends |= 1u << q;
+                }
+            }
+            if (lane == 0) seen[polls & 1][warp] = make_uint2(have_maps, have_ends);
+        };
+        if (SPLIT) ask();  // into the window that this tile's turn has
+        bool landed;
+        if constexpr (BWD) landed = reduce(k, t, No{});
+        else landed = reduce(k, t, Yes{});
+        if (!BWD && SPLIT && threadIdx.x == 0) {
+            ticket_at[(k + 1) & 1] = ahead_ticket;
+            tile_at[(k + 1) & 1] = ahead;
+        }
+        if (SPLIT) look();
+        __syncthreads();
+        float4 before, whole;
+        join(k, t, before, whole);
+        if (!BWD && landed) start(k + 1);  // the tile is in registers
+
+        // the state that enters the tile, in every warp
+        float2 in, group_in = make_float2(0.f, 0.f);  // state that enters the tile, its group
+        if (!SPLIT) {
+            in = carry[k & 1][lane];
+        } else {
+            bool closed = false;
+            const bool closes = inside == kGroup - 1 && !t.last;
+            const long long since = clock64();
+            int from = 0;  // entries up to the end that is taken
+            if (groups == 0)
+                group_in = un(first ? load2<false>(first + (size_t)t.seq * p.C + c, left) : pk(0.f, 0.f));
+            while (true) {
+                unsigned all_maps = 0, all_ends = 0;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const uint2 v = seen[polls & 1][w];
+                    all_maps |= v.x;
+                    all_ends |= v.y;
+                }
+                ++polls;
+                if (failed) break;
+                const bool known = !(~all_maps & ((1u << inside) - 1));
+                if (warp == 0 && closes && known && !closed) {  // the group's map
+                    float4 m = *(const float4 *)(window + (inside - 1) * kEntry + 16 * lane);
+                    for (int q = inside - 2; q >= -1; --q) {
+                        const float4 v = q < 0 ? whole : *(const float4 *)(window + q * kEntry + 16 * lane);
+                        const float2 to = through(v, make_float2(m.y, m.w));
+                        m = make_float4(m.x * v.x, to.x, m.z * v.z, to.y);
+                    }
+                    const size_t slot = ((size_t)t.index * p.groups + t.group) * kChan + 2 * lane;
+                    tell(p.maps + slot, m.x, m.y);
+                    tell(p.maps + slot + 1, m.z, m.w);
+                    whole = m;
+                    closed = true;
+                }
+                // the nearest end, if every nearer map is there too: the same in every warp
+                from = groups == 0 ? inside : __ffs(all_ends) - 1;
+                if (from >= 0 && !(~all_maps & ((1u << from) - 1))) break;
+                if (threadIdx.x == 0 && (polls & 63) == 0 &&
+                    (clock64() - since > kWaitLimit || *(volatile unsigned *)(p.control + ABORT))) {
                     *(volatile unsigned *)(p.control + ABORT) = 1;
                     failed = true;
                 }
+                if (from < 0 && __popc(all_maps) == asked) asked = min(2 * asked, most);
+                ask();
+                look();
+                __syncthreads();
+            }
+            if (!failed) {
+                if (groups > 0) {
+                    group_in = *(const float2 *)(window + from * kEntry + kChan * 8 + 8 * lane);
+#pragma unroll 4
+                    for (int q = from - 1; q >= inside; --q)
+                        group_in = through(*(const float4 *)(window + q * kEntry + 16 * lane), group_in);
+                }
+                in = group_in;
+#pragma unroll 4
+                for (int q = inside - 1; q >= 0; --q)
+                    in = through(*(const float4 *)(window + q * kEntry + 16 * lane), in);
             }
         }
         if (failed) {  // (set before a barrier that everyone has passed)
             if (threadIdx.x == 0) dev_fail(p.status, KDA_ERR_TIMEOUT);
-            if (BY == BY_TMA && pending) {  // let the copies land before the block exits
+            if (BY == BY_TMA && !BWD && landed) {
+                TileAt u;
                 volatile int never = 0;
-                mbar_wait(bar, landed ? par ^ 1 : par, &never, kWaitLimit);
+                if (turn(k + 1, u)) mbar_wait(smem_addr(&bars[warp]), (k + 1) & 1, &never, kWaitLimit);
+            } else if (BY == BY_TMA && !landed) {  // let the copies land before the block exits
+                volatile int never = 0;
+                mbar_wait(smem_addr(&bars[warp]), k & 1, &never, kWaitLimit);
             }
             return;
         }
         if (warp == 0) {
-            const float2 to = through(m, in);
-            if (SPLIT && !t.last) tell(p.ends + slot, to.x, to.y);
-            if (!SPLIT) carry[par ^ 1][lane] = to;
+            const bool closes = SPLIT && !t.last && t.place % kGroup == kGroup - 1;
+            const float2 to = through(whole, closes ? group_in : in);
+            if (closes) tell(p.ends + ((size_t)t.index * p.groups + t.group) * kChan + 2 * lane, to.x, to.y);
+            if (!SPLIT) carry[(k & 1) ^ 1][lane] = to;
             if (t.last && final_out)
                 store2<false>(final_out + (size_t)t.seq * p.C + c, left, pk(to.x, to.y));
         }
 
+        if (BWD && SPLIT && threadIdx.x == 0) take(ahead_ticket, ahead);
+
         // this warp's tokens, from the state that enters them
-        for (int w = BWD ? kWarps - 1 : 0; w != warp; w += BWD ? -1 : 1)
-            in = through(maps[par][w][lane], in);
+        in = through(before, in);
         f2 s = pk(in.x, in.y);
-        auto write = [&](auto whole) {
-            if constexpr (!BWD) {
-                T *to = (T *)p.h + (size_t)tok * p.C + c;
+        const int tok = t.t0 + warp * TOK, n = tokens(t);
+        const bool starts = (BWD ? t.last : t.place == 0) && warp == 0;  // token 0 is the sequence's
+        auto write = [&](auto all) {
 #pragma unroll
-                for (int j = 0; j < TOK; ++j) {
-                    s = fma2(a[j], s, b[j]);
-                    if (whole.value || j < n) store2<PAIRS>(to, left, s);
-                    to += p.C;
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < TOK; ++i) {
-                    const int j = TOK - 1 - i;
-                    if (!whole.value && j >= n) continue;
-                    const size_t row = (size_t)(tok + j) * p.C + c;
-                    f2 f, w, before;
+            for (int i = 0; i < TOK; ++i) {
+                const int j = BWD ? TOK - 1 - i : i;
+                if (!all.value && j >= n) continue;
+                const size_t row = (size_t)(tok + j) * p.C + c;
+                if constexpr (!BWD) {
+                    s = fma2(fa[j], s, fb[j]);
+                    store2<PAIRS>((T *)p.h + row, left, s);
+                } else {
+                    f2 f, w, v = item(S::v, j), before = item(S::h, j);
                     decay2(gate(j), f, w);
-                    if (j == 0 && warp == 0 && starts)
+                    if (j == 0 && starts)
                         before = p.h0 ? load2<false>(p.h0 + (size_t)t.seq * p.C + c, left) : pk(0.f, 0.f);
-                    else
-                        before = item(S::h, j);
-                    const f2 dh = add2(item(S::v, j), s);
+                    const f2 dh = add2(v, s);
                     s = mul2(f, dh);
                     if (MIX) before = fma2(item(S::x, j), both(-1.f), before);
                     store2<PAIRS>((T *)p.dx + row, left, MIX ? mul2(w, dh) : dh);
@@ -508,16 +589,23 @@ __global__ void __launch_bounds__(kThreads, Stage<T, BWD, MIX>::fit(4))
         if (n == TOK) write(Yes{});
         else write(No{});
         if (BWD) {
-            __syncwarp();  // every lane has read this tile
-            start(walk + 1);
+            if (SPLIT) {
+                if (threadIdx.x == 0) {
+                    ticket_at[(k + 1) & 1] = ahead_ticket;
+                    tile_at[(k + 1) & 1] = ahead;
+                }
+                __syncthreads();
+            } else {
+                __syncwarp();  // every lane has read this tile
+            }
+            start(k + 1);
         }
     }
 }
 
 // The tiles of every sequence, cleared maps and ends, and the states of empty sequences.
 __global__ void __launch_bounds__(1024) recurrence_tiles_kernel(const __grid_constant__ RecArgs p,
-                                                                bool backward) {
-    const int kTile = kWarps * tok_of(backward);
+                                                                bool backward, int tile) {
     __shared__ int sums[32];
     __shared__ int base;
     __shared__ bool bad;
@@ -557,10 +645,42 @@ __global__ void __launch_bounds__(1024) recurrence_tiles_kernel(const __grid_con
         }
         return;
     }
+    auto entry = [&](int seq, int row, int first, int end, int place, int tiles) {
+        return make_int4(row, first, (int)((unsigned)seq << 8) + min(tile, end - first) - 1,
+                         2 * place + (place == tiles - 1));
+    };
+    if (p.N <= 32) {  // their tiles take turns, so that those that wait for each other are apart
+        __shared__ int starts[33], counts[32];
+        if (warp == 0) {
+            const int count = lane < p.N ? (end_of(p, lane) - begin_of(p, lane) + tile - 1) / tile : 0;
+            int v = count;
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            counts[lane] = count;
+            starts[lane + 1] = v;
+            if (lane == 0) starts[0] = 0;
+        }
+        __syncthreads();
+        for (int row = threadIdx.x; row < starts[32]; row += 1024) {
+            int seq = 0;
+            while (row >= starts[seq + 1]) ++seq;
+            const int k = row - starts[seq], tiles = counts[seq], place = backward ? tiles - 1 - k : k;
+            int turn = 0;
+            for (int m = 0; m < p.N; ++m) turn += min(counts[m], place) + (m < seq && counts[m] > place);
+            p.tiles[turn] = entry(seq, row, begin_of(p, seq) + k * tile, end_of(p, seq), place, tiles);
+        }
+        if (threadIdx.x == 0) {
+            p.control[NEXT] = p.control[ABORT] = 0;
+            p.control[TILES] = starts[32];
+        }
+        return;
+    }
     for (int n0 = 0; n0 < p.N; n0 += 1024) {
         const int n = n0 + threadIdx.x;
         const int a = n < p.N ? begin_of(p, n) : 0, b = n < p.N ? end_of(p, n) : 0;
-        const int count = (b - a + kTile - 1) / kTile;
+        const int count = (b - a + tile - 1) / tile;
         int v = count;
         for (int o = 1; o < 32; o <<= 1) {
             const int u = __shfl_up_sync(0xffffffffu, v, o);
@@ -584,9 +704,7 @@ __global__ void __launch_bounds__(1024) recurrence_tiles_kernel(const __grid_con
             const int from = __shfl_sync(0xffffffffu, a, q), end = __shfl_sync(0xffffffffu, b, q);
             for (int k = lane; k < tiles; k += 32) {
                 const int place = backward ? tiles - 1 - k : k;
-                p.tiles[to + k] = make_int4(n0 + 32 * warp + q, from + k * kTile,
-                                            min(from + (k + 1) * kTile, end),
-                                            2 * place + (place == tiles - 1));
+                p.tiles[to + place] = entry(n0 + 32 * warp + q, to + k, from + k * tile, end, place, tiles);
             }
         }
         __syncthreads();
@@ -656,23 +774,25 @@ __global__ void __launch_bounds__(256)
 // ------------------------------------------------------------------ host side
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
 bool walks(const kda_recurrence_desc_t *d) { return d->tokens <= kWalkTokens; }
+long long most_tiles(long long tokens, long long seqs, int tile) {
+    const long long n = tokens / tile + seqs;
+    return n < tokens ? n : tokens;
+}
+// of any kernel that a call could take
 long long most_tiles(const kda_recurrence_desc_t *d, bool bwd) {
-    const long long n = (long long)d->tokens / (kWarps * tok_of(bwd)) + d->num_seqs;
-    return n < d->tokens ? n : d->tokens;
+    return most_tiles(d->tokens, d->num_seqs, tile_of(bwd, false));
 }
 int groups_of(const kda_recurrence_desc_t *d) { return (d->channels + kChan - 1) / kChan; }
 
 struct Layout {
-    size_t tiles, maps, ends, total;
+    size_t tiles, total;
 };
 Layout layout_for(const kda_recurrence_desc_t *d, bool bwd) {
     Layout l = {};
     if (walks(d)) return l;
     const size_t n = (size_t)most_tiles(d, bwd), g = groups_of(d);
     l.tiles = round256(n * sizeof(int4));
-    l.maps = n * g * kChan * sizeof(float2);
-    l.ends = n * g * kChan * sizeof(float);
-    l.total = 256 + l.tiles + l.maps + l.ends;
+    l.total = 256 + l.tiles + n * g * kEntry;
     return l;
 }
 
@@ -718,15 +838,35 @@ bool encode(CUtensorMap *m, const void *base, int size, int C, int T, long long 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMaxSmem = 96 * 1024;  // a stage of 64 KB, a window of 24
+constexpr int kMaxSmem = 180 * 1024;  // a stage of 128 KB, two windows of 24 entries
+
 
 template <typename T, bool BWD, bool MIX, int BY, bool SPLIT>
-cudaError_t launch_by(const RecArgs &a, long long blocks, const CUtensorMap (&m)[4], cudaStream_t st) {
+cudaError_t launch_by(RecArgs &a, const CUtensorMap (&m)[4], cudaStream_t st) {
     const auto kernel = recurrence_kernel<T, BWD, MIX, BY, SPLIT>;
-    const int smem = Stage<T, BWD, MIX>::block + 128 + (SPLIT ? a.window * kEntry : 0);
+    typedef Stage<T, BWD, MIX, BY == BY_TMA> S;
+    const int sms = device_sms();
+    long long blocks = (long long)a.N * a.groups;
+    int smem = S::block + 128;
+    if (SPLIT) {
+        a.most_tiles = (int)most_tiles(a.T, a.N, S::warps * S::tok);
+        const long long work = (long long)a.most_tiles * a.groups, pieces = work * (kEntry / 16);
+        a.ends = (float *)(a.maps + work * kChan);
+        const int clear = (int)(pieces / 4096 < 2 * sms ? pieces / 4096 : 2 * sms) + 1;
+        const cudaError_t e = launch_dependent(recurrence_tiles_kernel, dim3(1 + clear), dim3(1024), 0,
+                                               st, a, BWD, S::warps * S::tok);
+        if (e != cudaSuccess) return e;
+        // A look back reads a few more groups than are worked on at once in a chain.
+        const int chain = S::fit(kUsualWindow) * sms / (a.groups * kGroup);
+        a.window = chain + 3 < 16 ? chain + 3 : 16;
+        const int entries = a.window + kGroup - 1;
+        smem += (BWD ? 1 : 2) * entries * kEntry;
+        const long long most = (long long)S::fit(entries) * sms;
+        blocks = work < most ? work : most;
+    }
     const cudaError_t e = set_max_dynamic_smem((const void *)kernel, kMaxSmem);
     if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), smem, st, a, m[0], m[1],
+    return launch_dependent(kernel, dim3((unsigned)blocks), dim3(32 * S::warps), smem, st, a, m[0], m[1],
                             m[2], m[3]);
 }
 
@@ -734,40 +874,23 @@ template <typename T, bool BWD, bool MIX>
 cudaError_t launch_t(const kda_recurrence_desc_t *d, RecArgs &a, bool pairs, void *workspace,
                      cudaStream_t st) {
     CUtensorMap m[4] = {};
-    if (walks(d)) {
-        const long long blocks = (long long)a.N * a.groups;
-        return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, false>(a, blocks, m, st)
-                     : launch_by<T, BWD, MIX, BY_ONE, false>(a, blocks, m, st);
-    }
+    if (walks(d))
+        return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, false>(a, m, st)
+                     : launch_by<T, BWD, MIX, BY_ONE, false>(a, m, st);
     const Layout l = layout_for(d, BWD);
     uint8_t *ws = (uint8_t *)workspace;
     a.control = (unsigned *)ws;
     a.tiles = (int4 *)(ws + 256);
     a.maps = (float2 *)(ws + 256 + l.tiles);
-    a.ends = (float *)(ws + 256 + l.tiles + l.maps);
-    a.most_tiles = (int)most_tiles(d, BWD);
-    const long long work = (long long)a.most_tiles * a.groups, pieces = work * (kEntry / 16);
-    const int sms = device_sms();
-    const int clear = (int)(pieces / 4096 < 2 * sms ? pieces / 4096 : 2 * sms) + 1;
-    cudaError_t e = launch_dependent(recurrence_tiles_kernel, dim3(1 + clear), dim3(1024), 0, st, a,
-                                     BWD);
-    if (e != cudaSuccess) return e;
-    // A look back reads about as many tiles as are worked on at once in a chain: the nearest
-    // of them have published maps, the furthest their ends.
-    typedef Stage<T, BWD, MIX> S;
-    const int chain = S::fit(4) * sms / a.groups;
-    a.window = chain + 4 < 32 ? chain + 4 : 32;
-    const long long most = (long long)S::fit(a.window) * sms;
-    const long long blocks = work < most ? work : most;
-    constexpr int tok = tok_of(BWD), size = sizeof(T);
+    constexpr int tok = tok_of(BWD, true), size = sizeof(T);
     const bool tma =
         encode(&m[0], a.g, 4, a.C, a.T, a.g_stride, tok) &&
         (BWD ? encode(&m[1], a.d, size, a.C, a.T, a.C, tok) && encode(&m[2], a.hs, size, a.C, a.T, a.C, tok) &&
                    (!MIX || encode(&m[3], a.x, size, a.C, a.T, a.x_stride, tok))
              : encode(&m[1], a.x, size, a.C, a.T, a.x_stride, tok));
-    if (tma && pairs) return launch_by<T, BWD, MIX, BY_TMA, true>(a, blocks, m, st);
-    return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, true>(a, blocks, m, st)
-                 : launch_by<T, BWD, MIX, BY_ONE, true>(a, blocks, m, st);
+    if (tma && pairs) return launch_by<T, BWD, MIX, BY_TMA, true>(a, m, st);
+    return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, true>(a, m, st)
+                 : launch_by<T, BWD, MIX, BY_ONE, true>(a, m, st);
 }
 
 template <bool BWD>
