@@ -1,5 +1,6 @@
-// The cross entropy's products with an fp32 weight and few tokens (at most 128: one row
-// of tiles): z = x W^T (its statistics, or dz) and dx = dz W.
+// The products with an fp32 weight and few tokens (at most 128: one row of tiles) of the
+// cross entropy, z = x W^T (its statistics, or dz) and dx = dz W, and of the gated feed-forward
+// block, both of whose projections a tile takes half of its columns from.
 //
 // These are bound by W's bytes.  It is read as it is, 4 bytes an element, and split into
 // its three BF16 terms on the way from one place in shared memory to another; x and dz
@@ -121,8 +122,14 @@ __global__ void __launch_bounds__(kThreads32, 1)
                     ok = mbar_wait(bar(W_WE + sw), ((it / kStagesW) & 1) ^ 1, abort, kWaitLimit);
                     if (!ok) break;
                     mbar_arrive_expect_tx(bar(W_WF + sw), kStageW);
-                    tma_load_2d(sb + kOffW + sw * kStageW, tw, ROWS ? wn : kb * KB,
-                                ROWS ? kb * KB + p.bk_row0 : wn, bar(W_WF + sw));
+                    const uint32_t to = sb + kOffW + sw * kStageW;
+                    if (EPI == EPI_GLU) {  // half of the columns from each of W's matrices
+                        tma_load_2d(to, tw, kb * KB, wn / 2, bar(W_WF + sw));
+                        tma_load_2d(to + kStageW / 2, tw, kb * KB, p.cols + wn / 2, bar(W_WF + sw));
+                    } else {
+                        tma_load_2d(to, tw, ROWS ? wn : kb * KB, ROWS ? kb * KB + p.bk_row0 : wn,
+                                    bar(W_WF + sw));
+                    }
                     if ((kb - t.kb0) & 1) continue;
                     const int sa = ia % kStagesA;
                     ok = mbar_wait(bar(W_AE + sa), ((ia / kStagesA) & 1) ^ 1, abort, kWaitLimit);
@@ -234,7 +241,8 @@ __global__ void __launch_bounds__(kThreads32, 1)
         }
     } else {
         const int quarter = warp & 3, half = (warp - 2) >> 2;
-        const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + 64 * half;
+        constexpr int kHalf = EPI == EPI_GLU ? 32 : 64, kNext = 96 - kHalf;
+        const uint32_t src = tmem + ((uint32_t)(32 * quarter) << 16) + kHalf * half;
         const Turn turn = {sb + kOffOut + (warp - 2) * 4096, lane};
         int i = 0;
         bool ok = true;
@@ -256,7 +264,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
                     float v[32];
-                    tmem_ld32(src + NB * (i & 1) + 32 * ch, v);
+                    tmem_ld32(src + NB * (i & 1) + kNext * ch, v);
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) add2(acc[ch][j], acc[ch][j + 1], v[j], v[j + 1]);
                 }
@@ -306,7 +314,8 @@ cudaError_t launch(GemmArgs p, const W32Operands &o, cudaStream_t st) {
     if (!encode(&ta, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, o.a, o.a_inner, p.M, 3, 2 * KB, BM,
                 CU_TENSOR_MAP_SWIZZLE_128B) ||
         !encode(&tw, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, o.w, o.width, o.w_rows, 1,
-                by_rows ? NB : KB, by_rows ? KB : NB, CU_TENSOR_MAP_SWIZZLE_NONE))
+                by_rows ? NB : KB, by_rows ? KB : EPI == EPI_GLU ? NB / 2 : NB,
+                CU_TENSOR_MAP_SWIZZLE_NONE))
         return cudaErrorInvalidValue;
     const long long work = (long long)p.m_tiles * p.n_tiles * p.splits;
     const int n = device_sms();
@@ -320,6 +329,7 @@ cudaError_t launch_w32(int epi, const GemmArgs &p, const W32Operands &o, cudaStr
     switch (epi) {
         case EPI_STATS: return launch<EPI_STATS>(p, o, st);
         case EPI_DZ: return launch<EPI_DZ>(p, o, st);
+        case EPI_GLU: return launch<EPI_GLU>(p, o, st);
     }
     return launch<EPI_OUT>(p, o, st);
 }

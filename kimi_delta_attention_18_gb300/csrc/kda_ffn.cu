@@ -9,13 +9,125 @@
 // them would cost 2 T F elements), da and db in the products' operand type, then the two
 // products that read them.  fp32 operands are three BF16 terms each, six products, as in the
 // cross entropy, whose kernel this is.
+#include "kda_f2.cuh"
 #include "kda_gemm_kernel.cuh"
+#include "kda_vec.cuh"
 
 namespace kda {
 namespace {
 
+// Few tokens: the weight's bytes bound the block, and a tile of 128 rows would be mostly empty.
+// A warp takes two channels, four rows of W, and their products with every token's x, in fp32
+// pairs; where channels are few, up to eight warps share two of them, a slice of D each, and
+// their sums are joined in order.
+// BF16 up to four tokens: 7,168 x 14,336 64-77 us, eight 213, by tiles 69.  fp32 up to eight:
+// 123-298 us, by tiles 280 and more.
+constexpr int kFewWarps = 8;
+bool few(const kda_ffn_desc_t *d) { return d->tokens <= (d->act_dtype == KDA_DTYPE_BF16 ? 4 : 8); }
+
+template <typename T, int VEC>
+__device__ __forceinline__ void widen(const Piece<T, VEC> &p, f2 (&v)[(VEC + 1) / 2]) {
+    float t[VEC];
+    p.get(t);
+#pragma unroll
+    for (int j = 0; j < (VEC + 1) / 2; ++j) v[j] = pk(t[2 * j], VEC == 1 ? 0.f : t[(2 * j + 1) % VEC]);
+}
+
+template <typename T, int NT, int VEC>
+__global__ void __launch_bounds__(32 * kFewWarps, NT <= 2 ? 4 : 2)
+    ffn_few_kernel(const T *x, const T *w, T *h, int tokens, int D, int F, int act, int slices) {
+    constexpr int VP = (VEC + 1) / 2, UNROLL = VEC == 1 ? 4 : 2;
+    __shared__ float sums[kFewWarps][4 * NT];
+    griddep_wait();
+    griddep_launch_dependents();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, slice = warp % slices;
+    const int f0 = 2 * (blockIdx.x * (kFewWarps / slices) + warp / slices);
+    f2 acc[4][NT];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = 0;
+    if (f0 < F) {
+        const int pieces = D / VEC;  // VEC: D is a multiple of it
+        const int begin = (int)((long long)pieces * slice / slices),
+                  end = (int)((long long)pieces * (slice + 1) / slices);
+        const T *rows[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)  // gate, gate, up, up
+            rows[r] = w + ((size_t)(r >> 1) * F + min(f0 + (r & 1), F - 1)) * D;
+#pragma unroll UNROLL
+        for (int i = begin + lane; i < end; i += 32) {
+            Piece<T, VEC> pw[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) pw[r].load(rows[r] + (size_t)i * VEC);
+            f2 v[4][VP];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) widen(pw[r], v[r]);
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                Piece<T, VEC> px;
+                px.load(x + (size_t)min(t, tokens - 1) * D + (size_t)i * VEC);
+                f2 u[VP];
+                widen(px, u);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int j = 0; j < VP; ++j) acc[r][t] = fma2(v[r][j], u[j], acc[r][t]);
+            }
+        }
+    }
+    float s[4][NT];
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float2 v = un(acc[r][t]);
+            s[r][t] = v.x + v.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) s[r][t] += __shfl_xor_sync(0xffffffffu, s[r][t], o);
+        }
+    if (slices > 1) {
+        if (lane == 0)
+#pragma unroll
+            for (int i = 0; i < 4 * NT; ++i) sums[warp][i] = s[i / NT][i % NT];
+        __syncthreads();
+        if (slice > 0) return;
+#pragma unroll
+        for (int i = 0; i < 4 * NT; ++i) {
+            s[i / NT][i % NT] = 0.f;
+            for (int k = 0; k < slices; ++k) s[i / NT][i % NT] += sums[warp + k][i];
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            if (lane != 2 * t + r || t >= tokens || f0 + r >= F) continue;
+            float f, df;
+            glu_act(act, s[r][t], f, df);
+            act_st(h, (size_t)t * F + f0 + r, f * s[2 + r][t]);
+        }
+}
+
+template <typename T, int VEC>
+cudaError_t launch_few(const void *x, const void *w, void *h, const kda_ffn_desc_t *d, cudaStream_t st) {
+    const int F = d->hidden, tasks = (F + 1) / 2, sms = device_sms();
+    int slices = 1;  // as many warps as the SMs hold
+    while (slices < kFewWarps && (long long)tasks * slices < 32ll * sms &&
+           d->width / VEC >= 64 * slices)
+        slices *= 2;
+    const dim3 grid(cdiv(tasks, kFewWarps / slices)), block(32 * kFewWarps);
+    const int n = d->tokens;
+    const auto kernel = n == 1   ? ffn_few_kernel<T, 1, VEC>
+                        : n == 2 ? ffn_few_kernel<T, 2, VEC>
+                        : n <= 4 ? ffn_few_kernel<T, 4, VEC>
+                                 : ffn_few_kernel<T, sizeof(T) == 4 ? 8 : 4, VEC>;
+    return launch_dependent(kernel, grid, block, 0, st, (const T *)x, (const T *)w, (T *)h, n,
+                            d->width, F, (int)d->act, slices);
+}
+
 struct Layout {
-    bool f32, pack;
+    bool f32, pack, w32;
     int planes, pairs, chunk, pitch, piece, pieces, dx_splits, dw_splits;
     size_t xp, wp, dz, acc, dw_acc, total;
 };
@@ -41,11 +153,14 @@ Layout layout_for(const kda_ffn_desc_t *d, bool backward) {
     l.chunk = l.f32 ? kChunkF32 : kChunkBf16;
     // copies with a pitch of whole 128-byte lines: fp32 in terms, and BF16 rows that a
     // tensor map cannot address
-    l.pack = l.f32 || D % 8 != 0;
+    l.pack = (l.f32 || D % 8 != 0) && (backward || !few(d));
+    // fp32, one row of tiles: W is split into its terms on the way (7,168 x 14,336, 9 to 128
+    // tokens: @@ us, copied in terms first 707)
+    l.w32 = l.f32 && l.pack && !backward && d->tokens <= BM && D % 4 == 0;
     l.pitch = l.pack ? (D + 63) / 64 * 64 : D;
     if (l.pack) {
         l.xp = round256(T * l.pitch * l.planes * 2);
-        l.wp = round256(2 * F * l.pitch * l.planes * 2);
+        l.wp = l.w32 ? 0 : round256(2 * F * l.pitch * l.planes * 2);
     }
     if (backward) {
         l.piece = piece_cols(d, l.planes);
@@ -77,9 +192,9 @@ kda_status_t check(const kda_ffn_desc_t *d) {
 cudaError_t run_pack(const kda_ffn_desc_t *d, const Layout &l, const void *x, const void *w,
                      uint8_t *ws, const void *&xp, const void *&wp, cudaStream_t st) {
     xp = l.pack ? ws : x;
-    wp = l.pack ? ws + l.xp : w;
+    wp = l.pack && !l.w32 ? ws + l.xp : w;
     if (!l.pack) return cudaSuccess;
-    const long long T = d->tokens, R = 2ll * d->hidden, most = 16ll * device_sms();
+    const long long T = d->tokens, R = l.w32 ? 0 : 2ll * d->hidden, most = 16ll * device_sms();
     const long long need = ((T + R) * (l.pitch / 8) + 255) / 256;
     const dim3 grid((unsigned)(need < most ? need : most));
     __nv_bfloat16 *to = (__nv_bfloat16 *)ws, *to_w = (__nv_bfloat16 *)(ws + l.xp);
@@ -93,6 +208,8 @@ cudaError_t run_pack(const kda_ffn_desc_t *d, const Layout &l, const void *x, co
                             (float *)nullptr);
 }
 
+constexpr int kTileCost = 16;  // a tile's start and end, in columns' time
+
 // Both projections of `cols` channels from the v0-th on, with the epilogue EPI.
 template <int EPI>
 cudaError_t run_glu(GemmArgs p, const Layout &l, const CUtensorMap &tx, const CUtensorMap &tw,
@@ -104,6 +221,23 @@ cudaError_t run_glu(GemmArgs p, const Layout &l, const CUtensorMap &tx, const CU
     p.N = 2 * cdiv(cols, 64) * 64;
     p.b_row0 = v0;
     p.k_blocks = cdiv(width, BK);
+    // Few rows: the width whose tiles leave the fewest columns' time unused in their last round
+    // over the SMs (256 x 7,168 x 14,336: 112 tiles of 256 columns for 76 pairs 90 us, 150 of
+    // 192 @@).
+    const int n = device_sms(), rows = cdiv(p.M, BM);
+    if (rows <= 8) {
+        int best = 0;
+        for (int bn = BN; bn >= 64; bn -= 64) {
+            const long long tiles = cdiv(p.N, bn);
+            const long long one = (rows * tiles + n - 1) / n;
+            const long long two = n < 2 ? one : (cdiv(rows, 2) * tiles + n / 2 - 1) / (n / 2);
+            const int cost = (int)(one < two ? one : two) * (bn + kTileCost);
+            if (!best || cost < best) {
+                best = cost;
+                p.bn = bn;
+            }
+        }
+    }
     if (l.f32) return run_gemm<EPI, false, false, true, false>(p, tx, tw, st);
     return p.k_blocks > kLongStages ? run_gemm<EPI, false, false, true, true>(p, tx, tw, st)
                                     : run_gemm<EPI, false, false, false, true>(p, tx, tw, st);
@@ -139,11 +273,18 @@ kda_status_t kda_gated_ffn_forward(const kda_ffn_desc_t *desc, const void *x, co
     if (l.total > 0 && (!workspace || workspace_bytes < l.total || off(workspace, 16)))
         return KDA_ERR_WORKSPACE;
     cudaStream_t st = (cudaStream_t)stream;
+    if (few(desc)) {
+        const bool vec = desc->width % (16 / size) == 0;
+        const cudaError_t e =
+            size == 4 ? (vec ? launch_few<float, 4>(x, weight, h, desc, st)
+                             : launch_few<float, 1>(x, weight, h, desc, st))
+                      : (vec ? launch_few<__nv_bfloat16, 8>(x, weight, h, desc, st)
+                             : launch_few<__nv_bfloat16, 1>(x, weight, h, desc, st));
+        return e == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    }
     const void *xp, *wp;
     CUtensorMap tx, tw;
-    if (run_pack(desc, l, x, weight, (uint8_t *)workspace, xp, wp, st) != cudaSuccess ||
-        !encode(&tx, xp, l.pitch, desc->tokens, l.planes, kMajor) ||
-        !encode(&tw, wp, l.pitch, desc->hidden, 2 * l.planes, kHalfBox))
+    if (run_pack(desc, l, x, weight, (uint8_t *)workspace, xp, wp, st) != cudaSuccess)
         return KDA_ERR_CUDA;
     GemmArgs p = one_product();
     p.M = desc->tokens;
@@ -152,6 +293,17 @@ kda_status_t kda_gated_ffn_forward(const kda_ffn_desc_t *desc, const void *x, co
     p.out = h;
     p.out_ld = desc->hidden;
     p.vec = desc->hidden % 8 == 0 && !off(h, 16);
+    if (l.w32) {
+        p.pairs = l.pairs;
+        p.cols = desc->hidden;
+        p.N = 2 * cdiv(p.cols, 64) * 64;
+        p.k_blocks = cdiv(desc->width, kW32Step);
+        const W32Operands o = {xp, l.pitch, (const float *)weight, 2ll * p.cols, desc->width};
+        return launch_w32(EPI_GLU, p, o, st) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+    }
+    if (!encode(&tx, xp, l.pitch, desc->tokens, l.planes, kMajor) ||
+        !encode(&tw, wp, l.pitch, desc->hidden, 2 * l.planes, kHalfBox))
+        return KDA_ERR_CUDA;
     return run_glu<EPI_GLU>(p, l, tx, tw, 0, desc->hidden, desc->width, st) == cudaSuccess
                ? KDA_OK : KDA_ERR_CUDA;
 }

@@ -50,7 +50,8 @@ struct GemmArgs {
     int groups, batches;
     int a_group, b_group;      // matrices in A's and B's planes
     int chunk;                 // FINE: stages per accumulator
-    int m_tiles, n_tiles, bn;  // set at the launch; bn: columns per tile, a multiple of 64
+    int m_tiles, n_tiles, bn;  // set at the launch (bn, columns per tile, unless the caller did:
+                               // a multiple of 64)
     int b_row0;                // B's first row (of the vocabulary's piece)
     int bk_row0;               // the same where the contraction is along B's rows
     // EPI_STATS, EPI_DZ
@@ -508,7 +509,8 @@ __device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
 inline int cdiv(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // C = A B^T with A as three BF16 planes [3][p.M][a_inner], K-major, and B an fp32 weight
-// [w_rows][width] (EPI_OUT: its rows are the contraction's, else its columns).
+// [w_rows][width] (EPI_OUT: its rows are the contraction's, else its columns; EPI_GLU: two
+// matrices of p.cols rows).
 // p.k_blocks counts kW32Step; tiles have kW32Cols columns.
 struct W32Operands {
     const void *a;

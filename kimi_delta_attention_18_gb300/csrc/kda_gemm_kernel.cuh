@@ -449,8 +449,8 @@ cudaError_t start_gemm(GemmArgs p, const CUtensorMap &ta, const CUtensorMap &tb,
     cudaError_t e = set_max_dynamic_smem((const void *)kernel, Smem<CTAS>::bytes);
     if (e != cudaSuccess) return e;
     p.m_tiles = cdiv(p.M, BM * CTAS);
-    p.n_tiles = cdiv(p.N, BN);
-    p.bn = cdiv(cdiv(p.N, p.n_tiles), 64) * 64;  // tiles of about equal width
+    p.n_tiles = cdiv(p.N, p.bn ? p.bn : BN);
+    if (!p.bn) p.bn = cdiv(cdiv(p.N, p.n_tiles), 64) * 64;  // tiles of about equal width
     const long long work = (long long)p.m_tiles * p.n_tiles * p.splits * p.batches;
     const int groups = (int)(work < n / CTAS ? work : n / CTAS);
     cudaLaunchConfig_t cfg = {};

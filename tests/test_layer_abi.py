@@ -151,12 +151,14 @@ def test_gated_ffn_workspace():
     L = kda.lib()
     size = L.kda_gated_ffn_workspace_size
     assert size(_ffn(), 0) == 0  # BF16 rows of whole 16-byte pieces are read as they are
-    d = _ffn(width=63)
-    assert size(d, 0) == 4 * 64 * 2 + 2 * 96 * 64 * 2
+    assert size(_ffn(width=63), 0) == 0  # few tokens read any rows
+    d = _ffn(width=63, tokens=16)
+    assert size(d, 0) == 16 * 64 * 2 + 2 * 96 * 64 * 2
     assert L.kda_gated_ffn_forward(d, A, A, A, None, 0, None, None) == WORKSPACE
     assert L.kda_gated_ffn_forward(d, A, A, A, A, size(d, 0) - 1, None, None) == WORKSPACE
     assert L.kda_gated_ffn_forward(d, A, A, A, A + 8, 2 ** 40, None, None) == WORKSPACE
-    assert size(_ffn(act_dtype=0), 0) == 3 * (4 + 2 * 96) * 64 * 2
+    assert size(_ffn(act_dtype=0, tokens=16), 0) == 3 * 16 * 64 * 2  # fp32: x's terms only
+    assert size(_ffn(act_dtype=0, tokens=300), 0) == 3 * (300 + 2 * 96) * 64 * 2
     assert L.kda_gated_ffn_backward(_ffn(), A, A, A, A, A, A, size(_ffn(), 1) - 1, None, None) == WORKSPACE
     # the adjoints of a piece: 1 GiB at most, or 512 channels
     assert size(_ffn(tokens=2 ** 18, hidden=2 ** 16), 1) < 2 ** 30 + 2 ** 18 * 64 * 4 + 2 ** 12
