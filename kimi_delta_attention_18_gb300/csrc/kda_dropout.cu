@@ -21,7 +21,10 @@ __global__ void __launch_bounds__(256)
     constexpr int COLS = VEC == 1 ? 4 : VEC;
     griddep_wait();
     griddep_launch_dependents();
-    const Keep keep(drop);
+    __shared__ __align__(16) uint32_t keys[kKeys];
+    Keep::lay_keys(drop, keys, threadIdx.x);
+    __syncthreads();
+    const Keep keep(drop, keys);
     const int per_row = (D + COLS - 1) / COLS;
     const long long total = rows * per_row, step = gridDim.x * 256ll;
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += step) {
@@ -37,9 +40,9 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
             for (int j = 0; j < COLS; ++j) v[j] = c + j < D ? act_ld(x, (size_t)(at + j)) : 0.f;
         }
-        const uint32_t m = keep.bits<COLS, false>(row, c);
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) v[j] = m >> j & 1 ? v[j] * kept : 0.f;
+        for (int j = 0; j < COLS; ++j) v[j] *= kept;
+        keep.template floats<false>(v, row, c);
         if constexpr (VEC > 1) {
             Piece<T, VEC>::store(out + at, v);
         } else {

@@ -77,7 +77,10 @@ Ring ring_for(const NormArgs &a, int op, bool bwd, int size, bool pairs) {
     // 1,170 x 8 x 7,168 145 us, 187 without, 8,190 x 8 x 1,024 120 and 134; sigmoid, 65,536 x
     // 2,048 225 and 244), not of the residual norm (32,768 x 4,096 225 and 219, 131,072 x
     // 1,024 230 and 220, 16,384 x 8,192 225 and 206).
-    r.skew = size == 2 && bwd && !pairs && r.tpr > 32 && (op == OP_SIGMOID || op == OP_SILU);
+    // Dropout's random words are as long (40,960 x 7,168 678 us, 725 without, 81,920 x 1,024 169
+    // and 172; forward, where they must come before the sums, 637 and 548).
+    r.skew = size == 2 && bwd && !pairs && r.tpr > 32 &&
+             (op == OP_SIGMOID || op == OP_SILU || op == OP_DROP);
     const int most = kRingBytes / r.stage_bytes;
     r.stages = r.skew ? most : bytes_in_flight(op, bwd, size, pairs) / r.stage_bytes;
     if (r.stages < 2) r.stages = 2;
@@ -102,6 +105,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __shared__ __align__(8) uint64_t bars[2 * kMaxStages];
     __shared__ __align__(8) uint64_t sum_bars[kRed][kWarps / 2];
     __shared__ float2 red[kRed][2 * kWarps];  // r.join for a row, those beyond r.warps zero
+    __shared__ __align__(16) uint32_t keys[OP == OP_DROP ? kKeys : 4];
     __shared__ int abort_flag;
     volatile int *abort = &abort_flag;
     const uint32_t sb = smem_addr(sm), bb = smem_addr(bars);
@@ -196,7 +200,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     RowMath<is_residual(OP) ? OP_RESIDUAL : OP, BWD, T, VEC, NV, !SKEW> math;
     math.begin(load_w);
-    const Keep keep(OP == OP_DROP ? p.drop : Drop{});
+    if constexpr (OP == OP_DROP) {
+        Keep::lay_keys(p.drop, keys, threadIdx.x);
+        named_bar_sync(15, r.work);
+    }
+    const Keep keep(OP == OP_DROP ? p.drop : Drop{}, keys);
     bool failed = false;  // a wait gave up: go through the motions, store nothing
     P px[NV], pg[NV], pd[NV];
     auto row_of = [&](long long t) { return t * r.rows + group; };
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         se = u.y;
         warp_sums(ss, se, r.join);
     };
-    auto outputs = [&](long long t, float ss, float se) {
+    auto outputs = [&](long long t, float ss, float se, uint32_t kept = 0) {
         const long long row = row_of(t);
         math.outputs(p, px, pg, pd, load_w, ss, se, [&](int k, f2 (&a1)[VP], f2 (&a2)[VP]) {
             const int c = column(k);
@@ -254,7 +262,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float v[VEC];
                 floats<VEC>(o, v);
                 if constexpr (OP == OP_DROP && BWD)
-                    if (to == p.o2) keep_floats(v, keep.bits<VEC, false>(row, c));
+                    if (to == p.o2) {
+                        if constexpr (SKEW) {
+#pragma unroll
+                            for (int j = 0; j < VEC; ++j)
+                                v[j] = kept >> (VEC * k + j) & 1 ? v[j] : 0.f;
+                        } else {
+                            keep.template floats<false>(v, row, c);
+                        }
+                    }
                 if constexpr (PAIRS) P::store((T *)to + row * p.D + c, v, c + 1 < p.D);
                 else P::store((T *)to + row * p.D + c, v);
             };
@@ -264,7 +280,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int i = 0;
     if constexpr (SKEW) {
+        uint32_t kept = 0, next_kept = 0;  // OP_DROP: which of a row's elements
         auto first_half = [&](long long t, int i) {
+            if constexpr (OP == OP_DROP) {
+                next_kept = 0;
+#pragma unroll
+                for (int k = 0; k < NV; ++k)
+                    next_kept |= keep.template bits<VEC, false>(row_of(t), column(k)) << (VEC * k);
+            }
             wait(full(i % r.stages), (i / r.stages) & 1);
             load(t, i);
             float ss, se;
@@ -277,12 +300,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         if (blockIdx.x < r.tiles) first_half(blockIdx.x, 0);
         for (long long t = blockIdx.x; t < r.tiles; t += gridDim.x, ++i) {
+            kept = next_kept;
             if (t + gridDim.x < r.tiles) first_half(t + gridDim.x, i + 1);
             wait(smem_addr(&sum_bars[i % kRed][group]), (i / kRed) & 1);
             float ss, se;
             row_sums(i % kRed, ss, se);
             load(t, i);
-            outputs(t, ss, se);
+            outputs(t, ss, se, kept);
             release(i);
         }
     } else {
@@ -293,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if constexpr (OP == OP_DROP && !BWD) {
 #pragma unroll
                 for (int k = 0; k < NV; ++k)
-                    keep_piece(pg[k], keep.bits<VEC, false>(row_of(t), column(k)));
+                    keep.template piece<false>(pg[k], row_of(t), column(k));
             }
             float ss, se;
             math.sums(p, px, pg, pd, load_w, ss, se);
@@ -341,7 +365,7 @@ template <int OP, bool BWD, typename T>
 cudaError_t launch_t(const NormArgs &a, const Ring &r, bool pairs, int blocks, cudaStream_t st) {
     if constexpr (sizeof(T) == 2 && (OP == OP_SIGMOID || OP == OP_SILU))
         if (a.strided) return launch_k<OP, BWD, T, false, false, true>(a, r, blocks, st);
-    if constexpr (sizeof(T) == 2 && BWD && (OP == OP_SIGMOID || OP == OP_SILU))
+    if constexpr (sizeof(T) == 2 && BWD && (OP == OP_SIGMOID || OP == OP_SILU || OP == OP_DROP))
         if (r.skew) return launch_k<OP, BWD, T, true, false, false>(a, r, blocks, st);
     return pairs ? launch_k<OP, BWD, T, false, true, false>(a, r, blocks, st)
                  : launch_k<OP, BWD, T, false, false, false>(a, r, blocks, st);

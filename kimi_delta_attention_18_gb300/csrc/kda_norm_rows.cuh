@@ -92,7 +92,12 @@ __global__ void __launch_bounds__(VEC == 1 && NV == 16 ? 1024 : 512,
     RowMath<is_residual(OP) ? OP_RESIDUAL : OP, BWD, T, VEC, NV> math;
     griddep_wait();
     math.begin(load_w);
-    const Keep keep(OP == OP_DROP ? p.drop : Drop{});
+    __shared__ __align__(16) uint32_t keys[OP == OP_DROP ? kKeys : 4];
+    if constexpr (OP == OP_DROP) {
+        Keep::lay_keys(p.drop, keys, threadIdx.x);
+        __syncthreads();
+    }
+    const Keep keep(OP == OP_DROP ? p.drop : Drop{}, keys);
 
     P px[NV], pg[NV], pd[NV];
     auto load = [&](long long row, P (&px)[NV], P (&pg)[NV], P (&pd)[NV]) {
@@ -125,7 +130,7 @@ __global__ void __launch_bounds__(VEC == 1 && NV == 16 ? 1024 : 512,
         else load(row, px, pg, pd);
         if constexpr (OP == OP_DROP && !BWD) {
 #pragma unroll
-            for (int i = 0; i < NV; ++i) keep_piece(pg[i], keep.bits<VEC, SHIFT>(row, column(i)));
+            for (int i = 0; i < NV; ++i) keep.template piece<SHIFT>(pg[i], row, column(i));
         }
         float ss, se;
         math.sums(p, px, pg, pd, load_w, ss, se);
@@ -141,7 +146,7 @@ __global__ void __launch_bounds__(VEC == 1 && NV == 16 ? 1024 : 512,
             if ((BWD || is_residual(OP)) && o2) {
                 floats<VEC>(a2, t);
                 if constexpr (OP == OP_DROP && BWD)
-                    keep_floats(t, keep.bits<VEC, SHIFT>(row, column(i)));
+                    keep.template floats<SHIFT>(t, row, column(i));
                 store_piece<SHIFT, T, VEC>(o2 + base, column(i), p.D, t);
             }
         });
