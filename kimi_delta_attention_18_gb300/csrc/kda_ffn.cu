@@ -155,7 +155,7 @@ Layout layout_for(const kda_ffn_desc_t *d, bool backward) {
     // tensor map cannot address
     l.pack = (l.f32 || D % 8 != 0) && (backward || !few(d));
     // fp32, one row of tiles: W is split into its terms on the way (7,168 x 14,336, 9 to 128
-    // tokens: @@ us, copied in terms first 707)
+    // tokens: 345 us, copied in terms first 707)
     l.w32 = l.f32 && l.pack && !backward && d->tokens <= BM && D % 4 == 0;
     l.pitch = l.pack ? (D + 63) / 64 * 64 : D;
     if (l.pack) {
@@ -223,7 +223,7 @@ cudaError_t run_glu(GemmArgs p, const Layout &l, const CUtensorMap &tx, const CU
     p.k_blocks = cdiv(width, BK);
     // Few rows: the width whose tiles leave the fewest columns' time unused in their last round
     // over the SMs (256 x 7,168 x 14,336: 112 tiles of 256 columns for 76 pairs 90 us, 150 of
-    // 192 @@).
+    // 192 78).
     const int n = device_sms(), rows = cdiv(p.M, BM);
     if (rows <= 8) {
         int best = 0;

@@ -769,3 +769,28 @@ def test_wrong_tensors_are_refused():
                  lambda: kda.dropout(x, -0.5, rng), lambda: kda.residual_norm(x, x, dropout=1.5, rng=rng)):
         with pytest.raises(kda.KDAError):
             call()
+
+
+def test_example_runs_with_all_parts():
+    """The example's model with the recurrence, the feed-forward block and dropout: every
+    parameter gets a finite gradient, the same one for the same mask, another for another, and
+    the steps run."""
+    from examples.train_lm import Model, batch, train
+    torch.manual_seed(3)
+    model = Model(61, 128, 1, 2, full=True, dropout=0.25)
+    ids, targets, cu = batch(61, (40, 1, 23), _gen(3))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    grads = []
+    for rng in (_rng(1, 5), _rng(1, 5), _rng(1, 6)):
+        model.zero_grad()
+        model(ids, targets, cu, status, rng).backward()
+        rng += 1  # moved on after the backward pass has what it needs
+        grads.append([p.grad.clone() for p in model.parameters()])
+    names = [n for n, _ in model.named_parameters()]
+    assert any("gate_up" in n for n in names) and any("xgz" in n for n in names)
+    for n, a, b, c in zip(names, *grads):
+        assert bool(torch.isfinite(a).all()) and bool((a != 0).any()), n
+        assert torch.equal(a, b), n
+        assert not torch.equal(a, c), n
+    assert int(status) == 0
+    assert len(train(steps=3, layers=2, full=True, dropout=0.1, log=lambda s: None)) == 3
