@@ -563,7 +563,7 @@ typedef struct {
  * A malformed cu_seqlens is reported in dev_status (KDA_ERR_INVALID_ARG) and nothing or
  * only part of the outputs is written; KDA_ERR_TIMEOUT there: a bounded wait gave up.
  * The results do not depend on how the work was spread over the GPU.
- * Workspace: kda_recurrence_workspace_size(desc, 0), 16-byte aligned (0 up to 512 tokens and
+ * Workspace: kda_recurrence_workspace_size(desc, 0), 16-byte aligned (0 up to 256 tokens and
  * on invalid arguments).
  * Pointers aligned to their element; 64 channels or more, with strides and bases of whole 16
  * bytes, are the fast case.

@@ -150,7 +150,9 @@ Layout layout_for(const kda_ffn_desc_t *d, bool backward) {
     l.f32 = d->act_dtype == KDA_DTYPE_F32;
     l.planes = l.f32 ? 3 : 1;
     l.pairs = l.f32 ? 6 : 1;
-    l.chunk = l.f32 ? kChunkF32 : kChunkBf16;
+    // fp32: h and its gradients within 6e-7 of 64 bits (eight stages to an accumulator: 1.1e-6,
+    // 2,000 x 2,048 x 3,000 gradient 3 % faster; two: 4e-7, 13 % slower)
+    l.chunk = l.f32 ? 4 : kChunkBf16;
     // copies with a pitch of whole 128-byte lines: fp32 in terms, and BF16 rows that a
     // tensor map cannot address
     l.pack = (l.f32 || D % 8 != 0) && (backward || !few(d));

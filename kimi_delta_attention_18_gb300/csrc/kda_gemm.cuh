@@ -173,7 +173,22 @@ struct Turn {
                      : "memory");
         return v;
     }
+    // piece q of this thread's row
+    __device__ __forceinline__ float4 own(int q) const {
+        float4 v;
+        asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+                     : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                     : "r"(at + lane * 128 + ((q ^ (lane & 7)) << 4))
+                     : "memory");
+        return v;
+    }
     // word `lane` of row r
+    __device__ __forceinline__ void set_word(int r, float v) const {
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) +
+                                                     4 * (lane & 3)),
+                     "f"(v)
+                     : "memory");
+    }
     __device__ __forceinline__ float word(int r) const {
         float v;
         asm volatile("ld.shared.f32 %0, [%1];"
@@ -404,6 +419,24 @@ struct Row {
         if (f >= (p.cols + 63) / 64 * 64) return;
         const int n = p.cols - f;
         const size_t at = (size_t)row * p.out_ld + f;
+        if (!p.vec) {  // rows of any width: a row at a time (777 x 515 x 1,003, BF16: 27 us, each
+                       // thread its own row 28)
+            const int rows = (int)(p.M - row0 < 32 ? p.M - row0 : 32), l = turn.lane;
+            __syncwarp();
+            for (int r0 = 0; r0 < 32; r0 += kBatch) {
+                float v[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const size_t e = (size_t)(row0 + r0 + k) * p.out_ld + f + l;
+                    const bool in = r0 + k < rows && l < n;
+                    if (p.planes == 1) v[k] = in ? act_ld((const __nv_bfloat16 *)p.d_h, e) : 0.f;
+                    else v[k] = in ? act_ld((const float *)p.d_h, e) : 0.f;
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) turn.set_word(r0 + k, v[k]);
+            }
+            __syncwarp();
+        }
 #pragma unroll
         for (int i0 = 0; i0 < 32; i0 += 8) {
             float d[8];
@@ -422,12 +455,9 @@ struct Row {
                     *(float4 *)d = *(const float4 *)((const float *)p.d_h + at + i0);
                     *(float4 *)(d + 4) = *(const float4 *)((const float *)p.d_h + at + i0 + 4);
                 }
-            } else if (live) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (i0 + k < n)
-                        d[k] = p.planes == 1 ? act_ld((const __nv_bfloat16 *)p.d_h, at + i0 + k)
-                                             : act_ld((const float *)p.d_h, at + i0 + k);
+            } else if (!p.vec) {
+                *(float4 *)d = turn.own(i0 / 4);
+                *(float4 *)(d + 4) = turn.own(i0 / 4 + 1);
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
@@ -437,6 +467,7 @@ struct Row {
                 b[i0 + k] = d[k] * v;
             }
         }
+        __syncwarp();  // the lines are read
         // One plane (BF16): dz is rounded to the products' operand type, 2^-8 of a term at
         // most and at random, as large an error as the outputs' own rounding.
         for (int pl = 0; pl < p.planes; ++pl) {

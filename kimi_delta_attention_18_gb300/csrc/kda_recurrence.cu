@@ -54,8 +54,8 @@ constexpr int tok_of(bool bwd, bool tma) { return !bwd && tma ? 32 : 16; }
 constexpr int tile_of(bool bwd, bool tma) { return warps_of(bwd, tma) * tok_of(bwd, tma); }
 constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
 // Up to so many tokens one block walks a sequence; beyond, a launch lays out the tiles of a
-// batch first.
-constexpr int kWalkTokens = 512;
+// batch first (400 x 512 BF16: walking 17 us; 1,000 x 512: 4 and 9).
+constexpr int kWalkTokens = 256;
 
 struct RecArgs {
     const void *x;

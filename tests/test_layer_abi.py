@@ -85,7 +85,7 @@ def test_recurrence_refuses_pointers():
 def test_recurrence_workspace():
     size = kda.lib().kda_recurrence_workspace_size
     for backward, tile in ((0, 128), (1, 64)):
-        assert size(_rec(tokens=512), backward) == 0 and size(_rec(tokens=0), backward) == 0
+        assert size(_rec(tokens=256), backward) == 0 and size(_rec(tokens=0), backward) == 0
         d = _rec(tokens=1025, channels=100)
         need = size(d, backward)
         # tiles (one more for each sequence) x 64 channels: maps and ends
