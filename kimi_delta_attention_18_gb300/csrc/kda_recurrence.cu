@@ -603,9 +603,11 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
     }
 }
 
-// The tiles of every sequence, cleared maps and ends, and the states of empty sequences.
+// The tiles of every sequence, cleared maps and ends, the states of empty sequences, and, where
+// the states are updated in place, a copy of those that chains start from: every tile of a
+// chain's first group reads it, and the chain's last tile can be done before the others.
 __global__ void __launch_bounds__(1024) recurrence_tiles_kernel(const __grid_constant__ RecArgs p,
-                                                                bool backward, int tile) {
+                                                                bool backward, int tile, float *copy) {
     __shared__ int sums[32];
     __shared__ int base;
     __shared__ bool bad;
@@ -619,6 +621,8 @@ __global__ void __launch_bounds__(1024) recurrence_tiles_kernel(const __grid_con
         for (long long k = me; k < pieces; k += all) to[k] = make_uint4(kNone, kNone, kNone, kNone);
         const float *first = backward ? p.d_final : p.h0;
         float *final_out = backward ? p.d_h0 : p.h_final;
+        if (copy)
+            for (long long k = me; k < (long long)p.N * p.C; k += all) copy[k] = first[k];
         if (final_out && p.cu) {
             for (int n = blockIdx.x - 1; n < p.N; n += gridDim.x - 1) {
                 if (p.cu[n] != p.cu[n + 1]) continue;
@@ -785,14 +789,15 @@ long long most_tiles(const kda_recurrence_desc_t *d, bool bwd) {
 int groups_of(const kda_recurrence_desc_t *d) { return (d->channels + kChan - 1) / kChan; }
 
 struct Layout {
-    size_t tiles, total;
+    size_t tiles, maps, total;
 };
 Layout layout_for(const kda_recurrence_desc_t *d, bool bwd) {
     Layout l = {};
     if (walks(d)) return l;
     const size_t n = (size_t)most_tiles(d, bwd), g = groups_of(d);
     l.tiles = round256(n * sizeof(int4));
-    l.total = 256 + l.tiles + n * g * kEntry;
+    l.maps = n * g * kEntry;
+    l.total = 256 + l.tiles + l.maps + round256((size_t)d->num_seqs * d->channels * sizeof(float));
     return l;
 }
 
@@ -842,7 +847,7 @@ constexpr int kMaxSmem = 180 * 1024;  // a stage of 128 KB, two windows of 24 en
 
 
 template <typename T, bool BWD, bool MIX, int BY, bool SPLIT>
-cudaError_t launch_by(RecArgs &a, const CUtensorMap (&m)[4], cudaStream_t st) {
+cudaError_t launch_by(RecArgs &a, float *copy, const CUtensorMap (&m)[4], cudaStream_t st) {
     const auto kernel = recurrence_kernel<T, BWD, MIX, BY, SPLIT>;
     typedef Stage<T, BWD, MIX, BY == BY_TMA> S;
     const int sms = device_sms();
@@ -853,9 +858,12 @@ cudaError_t launch_by(RecArgs &a, const CUtensorMap (&m)[4], cudaStream_t st) {
         const long long work = (long long)a.most_tiles * a.groups, pieces = work * (kEntry / 16);
         a.ends = (float *)(a.maps + work * kChan);
         const int clear = (int)(pieces / 4096 < 2 * sms ? pieces / 4096 : 2 * sms) + 1;
+        const float *&first = BWD ? a.d_final : a.h0;
+        if (first != (BWD ? a.d_h0 : a.h_final)) copy = nullptr;
         const cudaError_t e = launch_dependent(recurrence_tiles_kernel, dim3(1 + clear), dim3(1024), 0,
-                                               st, a, BWD, S::warps * S::tok);
+                                               st, a, BWD, S::warps * S::tok, first ? copy : nullptr);
         if (e != cudaSuccess) return e;
+        if (first && copy) first = copy;
         // A look back reads a few more groups than are worked on at once in a chain.
         const int chain = S::fit(kUsualWindow) * sms / (a.groups * kGroup);
         a.window = chain + 3 < 16 ? chain + 3 : 16;
@@ -875,22 +883,23 @@ cudaError_t launch_t(const kda_recurrence_desc_t *d, RecArgs &a, bool pairs, voi
                      cudaStream_t st) {
     CUtensorMap m[4] = {};
     if (walks(d))
-        return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, false>(a, m, st)
-                     : launch_by<T, BWD, MIX, BY_ONE, false>(a, m, st);
+        return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, false>(a, nullptr, m, st)
+                     : launch_by<T, BWD, MIX, BY_ONE, false>(a, nullptr, m, st);
     const Layout l = layout_for(d, BWD);
     uint8_t *ws = (uint8_t *)workspace;
     a.control = (unsigned *)ws;
     a.tiles = (int4 *)(ws + 256);
     a.maps = (float2 *)(ws + 256 + l.tiles);
+    float *copy = (float *)(ws + 256 + l.tiles + l.maps);
     constexpr int tok = tok_of(BWD, true), size = sizeof(T);
     const bool tma =
         encode(&m[0], a.g, 4, a.C, a.T, a.g_stride, tok) &&
         (BWD ? encode(&m[1], a.d, size, a.C, a.T, a.C, tok) && encode(&m[2], a.hs, size, a.C, a.T, a.C, tok) &&
                    (!MIX || encode(&m[3], a.x, size, a.C, a.T, a.x_stride, tok))
              : encode(&m[1], a.x, size, a.C, a.T, a.x_stride, tok));
-    if (tma && pairs) return launch_by<T, BWD, MIX, BY_TMA, true>(a, m, st);
-    return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, true>(a, m, st)
-                 : launch_by<T, BWD, MIX, BY_ONE, true>(a, m, st);
+    if (tma && pairs) return launch_by<T, BWD, MIX, BY_TMA, true>(a, copy, m, st);
+    return pairs ? launch_by<T, BWD, MIX, BY_PAIRS, true>(a, copy, m, st)
+                 : launch_by<T, BWD, MIX, BY_ONE, true>(a, copy, m, st);
 }
 
 template <bool BWD>

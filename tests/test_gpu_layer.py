@@ -293,6 +293,42 @@ def test_recurrence_states_may_be_updated_in_place():
         assert same is state and torch.equal(state, last) and torch.equal(h2, h)
 
 
+def test_recurrence_updates_states_of_short_chains_in_place():
+    """Chains of a few tiles: the last tile may be done before the others have read where the
+    chain starts.  The C entry points update h0 and d_h_final in place."""
+    g, C = _gen(10), 200
+    lengths = [300, 700, 1100, 0, 1900, 257] * 20
+    cu, T, N = _cu(lengths), sum(lengths), len(lengths)
+    x, gate, h0 = _randn((T, C), g), -torch.rand((T, C), generator=g, device="cuda") * 1e-3, _randn((N, C), g)
+    h, last = kda.linear_recurrence(x, gate, h0, cu)
+    dx, dg, d_h0 = kda.linear_recurrence_backward(x, x, gate, h, h0, cu, last)
+    desc = kda._layer.RecurrenceDesc(0, 0, N, T, C, 0, 0)
+    ws = torch.empty(kda.lib().kda_recurrence_workspace_size(desc, 1), dtype=torch.uint8, device="cuda")
+    for _ in range(10):
+        state = h0.clone()
+        h2, same = kda.linear_recurrence(x, gate, state, cu, h_final=state)
+        assert torch.equal(state, last) and torch.equal(h2, h)
+        dx2, dg2 = torch.empty_like(x), torch.empty_like(gate)
+        assert kda.lib().kda_recurrence_backward(
+            desc, x.data_ptr(), None, gate.data_ptr(), h.data_ptr(), h0.data_ptr(), cu.data_ptr(),
+            state.data_ptr(), dx2.data_ptr(), dg2.data_ptr(), state.data_ptr(), ws.data_ptr(),
+            ws.numel(), None, torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(state, d_h0) and torch.equal(dx2, dx) and torch.equal(dg2, dg)
+
+
+def test_recurrence_of_no_tokens():
+    for write in ("add", "mix"):
+        x, g = torch.empty((0, 6), device="cuda"), torch.empty((0, 6), device="cuda")
+        h0 = torch.randn((3, 6), device="cuda")
+        h, last = kda.linear_recurrence(x, g, h0, _cu([0, 0, 0]), write=write)
+        assert h.shape == (0, 6) and torch.equal(last, h0)
+        dx, dg, d_h0 = kda.linear_recurrence_backward(x, x, g, h, h0, _cu([0, 0, 0]), last, write=write)
+        assert dx.shape == dg.shape == (0, 6) and torch.equal(d_h0, last)
+        assert bool((kda.linear_recurrence(x, g)[1] == 0).all())
+        state = torch.empty((0, 6), device="cuda")
+        assert kda.linear_recurrence_step(x, g, state, write=write)[0].shape == (0, 6)
+
+
 def test_recurrence_captured_and_on_another_stream():
     g, C, T = _gen(9), 192, 6000
     cu = _cu([2500, 0, 3500])
