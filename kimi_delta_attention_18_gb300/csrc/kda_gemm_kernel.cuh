@@ -472,7 +472,7 @@ cudaError_t start_gemm(GemmArgs p, const CUtensorMap &ta, const CUtensorMap &tb,
 // Pairs of CTAs unless single ones finish in fewer rounds over the SMs (few rows:
 // a pair's second half would be idle).
 bool use_pairs(const GemmArgs &p, int n) {
-    const long long cols = (long long)cdiv(p.N, BN) * p.splits * p.batches;
+    const long long cols = (long long)cdiv(p.N, p.bn ? p.bn : BN) * p.splits * p.batches;
     const long long one = (cdiv(p.M, BM) * cols + n - 1) / n;
     const long long two = (cdiv(p.M, 2 * BM) * cols + n / 2 - 1) / (n / 2);
     return n >= 2 && two <= one;

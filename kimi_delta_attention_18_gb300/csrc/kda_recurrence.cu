@@ -427,8 +427,8 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
         if (!BWD && SPLIT && threadIdx.x == 0) take(ahead_ticket, ahead);
         const int c = t.group * kChan + 2 * lane, left = p.C - c;
         // The look back's window: the maps of the group's earlier tiles, then of earlier groups
-        // their maps and ends, all nearest first; a warp reads every fourth entry, for the
-        // first time while the tile's tokens come, and again while it is not there.
+        // their maps and ends, all nearest first.  The warps read its entries in turn, for the
+        // first time while the tile's tokens come, and again while they are not there.
         const int inside = t.place % kGroup, groups = t.place / kGroup;
         uint8_t *window = windows + (BWD ? 0 : (k & 1) * (p.window + kGroup - 1) * kEntry);
         const int most = inside + min(p.window, groups);
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
         if (!BWD && landed) start(k + 1);  // the tile is in registers
 
         // the state that enters the tile, in every warp
-        float2 in, group_in = make_float2(0.f, 0.f);  // state that enters the tile, its group
+        float2 in, group_in = make_float2(0.f, 0.f);  // into the tile, into its group
         if (!SPLIT) {
             in = carry[k & 1][lane];
         } else {
@@ -538,11 +538,11 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
         }
         if (failed) {  // (set before a barrier that everyone has passed)
             if (threadIdx.x == 0) dev_fail(p.status, KDA_ERR_TIMEOUT);
-            if (BY == BY_TMA && !BWD && landed) {
+            if (BY == BY_TMA && !BWD && landed) {  // the next tile's copies land before the block exits
                 TileAt u;
                 volatile int never = 0;
                 if (turn(k + 1, u)) mbar_wait(smem_addr(&bars[warp]), (k + 1) & 1, &never, kWaitLimit);
-            } else if (BY == BY_TMA && !landed) {  // let the copies land before the block exits
+            } else if (BY == BY_TMA && !landed) {  // or this one's
                 volatile int never = 0;
                 mbar_wait(smem_addr(&bars[warp]), k & 1, &never, kWaitLimit);
             }
