@@ -20,10 +20,14 @@ namespace {
 // A warp takes two channels, four rows of W, and their products with every token's x, in fp32
 // pairs; where channels are few, up to eight warps share two of them, a slice of D each, and
 // their sums are joined in order.
-// BF16 up to four tokens: 7,168 x 14,336 64-77 us, eight 213, by tiles 69.  fp32 up to eight:
-// 123-298 us, by tiles 280 and more.
+// BF16, one token: 7,168 x 14,336 63.5 us, by tiles 67.1; 1,024 x 2,816 5.3 and 8.4.  Two: 73.9 and
+// 67.1, but 2,048 x 5,632 14.8 and 15.2; four: 77.0 and 67.2, 14.3 and 8.4.  fp32 up to eight:
+// 7,168 x 14,336 123-298 us, by tiles 345.
 constexpr int kFewWarps = 8;
-bool few(const kda_ffn_desc_t *d) { return d->tokens <= (d->act_dtype == KDA_DTYPE_BF16 ? 4 : 8); }
+bool few(const kda_ffn_desc_t *d) {
+    if (d->act_dtype != KDA_DTYPE_BF16) return d->tokens <= 8;
+    return d->tokens == 1 || (d->tokens == 2 && (long long)d->width * d->hidden <= 1ll << 24);
+}
 
 template <typename T, int VEC>
 __device__ __forceinline__ void widen(const Piece<T, VEC> &p, f2 (&v)[(VEC + 1) / 2]) {
@@ -120,8 +124,8 @@ cudaError_t launch_few(const void *x, const void *w, void *h, const kda_ffn_desc
     const int n = d->tokens;
     const auto kernel = n == 1   ? ffn_few_kernel<T, 1, VEC>
                         : n == 2 ? ffn_few_kernel<T, 2, VEC>
-                        : n <= 4 ? ffn_few_kernel<T, 4, VEC>
-                                 : ffn_few_kernel<T, sizeof(T) == 4 ? 8 : 4, VEC>;
+                        : n <= 4 ? ffn_few_kernel<T, sizeof(T) == 4 ? 4 : 2, VEC>
+                                 : ffn_few_kernel<T, sizeof(T) == 4 ? 8 : 2, VEC>;
     return launch_dependent(kernel, grid, block, 0, st, (const T *)x, (const T *)w, (T *)h, n,
                             d->width, F, (int)d->act, slices);
 }
