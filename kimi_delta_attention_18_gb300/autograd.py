@@ -91,7 +91,10 @@ def kda_gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, dev_st
 class ResidualNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, h, y, weight, scale, eps, dropout, rng, site, dev_status):
-        rng = rng.clone() if dropout and isinstance(rng, torch.Tensor) else rng
+        if not dropout:
+            rng = None
+        elif isinstance(rng, torch.Tensor):
+            rng = rng.clone()
         h_out, out = _lm.residual_norm(h, y, weight, scale=scale, eps=eps, dropout=dropout, rng=rng,
                                        site=site, dev_status=dev_status)
         ctx.save_for_backward(h_out, weight, rng)

@@ -830,3 +830,18 @@ def test_example_runs_with_all_parts():
         assert not torch.equal(a, c), n
     assert int(status) == 0
     assert len(train(steps=3, layers=2, full=True, dropout=0.1, log=lambda s: None)) == 3
+
+
+@pytest.mark.parametrize("p", [0.0, 0.25])
+def test_the_generator_moves_on_before_the_residual_norms_gradient(p):
+    """rng moves on between the passes, also while dropout is 0: the gradients are those of the
+    mask that the forward pass had."""
+    g = _gen(21)
+    h, y = _randn((9, 40), g).requires_grad_(), _randn((9, 40), g).requires_grad_()
+    grads = []
+    for moves in (0, 1):
+        rng = _rng(3)
+        out = autograd.kda_residual_norm(h, y, None, scale=0.5, dropout=p, rng=rng, site=2)
+        rng[1] += moves
+        grads.append(torch.autograd.grad(sum(t.square().sum() for t in out), (h, y)))
+    assert all(torch.equal(a, b) and bool((a != 0).any()) for a, b in zip(*grads))

@@ -236,3 +236,23 @@ def test_dropout_binding_refuses_tensors():
     from kimi_delta_attention_18_gb300 import autograd
     with pytest.raises(ValueError, match="needs y"):
         autograd.kda_residual_norm(x, dropout=0.5, rng=rng)
+
+
+def test_a_generator_may_move_on_before_the_gradient(monkeypatch):
+    """A step's rng moves on between its forward and its backward pass, with dropout and while a
+    schedule holds it at 0; the gradient with dropout has what rng was."""
+    from kimi_delta_attention_18_gb300 import autograd
+    seen = []
+
+    def backward(d, h, w, dh, want_dy, rng, **k):
+        seen.append(rng)
+        return d * 1.0, d * 1.0, None
+    monkeypatch.setattr(autograd._lm, "residual_norm", lambda h, y, w, **k: (h * 1.0, h * 1.0))
+    monkeypatch.setattr(autograd._lm, "residual_norm_backward", backward)
+    for p in (0.25, 0.0):
+        x, rng = torch.ones((2, 4), requires_grad=True), torch.tensor([3, 5])
+        h, out = autograd.kda_residual_norm(x, x * 2.0, None, dropout=p, rng=rng, site=1)
+        rng[1] += 1
+        (h + out).sum().backward()
+        assert bool((x.grad != 0).all())
+    assert seen[0].tolist() == [3, 5] and seen[1] is None
