@@ -141,10 +141,10 @@ struct Layout {
 int piece_cols(const kda_ffn_desc_t *d, int planes) {
     const long long all = (long long)cdiv(d->hidden, BN) * BN;
     long long cols = (1ll << 30) / ((long long)(d->tokens > 0 ? d->tokens : 1) * planes * 4);
+    cols = cols / BN * BN;  // so that the pieces' rounding up stays within it
     if (cols < 512) cols = 512;
-    if (cols < all) cols = cdiv(all, cdiv(all, cols));
-    cols = (long long)cdiv(cols, BN) * BN;
-    return (int)(cols < all ? cols : all);
+    if (cols >= all) return (int)all;
+    return cdiv(cdiv(all, cdiv(all, cols)), BN) * BN;
 }
 
 Layout layout_for(const kda_ffn_desc_t *d, bool backward) {

@@ -256,3 +256,17 @@ def test_a_generator_may_move_on_before_the_gradient(monkeypatch):
         (h + out).sum().backward()
         assert bool((x.grad != 0).all())
     assert seen[0].tolist() == [3, 5] and seen[1] is None
+
+
+def test_gated_ffn_adjoints_stay_within_their_bound():
+    """The adjoints of a piece take 1 GiB at most (or 512 channels) where the channels do not
+    divide evenly, too.  They lie beside x and weight in terms (fp32) and dx's sums [T, D]."""
+    size = kda.lib().kda_gated_ffn_workspace_size
+    for tokens, hidden, f32 in ((400000, 8192, False), (81920, 28672, True), (66000, 8200, False),
+                                (23000, 8200, True), (300001, 5000, False), (600000, 1000, False)):
+        d = _ffn(tokens=tokens, hidden=hidden, act_dtype=0 if f32 else 1)
+        planes, D = (3 if f32 else 1), 64
+        terms = planes * 2 * D * (tokens + 2 * hidden) if f32 else 0
+        adjoints = max(2 ** 30, 512 * 4 * tokens * planes)
+        # dx and d_weight of so many tokens are one part each but for a few channels' sums
+        assert size(d, 1) <= adjoints + terms + 4 * tokens * D + 2 ** 20, (tokens, hidden)
