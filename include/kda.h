@@ -685,6 +685,18 @@ const char *kda_build_info(void);
  */
 kda_status_t kda_selftest_wait_timeout(int32_t limit_us, int32_t *dev_status, void *stream);
 
+/*
+ * The same for a kernel whose blocks wait for one another: the linear recurrence of one
+ * sequence (KDA_WRITE_ADD, no states; h NULL: its forward pass from x to out [T, C]; else its
+ * gradient for the adjoint x, to out and dg) with no time to wait.  Of a long sequence some
+ * block gives up in the middle of the work, the others with it, and dev_status (required) is
+ * KDA_ERR_TIMEOUT; the outputs are then incomplete.  Workspace as for the call it stands for.
+ */
+kda_status_t kda_selftest_recurrence_timeout(const kda_recurrence_desc_t *desc, const void *x,
+                                             const float *g, const void *h, void *out, float *dg,
+                                             void *workspace, size_t workspace_bytes,
+                                             int32_t *dev_status, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

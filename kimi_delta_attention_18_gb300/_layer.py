@@ -40,6 +40,7 @@ def bind(L):
             ("kda_recurrence_forward", [R] + [P] * 7 + [Z, P, P]),
             ("kda_recurrence_backward", [R] + [P] * 11 + [Z, P, P]),
             ("kda_recurrence_step", [R] + [P] * 6),
+            ("kda_selftest_recurrence_timeout", [R] + [P] * 6 + [Z, P, P]),
             ("kda_dropout", [ctypes.POINTER(DropoutDesc), ctypes.c_int64, I, I] + [P] * 3),
             ("kda_gated_ffn_forward", [F] + [P] * 4 + [Z, P, P]),
             ("kda_gated_ffn_backward", [F] + [P] * 6 + [Z, P, P])):

@@ -77,6 +77,7 @@ struct RecArgs {
     float *ends;         // [tiles][64 groups], behind maps
     unsigned *control;   // next tile, tiles, a wait gave up
     int most_tiles, window;  // window: tiles that a look back reads
+    long long wait_limit;    // of a look back, in SM clocks
 };
 enum { NEXT = 0, TILES = 1, ABORT = 2 };
 
@@ -246,7 +247,9 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
     __shared__ int ticket_at[2];
     __shared__ __align__(8) uint64_t bars[kWarps];
     __shared__ int abort_flag;
-    __shared__ bool failed;
+    // Whether a wait gave up, told and read with `seen` (one thread's view at some moment could
+    // be another's at the next, and a warp would leave a loop whose barriers others still enter).
+    __shared__ bool gave_up[2];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const T *x = (const T *)p.x, *d = (const T *)p.d, *hs = (const T *)p.hs;
     const float *first = BWD ? p.d_final : p.h0;
@@ -255,7 +258,7 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
     uint8_t *windows = sm + S::block;
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        failed = false;
+        gave_up[0] = gave_up[1] = false;
         if (BY == BY_TMA) {
             for (int w = 0; w < kWarps; ++w) mbar_init(smem_addr(&bars[w]), 1);
             mbar_fence_init();
@@ -362,13 +365,14 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
     };
     auto tokens = [&](const TileAt &t) { return max(0, min(TOK, t.t1 - t.t0 - warp * TOK)); };
     f2 fa[BWD ? 1 : TOK], fb[BWD ? 1 : TOK];  // forward: the tile's factors and terms
+    unsigned polls = 0;
     // The map of this warp's tokens of the k-th tile; false if they did not come.
     auto reduce = [&](int k, const TileAt &t, auto hold) {
         bool landed = true;
         if (BY == BY_TMA) {
             landed = __all_sync(0xffffffffu, mbar_wait(smem_addr(&bars[warp]), k & 1, &abort_flag,
                                                        kWaitLimit));
-            if (!landed) failed = true;
+            if (!landed) gave_up[polls & 1] = true;
         } else {
             cp_async_wait_all();  // every lane reads what it copied itself
         }
@@ -419,7 +423,6 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
     };
 
     start(0);
-    unsigned polls = 0;
     TileAt t;
     for (int k = 0; turn(k, t); ++k) {
         int ahead_ticket = 0;
@@ -477,6 +480,7 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
 
         // the state that enters the tile, in every warp
         float2 in, group_in = make_float2(0.f, 0.f);  // into the tile, into its group
+        bool failed = false;
         if (!SPLIT) {
             in = carry[k & 1][lane];
         } else {
@@ -494,6 +498,7 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
                     all_maps |= v.x;
                     all_ends |= v.y;
                 }
+                failed = gave_up[polls & 1];
                 ++polls;
                 if (failed) break;
                 const bool known = !(~all_maps & ((1u << inside) - 1));
@@ -514,9 +519,9 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
                 from = groups == 0 ? inside : __ffs(all_ends) - 1;
                 if (from >= 0 && !(~all_maps & ((1u << from) - 1))) break;
                 if (threadIdx.x == 0 && (polls & 63) == 0 &&
-                    (clock64() - since > kWaitLimit || *(volatile unsigned *)(p.control + ABORT))) {
+                    (clock64() - since > p.wait_limit || *(volatile unsigned *)(p.control + ABORT))) {
                     *(volatile unsigned *)(p.control + ABORT) = 1;
-                    failed = true;
+                    gave_up[polls & 1] = true;
                 }
                 if (from < 0 && __popc(all_maps) == asked) asked = min(2 * asked, most);
                 ask();
@@ -536,7 +541,7 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
                     in = through(*(const float4 *)(window + q * kEntry + 16 * lane), in);
             }
         }
-        if (failed) {  // (set before a barrier that everyone has passed)
+        if (failed) {  // the same in every warp
             if (threadIdx.x == 0) dev_fail(p.status, KDA_ERR_TIMEOUT);
             if (BY == BY_TMA && !BWD && landed) {  // the next tile's copies land before the block exits
                 TileAt u;
@@ -923,21 +928,9 @@ bool bad_ws(const kda_recurrence_desc_t *d, bool bwd, const void *ws, size_t byt
     return need > 0 && (!ws || bytes < need || off(ws, 16));
 }
 
-}  // namespace
-}  // namespace kda
-
-using namespace kda;
-
-extern "C" {
-
-size_t kda_recurrence_workspace_size(const kda_recurrence_desc_t *desc, int32_t backward) {
-    return check(desc) == KDA_OK ? layout_for(desc, backward != 0).total : 0;
-}
-
-kda_status_t kda_recurrence_forward(const kda_recurrence_desc_t *desc, const void *x, const float *g,
-                                    const float *h0, const int32_t *cu_seqlens, void *h,
-                                    float *h_final, void *workspace, size_t workspace_bytes,
-                                    int32_t *dev_status, void *stream) {
+kda_status_t forward(const kda_recurrence_desc_t *desc, const void *x, const float *g, const float *h0,
+                     const int32_t *cu_seqlens, void *h, float *h_final, void *workspace,
+                     size_t workspace_bytes, int32_t *dev_status, long long wait_limit, void *stream) {
     const kda_status_t rc = check(desc);
     if (rc != KDA_OK) return rc;
     const int size = size_of(desc);
@@ -950,16 +943,16 @@ kda_status_t kda_recurrence_forward(const kda_recurrence_desc_t *desc, const voi
     RecArgs a = make_args(desc);
     a.x = x; a.g = g; a.h0 = h0; a.cu = cu_seqlens; a.h = h; a.h_final = h_final;
     a.status = dev_status;
+    a.wait_limit = wait_limit;
     const bool pairs = desc->channels % 2 == 0 && a.x_stride % 2 == 0 && a.g_stride % 2 == 0 &&
                      !off(x, 2 * size) && !off(h, 2 * size) && !off(g, 8);
     return launch<false>(desc, a, pairs, workspace, (cudaStream_t)stream);
 }
 
-kda_status_t kda_recurrence_backward(const kda_recurrence_desc_t *desc, const void *d_h,
-                                     const void *x, const float *g, const void *h, const float *h0,
-                                     const int32_t *cu_seqlens, const float *d_h_final, void *dx,
-                                     float *dg, float *d_h0, void *workspace, size_t workspace_bytes,
-                                     int32_t *dev_status, void *stream) {
+kda_status_t backward(const kda_recurrence_desc_t *desc, const void *d_h, const void *x,
+                      const float *g, const void *h, const float *h0, const int32_t *cu_seqlens,
+                      const float *d_h_final, void *dx, float *dg, float *d_h0, void *workspace,
+                      size_t workspace_bytes, int32_t *dev_status, long long wait_limit, void *stream) {
     const kda_status_t rc = check(desc);
     if (rc != KDA_OK) return rc;
     const int size = size_of(desc);
@@ -975,10 +968,50 @@ kda_status_t kda_recurrence_backward(const kda_recurrence_desc_t *desc, const vo
     a.x = x; a.g = g; a.h0 = h0; a.cu = cu_seqlens; a.d = d_h; a.hs = h; a.d_final = d_h_final;
     a.dx = dx; a.dg = dg; a.d_h0 = d_h0;
     a.status = dev_status;
+    a.wait_limit = wait_limit;
     const bool pairs = desc->channels % 2 == 0 && a.g_stride % 2 == 0 && !off(d_h, 2 * size) &&
                      !off(h, 2 * size) && !off(dx, 2 * size) && !off(g, 8) && !off(dg, 8) &&
                      (!mix || (a.x_stride % 2 == 0 && !off(x, 2 * size)));
     return launch<true>(desc, a, pairs, workspace, (cudaStream_t)stream);
+}
+
+}  // namespace
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" {
+
+size_t kda_recurrence_workspace_size(const kda_recurrence_desc_t *desc, int32_t backward) {
+    return check(desc) == KDA_OK ? layout_for(desc, backward != 0).total : 0;
+}
+
+kda_status_t kda_recurrence_forward(const kda_recurrence_desc_t *desc, const void *x, const float *g,
+                                    const float *h0, const int32_t *cu_seqlens, void *h,
+                                    float *h_final, void *workspace, size_t workspace_bytes,
+                                    int32_t *dev_status, void *stream) {
+    return forward(desc, x, g, h0, cu_seqlens, h, h_final, workspace, workspace_bytes, dev_status,
+                   kWaitLimit, stream);
+}
+
+kda_status_t kda_recurrence_backward(const kda_recurrence_desc_t *desc, const void *d_h,
+                                     const void *x, const float *g, const void *h, const float *h0,
+                                     const int32_t *cu_seqlens, const float *d_h_final, void *dx,
+                                     float *dg, float *d_h0, void *workspace, size_t workspace_bytes,
+                                     int32_t *dev_status, void *stream) {
+    return backward(desc, d_h, x, g, h, h0, cu_seqlens, d_h_final, dx, dg, d_h0, workspace,
+                    workspace_bytes, dev_status, kWaitLimit, stream);
+}
+
+kda_status_t kda_selftest_recurrence_timeout(const kda_recurrence_desc_t *desc, const void *x,
+                                             const float *g, const void *h, void *out, float *dg,
+                                             void *workspace, size_t workspace_bytes,
+                                             int32_t *dev_status, void *stream) {
+    if (!dev_status || !desc || desc->write != KDA_WRITE_ADD) return KDA_ERR_INVALID_ARG;
+    return h ? backward(desc, x, nullptr, g, h, nullptr, nullptr, nullptr, out, dg, nullptr, workspace,
+                        workspace_bytes, dev_status, 0, stream)
+             : forward(desc, x, g, nullptr, nullptr, out, nullptr, workspace, workspace_bytes,
+                       dev_status, 0, stream);
 }
 
 kda_status_t kda_recurrence_step(const kda_recurrence_desc_t *desc, const void *x, const float *g,

@@ -845,3 +845,34 @@ def test_the_generator_moves_on_before_the_residual_norms_gradient(p):
         rng[1] += moves
         grads.append(torch.autograd.grad(sum(t.square().sum() for t in out), (h, y)))
     assert all(torch.equal(a, b) and bool((a != 0).any()) for a, b in zip(*grads))
+
+
+@pytest.mark.parametrize("C", [64, 63])
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("backward", [False, True], ids=["forward", "gradient"])
+def test_recurrence_gives_up_together(backward, act, C):
+    """Blocks without time to wait for one another: some give up in the middle of a long chain,
+    the status says so, nothing outside the outputs is written, and the next call is right."""
+    T, dt, g = 1 << 20, DT[act], _gen(C)
+    x, gate = _randn((T, C), g, dt), _gates(T, C, g)
+    want = kda.linear_recurrence(x, gate, want_final_state=False)[0]
+    grads = kda.linear_recurrence_backward(x, x, gate, want) if backward else None
+    L, desc = kda.lib(), kda._layer.RecurrenceDesc(0, 0, 1, T, C, kda._lm._ACT[dt], 0)
+    ws = torch.empty(L.kda_recurrence_workspace_size(desc, int(backward)) + 256, dtype=torch.uint8,
+                     device="cuda").fill_(7)
+    out = torch.full((T + 1, C), 7.0, device="cuda", dtype=dt)
+    dg = torch.full((T + 1, C), 7.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert L.kda_selftest_recurrence_timeout(
+        desc, x.data_ptr(), gate.data_ptr(), want.data_ptr() if backward else None, out.data_ptr(),
+        dg.data_ptr(), ws.data_ptr(), ws.numel() - 256, status.data_ptr(),
+        torch.cuda.current_stream().cuda_stream) == 0
+    assert int(status) == 5
+    assert bool((out[T] == 7).all()) and bool((dg[T] == 7).all()) and bool((ws[-256:] == 7).all())
+    # what a block did write before it gave up is right
+    done = out[:T] == (grads[0] if backward else want)
+    assert bool((done | (out[:T] == 7)).all())
+    assert torch.equal(kda.linear_recurrence(x, gate, want_final_state=False)[0], want)
+    if backward:
+        again = kda.linear_recurrence_backward(x, x, gate, want)
+        assert all(torch.equal(p, q) for p, q in zip(again, grads))

@@ -270,3 +270,13 @@ def test_gated_ffn_adjoints_stay_within_their_bound():
         adjoints = max(2 ** 30, 512 * 4 * tokens * planes)
         # dx and d_weight of so many tokens are one part each but for a few channels' sums
         assert size(d, 1) <= adjoints + terms + 4 * tokens * D + 2 ** 20, (tokens, hidden)
+
+
+def test_recurrence_selftest_refuses_arguments():
+    call, d = kda.lib().kda_selftest_recurrence_timeout, _rec(num_seqs=1)
+    assert call(d, A, A, None, A, None, None, 0, None, None) == INVALID  # nowhere to tell
+    assert call(None, A, A, None, A, None, None, 0, A, None) == INVALID
+    assert call(_rec(), A, A, None, A, None, None, 0, A, None) == INVALID  # two sequences
+    assert call(_rec(num_seqs=1, write=1), A, A, None, A, None, None, 0, A, None) == INVALID
+    assert call(d, A, A, A, A, None, None, 0, A, None) == INVALID  # a gradient without dg
+    assert call(_rec(num_seqs=1, tokens=1000), A, A, None, A, None, None, 0, A, None) == WORKSPACE
