@@ -152,7 +152,8 @@ __device__ __forceinline__ void store2(__nv_bfloat16 *p, int n, f2 v) {
 }
 
 // A word of maps or ends that nobody has written yet: a NaN that arithmetic does not make
-// (its own is 0x7fffffff; were this one ever to come up, that is stored instead).
+// (its own is 0x7fffffff; were this one ever to come up, that is stored instead).  The copies
+// that poll them promise no order and nothing wider than a word, so each word is looked at.
 constexpr uint32_t kNone = 0xffffffffu;
 __device__ __forceinline__ bool there(float v) { return __float_as_uint(v) != kNone; }
 __device__ __forceinline__ float told(float v) { return there(v) ? v : __uint_as_float(0x7fffffffu); }
@@ -455,7 +456,8 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
                 const uint8_t *at = window + q * kEntry;
                 if (!(have_maps >> q & 1)) {
                     const float4 v = *(const float4 *)(at + 16 * lane);
-                    if (__all_sync(0xffffffffu, there(v.x) && there(v.z))) have_maps |= 1u << q;
+                    if (__all_sync(0xffffffffu, there(v.x) && there(v.y) && there(v.z) && there(v.w)))
+                        have_maps |= 1u << q;
                 }
                 if (q >= inside && !(have_ends >> q & 1)) {
                     const float2 v = *(const float2 *)(at + kChan * 8 + 8 * lane);

@@ -876,3 +876,26 @@ def test_recurrence_gives_up_together(backward, act, C):
     if backward:
         again = kda.linear_recurrence_backward(x, x, gate, want)
         assert all(torch.equal(p, q) for p, q in zip(again, grads))
+
+
+@pytest.mark.parametrize("write", ["add", "mix"])
+@pytest.mark.parametrize("C", [128, 63])
+def test_recurrence_of_states_that_come_from_far(C, write):
+    """Slow gates over several groups of tiles, each state the end of a long look back (copies of
+    whole rows and of single channels), and every entry of it: zeros but for the first token."""
+    g = _gen(C)
+    lengths = [9000, 0, 4100]
+    cu, T = _cu(lengths), sum(lengths)
+    x, gate, h0 = _randn((T, C), g), -torch.rand((T, C), generator=g, device="cuda") * 1e-3, _randn((3, C), g)
+    d_h, d_final = _randn((T, C), g), _randn((3, C), g)
+    for zeros in (False, True):
+        if zeros:
+            x, d_h = torch.zeros_like(x), torch.zeros_like(d_h)
+        h, last = kda.linear_recurrence(x, gate, h0, cu, write=write)
+        ref, err, final, final_err = _recurrence64(x, gate, h0, cu.tolist(), write)
+        _within(h, ref, U * ref.abs() + 2 * err, "h")
+        _within(last, final, final_err + U * final.abs(), "h_final")
+        got = kda.linear_recurrence_backward(d_h, x, gate, h, h0, cu, d_final, write=write)
+        want = _recurrence_grad64(d_h, x, gate, h, h0, cu.tolist(), d_final, write)
+        for name, a, r, e in zip(("dx", "dg", "d_h0"), got, want[::2], want[1::2]):
+            _within(a, r, U * r.abs() + 2 * e, name)
