@@ -12,9 +12,8 @@ import ctypes
 import torch
 
 from . import _native as _k
-from ._lm import (DropoutDesc, _dropout, _first, _fit, _is, _lib, _out, _ptr, _status, _stream,
-                  _workspace)
-from ._native import _check
+from ._lm import (DropoutDesc, _call, _dropout, _first, _fit, _is, _lib, _out, _ptr, _size,
+                  _status, _workspace)
 
 WRITES = {"add": 0, "mix": 1}
 FFN_ACTS = {"sigmoid": 1, "silu": 2, "gelu": 3}
@@ -50,24 +49,6 @@ def bind(L):
                        ("kda_gated_ffn_workspace_size", [F, I])):
         fn = getattr(L, name)
         fn.restype, fn.argtypes = Z, args
-
-
-def _call(dev, name, *args):
-    """The entry point on the tensors' device and its current stream."""
-    fn = getattr(_lib(), name)
-    if torch._C._cuda_getDevice() == dev.index:
-        return _check(name, fn(*args, _stream(dev)))
-    with torch.cuda.device(dev):
-        _check(name, fn(*args, _stream(dev)))
-
-
-def _size(dev, name, *args):
-    """A workspace's size, which can depend on the device's SMs."""
-    fn = getattr(_lib(), name)
-    if torch._C._cuda_getDevice() == dev.index:
-        return fn(*args)
-    with torch.cuda.device(dev):
-        return fn(*args)
 
 
 # ------------------------------------------------------------ linear recurrence

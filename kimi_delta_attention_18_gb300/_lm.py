@@ -100,6 +100,30 @@ def _stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+def _there(dev):
+    """Whether ``dev`` is the current device: a launch goes to the current one, whatever device
+    its tensors and stream are on."""
+    return dev.index is None or torch._C._cuda_getDevice() == dev.index
+
+
+def _call(dev, name, *args):
+    """The entry point on the tensors' device and its current stream."""
+    fn = getattr(_lib(), name)
+    if _there(dev):
+        return _check(name, fn(*args, _stream(dev)))
+    with torch.cuda.device(dev):
+        _check(name, fn(*args, _stream(dev)))
+
+
+def _size(dev, name, *args):
+    """A workspace's size, which can depend on the device's SMs."""
+    fn = getattr(_lib(), name)
+    if _there(dev):
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
+
+
 def _first(t, name, dims):
     """Device and act_dtype of the operator's first tensor."""
     try:
@@ -186,10 +210,8 @@ def gated_norm(x, gate=None, weight=None, *, act="sigmoid", eps=1e-6, out=None, 
                       dev_status=dev_status)
     dev, desc = _gated(x, gate, weight, act, eps)
     out = _out(out, "out", x)
-    _check("kda_gated_norm_forward",
-           _lib().kda_gated_norm_forward(desc, x.data_ptr(), _ptr(gate), _ptr(weight),
-                                         out.data_ptr(), _status(dev_status, dev),
-                                         _stream(dev)))
+    _call(dev, "kda_gated_norm_forward", desc, x.data_ptr(), _ptr(gate), _ptr(weight),
+          out.data_ptr(), _status(dev_status, dev))
     return out
 
 
@@ -203,18 +225,15 @@ def gated_norm_backward(d_out, x, gate=None, weight=None, *, act="sigmoid", eps=
                       want_d_weight=want_d_weight, workspace=workspace, dev_status=dev_status)
     dev, desc = _gated(x, gate, weight, act, eps)
     _is(d_out, "d_out", x.dtype, x.shape, dev)
-    L = _lib()
     dx = _out(None, "dx", x)
     d_gate = None if gate is None else _out(None, "d_gate", x)
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(x.shape[2], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
-    _check("kda_gated_norm_backward",
-           L.kda_gated_norm_backward(desc, d_out.data_ptr(), x.data_ptr(), _ptr(gate),
-                                     _ptr(weight), dx.data_ptr(), _ptr(d_gate), _ptr(d_weight),
-                                     _ptr(workspace), ws_len, _status(dev_status, dev),
-                                     _stream(dev)))
+        workspace, ws_len = _workspace(workspace, _size(dev, "kda_norm_backward_workspace_size", desc), dev)
+    _call(dev, "kda_gated_norm_backward", desc, d_out.data_ptr(), x.data_ptr(), _ptr(gate),
+          _ptr(weight), dx.data_ptr(), _ptr(d_gate), _ptr(d_weight), _ptr(workspace), ws_len,
+          _status(dev_status, dev))
     return dx, d_gate, d_weight
 
 
@@ -256,16 +275,12 @@ def residual_norm(h, y=None, weight=None, *, scale=1.0, eps=1e-6, dropout=0.0, r
     if dropout:
         if y is None:
             raise ValueError("dropout needs y")
-        _check("kda_residual_norm_dropout_forward",
-               _lib().kda_residual_norm_dropout_forward(
-                   desc, _dropout(dropout, rng, site, dev), h.data_ptr(), y.data_ptr(),
-                   _ptr(weight), scale, new_h.data_ptr(), out.data_ptr(),
-                   _status(dev_status, dev), _stream(dev)))
+        _call(dev, "kda_residual_norm_dropout_forward", desc, _dropout(dropout, rng, site, dev),
+              h.data_ptr(), y.data_ptr(), _ptr(weight), scale, new_h.data_ptr(), out.data_ptr(),
+              _status(dev_status, dev))
         return new_h, out
-    _check("kda_residual_norm_forward",
-           _lib().kda_residual_norm_forward(desc, h.data_ptr(), _ptr(y), _ptr(weight), scale,
-                                            _ptr(new_h), out.data_ptr(),
-                                            _status(dev_status, dev), _stream(dev)))
+    _call(dev, "kda_residual_norm_forward", desc, h.data_ptr(), _ptr(y), _ptr(weight), scale,
+          _ptr(new_h), out.data_ptr(), _status(dev_status, dev))
     return (h if y is None else new_h), out
 
 
@@ -284,27 +299,21 @@ def residual_norm_backward(d_out, h_out, weight=None, d_h_out=None, *, scale=1.0
     _is(d_out, "d_out", h_out.dtype, h_out.shape, dev)
     if d_h_out is not None:
         _is(d_h_out, "d_h_out", h_out.dtype, h_out.shape, dev)
-    L = _lib()
     dh = _out(None, "dh", h_out)
     dropped = bool(dropout) and want_dy
     dy = _out(None, "dy", h_out) if dropped or (want_dy and scale != 1.0) else None
     d_weight, ws_len = None, 0
     if want_d_weight:
         d_weight = torch.empty(h_out.shape[1], dtype=torch.float32, device=dev)
-        workspace, ws_len = _workspace(workspace, L.kda_norm_backward_workspace_size(desc), dev)
+        workspace, ws_len = _workspace(workspace, _size(dev, "kda_norm_backward_workspace_size", desc), dev)
     if dropped:
-        _check("kda_residual_norm_dropout_backward",
-               L.kda_residual_norm_dropout_backward(
-                   desc, _dropout(dropout, rng, site, dev), d_out.data_ptr(), _ptr(d_h_out),
-                   h_out.data_ptr(), _ptr(weight), scale, dh.data_ptr(), dy.data_ptr(),
-                   _ptr(d_weight), _ptr(workspace), ws_len, _status(dev_status, dev),
-                   _stream(dev)))
+        _call(dev, "kda_residual_norm_dropout_backward", desc, _dropout(dropout, rng, site, dev),
+              d_out.data_ptr(), _ptr(d_h_out), h_out.data_ptr(), _ptr(weight), scale, dh.data_ptr(),
+              dy.data_ptr(), _ptr(d_weight), _ptr(workspace), ws_len, _status(dev_status, dev))
         return dh, dy, d_weight
-    _check("kda_residual_norm_backward",
-           L.kda_residual_norm_backward(desc, d_out.data_ptr(), _ptr(d_h_out), h_out.data_ptr(),
-                                        _ptr(weight), scale, dh.data_ptr(), _ptr(dy),
-                                        _ptr(d_weight), _ptr(workspace), ws_len,
-                                        _status(dev_status, dev), _stream(dev)))
+    _call(dev, "kda_residual_norm_backward", desc, d_out.data_ptr(), _ptr(d_h_out),
+          h_out.data_ptr(), _ptr(weight), scale, dh.data_ptr(), _ptr(dy), _ptr(d_weight),
+          _ptr(workspace), ws_len, _status(dev_status, dev))
     return dh, (dh if want_dy and scale == 1.0 else dy), d_weight
 
 
@@ -337,10 +346,8 @@ def embedding(table, ids, *, scale=1.0, out=None, dev_status=None, stream=None):
         out = torch.empty((T, D), dtype=table.dtype, device=dev)
     else:
         _is(out, "out", table.dtype, (T, D), dev)
-    _check("kda_embedding_forward",
-           _lib().kda_embedding_forward(EmbedDesc(_fit(T), _fit(V), _fit(D), dtype, kind, scale),
-                                        table.data_ptr(), ids.data_ptr(), out.data_ptr(),
-                                        _status(dev_status, dev), _stream(dev)))
+    _call(dev, "kda_embedding_forward", EmbedDesc(_fit(T), _fit(V), _fit(D), dtype, kind, scale),
+          table.data_ptr(), ids.data_ptr(), out.data_ptr(), _status(dev_status, dev))
     return out
 
 
@@ -359,12 +366,9 @@ def embedding_backward(d_out, ids, num_rows, *, scale=1.0, d_table=None, workspa
         d_table = torch.empty((num_rows, D), dtype=d_out.dtype, device=dev)
     else:
         _is(d_table, "d_table", d_out.dtype, (num_rows, D), dev)
-    L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_embedding_backward_workspace_size(desc), dev)
-    _check("kda_embedding_backward",
-           L.kda_embedding_backward(desc, d_out.data_ptr(), ids.data_ptr(), d_table.data_ptr(),
-                                    workspace.data_ptr(), ws_len, _status(dev_status, dev),
-                                    _stream(dev)))
+    workspace, ws_len = _workspace(workspace, _size(dev, "kda_embedding_backward_workspace_size", desc), dev)
+    _call(dev, "kda_embedding_backward", desc, d_out.data_ptr(), ids.data_ptr(), d_table.data_ptr(),
+          workspace.data_ptr(), ws_len, _status(dev_status, dev))
     return d_table
 
 
@@ -400,13 +404,10 @@ def linear_cross_entropy(x, weight, targets, *, ignore_index=-100, loss=None, ls
     T = x.shape[0]
     loss, lse = _vector(loss, "loss", T, dev), _vector(lse, "lse", T, dev)
     mean = torch.empty((), dtype=torch.float32, device=dev)
-    L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 0), dev)
-    _check("kda_linear_ce_forward",
-           L.kda_linear_ce_forward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
-                                   loss.data_ptr(), lse.data_ptr(), mean.data_ptr(),
-                                   workspace.data_ptr(), ws_len, _status(dev_status, dev),
-                                   _stream(dev)))
+    workspace, ws_len = _workspace(workspace, _size(dev, "kda_linear_ce_workspace_size", desc, 0), dev)
+    _call(dev, "kda_linear_ce_forward", desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+          loss.data_ptr(), lse.data_ptr(), mean.data_ptr(), workspace.data_ptr(), ws_len,
+          _status(dev_status, dev))
     return loss, lse, mean
 
 
@@ -426,11 +427,8 @@ def linear_cross_entropy_backward(x, weight, targets, lse, d_loss, *, ignore_ind
     _is(d_loss, "d_loss", torch.float32, (T,), dev)
     dx = _out(None, "dx", x) if want_dx else None
     d_weight = _out(None, "d_weight", weight) if want_d_weight else None
-    L = _lib()
-    workspace, ws_len = _workspace(workspace, L.kda_linear_ce_workspace_size(desc, 1), dev)
-    _check("kda_linear_ce_backward",
-           L.kda_linear_ce_backward(desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
-                                    lse.data_ptr(), d_loss.data_ptr(), _ptr(dx), _ptr(d_weight),
-                                    workspace.data_ptr(), ws_len, _status(dev_status, dev),
-                                    _stream(dev)))
+    workspace, ws_len = _workspace(workspace, _size(dev, "kda_linear_ce_workspace_size", desc, 1), dev)
+    _call(dev, "kda_linear_ce_backward", desc, x.data_ptr(), weight.data_ptr(), targets.data_ptr(),
+          lse.data_ptr(), d_loss.data_ptr(), _ptr(dx), _ptr(d_weight), workspace.data_ptr(), ws_len,
+          _status(dev_status, dev))
     return dx, d_weight

@@ -280,3 +280,74 @@ def test_recurrence_selftest_refuses_arguments():
     assert call(_rec(num_seqs=1, write=1), A, A, None, A, None, None, 0, A, None) == INVALID
     assert call(d, A, A, A, A, None, None, 0, A, None) == INVALID  # a gradient without dg
     assert call(_rec(num_seqs=1, tokens=1000), A, A, None, A, None, None, 0, A, None) == WORKSPACE
+
+
+class _Elsewhere:
+    """What the binding looks at of a contiguous tensor on a device that is not the current one."""
+    is_cuda, device = True, torch.device("cuda", 1)
+
+    def __init__(self, *shape, dtype=torch.float32):
+        self.shape, self.dtype = torch.Size(shape), dtype
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.shape.numel()
+
+    def dim(self):
+        return len(self.shape)
+
+    def element_size(self):
+        return 4
+
+    def data_ptr(self):
+        return A
+
+
+def test_calls_run_on_their_tensors_device(monkeypatch):
+    """Launches and workspace sizes belong to the tensors' device, whichever is current: a launch on
+    another one would read addresses that it does not have."""
+    from kimi_delta_attention_18_gb300 import _layer, _lm
+    current, seen = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.index = dev.index
+
+        def __enter__(self):
+            self.was, current[0] = current[0], self.index
+
+        def __exit__(self, *e):
+            current[0] = self.was
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: seen.append((name, current[0])) or 0
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    for module in (_lm, _layer):
+        monkeypatch.setattr(module, "_lib", lambda: Lib())
+        monkeypatch.setattr(module, "_workspace", lambda ws, need, dev: (_Elsewhere(16), 1 << 60))
+        monkeypatch.setattr(module, "_out", lambda out, name, like: _Elsewhere(*like.shape, dtype=like.dtype))
+    monkeypatch.setattr(_lm, "_stream", lambda dev: None)
+    monkeypatch.setattr(_lm._k, "_need", lambda t, *a, **k: t)
+    monkeypatch.setattr(torch, "empty", lambda shape, **k: _Elsewhere(*([shape] if isinstance(shape, int) else shape)))
+    x, w, rng = _Elsewhere(4, 8), _Elsewhere(2, 6, 8), _Elsewhere(2, dtype=torch.int64)
+    ids, vec, heads, h = _Elsewhere(4, dtype=torch.int32), _Elsewhere(4), _Elsewhere(4, 1, 8), _Elsewhere(4, 6)
+    drop = dict(dropout=0.5, rng=rng)
+    for call in (lambda: kda.gated_norm(heads, heads), lambda: kda.gated_norm_backward(heads, heads, heads),
+                 lambda: kda.residual_norm(x, x), lambda: kda.residual_norm_backward(x, x),
+                 lambda: kda.residual_norm(x, x, **drop), lambda: kda.residual_norm_backward(x, x, **drop),
+                 lambda: kda.embedding(x, ids), lambda: kda.embedding_backward(x, ids, 9),
+                 lambda: kda.linear_cross_entropy(x, x, ids),
+                 lambda: kda.linear_cross_entropy_backward(x, x, ids, vec, vec),
+                 lambda: kda.linear_recurrence(x, x), lambda: kda.linear_recurrence_backward(x, x, x, x),
+                 lambda: kda.linear_recurrence_step(x, x, x), lambda: kda.gated_ffn(x, w),
+                 lambda: kda.gated_ffn_backward(h, x, w), lambda: kda.dropout(x, 0.5, rng)):
+        del seen[:]
+        call()
+        # (the recurrence's workspace is the same on every device)
+        ran = [(name, on) for name, on in seen if name != "kda_recurrence_workspace_size"]
+        assert ran and all(on == 1 for _, on in ran), ran
+        assert current == [0]
