@@ -884,7 +884,7 @@ def test_recurrence_of_states_that_come_from_far(C, write):
     """Slow gates over several groups of tiles, each state the end of a long look back (copies of
     whole rows and of single channels), and every entry of it: zeros but for the first token."""
     g = _gen(C)
-    lengths = [9000, 0, 4100]
+    lengths = [5200, 0, 2300]
     cu, T = _cu(lengths), sum(lengths)
     x, gate, h0 = _randn((T, C), g), -torch.rand((T, C), generator=g, device="cuda") * 1e-3, _randn((3, C), g)
     d_h, d_final = _randn((T, C), g), _randn((3, C), g)
@@ -899,3 +899,65 @@ def test_recurrence_of_states_that_come_from_far(C, write):
         want = _recurrence_grad64(d_h, x, gate, h, h0, cu.tolist(), d_final, write)
         for name, a, r, e in zip(("dx", "dg", "d_h0"), got, want[::2], want[1::2]):
             _within(a, r, U * r.abs() + 2 * e, name)
+
+
+# Batches of up to 256 tokens have a kernel without a look back; 257 is the first with one.
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1, 200, 256, 257])
+def test_recurrence_of_few_tokens_strided_and_odd_bases(T, act):
+    g, dt, C = _gen(T), DT[act], 70
+    wide, wide_g = _randn((T, 3, C), g, dt), _gates(T, 2 * C, g).view(T, 2, C)
+    h0, d_final = _randn((1, C), g), _randn((1, C), g)
+    for x, gate in ((wide[:, 1], wide_g[:, 1]), (wide.view(T, 3 * C)[:, 1:C + 1], wide_g[:, 0]),
+                    (wide[:, 2], wide_g.view(T, 2 * C)[:, 3:C + 3])):
+        for write in ("add", "mix"):
+            h, last = kda.linear_recurrence(x, gate, h0, write=write)
+            ref, err, final, final_err = _recurrence64(x, gate, h0, [0, T], write)
+            _within(h, ref, ROUND[act] * ref.abs() * (1 + 2 * U) + 2 * err, "h")
+            _within(last, final, final_err + U * final.abs(), "h_final")
+            got = kda.linear_recurrence_backward(h, x, gate, h, h0, None, d_final, write=write)
+            want = _recurrence_grad64(h, x, gate, h, h0, [0, T], d_final, write)
+            for name, a, r, e in zip(("dx", "dg", "d_h0"), got, want[::2], want[1::2]):
+                _within(a, r, (ROUND[act] if name == "dx" else U) * r.abs() + 2 * e, name)
+            plain = kda.linear_recurrence(x.contiguous(), gate.contiguous(), h0, write=write)
+            assert torch.equal(h, plain[0]) and torch.equal(last, plain[1])
+
+
+@pytest.mark.parametrize("T", [3, 200, 256, 257])
+def test_bad_sequences_of_few_tokens_are_reported(T):
+    """A status, and nothing written outside the outputs."""
+    x, g = torch.zeros((T, 70), device="cuda"), torch.zeros((T, 70), device="cuda")
+    room = torch.full((T + 2, 70), 7.0, device="cuda")
+    for cu in ([0, T - 1], [1, T], [0, T - 1, 1, T], [0, -3, T], [0, T + 7, T], [0, 2 ** 30, T],
+               [0, -2 ** 31, T], [0, 2 ** 31 - 1, T]):
+        for backward in (False, True):
+            status = torch.zeros(1, dtype=torch.int32, device="cuda")
+            seqs = torch.tensor(cu, dtype=torch.int32, device="cuda")
+            if backward:
+                kda.linear_recurrence_backward(x, x, g, x, None, seqs, dev_status=status)
+            else:
+                kda.linear_recurrence(x, g, None, seqs, h=room[1:T + 1], dev_status=status)
+            assert int(status) == 1, (cu, backward)
+    assert bool((room[0] == 7).all()) and bool((room[-1] == 7).all())
+
+
+@pytest.mark.parametrize("C", [64, 7])
+@pytest.mark.parametrize("lengths", [[1], [120, 0, 80], [0, 256], [0, 0], [100, 157]],
+                         ids=lambda v: "-".join(map(str, v)))
+def test_recurrence_updates_states_of_few_tokens_in_place(lengths, C):
+    """h_final may be h0, and (through the C entry point) d_h0 the d_h_final that was given."""
+    g, T, N = _gen(sum(lengths)), sum(lengths), len(lengths)
+    cu, x, gate, h0 = _cu(lengths), _randn((T, C), g), _gates(T, C, g), _randn((N, C), g)
+    h, last = kda.linear_recurrence(x, gate, h0, cu)
+    dx, dg, d_h0 = kda.linear_recurrence_backward(x, x, gate, h, h0, cu, last)
+    state = h0.clone()
+    h2, same = kda.linear_recurrence(x, gate, state, cu, h_final=state)
+    assert same is state and torch.equal(state, last) and torch.equal(h2, h)
+    desc = kda._layer.RecurrenceDesc(0, 0, N, T, C, 0, 0)
+    ws = torch.empty(kda.lib().kda_recurrence_workspace_size(desc, 1) + 16, dtype=torch.uint8, device="cuda")
+    dx2, dg2 = torch.empty_like(x), torch.empty_like(gate)
+    assert kda.lib().kda_recurrence_backward(
+        desc, x.data_ptr(), None, gate.data_ptr(), h.data_ptr(), h0.data_ptr(), cu.data_ptr(),
+        state.data_ptr(), dx2.data_ptr(), dg2.data_ptr(), state.data_ptr(), ws.data_ptr(),
+        ws.numel(), None, torch.cuda.current_stream().cuda_stream) == 0
+    assert torch.equal(state, d_h0) and torch.equal(dx2, dx) and torch.equal(dg2, dg)
