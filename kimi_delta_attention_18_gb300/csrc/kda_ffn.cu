@@ -214,7 +214,11 @@ cudaError_t run_pack(const kda_ffn_desc_t *d, const Layout &l, const void *x, co
                             (float *)nullptr);
 }
 
-constexpr int kTileCost = 16;  // a tile's start and end, in columns' time
+// What a round of tiles takes, in the time of a pair's column (1.36 ns a stage of 64).  Measured,
+// BF16: a pair's tiles of 256 columns 347 ns a stage, of 192, 128 and 64 286, 285 and 283 (what
+// comes from L2 then bounds them); of single CTAs 497, 425, 334 and 282.  The width it leads to is
+// within 5 % of the best one from 515 x 1,003 to 7,168 x 14,336, 100 to 1,000 tokens, fp32 too.
+int round_cost(bool pair, int bn) { return pair ? (bn > 210 ? bn : 210) : 154 + bn * 5 / 6; }
 
 // Both projections of `cols` channels from the v0-th on, with the epilogue EPI.
 template <int EPI>
@@ -227,20 +231,21 @@ cudaError_t run_glu(GemmArgs p, const Layout &l, const CUtensorMap &tx, const CU
     p.N = 2 * cdiv(cols, 64) * 64;
     p.b_row0 = v0;
     p.k_blocks = cdiv(width, BK);
-    // Few rows: the width whose tiles leave the fewest columns' time unused in their last round
-    // over the SMs (256 x 7,168 x 14,336: 112 tiles of 256 columns for 76 pairs 90 us, 150 of
-    // 192 78).
+    // Few rows: the width, of pairs or of single CTAs, whose rounds over the SMs take the least
+    // (7,168 x 14,336, 256 tokens: 112 pairs' tiles of 256 columns for 76 pairs 88 us, 150 of 192
+    // 78; 300 tokens: 118 and 131, single CTAs 143 at best; 4,096 x 10,240, 150 tokens: 53 and 46,
+    // 320 pairs' tiles of 64 93).
     const int n = device_sms(), rows = cdiv(p.M, BM);
     if (rows <= 8) {
-        int best = 0;
+        long long best = 0;
         for (int bn = BN; bn >= 64; bn -= 64) {
-            const long long tiles = cdiv(p.N, bn);
-            const long long one = (rows * tiles + n - 1) / n;
-            const long long two = n < 2 ? one : (cdiv(rows, 2) * tiles + n / 2 - 1) / (n / 2);
-            const int cost = (int)(one < two ? one : two) * (bn + kTileCost);
-            if (!best || cost < best) {
+            for (int ctas = n < 2 ? 1 : 2; ctas > 0; --ctas) {
+                const long long tiles = (long long)cdiv(rows, ctas) * cdiv(p.N, bn);
+                const long long cost = cdiv(tiles, n / ctas) * (long long)round_cost(ctas == 2, bn);
+                if (best && cost >= best) continue;
                 best = cost;
                 p.bn = bn;
+                p.ctas = ctas;
             }
         }
     }

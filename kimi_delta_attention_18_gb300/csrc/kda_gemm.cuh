@@ -52,6 +52,7 @@ struct GemmArgs {
     int chunk;                 // FINE: stages per accumulator
     int m_tiles, n_tiles, bn;  // set at the launch (bn, columns per tile, unless the caller did:
                                // a multiple of 64)
+    int ctas;                  // CTAs of a tile, 0: as use_pairs says
     int b_row0;                // B's first row (of the vocabulary's piece)
     int bk_row0;               // the same where the contraction is along B's rows
     // EPI_STATS, EPI_DZ

@@ -490,7 +490,7 @@ template <int EPI, bool A_MN, bool B_MN, bool FINE, bool BF16>
 cudaError_t run_gemm(const GemmArgs &p, const CUtensorMap &ta, const CUtensorMap &tb,
                      cudaStream_t st) {
     const int n = device_sms();
-    return use_pairs(p, n) ? start_gemm<EPI, A_MN, B_MN, FINE, BF16, 2>(p, ta, tb, n, st)
+    return (p.ctas ? p.ctas == 2 : use_pairs(p, n)) ? start_gemm<EPI, A_MN, B_MN, FINE, BF16, 2>(p, ta, tb, n, st)
                            : start_gemm<EPI, A_MN, B_MN, FINE, BF16, 1>(p, ta, tb, n, st);
 }
 
