@@ -456,8 +456,8 @@ __global__ void __launch_bounds__(32 * warps_of(BWD, BY == BY_TMA),
                 const uint8_t *at = window + q * kEntry;
                 if (!(have_maps >> q & 1)) {
                     const float4 v = *(const float4 *)(at + 16 * lane);
-                    if (__all_sync(0xffffffffu, there(v.x) && there(v.y) && there(v.z) && there(v.w)))
-                        have_maps |= 1u << q;
+                    const bool a = there(v.x) && there(v.z), b = there(v.y) && there(v.w);
+                    if (!__any_sync(0xffffffffu, !a || !b)) have_maps |= 1u << q;
                 }
                 if (q >= inside && !(have_ends >> q & 1)) {
                     const float2 v = *(const float2 *)(at + kChan * 8 + 8 * lane);
