@@ -552,7 +552,13 @@ typedef struct {
  * from the sequence's h0 on.
  *   x           [T, C] act_dtype, tokens x_stride elements apart (a slice of a wider
  *               projection's output).
- *   g           [T, C] fp32 log-decays, normally <= 0 (-inf: the state starts anew).
+ *   g           [T, C] fp32 log-decays, normally <= 0 (-inf: the state starts anew; as by the
+ *               formula, an infinite or NaN state does not).  Positive ones let a state grow:
+ *               then the product of e^g over any run of tokens within 2,048 consecutive ones
+ *               must stay between 2^-126 and 2^127.  Tokens are joined by such products, and
+ *               beyond that range a state that is itself still finite may become infinite, NaN
+ *               or zero.  (With g <= 0 a product below 2^-126 may count as zero.)  A state that
+ *               has become infinite may be NaN from a later token on.
  *   h0          [N, C] fp32, or NULL (zero).
  *   cu_seqlens  int32 [N+1] as for the prefill (sequences may be empty), or NULL with
  *               N = 1: one sequence.
@@ -613,7 +619,8 @@ typedef struct {
  *     h = act(x weight[0]^T) * (x weight[1]^T),   x [T, D], h [T, F];
  * the projections are never stored.  BF16: products of BF16 on tensor cores with fp32
  * accumulation; F32: each operand as three BF16 terms, six products, to about fp32's
- * own accuracy.  x and weight 16-byte aligned (tensor-map copies).  Workspace:
+ * own accuracy (of an infinite operand, or one that BF16 rounds to infinity, those terms are
+ * NaN).  x and weight 16-byte aligned (tensor-map copies).  Workspace:
  * kda_gated_ffn_workspace_size(desc, 0), 16-byte aligned (may be NULL when that is 0).
  * dev_status, here and below: KDA_ERR_TIMEOUT if a bounded wait gave up.
  */

@@ -98,6 +98,7 @@ def linear_recurrence(x, g, h0=None, cu_seqlens=None, *, write="add", h=None, h_
     w 1 (write "add") or ``1 - e^{g_t}`` ("mix") (see kda_recurrence_forward in kda.h).
     x ``[T, C]`` (fp32 or bf16) and the log-decay g ``[T, C]`` (fp32), tokens possibly
     strided; h0 ``[N, C]`` fp32 or None; cu_seqlens int32 ``[N+1]`` (None = one sequence).
+    Where g is positive, products of e^g over up to 2,048 tokens must stay within fp32.
     Returns ``(h [T, C], h_final [N, C] fp32)``."""
     if stream is not None:
         return _k._on(stream, linear_recurrence, x, g, h0, cu_seqlens, write=write, h=h,

@@ -961,3 +961,23 @@ def test_recurrence_updates_states_of_few_tokens_in_place(lengths, C):
         state.data_ptr(), dx2.data_ptr(), dg2.data_ptr(), state.data_ptr(), ws.data_ptr(),
         ws.numel(), None, torch.cuda.current_stream().cuda_stream) == 0
     assert torch.equal(state, d_h0) and torch.equal(dx2, dx) and torch.equal(dg2, dg)
+
+
+@pytest.mark.parametrize("write", ["add", "mix"])
+@pytest.mark.parametrize("C", [128, 63])
+def test_recurrence_of_growing_states(C, write):
+    """Positive gates whose factors' products over 2,048 tokens stay within fp32: states grow by
+    e^60 and come back, over several groups of tiles."""
+    g, T = _gen(C), 6000
+    drift = 0.03 * torch.where(torch.arange(T, device="cuda") // 2000 % 2 == 0, 1.0, -1.0)
+    gate = drift[:, None] + 0.02 * (torch.rand((T, C), generator=g, device="cuda") - 0.5)
+    x, h0, d_h = _randn((T, C), g), _randn((1, C), g, std=1e-8), _randn((T, C), g)
+    h, last = kda.linear_recurrence(x, gate, h0, write=write)
+    ref, err, final, final_err = _recurrence64(x, gate, h0, [0, T], write)
+    assert float(ref.abs().max()) > 1e20
+    _within(h, ref, U * ref.abs() + 2 * err, "h")
+    _within(last, final, final_err + U * final.abs(), "h_final")
+    got = kda.linear_recurrence_backward(d_h, x, gate, h, h0, write=write)
+    want = _recurrence_grad64(d_h, x, gate, h, h0, [0, T], None, write)
+    for name, a, r, e in zip(("dx", "dg", "d_h0"), got, want[::2], want[1::2]):
+        _within(a, r, U * r.abs() + 2 * e.abs(), name)  # (1 - e^g is negative here)
