@@ -100,28 +100,25 @@ def _stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
-def _there(dev):
-    """Whether ``dev`` is the current device: a launch goes to the current one, whatever device
-    its tensors and stream are on."""
-    return dev.index is None or torch._C._cuda_getDevice() == dev.index
-
-
 def _call(dev, name, *args):
-    """The entry point on the tensors' device and its current stream."""
-    fn = getattr(_lib(), name)
-    if _there(dev):
-        return _check(name, fn(*args, _stream(dev)))
-    with torch.cuda.device(dev):
-        _check(name, fn(*args, _stream(dev)))
+    """The entry point on the tensors' device and its current stream (a launch goes to the current
+    device, whatever device its tensors and stream are on)."""
+    index = dev.index
+    if index is None or torch._C._cuda_getDevice() == index:
+        rc = getattr(_lib(), name)(*args, _stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = getattr(_lib(), name)(*args, _stream(dev))
+    if rc:
+        _check(name, rc)
 
 
 def _size(dev, name, *args):
     """A workspace's size, which can depend on the device's SMs."""
-    fn = getattr(_lib(), name)
-    if _there(dev):
-        return fn(*args)
+    if dev.index is None or torch._C._cuda_getDevice() == dev.index:
+        return getattr(_lib(), name)(*args)
     with torch.cuda.device(dev):
-        return fn(*args)
+        return getattr(_lib(), name)(*args)
 
 
 def _first(t, name, dims):
