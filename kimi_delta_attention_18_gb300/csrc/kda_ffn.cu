@@ -20,13 +20,16 @@ namespace {
 // A warp takes two channels, four rows of W, and their products with every token's x, in fp32
 // pairs; where channels are few, up to eight warps share two of them, a slice of D each, and
 // their sums are joined in order.
-// BF16, one token: 7,168 x 14,336 63.5 us, by tiles 67.1; 1,024 x 2,816 5.3 and 8.4.  Two: 73.9 and
-// 67.1, but 2,048 x 5,632 14.8 and 15.2; four: 77.0 and 67.2, 14.3 and 8.4.  fp32 up to eight:
-// 7,168 x 14,336 123-298 us, by tiles 345.
+// BF16, one token: 7,168 x 14,336 65.0 us, by tiles 68.5; 1,024 x 2,816 5.3 and 8.4.  Two: 4,096 x
+// 4,096 16.4 and 23.3, 2,048 x 5,632 15.0 and 15.4, 4,096 x 10,240 33.6 and 33.4; element by element
+// (odd widths) 515 x 1,003 4.7 and 8.2, 1,001 x 2,817 14.4 and 13.5, 2,046 x 5,633 35 and 30.
+// fp32: eight tokens 512 x 1,408 16.6 and 17.6, 4,096 x 4,096 66 and 103, 7,168 x 14,336 303 and
+// 345 (one to four 124-128).
 constexpr int kFewWarps = 8;
 bool few(const kda_ffn_desc_t *d) {
     if (d->act_dtype != KDA_DTYPE_BF16) return d->tokens <= 8;
-    return d->tokens == 1 || (d->tokens == 2 && (long long)d->width * d->hidden <= 1ll << 24);
+    const long long most = 1ll << (d->width % 8 == 0 ? 24 : 21);  // weights of each projection
+    return d->tokens == 1 || (d->tokens == 2 && (long long)d->width * d->hidden <= most);
 }
 
 template <typename T, int VEC>
