@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
                     float v[32];
                     tmem_ld32(src + NB * (i & 1) + kNext * ch, v);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) add2(acc[ch][j], acc[ch][j + 1], v[j], v[j + 1]);
+                    for (int j = 0; j < 32; j += 2) add_pair(acc[ch][j], acc[ch][j + 1], v[j], v[j + 1]);
                 }
                 tc_fence_before();
                 __syncwarp();

@@ -531,7 +531,7 @@ struct Row {
     }
 };
 
-__device__ __forceinline__ void add2(float &x, float &y, float ax, float ay) {
+__device__ __forceinline__ void add_pair(float &x, float &y, float ax, float ay) {
     asm("{\n\t.reg .b64 a, b;\n\tmov.b64 a, {%0, %1};\n\tmov.b64 b, {%2, %3};\n\t"
         "add.rn.f32x2 a, a, b;\n\tmov.b64 {%0, %1}, a;\n\t}"
         : "+f"(x), "+f"(y)

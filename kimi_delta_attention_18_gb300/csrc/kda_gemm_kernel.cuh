@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         tmem_ld32(src + BN * (i & 1) + 32 * ch, v);
 #pragma unroll
                         for (int j = 0; j < 32; j += 2)
-                            add2(acc[ch][j], acc[ch][j + 1], v[j], v[j + 1]);
+                            add_pair(acc[ch][j], acc[ch][j + 1], v[j], v[j + 1]);
                     }
                     release();
                 }

@@ -97,15 +97,8 @@ struct Keep {
         return v & ((lo >= limit ? 0xffffu : 0u) | (hi >= limit ? 0xffff0000u : 0u));
     }
 
-    // The dropped of a piece's elements become zeros (whatever they were): from its bits, or
-    // for the columns from c on of a row.
-    static __device__ __forceinline__ void apply(Piece<__nv_bfloat16, 8> &p, uint32_t m) {
-        auto halves = [&](uint32_t v, int j) {
-            return v & ((m >> j & 1 ? 0xffffu : 0u) | (m >> j & 2 ? 0xffff0000u : 0u));
-        };
-        p.raw = make_uint4(halves(p.raw.x, 0), halves(p.raw.y, 2), halves(p.raw.z, 4),
-                           halves(p.raw.w, 6));
-    }
+    // The dropped of a piece's elements, the columns from c on of a row, become zeros (whatever
+    // they were).
     template <bool SHIFT, typename T, int VEC>
     __device__ __forceinline__ void piece(Piece<T, VEC> &p, long long row, int c) const {
         if constexpr (!SHIFT && VEC == 8) {

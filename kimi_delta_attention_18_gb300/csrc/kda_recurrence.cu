@@ -26,7 +26,7 @@
 // (TMA); tiles are large and few are in flight.  Measured, in ms (forward 81,920 x 7,168 and
 // gradient of 81,920 x 4,096, BF16, mix: their bytes take 0.69 and 0.79; forward 1,048,576 x
 // 512, add, 0.63): flags, and maps read four at a time, 1.62, 2.36, 3.75; words that mark
-// themselves 0.82, 1.06, 3.39; as it is now 0.84, 0.83, 1.22.
+// themselves 0.82, 1.06, 3.39; as it is now 0.84, 0.83, 1.19.
 //
 // Batches of few tokens have no look back: a block takes all tiles of a sequence's 64
 // channels one after another.
@@ -46,15 +46,18 @@ constexpr int kChan = 64;
 // With TMA one block of 256 tokens to an SM has all of its registers in use (a warp holds its
 // 32 tokens' factors and terms), and a chain has few steps: 81,920 x 7,168 BF16 takes 823 us,
 // two blocks of 128 810, three 950; 1,048,576 x 512 1.22, 1.76 and 2.51 ms; 81,920 x 2,048
-// fp32 297 us, 311, 311.  Loads of single lanes want warps: 81,920 x 2,047 BF16 790 us with
-// three blocks of eight warps, 1,414 as with TMA.  The backward pass holds nothing: with TMA
+// fp32, four sequences, 297 us, 311, 311 (one sequence takes 316).  Loads of single lanes want
+// warps: 81,920 x 2,047 BF16 800 us with three blocks of eight warps, 1,414 as with TMA, although
+// with 80 registers 390 to 480 bytes a thread of the held tile are in local memory (walking, 140
+// to 160).  The backward pass holds nothing: with TMA
 // 128 tokens 834 us (81,920 x 4,096), 64 872; lane by lane 147 and 116 (20,011 x 1,001 fp32).
 constexpr int warps_of(bool bwd, bool tma) { return bwd && !tma ? 4 : 8; }
 constexpr int tok_of(bool bwd, bool tma) { return !bwd && tma ? 32 : 16; }
 constexpr int tile_of(bool bwd, bool tma) { return warps_of(bwd, tma) * tok_of(bwd, tma); }
 constexpr long long kWaitLimit = 4000000000ll;  // ~2 s of SM clocks
 // Up to so many tokens one block walks a sequence; beyond, a launch lays out the tiles of a
-// batch first (400 x 512 BF16: walking 17 us; 1,000 x 512: 4 and 9).
+// batch first (BF16 forward, 512 channels: 257 tokens walking 9.2 us, so 7.4, 400 12.4 and 8.4;
+// 7,168: 11.1 and 12.9, 15.6 and 14.1).
 constexpr int kWalkTokens = 256;
 
 struct RecArgs {
