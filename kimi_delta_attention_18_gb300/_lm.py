@@ -9,6 +9,7 @@ outputs; the tensors' memory is kept for both streams), and every library error 
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -100,11 +101,15 @@ def _stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
+@functools.lru_cache(maxsize=None)
+def _several():
+    return torch.cuda.device_count() > 1
+
+
 def _call(dev, name, *args):
     """The entry point on the tensors' device and its current stream (a launch goes to the current
     device, whatever device its tensors and stream are on)."""
-    index = dev.index
-    if index is None or torch._C._cuda_getDevice() == index:
+    if not _several() or dev.index is None or torch._C._cuda_getDevice() == dev.index:
         rc = getattr(_lib(), name)(*args, _stream(dev))
     else:
         with torch.cuda.device(dev):
@@ -115,7 +120,7 @@ def _call(dev, name, *args):
 
 def _size(dev, name, *args):
     """A workspace's size, which can depend on the device's SMs."""
-    if dev.index is None or torch._C._cuda_getDevice() == dev.index:
+    if not _several() or dev.index is None or torch._C._cuda_getDevice() == dev.index:
         return getattr(_lib(), name)(*args)
     with torch.cuda.device(dev):
         return getattr(_lib(), name)(*args)

@@ -325,6 +325,7 @@ def test_calls_run_on_their_tensors_device(monkeypatch):
         def __getattr__(self, name):
             return lambda *a: seen.append((name, current[0])) or 0
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    monkeypatch.setattr(_lm, "_several", lambda: True, raising=False)
     monkeypatch.setattr(torch.cuda, "device", Device)
     for module in (_lm, _layer):
         monkeypatch.setattr(module, "_lib", lambda: Lib())
