@@ -981,3 +981,20 @@ def test_recurrence_of_growing_states(C, write):
     want = _recurrence_grad64(d_h, x, gate, h, h0, [0, T], None, write)
     for name, a, r, e in zip(("dx", "dg", "d_h0"), got, want[::2], want[1::2]):
         _within(a, r, U * r.abs() + 2 * e.abs(), name)  # (1 - e^g is negative here)
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("T,D,F", [
+    (150, 24, 1000), (300, 24, 5632), (600, 24, 5632), (130, 24, 10240), (900, 24, 10239), (100, 24, 10240),
+    (129, 24, 4097), (400, 24, 2816)])
+def test_gated_ffn_of_every_width_of_tile(T, D, F, kind):
+    """Few rows take tiles of 64 to 256 columns, of pairs of CTAs or of single ones, by how their
+    rounds over the SMs come out."""
+    g, dt = _gen(T + F), DT[kind]
+    x, w, d_h = _randn((T, D), g, dt), _randn((2, F, D), g, dt, 1.5 / math.sqrt(D)), _randn((T, F), g, dt)
+    ref, bound = _ffn64(x, w, "silu", kind=kind)
+    _within(kda.gated_ffn(x, w), ref, bound, "h")
+    dx, dw = kda.gated_ffn_backward(d_h, x, w)
+    rx, bx, rw, bw = _ffn64(x, w, "silu", d_h, kind)
+    _within(dx, rx, bx, "dx")
+    _within(dw, rw, bw, "d_weight")
